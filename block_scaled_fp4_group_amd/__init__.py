@@ -27,7 +27,8 @@ MOE_ALGO_AUTO, MOE_ALGO_DECODE, MOE_ALGO_PREFILL = 0, 1, 2
 EXPORTS = ("moe_status_string", "moe_last_error", "moe_version", "moe_route", "moe_permute_workspace_bytes",
            "moe_permute", "moe_route_permute", "moe_fp4_grouped_gemm", "moe_combine", "fp4_transcode_mx_to_nv", "moe_quantize_nvfp4",
            "moe_fp4_tile_weights", "moe_route_permute_noalloc", "moe_quantize_mxfp8", "moe_quantize_nvfp4_planes",
-           "moe_route_gemv_workspace_bytes", "moe_route_gemv", "moe_reap_saliency_accumulate", "moe_fp4_compact_mx")
+           "moe_route_gemv_workspace_bytes", "moe_route_gemv", "moe_reap_saliency_accumulate", "moe_fp4_compact_mx",
+           "moe_kv_slots", "moe_qk_norm_rope", "moe_attn_prompt", "moe_attn_decode_workspace_bytes", "moe_attn_decode")
 
 
 class RouteParams(ctypes.Structure):
@@ -52,6 +53,26 @@ class Out(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("output_scale", ctypes.c_float), ("dequant", ctypes.c_void_p), ("format", ctypes.c_int32),
                 ("row_sumsq", ctypes.c_void_p)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32)]
+
+
+class RopeParams(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("v_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("max_position", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class AttnParams(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("k_dim", ctypes.c_int32),
+                ("v_dim", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 def _load() -> ctypes.CDLL:
@@ -96,6 +117,19 @@ def _load() -> ctypes.CDLL:
     lib.moe_quantize_mxfp8.argtypes = [vp, i64, i32, vp, vp, vp]
     lib.moe_quantize_nvfp4_planes.restype = i32
     lib.moe_quantize_nvfp4_planes.argtypes = [vp, i64, i32, f32, vp, vp, vp]
+    lib.moe_kv_slots.restype = i32
+    lib.moe_kv_slots.argtypes = [vp, vp, i32, vp, i64, i32, vp, i64, i32, i32, i64, vp, vp, vp, vp, vp]
+    heads, cache = ctypes.POINTER(Heads), ctypes.POINTER(KvCache)
+    lib.moe_qk_norm_rope.restype = i32
+    lib.moe_qk_norm_rope.argtypes = [heads, heads, heads, i64, ctypes.POINTER(RopeParams), vp, vp, vp, vp, heads, heads,
+                                     cache, vp, vp]
+    lib.moe_attn_prompt.restype = i32
+    lib.moe_attn_prompt.argtypes = [heads, heads, heads, vp, vp, i32, i64, i64, ctypes.POINTER(AttnParams), heads, vp, vp]
+    lib.moe_attn_decode_workspace_bytes.restype = sz
+    lib.moe_attn_decode_workspace_bytes.argtypes = [i32, i64, i64, ctypes.POINTER(AttnParams)]
+    lib.moe_attn_decode.restype = i32
+    lib.moe_attn_decode.argtypes = [heads, cache, vp, i64, i32, vp, i32, i64, vp, i32, i64, ctypes.POINTER(AttnParams),
+                                    heads, vp, vp, sz, vp]
     lib.moe_fp4_tile_weights.restype = i32
     lib.moe_fp4_tile_weights.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp]
     return lib
@@ -389,6 +423,235 @@ def quantize_nvfp4_planes(x: torch.Tensor, input_scale: float = 1.0, planes=None
     _check(lib.moe_quantize_nvfp4_planes(_ptr(x), rows, k, float(input_scale), _ptr(planes), _ptr(scales),
                                          _stream(stream)), "moe_quantize_nvfp4_planes")
     return planes, scales
+
+
+# ----------------------------------------------------------------- attention
+def _want(t, name: str, dtype, ndim: int, device):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.ndim != ndim or t.device != device:
+        raise ValueError(f"{name} must be a {ndim}-d {dtype} tensor on {device}")
+
+
+def _want_flat(t, name: str, dtype, ndim: int, device):
+    _want(t, name, dtype, ndim, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _heads(t, name: str, device, heads=None, dim=None) -> Heads:
+    """bf16 [tokens, heads, dim], any token and head strides, dim contiguous."""
+    _want(t, name, torch.bfloat16, 3, device)
+    if (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} does not fit (heads {heads}, dim {dim})")
+    ts, hs, ds = t.stride()
+    if ds != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # the strides of dimensions of one element say nothing
+    hs = hs if t.shape[1] > 1 else t.shape[2]
+    ts = ts if t.shape[0] > 1 else (t.shape[1] - 1) * hs + t.shape[2]
+    return Heads(t.data_ptr(), ts, hs)
+
+
+def _cuda(t, name: str):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.device
+
+
+def _made(stream, *tensors):
+    """Tensors allocated here belong to the current stream; a call on another one has to be known to the allocator."""
+    if stream is not None and stream != torch.cuda.current_stream():
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def kv_slots(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
+             page_size: int, max_new: int, position_base: int = 0, slots=None, positions=None, cu_new=None, counts=None,
+             stream=None):
+    """Cache slots of a step's new tokens.  int32 tensors: cached_lens, new_lens [B], free_pages [F], block_table
+    [B, blocks] (new pages are entered in place).  -> (slots [max_new], positions [max_new], cu_new [B + 1],
+    counts [3]: pages taken, pages needed, tokens without a slot).  ``position_base``: length of a shared prefix."""
+    dev = _cuda(cached_lens, "cached_lens")
+    i32 = torch.int32
+    B = cached_lens.shape[0]
+    _want_flat(cached_lens, "cached_lens", i32, 1, dev)
+    _want_flat(new_lens, "new_lens", i32, 1, dev)
+    _want_flat(free_pages, "free_pages", i32, 1, dev)
+    _want(block_table, "block_table", i32, 2, dev)
+    if new_lens.shape[0] != B or block_table.shape[0] != B or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("new_lens and block_table must have a row for each request, rows contiguous")
+    stride = block_table.stride(0) if B > 1 else block_table.shape[1]
+    made = []
+    if slots is None:
+        made.append(slots := torch.empty(max_new, dtype=i32, device=dev))
+    if positions is None:
+        made.append(positions := torch.empty(max_new, dtype=i32, device=dev))
+    if cu_new is None:
+        made.append(cu_new := torch.empty(B + 1, dtype=i32, device=dev))
+    if counts is None:
+        made.append(counts := torch.empty(3, dtype=i32, device=dev))
+    for t, name, n in ((slots, "slots", max_new), (positions, "positions", max_new), (cu_new, "cu_new", B + 1),
+                       (counts, "counts", 3)):
+        _want_flat(t, name, i32, 1, dev)
+        if t.shape[0] < n:
+            raise ValueError(f"{name} needs {n} elements")
+    _check(lib.moe_kv_slots(_ptr(cached_lens), _ptr(new_lens), B, _ptr(free_pages), free_pages.shape[0], page_size,
+                            _ptr(block_table), stride, block_table.shape[1], position_base, max_new, _ptr(slots),
+                            _ptr(positions), _ptr(cu_new), _ptr(counts), _stream(stream)), "moe_kv_slots")
+    _made(stream, *made)
+    return slots, positions, cu_new, counts
+
+
+def _cache(k_cache, v_cache, device, kv_heads: int, k_dim: int) -> KvCache:
+    _want_flat(k_cache, "k_cache", torch.bfloat16, 4, device)
+    _want_flat(v_cache, "v_cache", torch.bfloat16, 4, device)
+    if k_cache.shape[:3] != v_cache.shape[:3] or k_cache.shape[2] != kv_heads or k_cache.shape[3] != k_dim:
+        raise ValueError(f"k_cache {tuple(k_cache.shape)} / v_cache {tuple(v_cache.shape)} do not fit "
+                         f"(pages, page_size, {kv_heads}, {k_dim})")
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], k_cache.shape[1])
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor],
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 interleaved: bool = False, v: Optional[torch.Tensor] = None, k_cache: Optional[torch.Tensor] = None,
+                 v_cache: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None, want_k: bool = True,
+                 q_out=None, k_out=None, stream=None):
+    """RMS norm of each head of q [T, Hq, D] and k [T, Hkv, D] (weights float32 [D]; None: no norm), the rotation by
+    ``cos_sin`` float32 [positions, rot_dim] (cosines, then sines; None: no rotation), and with a cache the write of
+    the finished keys and of v [T, Hkv, Dv] to its rows ``slots``.  -> (q_out, k_out); k_out is None with
+    ``want_k=False`` (cache only).  q_out / k_out may be q / k."""
+    dev = _cuda(q, "q")
+    hq = _heads(q, "q", dev)
+    T, Hq, D = q.shape
+    hk = _heads(k, "k", dev, dim=D)
+    Hkv = k.shape[1]
+    f32, i32 = torch.float32, torch.int32
+    if k.shape[0] != T:
+        raise ValueError("q and k must have the same tokens")
+    rot = 0
+    if cos_sin is not None:
+        _want_flat(cos_sin, "cos_sin", f32, 2, dev)
+        _want_flat(positions, "positions", i32, 1, dev)
+        if positions.shape[0] < T:
+            raise ValueError("positions needs an entry for each token")
+        rot = cos_sin.shape[1]
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _want_flat(t, name, f32, 1, dev)
+            if t.shape[0] != D:
+                raise ValueError(f"{name} needs {D} elements")
+    cache = hv = None
+    Dv = 0
+    if k_cache is not None:
+        cache = _cache(k_cache, v_cache, dev, Hkv, D)
+        Dv = v_cache.shape[3]
+        hv = _heads(v, "v", dev, Hkv, Dv)
+        _want_flat(slots, "slots", i32, 1, dev)
+        if v.shape[0] != T or slots.shape[0] < T:
+            raise ValueError("v and slots need an entry for each token")
+    made = []
+    if q_out is None:
+        made.append(q_out := torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev))
+    if k_out is None and want_k:
+        made.append(k_out := torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=dev))
+    ho = _heads(q_out, "q_out", dev, Hq, D)
+    hko = None if k_out is None else _heads(k_out, "k_out", dev, Hkv, D)
+    if q_out.shape[0] != T or (k_out is not None and k_out.shape[0] != T):
+        raise ValueError("q_out and k_out need a row for each token")
+    p = RopeParams(Hq, Hkv, D, Dv, rot, int(interleaved), 0 if cos_sin is None else cos_sin.shape[0], eps)
+    _check(lib.moe_qk_norm_rope(hq, hk, hv, T, p, _ptr(positions), _ptr(cos_sin), _ptr(q_weight), _ptr(k_weight), ho, hko,
+                                cache, _ptr(slots), _stream(stream)), "moe_qk_norm_rope")
+    _made(stream, *made)
+    return q_out, k_out
+
+
+def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                cu_k: Optional[torch.Tensor] = None, scale: Optional[float] = None, out=None, lse=None,
+                want_lse: bool = False, stream=None):
+    """Causal attention over packed prompts: q [Tq, Hq, D], k [Tk, Hkv, D], v [Tk, Hkv, Dv], offsets cu_q, cu_k int32
+    [B + 1] (cu_k None: cu_q).  Query i of a sequence sees keys 0 .. i + Lk - Lq.  -> (out [Tq, Hq, Dv], lse float32
+    [Tq, Hq] or None).  Rows outside the offsets' ranges are not written."""
+    dev = _cuda(q, "q")
+    cu_k = cu_q if cu_k is None else cu_k
+    hq = _heads(q, "q", dev)
+    Tq, Hq, D = q.shape
+    hk = _heads(k, "k", dev, dim=D)
+    Tk, Hkv, _ = k.shape
+    hv = _heads(v, "v", dev, heads=Hkv)
+    Dv = v.shape[2]
+    _want_flat(cu_q, "cu_q", torch.int32, 1, dev)
+    _want_flat(cu_k, "cu_k", torch.int32, 1, dev)
+    if v.shape[0] != Tk or cu_q.shape != cu_k.shape or cu_q.shape[0] < 1:
+        raise ValueError("v needs a row for each key, cu_q and cu_k an entry for each sequence and the end")
+    made = []
+    if out is None:
+        made.append(out := torch.empty((Tq, Hq, Dv), dtype=torch.bfloat16, device=dev))
+    if lse is None and want_lse:
+        made.append(lse := torch.empty((Tq, Hq), dtype=torch.float32, device=dev))
+    ho = _heads(out, "out", dev, Hq, Dv)
+    if lse is not None:
+        _want_flat(lse, "lse", torch.float32, 2, dev)
+    if out.shape[0] != Tq or (lse is not None and lse.shape != (Tq, Hq)):
+        raise ValueError("out and lse need a row for each query")
+    p = AttnParams(Hq, Hkv, D, Dv, D ** -0.5 if scale is None else scale)
+    _check(lib.moe_attn_prompt(hq, hk, hv, _ptr(cu_q), _ptr(cu_k), cu_q.shape[0] - 1, Tq, Tk, p, ho, _ptr(lse),
+                               _stream(stream)), "moe_attn_prompt")
+    _made(stream, *made)
+    return out, lse
+
+
+def attn_decode_workspace_bytes(num_requests: int, prefix_len: int, max_len: int, q_heads: int, kv_heads: int, k_dim: int,
+                                v_dim: int) -> int:
+    p = AttnParams(q_heads, kv_heads, k_dim, v_dim, 1.0)
+    return int(lib.moe_attn_decode_workspace_bytes(num_requests, prefix_len, max_len, p))
+
+
+def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                lens: torch.Tensor, max_len: int, prefix_table: Optional[torch.Tensor] = None, prefix_len: int = 0,
+                scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None, out=None, lse=None,
+                want_lse: bool = False, stream=None):
+    """One query per request, q [B, Hq, D], over the paged cache: the shared prefix (``prefix_len`` keys in the pages
+    ``prefix_table``), then the request's own ``lens`` keys in its ``block_table`` pages (int32).  ``max_len``: a
+    longest own length known on the host.  -> (out [B, Hq, Dv], lse float32 [B, Hq] or None)."""
+    dev = _cuda(q, "q")
+    hq = _heads(q, "q", dev)
+    B, Hq, D = q.shape
+    if k_cache.ndim != 4 or v_cache.ndim != 4:
+        raise ValueError("k_cache and v_cache must be [pages, page_size, heads, dim]")
+    Hkv, Dv = k_cache.shape[2], v_cache.shape[3]
+    cache = _cache(k_cache, v_cache, dev, Hkv, D)
+    i32 = torch.int32
+    _want(block_table, "block_table", i32, 2, dev)
+    _want_flat(lens, "lens", i32, 1, dev)
+    if lens.shape[0] < B or block_table.shape[0] < B or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("lens and block_table must have a row for each request, rows contiguous")
+    if prefix_table is not None:
+        _want_flat(prefix_table, "prefix_table", i32, 1, dev)
+    stride = block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
+    p = AttnParams(Hq, Hkv, D, Dv, D ** -0.5 if scale is None else scale)
+    made = []
+    if workspace is None:
+        need = int(lib.moe_attn_decode_workspace_bytes(B, prefix_len, max_len, p))
+        if need:
+            made.append(workspace := torch.empty(need, dtype=torch.uint8, device=dev))
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor")
+    if out is None:
+        made.append(out := torch.empty((B, Hq, Dv), dtype=torch.bfloat16, device=dev))
+    if lse is None and want_lse:
+        made.append(lse := torch.empty((B, Hq), dtype=torch.float32, device=dev))
+    ho = _heads(out, "out", dev, Hq, Dv)
+    if lse is not None:
+        _want_flat(lse, "lse", torch.float32, 2, dev)
+    if out.shape[0] != B or (lse is not None and lse.shape != (B, Hq)):
+        raise ValueError("out and lse need a row for each request")
+    _check(lib.moe_attn_decode(hq, cache, _ptr(block_table), stride, block_table.shape[1], _ptr(lens), B, max_len,
+                               _ptr(prefix_table), 0 if prefix_table is None else prefix_table.shape[0], prefix_len, p,
+                               ho, _ptr(lse), _ptr(workspace),
+                               0 if workspace is None else workspace.numel() * workspace.element_size(),
+                               _stream(stream)), "moe_attn_decode")
+    _made(stream, *made)
+    return out, lse
 
 
 from .layer import MoELayer, LayerWeights  # noqa: E402  (composition of the calls above)

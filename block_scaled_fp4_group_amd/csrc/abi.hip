@@ -3,6 +3,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "abi_check.h"
 #include "gemm_common.h"
 
 namespace moe {
@@ -47,22 +48,12 @@ moe_status launch_saliency(const float*, int64_t, int, const int32_t*, int, cons
 moe_status launch_quant_planes(const void*, int64_t, int, float, uint8_t*, uint8_t*, hipStream_t);
 moe_status launch_compact(const uint8_t*, const uint8_t*, int64_t, int, int, uint8_t*, float*, int64_t*, hipStream_t);
 
-static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
 static bool is_pow2_float(float g) {
   if (!(g > 0.0f)) return false;
   int e;
   float m = frexpf(g, &e);
   return m == 0.5f;
 }
-
-#define MOE_CHECK(cond, ...)      \
-  do {                            \
-    if (!(cond)) {                \
-      moe::set_error(__VA_ARGS__); \
-      return MOE_ERR_INVALID;     \
-    }                             \
-  } while (0)
 
 }  // namespace moe
 

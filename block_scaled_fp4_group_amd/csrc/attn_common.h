@@ -1,0 +1,216 @@
+// One wave's part of attention on gfx950's bf16 matrix cores, shared by the
+// prompt and the decode kernel: 32 query rows against a tile of keys in LDS.
+//
+// The scores are formed transposed, S^T = K Q^T (32x32x16 MFMA, K rows as the
+// first operand), so lane l holds the scores of ONE query row, l % 32, against
+// half of the tile's keys; lane l ^ 32 holds the other half.  Row maximum and
+// sum are then in-lane except for one exchange between the lane's halves, and
+// the running scale factors need no broadcast.  The weights P^T come out of the
+// score accumulator in an order that is already a second MFMA operand if the
+// contraction index (the key) is enumerated as the accumulator holds it: for
+// keys 16 s .. 16 s + 15, lane half h and element j stand for key
+// 16 s + 8 (j / 4) + 4 h + j % 4.  The same enumeration of V's rows is what two
+// transposing LDS reads (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16
+// columns, each receives one column's 4 values) deliver, so O^T = V^T P^T needs
+// no exchange of weights between lanes at all.
+//
+// Online softmax in base 2: m is the running maximum of the scores times
+// c = scale log2(e), p = 2^(s c - m); l (float) sums the unrounded weights,
+// O (float) accumulates the weights rounded to bf16, the matrix cores' operand
+// (relative error 2^-9 of each weight, of random sign: as much as the rounding
+// of the output itself).
+//
+// Layouts measured on the chip: 32x32x16 operands hold row l % 32, k = 8 (l / 32)
+// + j, j < 8; the accumulator holds column l % 32, row 8 (i / 4) + 4 (l / 32) +
+// i % 4, i < 16.
+#pragma once
+#include <type_traits>
+
+#include "common.h"
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+namespace moe {
+
+typedef __attribute__((address_space(3))) void at_lds_void;
+typedef __attribute__((address_space(3))) s16x4 at_lds_s16x4;
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// max / sum over the two lanes (l, l ^ 32) that share a query row
+__device__ __forceinline__ float half_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Rows of D bf16 in LDS: 16-byte chunk c of row r sits at chunk c ^ at_swz(r).
+// A score operand read takes chunk c of 32 rows, a V read 4 chunks of 4
+// consecutive rows; the maps spread both over all banks (rows of 128 bytes: two
+// to a 256-byte bank sweep; of 384 bytes: alternating halves).
+template <int D>
+__device__ __forceinline__ int at_swz(int r) {
+  if (D == 128) return ((r & 3) << 2) | ((r >> 2) & 3);
+  if (D == 64) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+  return (r >> 1) & 7;                                              // D == 192 (keys only)
+}
+
+// NB blocks of 32 keys per tile; DQ-wide keys, DV-wide values
+template <int DQ, int DV, int NB>
+struct AttnWave {
+  static constexpr int KQ = DQ / 16, OB = DV / 32;
+  static constexpr int kKeyBytes = NB * 32 * DQ * 2, kValBytes = NB * 32 * DV * 2;
+  bf16x8 q[KQ];
+  f32x16 o[OB];
+  float m, l;
+
+  // q: this lane's query row (16-byte aligned)
+  __device__ __forceinline__ void init(const uint16_t* row, int h) {
+#pragma unroll
+    for (int s = 0; s < KQ; ++s) q[s] = __builtin_bit_cast(bf16x8, *(const u32x4*)(row + 16 * s + 8 * h));
+#pragma unroll
+    for (int b = 0; b < OB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[b][i] = 0.0f;
+    m = neg_inf();
+    l = 0.0f;
+  }
+
+  __device__ __forceinline__ static bf16x8 read_v(const uint8_t* vs, int lane, int key0, int db) {
+    const int g = lane >> 4, i = lane & 15, h = lane >> 5;
+    s16x4 part[2];
+#pragma unroll
+    for (int jj = 0; jj < 2; ++jj) {
+      const int row = key0 + 8 * jj + 4 * h + (i >> 2);
+      const int chunk = (4 * db + 2 * (g & 1) + ((i & 3) >> 1)) ^ at_swz<DV>(row);
+      part[jj] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (at_lds_s16x4*)(vs + row * (DV * 2) + chunk * 16 + 8 * (i & 1)));
+    }
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+
+  // V's infinities and NaN as zeros
+  __device__ __forceinline__ static bf16x8 finite_only(bf16x8 v) {
+    u32x4 w = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
+      if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0x0000FFFFu;
+    }
+    return __builtin_bit_cast(bf16x8, w);
+  }
+
+  // One tile.  MASKED: lane's row sees keys 0 .. last of the tile (last may be
+  // negative or past the end); otherwise it sees all of them.
+  template <bool MASKED>
+  __device__ __forceinline__ void tile(const uint8_t* ks, const uint8_t* vs, int lane, float c, int last) {
+    const int h = lane >> 5, r = lane & 31;
+    f32x16 s[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < KQ; ++k) {
+        const int chunk = (2 * k + h) ^ at_swz<DQ>(r);
+        const bf16x8 kf = *(const bf16x8*)(ks + (32 * b + r) * (DQ * 2) + chunk * 16);
+        s[b] = mfma32(kf, q[k], s[b]);
+      }
+    }
+    if (MASKED) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s[b][i] = 32 * b + 8 * (i / 4) + 4 * h + (i & 3) <= last ? s[b][i] : neg_inf();
+    }
+    float mx = neg_inf();
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
+    // The old and the new maximum are both kept as rounded (m is c times the raw
+    // maximum), so a tile that does not raise it scales by exactly 1: with a
+    // freshly formed product the rounding of m c would be applied once per tile
+    // (2e-5 off in lse after 256 tiles).  A row that has seen no key (or only
+    // scores of -inf) keeps m = -inf; its weights are then 2^-inf = 0.
+    mx = fmaxf(m, half_max(mx) * c);
+    const float base = mx == neg_inf() ? 0.0f : mx;
+    const float alpha = __builtin_amdgcn_exp2f(m - base);
+    m = mx;
+    float sum = 0.0f;
+    bf16x8 p[2 * NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; i += 8) {
+        float w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          w[j] = __builtin_amdgcn_exp2f(fmaf(s[b][i + j], c, -base));
+          sum += w[j];
+        }
+        p[2 * b + i / 8] = __builtin_bit_cast(
+            bf16x8, u32x4{cvt_bf16x2(w[0], w[1]), cvt_bf16x2(w[2], w[3]), cvt_bf16x2(w[4], w[5]), cvt_bf16x2(w[6], w[7])});
+      }
+    l = fmaf(l, alpha, half_sum(sum));
+#pragma unroll
+    for (int b = 0; b < OB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[b][i] *= alpha;
+    bool poisoned = false;
+    if (MASKED) {
+      // A weight of 0 times an infinite or NaN value is NaN, so a value that is
+      // masked for a row would reach it.  Zero times the tile's values shows
+      // whether there is one (finite values add nothing).
+      f32x16 z;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+      const bf16x8 zero = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+#pragma unroll
+      for (int st = 0; st < 2 * NB; ++st)
+#pragma unroll
+        for (int b = 0; b < OB; ++b) z = mfma32(read_v(vs, lane, 16 * st, b), zero, z);
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) bad |= z[i] != 0.0f;
+      poisoned = __any(bad);
+    }
+    if (!MASKED || !poisoned) {
+#pragma unroll
+      for (int st = 0; st < 2 * NB; ++st)
+#pragma unroll
+        for (int b = 0; b < OB; ++b) o[b] = mfma32(read_v(vs, lane, 16 * st, b), p[st], o[b]);
+    } else {
+#pragma unroll
+      for (int st = 0; st < 2 * NB; ++st)
+#pragma unroll
+        for (int b = 0; b < OB; ++b) o[b] = mfma32(finite_only(read_v(vs, lane, 16 * st, b)), p[st], o[b]);
+      // the values that are not finite reach the rows that see them, as they
+      // are (a positive weight leaves an infinity or NaN what it is)
+#pragma unroll 1
+      for (int key = 0; key < 32 * NB; ++key) {
+#pragma unroll
+        for (int b = 0; b < OB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int d = 32 * b + 8 * (i / 4) + 4 * h + (i & 3);
+            const uint32_t bits = *(const uint16_t*)(vs + key * (DV * 2) + (((d >> 3) ^ at_swz<DV>(key)) * 16) + (d & 7) * 2);
+            if ((bits & 0x7F80u) == 0x7F80u && key <= last) o[b][i] += __uint_as_float(bits << 16);
+          }
+      }
+    }
+  }
+};
+
+}  // namespace moe

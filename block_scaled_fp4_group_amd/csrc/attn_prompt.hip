@@ -1,0 +1,167 @@
+// Causal attention over whole prompts: packed sequences, grouped heads.
+//
+//   out[i, h] = sum_j p_ij v[j, h / G],  p_i = softmax over the keys row i sees
+// of q_i . k_j * scale.  Row i of a sequence with Lq queries and Lk keys sees
+// keys 0 .. i + Lk - Lq (the last query sees every key; with Lk < Lq the first
+// rows see none and give 0).
+//
+// A workgroup takes kRows consecutive queries of one sequence and one head, 32
+// per wave (attn_common.h), and walks the keys in tiles of 64 through LDS.
+#include "attn_common.h"
+
+namespace moe {
+
+constexpr int kPromptWaves = 4;
+constexpr int kPromptThreads = kPromptWaves * 64;
+constexpr int kPromptRows = kPromptWaves * 32;
+constexpr int kPromptKeys = 64;
+
+struct PromptArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* out;
+  float* lse;
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int64_t total_q, total_k;
+  int32_t num_seqs, q_heads, kv_heads;
+  float c;            // scale * log2(e)
+};
+
+struct PromptTile {
+  int64_t q0, k0;     // the sequence's first query and key
+  int lq, lk, row0;   // its lengths; the tile's first row
+};
+
+// Row tiles without a plan made beforehand: sequence b owns the virtual tiles
+// from cu_q[b] / rows + b on, at least as many as it needs, so a tile's
+// sequence is found by searching cu_q itself (64 probes at a time), and
+// total_q / rows + num_seqs workgroups per head cover any lengths.  Tiles past
+// a sequence's end have row0 >= lq.  Within a sequence the last tile (the one
+// that sees most keys) comes first.
+__device__ __forceinline__ PromptTile prompt_tile(const PromptArgs& a, int64_t vt, int rows, int lane) {
+  auto cu = [&](const int32_t* p, int i, int64_t total) { return min(max((int64_t)p[i], (int64_t)0), total); };
+  int lo = 0, n = a.num_seqs;
+  while (n > 1) {
+    const int stride = (n + 63) >> 6;
+    const int off = lane * stride;
+    const bool le = off < n && cu(a.cu_q, lo + off, a.total_q) / rows + lo + off <= vt;
+    const uint64_t mask = __ballot(le) | 1;
+    const int seg = (63 - __builtin_clzll(mask)) * stride;
+    lo += seg;
+    n = min(stride, n - seg);
+  }
+  const int b = __builtin_amdgcn_readfirstlane(lo);
+  PromptTile t;
+  t.q0 = cu(a.cu_q, b, a.total_q);
+  t.lq = (int)(max(cu(a.cu_q, b + 1, a.total_q), t.q0) - t.q0);
+  t.k0 = cu(a.cu_k, b, a.total_k);
+  t.lk = (int)(max(cu(a.cu_k, b + 1, a.total_k), t.k0) - t.k0);
+  const int64_t idx = vt - (t.q0 / rows + b), need = (t.lq + rows - 1) / rows;
+  t.row0 = idx < 0 || idx >= need ? t.lq : (int)((need - 1 - idx) * rows);
+  return t;
+}
+
+template <int DQ, int DV>
+__global__ __launch_bounds__(kPromptThreads) void attn_prompt_kernel(PromptArgs a) {
+  using W = AttnWave<DQ, DV, kPromptKeys / 32>;
+  __shared__ __attribute__((aligned(16))) uint8_t ks[W::kKeyBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t vs[W::kValBytes];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, h = lane >> 5;
+  // the key head varies fastest (workgroups go to the XCDs in turn, so one
+  // key head's workgroups meet in few L2s), then the heads that share it
+  const int G = a.q_heads / a.kv_heads;
+  const int kvh = blockIdx.x % a.kv_heads;
+  const int g = (blockIdx.x / a.kv_heads) % G;
+  const int64_t vt = blockIdx.x / (uint32_t)a.q_heads;
+  const PromptTile T = prompt_tile(a, vt, kPromptRows, lane);
+  if (T.row0 >= T.lq) return;
+  const int hq = kvh * G + g;
+  const int row = min(T.row0 + wv * 32 + (lane & 31), T.lq - 1);    // rows past the end repeat the last
+  const int pos = row + T.lk - T.lq;                                // last key this row sees
+  W w;
+  w.init(a.q + (T.q0 + row) * a.q_ts + hq * a.q_hs, h);
+  // the workgroup's and this wave's key ranges
+  const int last_row = min(T.row0 + kPromptRows, T.lq) - 1;
+  const int n_keys = max(0, min(T.lk, last_row + T.lk - T.lq + 1));
+  const int wave_last = min(T.row0 + wv * 32 + 31, T.lq - 1) + T.lk - T.lq;    // most keys of a row of this wave
+  const int wave_first = min(T.row0 + wv * 32, T.lq - 1) + T.lk - T.lq;        // fewest
+  const uint16_t* kp = a.k + T.k0 * a.k_ts + kvh * a.k_hs;
+  const uint16_t* vp = a.v + T.k0 * a.v_ts + kvh * a.v_hs;
+  for (int key0 = 0; key0 < n_keys; key0 += kPromptKeys) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < W::kKeyBytes / 16 / kPromptThreads; ++i) {
+      constexpr int C = DQ / 8;
+      const int f = i * kPromptThreads + threadIdx.x, r = f / C, ch = f % C;
+      const int key = min(key0 + r, T.lk - 1);                      // rows past the end repeat the last key
+      *(u32x4*)(ks + r * (DQ * 2) + (ch ^ at_swz<DQ>(r)) * 16) = *(const u32x4*)(kp + key * a.k_ts + ch * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < W::kValBytes / 16 / kPromptThreads; ++i) {
+      constexpr int C = DV / 8;
+      const int f = i * kPromptThreads + threadIdx.x, r = f / C, ch = f % C;
+      const int key = min(key0 + r, T.lk - 1);
+      *(u32x4*)(vs + r * (DV * 2) + (ch ^ at_swz<DV>(r)) * 16) = *(const u32x4*)(vp + key * a.v_ts + ch * 8);
+    }
+    __syncthreads();
+    if (key0 + kPromptKeys - 1 <= wave_first)
+      w.template tile<false>(ks, vs, lane, a.c, 0);
+    else if (key0 <= wave_last)
+      w.template tile<true>(ks, vs, lane, a.c, pos - key0);
+  }
+  if (T.row0 + wv * 32 + (lane & 31) >= T.lq) return;
+  const float inv = w.l == 0.0f ? 0.0f : 1.0f / w.l;
+  uint16_t* op = a.out + (T.q0 + row) * a.o_ts + hq * a.o_hs;
+#pragma unroll
+  for (int b = 0; b < W::OB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u32x2 v = {cvt_bf16x2(w.o[b][4 * i] * inv, w.o[b][4 * i + 1] * inv),
+                       cvt_bf16x2(w.o[b][4 * i + 2] * inv, w.o[b][4 * i + 3] * inv)};
+      *(u32x2*)(op + 32 * b + 8 * i + 4 * h) = v;
+    }
+  if (a.lse && h == 0)
+    a.lse[(T.q0 + row) * a.q_heads + hq] = w.l == 0.0f ? neg_inf() : (w.m + __builtin_amdgcn_logf(w.l)) * kLn2;
+}
+
+template <int DQ, int DV>
+static void launch_prompt(const PromptArgs& a, hipStream_t stream) {
+  const int64_t tiles = a.total_q / kPromptRows + a.num_seqs;
+  hipLaunchKernelGGL((attn_prompt_kernel<DQ, DV>), dim3((uint32_t)(tiles * a.q_heads)), dim3(kPromptThreads), 0, stream, a);
+}
+
+moe_status launch_attn_prompt(const moe_heads& q, const moe_heads& k, const moe_heads& v, const int32_t* cu_q,
+                              const int32_t* cu_k, int num_seqs, int64_t total_q, int64_t total_k,
+                              const moe_attn_params& p, const moe_heads& out, float* lse, hipStream_t stream) {
+  PromptArgs a;
+  a.q = (const uint16_t*)q.data;
+  a.q_ts = q.token_stride;
+  a.q_hs = q.head_stride;
+  a.k = (const uint16_t*)k.data;
+  a.k_ts = k.token_stride;
+  a.k_hs = k.head_stride;
+  a.v = (const uint16_t*)v.data;
+  a.v_ts = v.token_stride;
+  a.v_hs = v.head_stride;
+  a.out = (uint16_t*)out.data;
+  a.o_ts = out.token_stride;
+  a.o_hs = out.head_stride;
+  a.lse = lse;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.num_seqs = num_seqs;
+  a.total_q = total_q;
+  a.total_k = total_k;
+  a.q_heads = p.q_heads;
+  a.kv_heads = p.kv_heads;
+  a.c = p.scale * kLog2e;
+  if (p.k_dim == 64) launch_prompt<64, 64>(a, stream);
+  else if (p.k_dim == 128) launch_prompt<128, 128>(a, stream);
+  else launch_prompt<192, 128>(a, stream);
+  return launch_status("moe_attn_prompt");
+}
+
+}  // namespace moe

@@ -415,6 +415,140 @@ moe_status moe_quantize_mxfp8(const void* x, int64_t rows, int32_t k, uint8_t* c
 moe_status moe_quantize_nvfp4_planes(const void* x, int64_t rows, int32_t k, float input_scale, uint8_t* planes,
                                      uint8_t* plane_scales, hipStream_t stream);
 
+/* =================================================================== attention
+ * The attention half of a decoder layer around one paged key / value cache:
+ * cache slots, head norm + rotation + cache write, attention over whole
+ * prompts, attention of single tokens behind a shared prefix.  Conventions as
+ * above (caller-owned device memory, asynchronous, host-checked, no atomics:
+ * the same inputs give the same bits).  bf16 data, FP32 statistics and sums.
+ *
+ * Heads: bf16 [tokens, heads, dim], strides in elements, dim contiguous; data
+ * 16-byte aligned and strides multiples of 8.  Input rows may overlap or repeat
+ * (stride 0); output rows may not.
+ * Head sizes (k_dim, v_dim) of the attention calls: (64, 64), (128, 128) and
+ * (192, 128), the asymmetric key / value heads of the "AxionML /
+ * MiMo-V2.6-Flash-MOPD-NVFP4" deployment; others give MOE_ERR_UNSUPPORTED.
+ * Query head h uses key head h / (q_heads / kv_heads).
+ */
+typedef struct {
+  void* data;
+  int64_t token_stride, head_stride;
+} moe_heads;
+
+/* k bf16 [num_pages, page_size, kv_heads, k_dim], v bf16 [num_pages, page_size,
+ * kv_heads, v_dim], contiguous, 16-byte aligned.  page_size: a power of two up
+ * to 1024; num_pages * page_size < 2^31 (the bytes may pass 2^32).  Slot s is
+ * row s % page_size of page s / page_size. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t num_pages;
+  int32_t page_size;
+} moe_kv_cache;
+
+/* ------------------------------------------------------- cache slots
+ * Block tables and slot maps of a step's new tokens from the request lengths.
+ * Request b holds cached_lens[b] tokens in its first ceil(cached / page_size)
+ * pages and brings new_lens[b] tokens (negative lengths count as 0).  The pages
+ * it still needs are the next entries of free_pages, in request order; they are
+ * written to block_table[b, ceil(cached / page_size) ...] (other entries keep
+ * their values).  With cu_new the exclusive prefix sums of new_lens, token
+ * t = cu_new[b] + i of the step gets
+ *   positions[t] = position_base + cached_lens[b] + i
+ *   slots[t]     = block_table[b, (cached_lens[b] + i) / page_size] * page_size
+ *                  + (cached_lens[b] + i) % page_size
+ * position_base: the length of a prefix that lies before every request's own
+ * tokens (moe_attn_decode).  A page that the free list no longer has is entered
+ * as -1; tokens in it, and tokens past max_blocks pages, get slot -1 (and no
+ * page).  Entries t >= cu_new[num_requests] of slots / positions are -1 / 0.
+ *   cached_lens, new_lens int32 [num_requests]; free_pages int32 [num_free];
+ *   block_table int32 [num_requests, max_blocks], rows table_stride apart;
+ *   slots, positions int32 [max_new]; cu_new int32 [num_requests + 1];
+ *   counts int32 [3]: free pages taken, pages needed, new tokens without a slot
+ *   (those past max_new are not written anywhere).
+ * num_requests <= 4096 (else MOE_ERR_UNSUPPORTED); max_blocks * page_size < 2^31.
+ * A cached length beyond max_blocks pages counts as that many.  One launch.
+ */
+moe_status moe_kv_slots(const int32_t* cached_lens, const int32_t* new_lens, int32_t num_requests,
+                        const int32_t* free_pages, int64_t num_free, int32_t page_size, int32_t* block_table,
+                        int64_t table_stride, int32_t max_blocks, int32_t position_base, int64_t max_new, int32_t* slots,
+                        int32_t* positions, int32_t* cu_new, int32_t* counts, hipStream_t stream);
+
+/* ------------------------------------- head norms, rotation, cache write
+ * For every token and every query and key head x (head_dim values), in one pass:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight     (weight NULL: y = x)
+ *   the first rot_dim values of y are turned in pairs by the token's position:
+ *   (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i), pair i being values
+ *   (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved != 0
+ * in float, rounded once to bf16.  cos_sin float [max_position, rot_dim]: row p
+ * holds rot_dim / 2 cosines, then rot_dim / 2 sines; positions int32 [T] are
+ * clamped to [0, max_position).  q_weight, k_weight float [head_dim] or NULL.
+ * q_out and k_out may be q and k themselves.  With a cache, the finished key
+ * heads and the value heads (copied) of token t go to row slots[t] (int32 [T];
+ * values outside the cache are skipped; two tokens must not share a slot), and
+ * k_out may be NULL; without one, v, slots and v_dim are not used.
+ * head_dim: 64, 128 or 192; rot_dim a multiple of 16; v_dim a multiple of 8;
+ * weights and cos_sin 16-byte aligned.  T == 0 is a no-op.
+ */
+typedef struct {
+  int32_t q_heads, kv_heads, head_dim, v_dim;
+  int32_t rot_dim, interleaved, max_position;
+  float eps;
+} moe_rope_params;
+
+moe_status moe_qk_norm_rope(const moe_heads* q, const moe_heads* k, const moe_heads* v, int64_t T,
+                            const moe_rope_params* p, const int32_t* positions, const float* cos_sin,
+                            const float* q_weight, const float* k_weight, const moe_heads* q_out, const moe_heads* k_out,
+                            const moe_kv_cache* cache, const int32_t* slots, hipStream_t stream);
+
+typedef struct {
+  int32_t q_heads, kv_heads, k_dim, v_dim;
+  float scale;                /* > 0; usually k_dim^-0.5 */
+} moe_attn_params;
+
+/* ------------------------------------------------- attention over prompts
+ * Packed sequences: sequence b's queries are rows cu_q[b] .. cu_q[b + 1] - 1 of
+ * q and out (Lq of them), its keys rows cu_k[b] .. cu_k[b + 1] - 1 of k and v
+ * (Lk).  Query i sees keys 0 .. i + Lk - Lq (causal; the last query sees every
+ * key, so cached context goes before the prompt's own keys):
+ *   out[i, h] = sum_j softmax_j(scale q[i, h] . k[j, h']) v[j, h']
+ *   lse[i, h] = log sum_j exp(scale q[i, h] . k[j, h'])
+ * A query that sees no key (Lk < Lq) gives 0 and lse -inf; keys and values it
+ * does not see do not reach it, infinities and NaN included.
+ *   cu_q, cu_k int32 [num_seqs + 1], not descending, from 0 to total_q / total_k
+ *   (rows outside the ranges keep their values; entries are clamped to them);
+ *   lse float [total_q, q_heads] or NULL.
+ * num_seqs == 0 or total_q == 0 is a no-op.  One launch.
+ */
+moe_status moe_attn_prompt(const moe_heads* q, const moe_heads* k, const moe_heads* v, const int32_t* cu_q,
+                           const int32_t* cu_k, int32_t num_seqs, int64_t total_q, int64_t total_k,
+                           const moe_attn_params* p, const moe_heads* out, float* lse, hipStream_t stream);
+
+/* ------------------------------ attention of single tokens, shared prefix
+ * One query per request over a paged cache (row b of q and out: request b).
+ * Request b sees the prefix_len keys of the shared prefix -- pages
+ * prefix_table[0 .. prefix_blocks) -- and its own lens[b] keys, pages
+ * block_table[b, ...]; own keys start on a page of their own.  The prefix is
+ * read once for all requests.  prefix_len = 0: plain decode attention.
+ * A request without any key gives 0 and lse -inf.
+ *   block_table int32 [num_requests, max_blocks], rows table_stride apart;
+ *   lens int32 [num_requests], clamped to [0, max_len]; max_len <= max_blocks *
+ *   page_size sizes the launch (a longest length known on the host);
+ *   prefix_table int32 [prefix_blocks]; lse float [num_requests, q_heads] or NULL.
+ *   Table entries are clamped to the cache's pages (an entry that a length
+ *   reaches and that is not one of them gives an unspecified result).
+ * workspace: moe_attn_decode_workspace_bytes() bytes for the same sizes, 16-byte
+ * aligned (may be NULL when that is 0); calls that share one must not overlap.
+ * One or two launches.  num_requests == 0 is a no-op.
+ */
+size_t moe_attn_decode_workspace_bytes(int32_t num_requests, int64_t prefix_len, int64_t max_len,
+                                       const moe_attn_params* p);
+moe_status moe_attn_decode(const moe_heads* q, const moe_kv_cache* cache, const int32_t* block_table,
+                           int64_t table_stride, int32_t max_blocks, const int32_t* lens, int32_t num_requests,
+                           int64_t max_len, const int32_t* prefix_table, int32_t prefix_blocks, int64_t prefix_len,
+                           const moe_attn_params* p, const moe_heads* out, float* lse, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
