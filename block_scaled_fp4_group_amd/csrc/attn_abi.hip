@@ -157,6 +157,11 @@ moe_status moe_attn_prompt(const moe_heads* q, const moe_heads* k, const moe_hea
   }
   MOE_PASS(check_heads(fn, "out", out, p->q_heads, p->v_dim, total_q));
   MOE_CHECK(aligned4(lse), "%s: lse not 4-byte aligned", fn);
+  // a tile of 64 rows is addressed with 31 bits
+  if (total_k > 0 && (k->token_stride > (1 << 23) || v->token_stride > (1 << 23))) {
+    set_error("%s: token strides of k and v over 2^23 elements are not supported", fn);
+    return MOE_ERR_UNSUPPORTED;
+  }
   MOE_CHECK((total_q / 32 + num_seqs) * (int64_t)p->q_heads < ((int64_t)1 << 31), "%s: too many rows", fn);
   static const moe_heads none = {nullptr, 0, 0};
   return launch_attn_prompt(*q, total_k > 0 ? *k : none, total_k > 0 ? *v : none, cu_q, cu_k, num_seqs, total_q, total_k,

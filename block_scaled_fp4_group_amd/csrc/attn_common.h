@@ -65,6 +65,34 @@ __device__ __forceinline__ int at_swz(int r) {
   return (r >> 1) & 7;                                              // D == 192 (keys only)
 }
 
+// Direct load of 16 bytes per lane into LDS: lane i's bytes land at lds + 16 i.
+// As one asm block because the compiler makes every later LDS read that it
+// cannot tell apart from the target wait for all loads in flight; here the
+// kernel's own waits order them (at_wait_barrier).  No register but m0 is written
+// (the compiler sets m0 itself right before a use of its own); the
+// wait state between m0 and its use is in the block.
+typedef uint32_t at_rsrc __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ at_rsrc at_make_rsrc(const void* base) {
+  const uint64_t b = (uint64_t)base;
+  return at_rsrc{(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, 0x7fffffffu, 0x00020000u};
+}
+__device__ __forceinline__ void at_load_lds(uint32_t lds, at_rsrc r, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(off), "s"(r) : "memory");
+}
+__device__ __forceinline__ uint32_t at_lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// Every LDS read of this wave has arrived and at most N of its direct loads are
+// still in flight; then the workgroup's barrier.  Nothing moves across.
+template <int N>
+__device__ __forceinline__ void at_wait_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(N) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // NB blocks of 32 keys per tile; DQ-wide keys, DV-wide values
 template <int DQ, int DV, int NB>
 struct AttnWave {
@@ -72,12 +100,14 @@ struct AttnWave {
   static constexpr int kKeyBytes = NB * 32 * DQ * 2, kValBytes = NB * 32 * DV * 2;
   bf16x8 q[KQ];
   f32x16 o[OB];
+  f32x16 s[NB];
+  bf16x8 p[2 * NB];
   float m, l;
 
   // q: this lane's query row (16-byte aligned)
   __device__ __forceinline__ void init(const uint16_t* row, int h) {
 #pragma unroll
-    for (int s = 0; s < KQ; ++s) q[s] = __builtin_bit_cast(bf16x8, *(const u32x4*)(row + 16 * s + 8 * h));
+    for (int i = 0; i < KQ; ++i) q[i] = __builtin_bit_cast(bf16x8, *(const u32x4*)(row + 16 * i + 8 * h));
 #pragma unroll
     for (int b = 0; b < OB; ++b)
 #pragma unroll
@@ -110,30 +140,35 @@ struct AttnWave {
     return __builtin_bit_cast(bf16x8, w);
   }
 
-  // One tile.  MASKED: lane's row sees keys 0 .. last of the tile (last may be
-  // negative or past the end); otherwise it sees all of them.
-  template <bool MASKED>
-  __device__ __forceinline__ void tile(const uint8_t* ks, const uint8_t* vs, int lane, float c, int last) {
+  // s = the tile's raw scores
+  __device__ __forceinline__ void scores(const uint8_t* ks, int lane) {
     const int h = lane >> 5, r = lane & 31;
-    f32x16 s[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
 #pragma unroll
-      for (int k = 0; k < KQ; ++k) {
+    for (int k = 0; k < KQ; ++k)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
         const int chunk = (2 * k + h) ^ at_swz<DQ>(r);
         const bf16x8 kf = *(const bf16x8*)(ks + (32 * b + r) * (DQ * 2) + chunk * 16);
         s[b] = mfma32(kf, q[k], s[b]);
       }
-    }
-    if (MASKED) {
+  }
+
+  // this lane's row sees keys 0 .. last of the tile (last may be negative or past the end)
+  __device__ __forceinline__ void mask(int lane, int last) {
+    const int h = lane >> 5;
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          s[b][i] = 32 * b + 8 * (i / 4) + 4 * h + (i & 3) <= last ? s[b][i] : neg_inf();
-    }
+      for (int i = 0; i < 16; ++i)
+        s[b][i] = 32 * b + 8 * (i / 4) + 4 * h + (i & 3) <= last ? s[b][i] : neg_inf();
+  }
+
+  // p = the tile's weights; m, l and o brought to the new maximum.
+  __device__ __forceinline__ void weights(float c) {
     float mx = neg_inf();
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -149,7 +184,6 @@ struct AttnWave {
     const float alpha = __builtin_amdgcn_exp2f(m - base);
     m = mx;
     float sum = 0.0f;
-    bf16x8 p[2 * NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -168,48 +202,63 @@ struct AttnWave {
     for (int b = 0; b < OB; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[b][i] *= alpha;
-    bool poisoned = false;
-    if (MASKED) {
-      // A weight of 0 times an infinite or NaN value is NaN, so a value that is
-      // masked for a row would reach it.  Zero times the tile's values shows
-      // whether there is one (finite values add nothing).
-      f32x16 z;
+  }
+
+  // o += the tile's values times their weights
+  __device__ __forceinline__ void values(const uint8_t* vs, int lane) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) z[i] = 0.0f;
-      const bf16x8 zero = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+    for (int st = 0; st < 2 * NB; ++st)
 #pragma unroll
-      for (int st = 0; st < 2 * NB; ++st)
+      for (int b = 0; b < OB; ++b) o[b] = mfma32(read_v(vs, lane, 16 * st, b), p[st], o[b]);
+  }
+
+  // The same for a tile with masked places.  A weight of 0 times an infinite or
+  // NaN value is NaN, so a value that is masked for a row would reach it.  Zero
+  // times the tile's values shows whether there is one (finite values add
+  // nothing); then the product runs on the finite values, and the others are
+  // added to the rows that see them, as they are (a positive weight leaves an
+  // infinity or NaN what it is).
+  __device__ __forceinline__ void values_masked(const uint8_t* vs, int lane, int last) {
+    const int h = lane >> 5;
+    f32x16 z;
 #pragma unroll
-        for (int b = 0; b < OB; ++b) z = mfma32(read_v(vs, lane, 16 * st, b), zero, z);
-      bool bad = false;
+    for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+    const bf16x8 zero = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
 #pragma unroll
-      for (int i = 0; i < 16; ++i) bad |= z[i] != 0.0f;
-      poisoned = __any(bad);
+    for (int st = 0; st < 2 * NB; ++st)
+#pragma unroll
+      for (int b = 0; b < OB; ++b) z = mfma32(read_v(vs, lane, 16 * st, b), zero, z);
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) bad |= z[i] != 0.0f;
+    if (!__any(bad)) {
+      values(vs, lane);
+      return;
     }
-    if (!MASKED || !poisoned) {
 #pragma unroll
-      for (int st = 0; st < 2 * NB; ++st)
+    for (int st = 0; st < 2 * NB; ++st)
 #pragma unroll
-        for (int b = 0; b < OB; ++b) o[b] = mfma32(read_v(vs, lane, 16 * st, b), p[st], o[b]);
-    } else {
-#pragma unroll
-      for (int st = 0; st < 2 * NB; ++st)
-#pragma unroll
-        for (int b = 0; b < OB; ++b) o[b] = mfma32(finite_only(read_v(vs, lane, 16 * st, b)), p[st], o[b]);
-      // the values that are not finite reach the rows that see them, as they
-      // are (a positive weight leaves an infinity or NaN what it is)
+      for (int b = 0; b < OB; ++b) o[b] = mfma32(finite_only(read_v(vs, lane, 16 * st, b)), p[st], o[b]);
 #pragma unroll 1
-      for (int key = 0; key < 32 * NB; ++key) {
+    for (int key = 0; key < 32 * NB; ++key) {
 #pragma unroll
-        for (int b = 0; b < OB; ++b)
+      for (int b = 0; b < OB; ++b)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int d = 32 * b + 8 * (i / 4) + 4 * h + (i & 3);
-            const uint32_t bits = *(const uint16_t*)(vs + key * (DV * 2) + (((d >> 3) ^ at_swz<DV>(key)) * 16) + (d & 7) * 2);
-            if ((bits & 0x7F80u) == 0x7F80u && key <= last) o[b][i] += __uint_as_float(bits << 16);
-          }
-      }
+        for (int i = 0; i < 16; ++i) {
+          const int d = 32 * b + 8 * (i / 4) + 4 * h + (i & 3);
+          const uint32_t bits = *(const uint16_t*)(vs + key * (DV * 2) + (((d >> 3) ^ at_swz<DV>(key)) * 16) + (d & 7) * 2);
+          if ((bits & 0x7F80u) == 0x7F80u && key <= last) o[b][i] += __uint_as_float(bits << 16);
+        }
     }
+  }
+
+  // a whole tile; masked: see mask()
+  __device__ __forceinline__ void tile(const uint8_t* ks, const uint8_t* vs, int lane, float c, bool masked, int last) {
+    scores(ks, lane);
+    if (masked) mask(lane, last);
+    weights(c);
+    if (masked) values_masked(vs, lane, last);
+    else values(vs, lane);
   }
 };
 

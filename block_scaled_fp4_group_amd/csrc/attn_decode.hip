@@ -118,8 +118,7 @@ __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(DecodeArgs a) 
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    if (t0 + kDecKeys <= key1) w.template tile<false>(ks, vs, lane, a.c, 0);
-    else w.template tile<true>(ks, vs, lane, a.c, (int)(key1 - 1 - t0));
+    w.tile(ks, vs, lane, a.c, t0 + kDecKeys > key1, (int)min(key1 - 1 - t0, (int64_t)kDecKeys));
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
   // join the four waves: 4 floats of a row at a time, chunks spread over the banks

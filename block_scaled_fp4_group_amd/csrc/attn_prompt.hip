@@ -65,11 +65,11 @@ __device__ __forceinline__ PromptTile prompt_tile(const PromptArgs& a, int64_t v
 }
 
 template <int DQ, int DV>
-__global__ __launch_bounds__(kPromptThreads) void attn_prompt_kernel(PromptArgs a) {
+__global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptArgs a) {
   using W = AttnWave<DQ, DV, kPromptKeys / 32>;
-  __shared__ __attribute__((aligned(16))) uint8_t ks[W::kKeyBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t vs[W::kValBytes];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, h = lane >> 5;
+  __shared__ __attribute__((aligned(16))) uint8_t ks[2 * W::kKeyBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t vs[2 * W::kValBytes];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
   // the key head varies fastest (workgroups go to the XCDs in turn, so one
   // key head's workgroups meet in few L2s), then the heads that share it
   const int G = a.q_heads / a.kv_heads;
@@ -90,27 +90,47 @@ __global__ __launch_bounds__(kPromptThreads) void attn_prompt_kernel(PromptArgs 
   const int wave_first = min(T.row0 + wv * 32, T.lq - 1) + T.lk - T.lq;        // fewest
   const uint16_t* kp = a.k + T.k0 * a.k_ts + kvh * a.k_hs;
   const uint16_t* vp = a.v + T.k0 * a.v_ts + kvh * a.v_hs;
-  for (int key0 = 0; key0 < n_keys; key0 += kPromptKeys) {
-    __syncthreads();
+  // each lane's share of a tile: 16-byte chunk i * threads + thread of the
+  // swizzled tile, i.e. of row r the chunk that belongs there
+  constexpr int kKeyLoads = W::kKeyBytes / 16 / kPromptThreads, kValLoads = W::kValBytes / 16 / kPromptThreads;
+  int krow[kKeyLoads], vrow[kValLoads];
+  uint32_t kchunk[kKeyLoads], vchunk[kValLoads];
 #pragma unroll
-    for (int i = 0; i < W::kKeyBytes / 16 / kPromptThreads; ++i) {
-      constexpr int C = DQ / 8;
-      const int f = i * kPromptThreads + threadIdx.x, r = f / C, ch = f % C;
-      const int key = min(key0 + r, T.lk - 1);                      // rows past the end repeat the last key
-      *(u32x4*)(ks + r * (DQ * 2) + (ch ^ at_swz<DQ>(r)) * 16) = *(const u32x4*)(kp + key * a.k_ts + ch * 8);
-    }
+  for (int i = 0; i < kKeyLoads; ++i) {
+    const int f = i * kPromptThreads + threadIdx.x;
+    krow[i] = f / (DQ / 8);
+    kchunk[i] = (uint32_t)((f % (DQ / 8)) ^ at_swz<DQ>(krow[i])) * 16u;
+  }
 #pragma unroll
-    for (int i = 0; i < W::kValBytes / 16 / kPromptThreads; ++i) {
-      constexpr int C = DV / 8;
-      const int f = i * kPromptThreads + threadIdx.x, r = f / C, ch = f % C;
-      const int key = min(key0 + r, T.lk - 1);
-      *(u32x4*)(vs + r * (DV * 2) + (ch ^ at_swz<DV>(r)) * 16) = *(const u32x4*)(vp + key * a.v_ts + ch * 8);
-    }
-    __syncthreads();
-    if (key0 + kPromptKeys - 1 <= wave_first)
-      w.template tile<false>(ks, vs, lane, a.c, 0);
-    else if (key0 <= wave_last)
-      w.template tile<true>(ks, vs, lane, a.c, pos - key0);
+  for (int i = 0; i < kValLoads; ++i) {
+    const int f = i * kPromptThreads + threadIdx.x;
+    vrow[i] = f / (DV / 8);
+    vchunk[i] = (uint32_t)((f % (DV / 8)) ^ at_swz<DV>(vrow[i])) * 16u;
+  }
+  const uint32_t k_row = (uint32_t)(a.k_ts * 2), v_row = (uint32_t)(a.v_ts * 2);   // bytes; a tile spans < 2 GiB (host)
+  const uint32_t wave_lds = (uint32_t)wv * 1024u;
+  auto load = [&](int key0, int st) {
+    const at_rsrc kr = at_make_rsrc(kp + key0 * a.k_ts), vr = at_make_rsrc(vp + key0 * a.v_ts);
+    const int end = T.lk - 1 - key0;                                // rows past the end repeat the last key
+#pragma unroll
+    for (int i = 0; i < kKeyLoads; ++i)
+      at_load_lds(at_lds_addr(ks) + st * W::kKeyBytes + i * kPromptThreads * 16 + wave_lds, kr,
+                  (uint32_t)min(krow[i], end) * k_row + kchunk[i]);
+#pragma unroll
+    for (int i = 0; i < kValLoads; ++i)
+      at_load_lds(at_lds_addr(vs) + st * W::kValBytes + i * kPromptThreads * 16 + wave_lds, vr,
+                  (uint32_t)min(vrow[i], end) * v_row + vchunk[i]);
+  };
+  const int n_tiles = (n_keys + kPromptKeys - 1) / kPromptKeys;
+  if (n_tiles > 0) load(0, 0);
+  for (int t = 0; t < n_tiles; ++t) {
+    // this wave's part of tile t has landed, then everyone's; and everyone is
+    // done with tile t - 1, whose stage the next loads refill
+    at_wait_barrier<0>();
+    const int key0 = t * kPromptKeys, st = t & 1;
+    if (t + 1 < n_tiles) load(key0 + kPromptKeys, st ^ 1);
+    if (key0 <= wave_last)
+      w.tile(ks + st * W::kKeyBytes, vs + st * W::kValBytes, lane, a.c, key0 + kPromptKeys - 1 > wave_first, pos - key0);
   }
   if (T.row0 + wv * 32 + (lane & 31) >= T.lq) return;
   const float inv = w.l == 0.0f ? 0.0f : 1.0f / w.l;
