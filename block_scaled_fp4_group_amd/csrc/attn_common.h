@@ -103,11 +103,32 @@ struct AttnWave {
   f32x16 s[NB];
   bf16x8 p[2 * NB];
   float m, l;
+  // This lane's byte offsets within a tile: of its operand chunk of key row
+  // l % 32 (chunks repeat their swizzle every KA steps), and of its 8 bytes of
+  // the transposing reads of value block b, lower and upper 8 keys.  All other
+  // offsets are constants added to these.
+  static constexpr int KA = DQ == 192 ? 4 : KQ;
+  uint32_t ka[KA], va[OB][2];
 
   // q: this lane's query row (16-byte aligned)
-  __device__ __forceinline__ void init(const uint16_t* row, int h) {
+  __device__ __forceinline__ void init(const uint16_t* row, int lane) {
+    const int h = lane >> 5, r = lane & 31, g = lane >> 4, i16 = lane & 15;
 #pragma unroll
     for (int i = 0; i < KQ; ++i) q[i] = __builtin_bit_cast(bf16x8, *(const u32x4*)(row + 16 * i + 8 * h));
+    // the loads are waited for here, not by the first use in the key loop (whose
+    // wait would take the direct loads in flight with it, tile after tile)
+#pragma unroll
+    for (int i = 0; i < KQ; ++i) asm volatile("" : "+v"(q[i]));
+#pragma unroll
+    for (int k = 0; k < KA; ++k) ka[k] = (uint32_t)(r * (DQ * 2) + ((2 * k + h) ^ at_swz<DQ>(r)) * 16);
+#pragma unroll
+    for (int b = 0; b < OB; ++b)
+#pragma unroll
+      for (int jj = 0; jj < 2; ++jj) {
+        const int row16 = 8 * jj + 4 * h + (i16 >> 2);              // at_swz repeats every 16 rows
+        const int chunk = (4 * b + 2 * (g & 1) + ((i16 & 3) >> 1)) ^ at_swz<DV>(row16);
+        va[b][jj] = (uint32_t)(row16 * (DV * 2) + chunk * 16 + 8 * (i16 & 1));
+      }
 #pragma unroll
     for (int b = 0; b < OB; ++b)
 #pragma unroll
@@ -116,16 +137,16 @@ struct AttnWave {
     l = 0.0f;
   }
 
-  __device__ __forceinline__ static bf16x8 read_v(const uint8_t* vs, int lane, int key0, int db) {
-    const int g = lane >> 4, i = lane & 15, h = lane >> 5;
+  // operand of keys 32 b .. 32 b + 31, columns 16 k .. 16 k + 15
+  __device__ __forceinline__ bf16x8 read_k(const uint8_t* ks, int b, int k) const {
+    return *(const bf16x8*)(ks + ka[k % KA] + (32 * b * (DQ * 2) + (k / KA) * (KA * 32)));
+  }
+  // operand of value columns 32 b .. 32 b + 31, keys 16 st .. 16 st + 15
+  __device__ __forceinline__ bf16x8 read_v(const uint8_t* vs, int st, int b) const {
     s16x4 part[2];
 #pragma unroll
-    for (int jj = 0; jj < 2; ++jj) {
-      const int row = key0 + 8 * jj + 4 * h + (i >> 2);
-      const int chunk = (4 * db + 2 * (g & 1) + ((i & 3) >> 1)) ^ at_swz<DV>(row);
-      part[jj] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (at_lds_s16x4*)(vs + row * (DV * 2) + chunk * 16 + 8 * (i & 1)));
-    }
+    for (int jj = 0; jj < 2; ++jj)
+      part[jj] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at_lds_s16x4*)(vs + va[b][jj] + 16 * st * (DV * 2)));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7));
   }
 
@@ -141,8 +162,7 @@ struct AttnWave {
   }
 
   // s = the tile's raw scores
-  __device__ __forceinline__ void scores(const uint8_t* ks, int lane) {
-    const int h = lane >> 5, r = lane & 31;
+  __device__ __forceinline__ void scores(const uint8_t* ks) {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -150,11 +170,7 @@ struct AttnWave {
 #pragma unroll
     for (int k = 0; k < KQ; ++k)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int chunk = (2 * k + h) ^ at_swz<DQ>(r);
-        const bf16x8 kf = *(const bf16x8*)(ks + (32 * b + r) * (DQ * 2) + chunk * 16);
-        s[b] = mfma32(kf, q[k], s[b]);
-      }
+      for (int b = 0; b < NB; ++b) s[b] = mfma32(read_k(ks, b, k), q[k], s[b]);
   }
 
   // this lane's row sees keys 0 .. last of the tile (last may be negative or past the end)
@@ -167,22 +183,33 @@ struct AttnWave {
         s[b][i] = 32 * b + 8 * (i / 4) + 4 * h + (i & 3) <= last ? s[b][i] : neg_inf();
   }
 
-  // p = the tile's weights; m, l and o brought to the new maximum.
+  // p = the tile's weights.  A row's m is raised, and its l and o scaled, only
+  // when its maximum has grown by more than kSlack powers of two: until then
+  // weights up to 2^kSlack simply stand (float and bf16 keep their relative
+  // precision), and a wave none of whose rows has grown so much skips the
+  // multiplications.  The decision is the row's own, so its result does not
+  // depend on the rows beside it.
+  static constexpr float kSlack = 8.0f;
   __device__ __forceinline__ void weights(float c) {
     float mx = neg_inf();
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
-    // The old and the new maximum are both kept as rounded (m is c times the raw
-    // maximum), so a tile that does not raise it scales by exactly 1: with a
-    // freshly formed product the rounding of m c would be applied once per tile
-    // (2e-5 off in lse after 256 tiles).  A row that has seen no key (or only
-    // scores of -inf) keeps m = -inf; its weights are then 2^-inf = 0.
-    mx = fmaxf(m, half_max(mx) * c);
-    const float base = mx == neg_inf() ? 0.0f : mx;
-    const float alpha = __builtin_amdgcn_exp2f(m - base);
-    m = mx;
+    mx = half_max(mx) * c;
+    const bool grown = mx > m + kSlack;
+    if (__any(grown)) {
+      const float alpha = grown ? __builtin_amdgcn_exp2f(m - mx) : 1.0f;
+      m = grown ? mx : m;
+      l *= alpha;
+#pragma unroll
+      for (int b = 0; b < OB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[b][i] *= alpha;
+    }
+    // a row that has seen no key (or only scores of -inf) keeps m = -inf; its
+    // weights are 2^-inf = 0
+    const float base = m == neg_inf() ? 0.0f : m;
     float sum = 0.0f;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -197,19 +224,15 @@ struct AttnWave {
         p[2 * b + i / 8] = __builtin_bit_cast(
             bf16x8, u32x4{cvt_bf16x2(w[0], w[1]), cvt_bf16x2(w[2], w[3]), cvt_bf16x2(w[4], w[5]), cvt_bf16x2(w[6], w[7])});
       }
-    l = fmaf(l, alpha, half_sum(sum));
-#pragma unroll
-    for (int b = 0; b < OB; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[b][i] *= alpha;
+    l += half_sum(sum);
   }
 
   // o += the tile's values times their weights
-  __device__ __forceinline__ void values(const uint8_t* vs, int lane) {
+  __device__ __forceinline__ void values(const uint8_t* vs) {
 #pragma unroll
     for (int st = 0; st < 2 * NB; ++st)
 #pragma unroll
-      for (int b = 0; b < OB; ++b) o[b] = mfma32(read_v(vs, lane, 16 * st, b), p[st], o[b]);
+      for (int b = 0; b < OB; ++b) o[b] = mfma32(read_v(vs, st, b), p[st], o[b]);
   }
 
   // The same for a tile with masked places.  A weight of 0 times an infinite or
@@ -227,18 +250,18 @@ struct AttnWave {
 #pragma unroll
     for (int st = 0; st < 2 * NB; ++st)
 #pragma unroll
-      for (int b = 0; b < OB; ++b) z = mfma32(read_v(vs, lane, 16 * st, b), zero, z);
+      for (int b = 0; b < OB; ++b) z = mfma32(read_v(vs, st, b), zero, z);
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < 16; ++i) bad |= z[i] != 0.0f;
     if (!__any(bad)) {
-      values(vs, lane);
+      values(vs);
       return;
     }
 #pragma unroll
     for (int st = 0; st < 2 * NB; ++st)
 #pragma unroll
-      for (int b = 0; b < OB; ++b) o[b] = mfma32(finite_only(read_v(vs, lane, 16 * st, b)), p[st], o[b]);
+      for (int b = 0; b < OB; ++b) o[b] = mfma32(finite_only(read_v(vs, st, b)), p[st], o[b]);
 #pragma unroll 1
     for (int key = 0; key < 32 * NB; ++key) {
 #pragma unroll
@@ -254,11 +277,11 @@ struct AttnWave {
 
   // a whole tile; masked: see mask()
   __device__ __forceinline__ void tile(const uint8_t* ks, const uint8_t* vs, int lane, float c, bool masked, int last) {
-    scores(ks, lane);
+    scores(ks);
     if (masked) mask(lane, last);
     weights(c);
     if (masked) values_masked(vs, lane, last);
-    else values(vs, lane);
+    else values(vs);
   }
 };
 

@@ -93,7 +93,7 @@ __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(DecodeArgs a) 
   const int64_t row = min(row0 + r, rows - 1);
   const int b = b0 + (int)(row / G), hq = kvh * G + (int)(row % G);
   W w;
-  w.init(a.q + b * a.q_ts + hq * a.q_hs, h);
+  w.init(a.q + b * a.q_ts + hq * a.q_hs, lane);
   uint8_t* ks = mem[wv];
   uint8_t* vs = mem[wv] + W::kKeyBytes;
   for (int64_t t0 = key0 + wv * kDecKeys; t0 < key1; t0 += kDecStep) {

@@ -82,7 +82,7 @@ __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptAr
   const int row = min(T.row0 + wv * 32 + (lane & 31), T.lq - 1);    // rows past the end repeat the last
   const int pos = row + T.lk - T.lq;                                // last key this row sees
   W w;
-  w.init(a.q + (T.q0 + row) * a.q_ts + hq * a.q_hs, h);
+  w.init(a.q + (T.q0 + row) * a.q_ts + hq * a.q_hs, lane);
   // the workgroup's and this wave's key ranges
   const int last_row = min(T.row0 + kPromptRows, T.lq) - 1;
   const int n_keys = max(0, min(T.lk, last_row + T.lk - T.lq + 1));
@@ -123,14 +123,19 @@ __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptAr
   };
   const int n_tiles = (n_keys + kPromptKeys - 1) / kPromptKeys;
   if (n_tiles > 0) load(0, 0);
-  for (int t = 0; t < n_tiles; ++t) {
+  auto step = [&](auto stage, int t) {
+    constexpr int st = decltype(stage)::value;
     // this wave's part of tile t has landed, then everyone's; and everyone is
     // done with tile t - 1, whose stage the next loads refill
     at_wait_barrier<0>();
-    const int key0 = t * kPromptKeys, st = t & 1;
+    const int key0 = t * kPromptKeys;
     if (t + 1 < n_tiles) load(key0 + kPromptKeys, st ^ 1);
     if (key0 <= wave_last)
       w.tile(ks + st * W::kKeyBytes, vs + st * W::kValBytes, lane, a.c, key0 + kPromptKeys - 1 > wave_first, pos - key0);
+  };
+  for (int t = 0; t < n_tiles; t += 2) {
+    step(std::integral_constant<int, 0>(), t);
+    if (t + 1 < n_tiles) step(std::integral_constant<int, 1>(), t + 1);
   }
   if (T.row0 + wv * 32 + (lane & 31) >= T.lq) return;
   const float inv = w.l == 0.0f ? 0.0f : 1.0f / w.l;
