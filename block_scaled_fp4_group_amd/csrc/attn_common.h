@@ -84,6 +84,12 @@ __device__ __forceinline__ uint32_t at_lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 
+// At most N of this wave's direct loads are still in flight.
+template <int N>
+__device__ __forceinline__ void at_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
+}
+
 // Every LDS read of this wave has arrived and at most N of its direct loads are
 // still in flight; then the workgroup's barrier.  Nothing moves across.
 template <int N>
@@ -161,26 +167,59 @@ struct AttnWave {
     return __builtin_bit_cast(bf16x8, w);
   }
 
-  // s = the tile's raw scores
-  __device__ __forceinline__ void scores(const uint8_t* ks) {
+  // The matrix products take their LDS operands through a queue kAhead deep: the
+  // read of operand i + kAhead goes out right after MFMA i, so the LDS latency
+  // passes behind kAhead MFMAs of 32 cycles each.  (Left to itself the compiler
+  // reads one step ahead and waits for it in each.)
+  static constexpr int kAhead = 2;                                  // 3, 4 and 6 measured the same
+  static constexpr int kScoreOps = KQ * NB, kValueOps = 2 * NB * OB;
+  __device__ __forceinline__ bf16x8 operand(const uint8_t* ks, const uint8_t* vs, int i) const {
+    if (i < kScoreOps) return read_k(ks, i % NB, i / NB);
+    i -= kScoreOps;
+    return read_v(vs, i / OB, i % OB);
+  }
+  // operands FIRST .. LAST - 1: scores (s must be zero before the first), then values
+  template <int FIRST, int LAST>
+  __device__ __forceinline__ void products(const uint8_t* ks, const uint8_t* vs) {
+    bf16x8 f[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) f[i] = operand(ks, vs, FIRST + i);
+#pragma unroll
+    for (int i = FIRST; i < LAST; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      bf16x8& x = f[(i - FIRST) % kAhead];
+      if (i < kScoreOps) {
+        s[i % NB] = mfma32(x, q[i / NB], s[i % NB]);
+      } else {
+        const int j = i - kScoreOps;
+        o[j % OB] = mfma32(x, p[j / OB], o[j % OB]);
+      }
+      if (i + kAhead < LAST) x = operand(ks, vs, i + kAhead);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __device__ __forceinline__ void clear_scores() {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
-#pragma unroll
-    for (int k = 0; k < KQ; ++k)
-#pragma unroll
-      for (int b = 0; b < NB; ++b) s[b] = mfma32(read_k(ks, b, k), q[k], s[b]);
   }
-
+  // s = the tile's raw scores
+  __device__ __forceinline__ void scores(const uint8_t* ks) {
+    clear_scores();
+    products<0, kScoreOps>(ks, nullptr);
+  }
+  // o += the tile's values times their weights
+  __device__ __forceinline__ void values(const uint8_t* vs) {
+    products<kScoreOps, kScoreOps + kValueOps>(nullptr, vs);
+  }
   // this lane's row sees keys 0 .. last of the tile (last may be negative or past the end)
   __device__ __forceinline__ void mask(int lane, int last) {
-    const int h = lane >> 5;
+    const int seen = last - 4 * (lane >> 5);                        // the other part of a key's number is a constant
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        s[b][i] = 32 * b + 8 * (i / 4) + 4 * h + (i & 3) <= last ? s[b][i] : neg_inf();
+      for (int i = 0; i < 16; ++i) s[b][i] = 32 * b + 8 * (i / 4) + (i & 3) <= seen ? s[b][i] : neg_inf();
   }
 
   // p = the tile's weights.  A row's m is raised, and its l and o scaled, only
@@ -227,60 +266,90 @@ struct AttnWave {
     l += half_sum(sum);
   }
 
-  // o += the tile's values times their weights
-  __device__ __forceinline__ void values(const uint8_t* vs) {
-#pragma unroll
-    for (int st = 0; st < 2 * NB; ++st)
-#pragma unroll
-      for (int b = 0; b < OB; ++b) o[b] = mfma32(read_v(vs, st, b), p[st], o[b]);
-  }
-
-  // The same for a tile with masked places.  A weight of 0 times an infinite or
-  // NaN value is NaN, so a value that is masked for a row would reach it.  Zero
-  // times the tile's values shows whether there is one (finite values add
-  // nothing); then the product runs on the finite values, and the others are
-  // added to the rows that see them, as they are (a positive weight leaves an
-  // infinity or NaN what it is).
-  __device__ __forceinline__ void values_masked(const uint8_t* vs, int lane, int last) {
-    const int h = lane >> 5;
+  // Whether some value of the tile is infinite or NaN: zero times it is not zero.
+  __device__ __forceinline__ bool not_finite(const uint8_t* vs) const {
     f32x16 z;
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[i] = 0.0f;
     const bf16x8 zero = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+    bf16x8 f[4];
 #pragma unroll
-    for (int st = 0; st < 2 * NB; ++st)
+    for (int i = 0; i < 4; ++i) f[i] = operand(nullptr, vs, kScoreOps + i);
 #pragma unroll
-      for (int b = 0; b < OB; ++b) z = mfma32(read_v(vs, st, b), zero, z);
+    for (int i = 0; i < kValueOps; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      z = mfma32(f[i % 4], zero, z);
+      if (i + 4 < kValueOps) f[i % 4] = operand(nullptr, vs, kScoreOps + i + 4);
+    }
+    __builtin_amdgcn_sched_barrier(0);
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < 16; ++i) bad |= z[i] != 0.0f;
-    if (!__any(bad)) {
-      values(vs);
-      return;
-    }
+    return __any(bad);
+  }
+
+  // values() of a tile with masked places and values that are not all finite.  A
+  // weight of 0 times an infinite or NaN value is NaN, so a value that is masked
+  // for a row would reach it.  So the product runs on the finite values, and
+  // which rows see a +infinity, a -infinity or a NaN in which column is counted
+  // by products of 0s and 1s (a positive weight leaves such a value what it is).
+  // Few registers and little code rather than speed.
+  __device__ __forceinline__ void values_careful(const uint8_t* vs, int lane, int last) {
 #pragma unroll
     for (int st = 0; st < 2 * NB; ++st)
 #pragma unroll
-      for (int b = 0; b < OB; ++b) o[b] = mfma32(finite_only(read_v(vs, st, b)), p[st], o[b]);
+      for (int b = 0; b < OB; ++b) {
+        o[b] = mfma32(finite_only(read_v(vs, st, b)), p[st], o[b]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    const int seen = last - 4 * (lane >> 5);
+#pragma unroll
+    for (int st = 0; st < 2 * NB; ++st) {
+      u32x4 w;                                                      // 1.0 where the row sees the key
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = 16 * st + 8 * (j / 2) + 2 * (j & 1);
+        w[j] = (key <= seen ? 0x3F80u : 0u) | (key + 1 <= seen ? 0x3F800000u : 0u);
+      }
+      p[st] = __builtin_bit_cast(bf16x8, w);
+    }
 #pragma unroll 1
-    for (int key = 0; key < 32 * NB; ++key) {
+    for (int kind = 0; kind < 3; ++kind) {                          // +infinity, -infinity, NaN
+      // the kind's bit patterns: (x & care) - first < count
+      const uint32_t care = kind == 2 ? 0x7FFFu : 0xFFFFu, count = kind == 2 ? 0x7Fu : 1u;
+      const uint32_t first = kind == 0 ? 0x7F80u : (kind == 1 ? 0xFF80u : 0x7F81u);
+      const float value = kind == 0 ? -neg_inf() : (kind == 1 ? neg_inf() : __builtin_nanf(""));
 #pragma unroll
-      for (int b = 0; b < OB; ++b)
+      for (int b = 0; b < OB; ++b) {
+        f32x16 z;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int d = 32 * b + 8 * (i / 4) + 4 * h + (i & 3);
-          const uint32_t bits = *(const uint16_t*)(vs + key * (DV * 2) + (((d >> 3) ^ at_swz<DV>(key)) * 16) + (d & 7) * 2);
-          if ((bits & 0x7F80u) == 0x7F80u && key <= last) o[b][i] += __uint_as_float(bits << 16);
+        for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < 2 * NB; ++st) {
+          u32x4 w = __builtin_bit_cast(u32x4, read_v(vs, st, b));
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = ((w[j] & care) - first < count ? 0x3F80u : 0u) | (((w[j] >> 16) & care) - first < count ? 0x3F800000u : 0u);
+          z = mfma32(__builtin_bit_cast(bf16x8, w), p[st], z);
+          __builtin_amdgcn_sched_barrier(0);
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[b][i] += z[i] > 0.0f ? value : 0.0f;
+      }
     }
   }
 
-  // a whole tile; masked: see mask()
-  __device__ __forceinline__ void tile(const uint8_t* ks, const uint8_t* vs, int lane, float c, bool masked, int last) {
+  // a whole tile that every row sees; one with masked places, see mask()
+  __device__ __forceinline__ void tile(const uint8_t* ks, const uint8_t* vs, float c) {
     scores(ks);
-    if (masked) mask(lane, last);
     weights(c);
-    if (masked) values_masked(vs, lane, last);
+    values(vs);
+  }
+  __device__ __forceinline__ void tile_masked(const uint8_t* ks, const uint8_t* vs, int lane, float c, int last) {
+    scores(ks);
+    mask(lane, last);
+    weights(c);
+    if (not_finite(vs)) values_careful(vs, lane, last);
     else values(vs);
   }
 };

@@ -118,7 +118,8 @@ __global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(DecodeArgs a) 
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    w.tile(ks, vs, lane, a.c, t0 + kDecKeys > key1, (int)min(key1 - 1 - t0, (int64_t)kDecKeys));
+    if (t0 + kDecKeys <= key1) w.tile(ks, vs, a.c);
+    else w.tile_masked(ks, vs, lane, a.c, (int)(key1 - 1 - t0));
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
   // join the four waves: 4 floats of a row at a time, chunks spread over the banks

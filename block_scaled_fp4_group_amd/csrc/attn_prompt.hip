@@ -5,15 +5,14 @@
 // keys 0 .. i + Lk - Lq (the last query sees every key; with Lk < Lq the first
 // rows see none and give 0).
 //
-// A workgroup takes kRows consecutive queries of one sequence and one head, 32
+// A workgroup takes kPromptRows consecutive queries of one sequence and one head, 32
 // per wave (attn_common.h), and walks the keys in tiles of 64 through LDS.
 #include "attn_common.h"
 
 namespace moe {
 
-constexpr int kPromptWaves = 4;
-constexpr int kPromptThreads = kPromptWaves * 64;
-constexpr int kPromptRows = kPromptWaves * 32;
+constexpr int kPromptThreads = 256;
+constexpr int kPromptRows = kPromptThreads / 64 * 32;
 constexpr int kPromptKeys = 64;
 
 struct PromptArgs {
@@ -67,6 +66,7 @@ __device__ __forceinline__ PromptTile prompt_tile(const PromptArgs& a, int64_t v
 template <int DQ, int DV>
 __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptArgs a) {
   using W = AttnWave<DQ, DV, kPromptKeys / 32>;
+  constexpr int kThreads = kPromptThreads;
   __shared__ __attribute__((aligned(16))) uint8_t ks[2 * W::kKeyBytes];
   __shared__ __attribute__((aligned(16))) uint8_t vs[2 * W::kValBytes];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
@@ -79,65 +79,82 @@ __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptAr
   const PromptTile T = prompt_tile(a, vt, kPromptRows, lane);
   if (T.row0 >= T.lq) return;
   const int hq = kvh * G + g;
-  const int row = min(T.row0 + wv * 32 + (lane & 31), T.lq - 1);    // rows past the end repeat the last
+  const int wrow = T.row0 + wv * 32;                                // this wave's rows
+  const int row = min(wrow + (lane & 31), T.lq - 1);                // rows past the end repeat the last
   const int pos = row + T.lk - T.lq;                                // last key this row sees
   W w;
   w.init(a.q + (T.q0 + row) * a.q_ts + hq * a.q_hs, lane);
-  // the workgroup's and this wave's key ranges
+  // the workgroup's keys, and the last that a row of this wave sees
   const int last_row = min(T.row0 + kPromptRows, T.lq) - 1;
   const int n_keys = max(0, min(T.lk, last_row + T.lk - T.lq + 1));
-  const int wave_last = min(T.row0 + wv * 32 + 31, T.lq - 1) + T.lk - T.lq;    // most keys of a row of this wave
-  const int wave_first = min(T.row0 + wv * 32, T.lq - 1) + T.lk - T.lq;        // fewest
+  const int wave_last = min(wrow + 31, T.lq - 1) + T.lk - T.lq;
   const uint16_t* kp = a.k + T.k0 * a.k_ts + kvh * a.k_hs;
   const uint16_t* vp = a.v + T.k0 * a.v_ts + kvh * a.v_hs;
-  // each lane's share of a tile: 16-byte chunk i * threads + thread of the
-  // swizzled tile, i.e. of row r the chunk that belongs there
-  constexpr int kKeyLoads = W::kKeyBytes / 16 / kPromptThreads, kValLoads = W::kValBytes / 16 / kPromptThreads;
-  int krow[kKeyLoads], vrow[kValLoads];
-  uint32_t kchunk[kKeyLoads], vchunk[kValLoads];
-#pragma unroll
-  for (int i = 0; i < kKeyLoads; ++i) {
-    const int f = i * kPromptThreads + threadIdx.x;
-    krow[i] = f / (DQ / 8);
-    kchunk[i] = (uint32_t)((f % (DQ / 8)) ^ at_swz<DQ>(krow[i])) * 16u;
-  }
-#pragma unroll
-  for (int i = 0; i < kValLoads; ++i) {
-    const int f = i * kPromptThreads + threadIdx.x;
-    vrow[i] = f / (DV / 8);
-    vchunk[i] = (uint32_t)((f % (DV / 8)) ^ at_swz<DV>(vrow[i])) * 16u;
-  }
+  // Each lane's share of a tile: 16-byte chunk i * threads + thread of the
+  // swizzled tile, i.e. of row r the chunk that belongs there; its offset from
+  // the tile's first row in memory.  Rows past the last key repeat it.
+  constexpr int kKeyLoads = W::kKeyBytes / 16 / kThreads, kValLoads = W::kValBytes / 16 / kThreads;
   const uint32_t k_row = (uint32_t)(a.k_ts * 2), v_row = (uint32_t)(a.v_ts * 2);   // bytes; a tile spans < 2 GiB (host)
-  const uint32_t wave_lds = (uint32_t)wv * 1024u;
-  auto load = [&](int key0, int st) {
+  auto k_off = [&](int i, int end) {
+    const int f = i * kThreads + threadIdx.x, r = f / (DQ / 8);
+    return (uint32_t)min(r, end) * k_row + (uint32_t)((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16u;
+  };
+  auto v_off = [&](int i, int end) {
+    const int f = i * kThreads + threadIdx.x, r = f / (DV / 8);
+    return (uint32_t)min(r, end) * v_row + (uint32_t)((f % (DV / 8)) ^ at_swz<DV>(r)) * 16u;
+  };
+  uint32_t koff[kKeyLoads], voff[kValLoads];
+#pragma unroll
+  for (int i = 0; i < kKeyLoads; ++i) koff[i] = k_off(i, kPromptKeys - 1);
+#pragma unroll
+  for (int i = 0; i < kValLoads; ++i) voff[i] = v_off(i, kPromptKeys - 1);
+  const uint32_t k_lds = at_lds_addr(ks) + (uint32_t)wv * 1024u, v_lds = at_lds_addr(vs) + (uint32_t)wv * 1024u;
+  auto load = [&](int t, int st) {
+    const int key0 = t * kPromptKeys, end = T.lk - 1 - key0;
     const at_rsrc kr = at_make_rsrc(kp + key0 * a.k_ts), vr = at_make_rsrc(vp + key0 * a.v_ts);
-    const int end = T.lk - 1 - key0;                                // rows past the end repeat the last key
+    const uint32_t kt = k_lds + (uint32_t)(st * W::kKeyBytes), vt = v_lds + (uint32_t)(st * W::kValBytes);
+    if (end >= kPromptKeys - 1) {
 #pragma unroll
-    for (int i = 0; i < kKeyLoads; ++i)
-      at_load_lds(at_lds_addr(ks) + st * W::kKeyBytes + i * kPromptThreads * 16 + wave_lds, kr,
-                  (uint32_t)min(krow[i], end) * k_row + kchunk[i]);
+      for (int i = 0; i < kKeyLoads; ++i) at_load_lds(kt + i * kThreads * 16, kr, koff[i]);
 #pragma unroll
-    for (int i = 0; i < kValLoads; ++i)
-      at_load_lds(at_lds_addr(vs) + st * W::kValBytes + i * kPromptThreads * 16 + wave_lds, vr,
-                  (uint32_t)min(vrow[i], end) * v_row + vchunk[i]);
+      for (int i = 0; i < kValLoads; ++i) at_load_lds(vt + i * kThreads * 16, vr, voff[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kKeyLoads; ++i) at_load_lds(kt + i * kThreads * 16, kr, k_off(i, end));
+#pragma unroll
+      for (int i = 0; i < kValLoads; ++i) at_load_lds(vt + i * kThreads * 16, vr, v_off(i, end));
+    }
   };
   const int n_tiles = (n_keys + kPromptKeys - 1) / kPromptKeys;
+  // tiles that every row of the workgroup sees whole come first; for the others
+  // (around the diagonal) each wave looks whether it sees any of it at all
+  const int n_whole = max(0, min(n_tiles, (T.row0 + T.lk - T.lq + 1) / kPromptKeys));
+  auto seen = [&](int t) { return t * kPromptKeys <= wave_last; };
   if (n_tiles > 0) load(0, 0);
-  auto step = [&](auto stage, int t) {
+  auto step = [&](auto stage, auto whole, int t) {
     constexpr int st = decltype(stage)::value;
+    const uint8_t* k = ks + st * W::kKeyBytes;
+    const uint8_t* v = vs + st * W::kValBytes;
     // this wave's part of tile t has landed, then everyone's; and everyone is
     // done with tile t - 1, whose stage the next loads refill
     at_wait_barrier<0>();
-    const int key0 = t * kPromptKeys;
-    if (t + 1 < n_tiles) load(key0 + kPromptKeys, st ^ 1);
-    if (key0 <= wave_last)
-      w.tile(ks + st * W::kKeyBytes, vs + st * W::kValBytes, lane, a.c, key0 + kPromptKeys - 1 > wave_first, pos - key0);
+    if (t + 1 < n_tiles) load(t + 1, st ^ 1);
+    if (decltype(whole)::value) w.tile(k, v, a.c);
+    else if (seen(t)) w.tile_masked(k, v, lane, a.c, pos - t * kPromptKeys);
   };
-  for (int t = 0; t < n_tiles; t += 2) {
-    step(std::integral_constant<int, 0>(), t);
-    if (t + 1 < n_tiles) step(std::integral_constant<int, 1>(), t + 1);
+  using S0 = std::integral_constant<int, 0>;
+  using S1 = std::integral_constant<int, 1>;
+  int t = 0;
+  for (; t + 1 < n_whole; t += 2) {
+    step(S0(), std::true_type(), t);
+    step(S1(), std::true_type(), t + 1);
   }
-  if (T.row0 + wv * 32 + (lane & 31) >= T.lq) return;
+  // (a last odd whole tile goes with the others)
+  for (; t < n_tiles; t += 2) {
+    step(S0(), std::false_type(), t);
+    if (t + 1 < n_tiles) step(S1(), std::false_type(), t + 1);
+  }
+  if (wrow + (lane & 31) >= T.lq) return;
   const float inv = w.l == 0.0f ? 0.0f : 1.0f / w.l;
   uint16_t* op = a.out + (T.q0 + row) * a.o_ts + hq * a.o_hs;
 #pragma unroll
