@@ -80,6 +80,10 @@ __device__ __forceinline__ void at_load_lds(uint32_t lds, at_rsrc r, uint32_t of
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "s"(lds), "v"(off), "s"(r) : "memory");
 }
+// the same from a 64-bit address per lane
+__device__ __forceinline__ void at_load_lds(uint32_t lds, const void* from) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(from) : "memory");
+}
 __device__ __forceinline__ uint32_t at_lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }

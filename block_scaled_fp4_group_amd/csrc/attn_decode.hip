@@ -11,21 +11,30 @@
 //   M = max m_i,  out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 // With a single part the first kernel writes the result itself.
 //
-// A workgroup's four waves take every fourth tile of 32 keys for the same 32
-// query rows, each from its own LDS, and join their sums at the end.
+// Workgroups of four waves walk the keys in tiles of 64 through two LDS stages
+// that all waves fill (direct loads; every lane finds its rows through the block
+// table) while the other stage is computed on.  Who computes what:
+//   wide   (prefix, many rows): 128 rows, 32 per wave, each wave all 64 keys; the
+//          prefix's tile is read once per 128 rows.  Bound by the matrix cores.
+//   narrow (own keys, and a prefix with few rows): 64 rows, 2 blocks of 32 rows x
+//          2 halves of the keys; the halves are joined through LDS at the end.
+//          Bound by reading the cache.
+// Both kinds run in one launch, their workgroups interleaved, so that the one's
+// matrix work and the other's reads share the chip.
+#include <algorithm>
+
 #include "attn_common.h"
 
 namespace moe {
 
-constexpr int kDecWaves = 4;
-constexpr int kDecThreads = kDecWaves * 64;
-constexpr int kDecKeys = 32;                        // per wave and tile
-constexpr int kDecStep = kDecWaves * kDecKeys;      // per workgroup and round
+constexpr int kDecThreads = 256;
+constexpr int kDecKeys = 64;
 
 struct DecodePlan {
-  int64_t chunk_p, chunk_s;                         // keys per part
+  int32_t wide;                                     // prefix workgroups are wide
+  int32_t chunk_p, chunk_s;                         // tiles per part
   int32_t parts_p, parts_s;                         // parts of the prefix, of a request's own keys
-  int32_t blocks_p, blocks_s;                       // 32-row blocks of B * G rows, of G rows
+  int32_t blocks_p, blocks_s;                       // row blocks of B * G rows, of G rows
 };
 
 struct DecodeArgs {
@@ -51,177 +60,286 @@ __device__ __forceinline__ int64_t own_len(const DecodeArgs& a, int b) {
   return min(max((int64_t)a.lens[b], (int64_t)0), a.max_len);
 }
 
-template <int DQ, int DV>
-__global__ __launch_bounds__(kDecThreads) void attn_decode_kernel(DecodeArgs a) {
-  using W = AttnWave<DQ, DV, 1>;
-  constexpr int kTile = W::kKeyBytes + W::kValBytes;
-  static_assert(kTile >= 32 * DV * 4, "a wave's tile memory holds its sums");
-  __shared__ __attribute__((aligned(16))) uint8_t mem[kDecWaves][kTile];
-  __shared__ float2 ml[kDecWaves][32];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, h = lane >> 5, r = lane & 31;
-  const int G = a.q_heads / a.kv_heads;
-  const int kvh = blockIdx.x % a.kv_heads;
-  int64_t item = blockIdx.x / a.kv_heads;
-  const int64_t prefix_items = (int64_t)a.plan.parts_p * a.plan.blocks_p;
-  // this workgroup's rows (request row / G, head row % G from row0 on), keys and part
+// One workgroup's share: rows row0 .. of `rows` (row r is request b0 + r / G, its
+// head r % G of key head kvh) against keys key0 .. key1 - 1 of `table`.
+struct DecodeItem {
   const int32_t* table;
-  int64_t key0, key1, rows, row0;
-  int b0, part;
-  if (item < prefix_items) {
-    part = (int)(item / a.plan.blocks_p);
-    row0 = (item % a.plan.blocks_p) * 32;
-    rows = (int64_t)a.num_requests * G;
-    b0 = 0;
-    table = a.prefix_table;
-    key0 = part * a.plan.chunk_p;
-    key1 = min(key0 + a.plan.chunk_p, a.prefix_len);
-  } else {
-    item -= prefix_items;
-    const int s = (int)(item % a.plan.parts_s);
-    item /= a.plan.parts_s;
-    row0 = (item % a.plan.blocks_s) * 32;
-    b0 = (int)(item / a.plan.blocks_s);
-    rows = G;
-    part = a.plan.parts_p + s;
-    table = a.table + b0 * a.table_stride;
-    key0 = s * a.plan.chunk_s;
-    key1 = min(key0 + a.plan.chunk_s, own_len(a, b0));
-    // nothing here: the joining kernel skips the part (a single part of a request
-    // without keys still writes its empty row)
-    if (key1 <= key0 && a.part_o) return;
-  }
-  const int64_t row = min(row0 + r, rows - 1);
-  const int b = b0 + (int)(row / G), hq = kvh * G + (int)(row % G);
+  int64_t key0, key1, row0, rows;
+  int b0, kvh, part;
+};
+
+template <int DQ, int DV, bool WIDE>
+__device__ __forceinline__ void decode_item(const DecodeArgs& a, const DecodeItem& it, uint8_t* ks, uint8_t* vs) {
+  constexpr int NB = WIDE ? 2 : 1;
+  using W = AttnWave<DQ, DV, NB>;
+  constexpr int kKeyBytes = kDecKeys * DQ * 2, kValBytes = kDecKeys * DV * 2;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+  const int rb = WIDE ? wv : wv >> 1, half = WIDE ? 0 : wv & 1;
+  const int G = a.q_heads / a.kv_heads;
+  const int64_t wrow = it.row0 + rb * 32;                           // this wave's first row
+  const bool active = wrow < it.rows;
+  const int64_t row = min(wrow + (lane & 31), it.rows - 1);
+  const int b = it.b0 + (int)(row / G), hq = it.kvh * G + (int)(row % G);
   W w;
   w.init(a.q + b * a.q_ts + hq * a.q_hs, lane);
-  uint8_t* ks = mem[wv];
-  uint8_t* vs = mem[wv] + W::kKeyBytes;
-  for (int64_t t0 = key0 + wv * kDecKeys; t0 < key1; t0 += kDecStep) {
-    // the row of the cache that holds key t0 + r (keys past the end: the last)
-    const int64_t key = min(t0 + r, key1 - 1);
-    const int page = min(max(table[key >> a.page_shift], 0), a.num_pages - 1);
-    const int slot = (int)(((int64_t)page << a.page_shift) + (key & (((int64_t)1 << a.page_shift) - 1)));
-    __builtin_amdgcn_wave_barrier();
+  // Lane l looks up the cache row of key l of a tile (past the end: the last
+  // key), one tile ahead of the loads that use it: the table entry of tile t + 2
+  // is read when the loads of tile t + 1 go out.
+  const int64_t n_keys = it.key1 - it.key0;
+  const int n_tiles = (int)((n_keys + kDecKeys - 1) / kDecKeys), n_whole = (int)(n_keys / kDecKeys);
+  auto key_of = [&](int t) { return min(it.key0 + (int64_t)t * kDecKeys + lane, it.key1 - 1); };
+  auto entry = [&](int t) { return it.table[key_of(t) >> a.page_shift]; };
+  auto slot_of = [&](int e, int t) {
+    return (int)(((int64_t)min(max(e, 0), a.num_pages - 1) << a.page_shift) +
+                 (key_of(t) & (((int64_t)1 << a.page_shift) - 1)));
+  };
+  const uint32_t k_lds = at_lds_addr(ks) + (uint32_t)wv * 1024u, v_lds = at_lds_addr(vs) + (uint32_t)wv * 1024u;
+  const uint8_t* kc = (const uint8_t*)(a.k_cache + (int64_t)it.kvh * DQ);
+  const uint8_t* vc = (const uint8_t*)(a.v_cache + (int64_t)it.kvh * DV);
+  const int64_t k_row = (int64_t)a.kv_heads * DQ * 2, v_row = (int64_t)a.kv_heads * DV * 2;
+  auto load = [&](int slot, int st) {
 #pragma unroll
-    for (int i = 0; i < W::kKeyBytes / 1024; ++i) {
-      constexpr int C = DQ / 8;
-      const int f = i * 64 + lane, kr = f / C, ch = f % C;
-      const int64_t at = ((int64_t)__shfl(slot, kr) * a.kv_heads + kvh) * DQ + ch * 8;
-      *(u32x4*)(ks + kr * (DQ * 2) + (ch ^ at_swz<DQ>(kr)) * 16) = *(const u32x4*)(a.k_cache + at);
+    for (int i = 0; i < kKeyBytes / 16 / kDecThreads; ++i) {
+      const int f = i * kDecThreads + threadIdx.x, r = f / (DQ / 8);
+      at_load_lds(k_lds + (uint32_t)(st * kKeyBytes + i * kDecThreads * 16),
+                  kc + (int64_t)__shfl(slot, r) * k_row + ((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16);
     }
 #pragma unroll
-    for (int i = 0; i < W::kValBytes / 1024; ++i) {
-      constexpr int C = DV / 8;
-      const int f = i * 64 + lane, kr = f / C, ch = f % C;
-      const int64_t at = ((int64_t)__shfl(slot, kr) * a.kv_heads + kvh) * DV + ch * 8;
-      *(u32x4*)(vs + kr * (DV * 2) + (ch ^ at_swz<DV>(kr)) * 16) = *(const u32x4*)(a.v_cache + at);
+    for (int i = 0; i < kValBytes / 16 / kDecThreads; ++i) {
+      const int f = i * kDecThreads + threadIdx.x, r = f / (DV / 8);
+      at_load_lds(v_lds + (uint32_t)(st * kValBytes + i * kDecThreads * 16),
+                  vc + (int64_t)__shfl(slot, r) * v_row + ((f % (DV / 8)) ^ at_swz<DV>(r)) * 16);
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    if (t0 + kDecKeys <= key1) w.tile(ks, vs, a.c);
-    else w.tile_masked(ks, vs, lane, a.c, (int)(key1 - 1 - t0));
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  };
+  int next = 0;
+  if (n_tiles > 0) {
+    load(slot_of(entry(0), 0), 0);
+    next = entry(1);
   }
-  // join the four waves: 4 floats of a row at a time, chunks spread over the banks
-  constexpr int kChunks = DV / 4;
-  auto at = [](int rr, int ch) { return rr * kChunks + (ch ^ (rr & (kChunks - 1))); };
-  f32x4* mine = (f32x4*)mem[wv];
-#pragma unroll
-  for (int ob = 0; ob < W::OB; ++ob)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      mine[at(r, 8 * ob + 2 * i + h)] = f32x4{w.o[ob][4 * i], w.o[ob][4 * i + 1], w.o[ob][4 * i + 2], w.o[ob][4 * i + 3]};
-  if (h == 0) ml[wv][r] = float2{w.m, w.l};
-  __syncthreads();
-  const int64_t Hall = (int64_t)a.num_requests * a.q_heads;
-  for (int f = threadIdx.x; f < 32 * kChunks; f += kDecThreads) {
-    const int rr = f / kChunks, ch = f % kChunks;
-    if (row0 + rr >= rows) continue;
-    float M = neg_inf();
-#pragma unroll
-    for (int i = 0; i < kDecWaves; ++i) M = fmaxf(M, ml[i][rr].x);
-    const float base = M == neg_inf() ? 0.0f : M;
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    float L = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kDecWaves; ++i) {
-      // a wave without keys for the row has m = -inf, weight 0 and sums of 0
-      const float e = __builtin_amdgcn_exp2f(ml[i][rr].x - base);
-      L = fmaf(e, ml[i][rr].y, L);
-      const f32x4 x = ((const f32x4*)mem[i])[at(rr, ch)];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = fmaf(e, x[j], o[j]);
+  auto step = [&](auto stage, auto whole, int t) {
+    constexpr int st = decltype(stage)::value;
+    const uint8_t* k = ks + st * kKeyBytes + half * 32 * (DQ * 2);
+    const uint8_t* v = vs + st * kValBytes + half * 32 * (DV * 2);
+    // tile t has landed; everyone is done with tile t - 1, whose stage the next loads refill
+    at_wait_barrier<0>();
+    if (t + 1 < n_tiles) {
+      load(slot_of(next, t + 1), st ^ 1);
+      next = entry(t + 2);
     }
-    const int bb = b0 + (int)((row0 + rr) / G), hh = kvh * G + (int)((row0 + rr) % G);
-    const int64_t at_row = (int64_t)bb * a.q_heads + hh;
-    if (a.part_o) {
-      *(f32x4*)(a.part_o + (part * Hall + at_row) * DV + ch * 4) = o;
-      if (ch == 0) a.part_ml[part * Hall + at_row] = float2{M, L};
+    if (!active) return;
+    if (decltype(whole)::value) {
+      w.tile(k, v, a.c);
     } else {
-      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-      *(u32x2*)(a.out + bb * a.o_ts + hh * a.o_hs + ch * 4) =
-          u32x2{cvt_bf16x2(o[0] * inv, o[1] * inv), cvt_bf16x2(o[2] * inv, o[3] * inv)};
-      if (a.lse && ch == 0) a.lse[at_row] = L == 0.0f ? neg_inf() : (M + __builtin_amdgcn_logf(L)) * kLn2;
+      const int last = (int)min(n_keys - 1 - (int64_t)t * kDecKeys - half * 32, (int64_t)kDecKeys);
+      if (last >= 0) w.tile_masked(k, v, lane, a.c, last);
     }
+  };
+  using S0 = std::integral_constant<int, 0>;
+  using S1 = std::integral_constant<int, 1>;
+  int t = 0;
+  for (; t + 1 < n_whole; t += 2) {
+    step(S0(), std::true_type(), t);
+    step(S1(), std::true_type(), t + 1);
+  }
+  for (; t < n_tiles; t += 2) {
+    step(S0(), std::false_type(), t);
+    if (t + 1 < n_tiles) step(S1(), std::false_type(), t + 1);
+  }
+  if (!WIDE) {
+    // the second half's sums reach the first half's wave through the tiles' memory
+    // (same rows and columns in the same lanes)
+    at_wait_barrier<0>();
+    f32x4* box = (f32x4*)(ks + rb * (W::OB * 4 + 1) * 1024);
+    if (half == 1) {
+#pragma unroll
+      for (int x = 0; x < W::OB; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          box[(4 * x + i) * 64 + lane] = f32x4{w.o[x][4 * i], w.o[x][4 * i + 1], w.o[x][4 * i + 2], w.o[x][4 * i + 3]};
+      box[W::OB * 4 * 64 + lane] = f32x4{w.m, w.l, 0.0f, 0.0f};
+    }
+    at_wait_barrier<0>();
+    if (half == 1) return;
+    const f32x4 ml = box[W::OB * 4 * 64 + lane];
+    const float M = fmaxf(w.m, ml[0]), base = M == neg_inf() ? 0.0f : M;
+    const float e0 = __builtin_amdgcn_exp2f(w.m - base), e1 = __builtin_amdgcn_exp2f(ml[0] - base);
+    w.m = M;
+    w.l = w.l * e0 + ml[1] * e1;
+#pragma unroll
+    for (int x = 0; x < W::OB; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 y = box[(4 * x + i) * 64 + lane];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w.o[x][4 * i + j] = w.o[x][4 * i + j] * e0 + y[j] * e1;
+      }
+  }
+  if (wrow + (lane & 31) >= it.rows) return;
+  const int64_t at_row = (int64_t)b * a.q_heads + hq;
+  if (a.part_o) {
+    const int64_t at = (int64_t)it.part * a.num_requests * a.q_heads + at_row;
+    float* po = a.part_o + at * DV + 4 * h;
+#pragma unroll
+    for (int x = 0; x < W::OB; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *(f32x4*)(po + 32 * x + 8 * i) = f32x4{w.o[x][4 * i], w.o[x][4 * i + 1], w.o[x][4 * i + 2], w.o[x][4 * i + 3]};
+    if (h == 0) a.part_ml[at] = float2{w.m, w.l};
+  } else {
+    const float inv = w.l == 0.0f ? 0.0f : 1.0f / w.l;
+    uint16_t* op = a.out + b * a.o_ts + hq * a.o_hs + 4 * h;
+#pragma unroll
+    for (int x = 0; x < W::OB; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *(u32x2*)(op + 32 * x + 8 * i) = u32x2{cvt_bf16x2(w.o[x][4 * i] * inv, w.o[x][4 * i + 1] * inv),
+                                               cvt_bf16x2(w.o[x][4 * i + 2] * inv, w.o[x][4 * i + 3] * inv)};
+    if (a.lse && h == 0) a.lse[at_row] = w.l == 0.0f ? neg_inf() : (w.m + __builtin_amdgcn_logf(w.l)) * kLn2;
   }
 }
 
-// One workgroup per output row: its four waves take every fourth part.
-template <int DV>
+template <int DQ, int DV>
+__global__ __launch_bounds__(kDecThreads, 2) void attn_decode_kernel(DecodeArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t mem[2 * kDecKeys * (DQ + DV) * 2];
+  uint8_t* ks = mem;
+  uint8_t* vs = mem + 2 * kDecKeys * DQ * 2;
+  const DecodePlan& p = a.plan;
+  DecodeItem it;
+  it.kvh = blockIdx.x % a.kv_heads;
+  const int64_t i = blockIdx.x / (uint32_t)a.kv_heads;
+  const int64_t np = (int64_t)p.parts_p * p.blocks_p, n = np + (int64_t)a.num_requests * p.blocks_s * p.parts_s;
+  const int64_t ip = i * np / n;                                    // prefix items spread evenly over the launch
+  if ((i + 1) * np / n != ip) {
+    // row blocks of one part side by side: they share the part's keys in L2
+    it.part = (int)(ip / p.blocks_p);
+    it.row0 = (ip % p.blocks_p) * (p.wide ? 128 : 64);
+    it.rows = (int64_t)a.num_requests * (a.q_heads / a.kv_heads);
+    it.b0 = 0;
+    it.table = a.prefix_table;
+    it.key0 = (int64_t)it.part * p.chunk_p * kDecKeys;
+    it.key1 = min(it.key0 + (int64_t)p.chunk_p * kDecKeys, a.prefix_len);
+    if (p.wide) return decode_item<DQ, DV, true>(a, it, ks, vs);
+  } else {
+    // first parts of all requests first: later ones may not exist
+    int64_t is = i - ip;
+    const int s = (int)(is / ((int64_t)a.num_requests * p.blocks_s));
+    is %= (int64_t)a.num_requests * p.blocks_s;
+    it.row0 = (is % p.blocks_s) * 64;
+    it.b0 = (int)(is / p.blocks_s);
+    it.rows = a.q_heads / a.kv_heads;
+    it.part = p.parts_p + s;
+    it.table = a.table + it.b0 * a.table_stride;
+    it.key0 = (int64_t)s * p.chunk_s * kDecKeys;
+    it.key1 = min(it.key0 + (int64_t)p.chunk_s * kDecKeys, own_len(a, it.b0));
+    // nothing here: the joining kernel skips the part (a single part of a request
+    // without keys still writes its empty row)
+    if (it.key1 <= it.key0) {
+      if (a.part_o) return;
+      it.key1 = it.key0;
+    }
+  }
+  decode_item<DQ, DV, false>(a, it, ks, vs);
+}
+
+// The parts of an output row joined: WPR waves per row take every WPR-th part.
+// Each wave first finds its parts' maximum (64 parts at a time, one per lane), so
+// the sums' loads follow without waiting for one another.
+template <int DV, int WPR>
 __global__ __launch_bounds__(kDecThreads) void attn_join_kernel(DecodeArgs a) {
-  __shared__ float red[kDecWaves][DV];
-  __shared__ float2 ml[kDecWaves];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t Hall = (int64_t)a.num_requests * a.q_heads, at_row = blockIdx.x;
-  const int b = (int)(at_row / a.q_heads), hq = (int)(at_row % a.q_heads);
-  const int64_t len = own_len(a, b);
-  const int n = a.plan.parts_p + (int)((len + a.plan.chunk_s - 1) / a.plan.chunk_s);
-  float M = neg_inf(), L = 0.0f, o[DV / 64];
+  constexpr int kRows = 4 / WPR;
+  __shared__ float2 red[4][64];
+  __shared__ float2 ml[4];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = wv % WPR;
+  const int64_t Hall = (int64_t)a.num_requests * a.q_heads;
+  const int64_t at_row = (int64_t)blockIdx.x * kRows + wv / WPR;
+  const bool live = at_row < Hall;                                  // whole waves; a row's waves agree
+  constexpr int E = DV / 64;                                        // values per lane
+  float M = neg_inf(), L = 0.0f, o[2] = {0.0f, 0.0f};
+  if (live) {
+    const int b = (int)(at_row / a.q_heads);
+    const int64_t chunk = (int64_t)a.plan.chunk_s * kDecKeys;
+    const int n = a.plan.parts_p + (int)((own_len(a, b) + chunk - 1) / chunk);
+    const int mine = (n - sub + WPR - 1) / WPR;                     // parts sub, sub + WPR, ...
+    for (int base = 0; base < mine; base += 64) {
+      const int cnt = min(64, mine - base);
+      float2 x = float2{neg_inf(), 0.0f};
+      if (lane < cnt) x = a.part_ml[(int64_t)(sub + (base + lane) * WPR) * Hall + at_row];
+      float mx = x.x;
 #pragma unroll
-  for (int j = 0; j < DV / 64; ++j) o[j] = 0.0f;
-  for (int p = wv; p < n; p += kDecWaves) {
-    const float2 x = a.part_ml[p * Hall + at_row];
-    const float M1 = fmaxf(M, x.x), base = M1 == neg_inf() ? 0.0f : M1;
-    const float e0 = __builtin_amdgcn_exp2f(M - base), e1 = __builtin_amdgcn_exp2f(x.x - base);
-    L = fmaf(L, e0, x.y * e1);
-    const float* src = a.part_o + (p * Hall + at_row) * DV + lane * (DV / 64);
+      for (int d = 32; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+      const float M1 = fmaxf(M, mx), ref = M1 == neg_inf() ? 0.0f : M1;
+      const float e = __builtin_amdgcn_exp2f(x.x - ref), e0 = __builtin_amdgcn_exp2f(M - ref);
+      float l = x.y * e;
 #pragma unroll
-    for (int j = 0; j < DV / 64; ++j) o[j] = fmaf(o[j], e0, src[j] * e1);
+      for (int d = 32; d > 0; d >>= 1) l += __shfl_xor(l, d);
+      L = L * e0 + l;
+      M = M1;
+#pragma unroll
+      for (int j = 0; j < E; ++j) o[j] *= e0;
+#pragma unroll 4
+      for (int p = 0; p < cnt; ++p) {
+        const float ep = __shfl(e, p);
+        const float* src = a.part_o + ((int64_t)(sub + (base + p) * WPR) * Hall + at_row) * DV + lane * E;
+        if (E == 2) {
+          const float2 y = *(const float2*)src;
+          o[0] = fmaf(ep, y.x, o[0]);
+          o[1] = fmaf(ep, y.y, o[1]);
+        } else {
+          o[0] = fmaf(ep, src[0], o[0]);
+        }
+      }
+    }
+  }
+  if (WPR > 1) {
+    red[wv][lane] = float2{o[0], o[1]};
+    if (lane == 0) ml[wv] = float2{M, L};
+    __syncthreads();
+    if (sub != 0) return;
+    float M1 = M;
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) M1 = fmaxf(M1, ml[wv + i].x);
+    const float ref = M1 == neg_inf() ? 0.0f : M1;
+    float e = __builtin_amdgcn_exp2f(M - ref);
+    L *= e;
+    o[0] *= e;
+    o[1] *= e;
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) {
+      e = __builtin_amdgcn_exp2f(ml[wv + i].x - ref);
+      const float2 y = red[wv + i][lane];
+      L = fmaf(e, ml[wv + i].y, L);
+      o[0] = fmaf(e, y.x, o[0]);
+      o[1] = fmaf(e, y.y, o[1]);
+    }
     M = M1;
   }
-#pragma unroll
-  for (int j = 0; j < DV / 64; ++j) red[wv][lane * (DV / 64) + j] = o[j];
-  if (lane == 0) ml[wv] = float2{M, L};
-  __syncthreads();
-  if (threadIdx.x >= DV / 2) return;
-  float M1 = neg_inf(), L1 = 0.0f, x0 = 0.0f, x1 = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kDecWaves; ++i) M1 = fmaxf(M1, ml[i].x);
-  const float base = M1 == neg_inf() ? 0.0f : M1;
-#pragma unroll
-  for (int i = 0; i < kDecWaves; ++i) {
-    const float e = __builtin_amdgcn_exp2f(ml[i].x - base);
-    L1 = fmaf(e, ml[i].y, L1);
-    x0 = fmaf(e, red[i][2 * threadIdx.x], x0);
-    x1 = fmaf(e, red[i][2 * threadIdx.x + 1], x1);
-  }
-  const float inv = L1 == 0.0f ? 0.0f : 1.0f / L1;
-  *(uint32_t*)(a.out + b * a.o_ts + hq * a.o_hs + 2 * threadIdx.x) = cvt_bf16x2(x0 * inv, x1 * inv);
-  if (a.lse && threadIdx.x == 0) a.lse[at_row] = L1 == 0.0f ? neg_inf() : (M1 + __builtin_amdgcn_logf(L1)) * kLn2;
+  if (!live) return;
+  const int b = (int)(at_row / a.q_heads), hq = (int)(at_row % a.q_heads);
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  uint16_t* dst = a.out + b * a.o_ts + hq * a.o_hs + lane * E;
+  if (E == 2) *(uint32_t*)dst = cvt_bf16x2(o[0] * inv, o[1] * inv);
+  else *dst = (uint16_t)f32_to_bf16_bits(o[0] * inv);
+  if (a.lse && lane == 0) a.lse[at_row] = L == 0.0f ? neg_inf() : (M + __builtin_amdgcn_logf(L)) * kLn2;
 }
 
 static DecodePlan decode_plan(int64_t B, int q_heads, int kv_heads, int64_t prefix_len, int64_t max_len) {
   DecodePlan p;
-  const int G = q_heads / kv_heads;
-  p.blocks_p = (int32_t)((B * G + 31) / 32);
-  p.blocks_s = (G + 31) / 32;
-  // keys per workgroup so that about 1024 workgroups share the work
-  const int64_t work = kv_heads * (prefix_len * p.blocks_p + B * max_len * p.blocks_s);
-  int64_t chunk = (work / 1024 + kDecStep - 1) / kDecStep * kDecStep;
-  if (chunk < 2 * kDecStep) chunk = 2 * kDecStep;
-  p.chunk_p = p.chunk_s = chunk;
-  p.parts_p = (int32_t)((prefix_len + chunk - 1) / chunk);
-  p.parts_s = (int32_t)((max_len + chunk - 1) / chunk);
+  const int64_t G = q_heads / kv_heads, rows = B * G;
+  auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  p.wide = rows > 64;
+  p.blocks_p = (int32_t)up(rows, p.wide ? 128 : 64);
+  p.blocks_s = (int32_t)up(G, 64);
+  // Two workgroups run on each of the 256 CUs, and a tile takes about as long in
+  // either kind (2.1 us of matrix work, 2.6 us of its share of the reads): parts
+  // of tiles / 512 tiles each fill the chip once.  Own keys go in finer parts
+  // (their lengths differ; max_len is only a bound), at least 2 tiles.
+  const int64_t tiles_p = up(prefix_len, kDecKeys), tiles_s = up(max_len, kDecKeys);
+  const int64_t work = kv_heads * (tiles_p * p.blocks_p + tiles_s * B * p.blocks_s);
+  const int64_t fill = std::max<int64_t>(2, up(work, 512));
+  p.parts_p = (int32_t)up(tiles_p, fill);
+  p.chunk_p = (int32_t)std::max<int64_t>(1, up(tiles_p, std::max(p.parts_p, 1)));
+  p.chunk_s = (int32_t)std::max<int64_t>(2, up(fill, 2));
+  p.parts_s = (int32_t)up(tiles_s, p.chunk_s);
   if (p.parts_p + p.parts_s == 0) p.parts_s = 1;      // no key anywhere: the single part writes the empty rows
   return p;
 }
@@ -244,9 +362,13 @@ template <int DQ, int DV>
 static void launch_decode(const DecodeArgs& a, hipStream_t stream) {
   const uint32_t grid = (uint32_t)plan_grid(a.plan, a.num_requests, a.kv_heads);
   hipLaunchKernelGGL((attn_decode_kernel<DQ, DV>), dim3(grid), dim3(kDecThreads), 0, stream, a);
-  if (a.part_o)
-    hipLaunchKernelGGL((attn_join_kernel<DV>), dim3((uint32_t)(a.num_requests * a.q_heads)), dim3(kDecThreads), 0,
-                       stream, a);
+  if (!a.part_o) return;
+  const uint32_t rows = (uint32_t)(a.num_requests * a.q_heads);
+  // a wave per row while there are few parts; four, when a row has many
+  if (a.plan.parts_p + a.plan.parts_s <= 16)
+    hipLaunchKernelGGL((attn_join_kernel<DV, 1>), dim3((rows + 3) / 4), dim3(kDecThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((attn_join_kernel<DV, 4>), dim3(rows), dim3(kDecThreads), 0, stream, a);
 }
 
 moe_status launch_attn_decode(const moe_heads& q, const moe_kv_cache& cache, const int32_t* table,
