@@ -426,43 +426,86 @@ def quantize_nvfp4_planes(x: torch.Tensor, input_scale: float = 1.0, planes=None
 
 
 # ----------------------------------------------------------------- attention
-def _want(t, name: str, dtype, ndim: int, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.ndim != ndim or t.device != device:
-        raise ValueError(f"{name} must be a {ndim}-d {dtype} tensor on {device}")
+# (The decode step's calls run in a few microseconds on the GPU, so the checks
+# here are written to cost little: a wrong argument is described in the slow path.)
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _want_flat(t, name: str, dtype, ndim: int, device):
-    _want(t, name, dtype, ndim, device)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _bad(t, name: str, dtype, ndim: int, index: int):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if index < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    raise ValueError(f"{name} must be a {ndim}-d {dtype} tensor on cuda:{index}, its last dimension contiguous (got "
+                     f"{tuple(t.shape)}, strides {t.stride()}, {t.dtype}, {t.device})")
 
 
-def _heads(t, name: str, device, heads=None, dim=None) -> Heads:
+def _gpu(t, name: str) -> int:
+    """The tensor's device index."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.get_device()
+
+
+def _flat(t, name: str, dtype, ndim: int, index: int) -> int:
+    """Address of a contiguous tensor."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index or t.dim() != ndim \
+            or not t.is_contiguous():
+        _bad(t, name, dtype, ndim, index)
+    return t.data_ptr()
+
+
+def _table(t, name: str, rows: int, index: int):
+    """(address, row stride, columns) of an int32 table whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.get_device() != index or t.dim() != 2:
+        _bad(t, name, _I32, 2, index)
+    n, cols = t.shape
+    if n < rows:
+        raise ValueError(f"{name} needs a row for each of {rows} requests")
+    rs, cs = t.stride()
+    if cols > 1 and cs != 1:
+        _bad(t, name, _I32, 2, index)
+    return t.data_ptr(), rs if n > 1 else cols, cols
+
+
+def _heads(t, name: str, index: int, tokens=None, heads=None, dim=None) -> Heads:
     """bf16 [tokens, heads, dim], any token and head strides, dim contiguous."""
-    _want(t, name, torch.bfloat16, 3, device)
-    if (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
-        raise ValueError(f"{name}: shape {tuple(t.shape)} does not fit (heads {heads}, dim {dim})")
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != index or t.dim() != 3:
+        _bad(t, name, _BF16, 3, index)
+    T, H, D = t.shape
     ts, hs, ds = t.stride()
-    if ds != 1 and t.shape[2] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if ds != 1 and D > 1:
+        _bad(t, name, _BF16, 3, index)
+    if (tokens is not None and T != tokens) or (heads is not None and H != heads) or (dim is not None and D != dim):
+        raise ValueError(f"{name}: shape {(T, H, D)} does not fit (tokens {tokens}, heads {heads}, dim {dim})")
     # the strides of dimensions of one element say nothing
-    hs = hs if t.shape[1] > 1 else t.shape[2]
-    ts = ts if t.shape[0] > 1 else (t.shape[1] - 1) * hs + t.shape[2]
+    if H == 1:
+        hs = D
+    if T == 1:
+        ts = (H - 1) * hs + D
     return Heads(t.data_ptr(), ts, hs)
 
 
-def _cuda(t, name: str):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    return t.device
+def _cache(k_cache, v_cache, index: int, kv_heads: int, k_dim: int) -> KvCache:
+    k, v = _flat(k_cache, "k_cache", _BF16, 4, index), _flat(v_cache, "v_cache", _BF16, 4, index)
+    pages, page, heads, dim = k_cache.shape
+    if heads != kv_heads or dim != k_dim or v_cache.shape[:3] != (pages, page, heads):
+        raise ValueError(f"k_cache {tuple(k_cache.shape)} / v_cache {tuple(v_cache.shape)} do not fit "
+                         f"(pages, page_size, {kv_heads}, {k_dim})")
+    return KvCache(k, v, pages, page)
 
 
-def _made(stream, *tensors):
-    """Tensors allocated here belong to the current stream; a call on another one has to be known to the allocator."""
-    if stream is not None and stream != torch.cuda.current_stream():
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _at(stream, index: int, *made) -> int:
+    """The stream to launch on.  Tensors made here belong to the current stream; their use on another one has to be
+    known to the allocator."""
+    if stream is None:
+        return _raw_stream(index)
+    for t in made:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
 
 
 def kv_slots(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
@@ -471,44 +514,34 @@ def kv_slots(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torc
     """Cache slots of a step's new tokens.  int32 tensors: cached_lens, new_lens [B], free_pages [F], block_table
     [B, blocks] (new pages are entered in place).  -> (slots [max_new], positions [max_new], cu_new [B + 1],
     counts [3]: pages taken, pages needed, tokens without a slot).  ``position_base``: length of a shared prefix."""
-    dev = _cuda(cached_lens, "cached_lens")
-    i32 = torch.int32
-    B = cached_lens.shape[0]
-    _want_flat(cached_lens, "cached_lens", i32, 1, dev)
-    _want_flat(new_lens, "new_lens", i32, 1, dev)
-    _want_flat(free_pages, "free_pages", i32, 1, dev)
-    _want(block_table, "block_table", i32, 2, dev)
-    if new_lens.shape[0] != B or block_table.shape[0] != B or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("new_lens and block_table must have a row for each request, rows contiguous")
-    stride = block_table.stride(0) if B > 1 else block_table.shape[1]
+    dev = _gpu(cached_lens, "cached_lens")
+    cached, new = _flat(cached_lens, "cached_lens", _I32, 1, dev), _flat(new_lens, "new_lens", _I32, 1, dev)
+    free = _flat(free_pages, "free_pages", _I32, 1, dev)
+    B = cached_lens.numel()
+    if new_lens.numel() != B:
+        raise ValueError("cached_lens and new_lens must have an entry for each request")
+    table, stride, blocks = _table(block_table, "block_table", B, dev)
     made = []
-    if slots is None:
-        made.append(slots := torch.empty(max_new, dtype=i32, device=dev))
-    if positions is None:
-        made.append(positions := torch.empty(max_new, dtype=i32, device=dev))
-    if cu_new is None:
-        made.append(cu_new := torch.empty(B + 1, dtype=i32, device=dev))
-    if counts is None:
-        made.append(counts := torch.empty(3, dtype=i32, device=dev))
-    for t, name, n in ((slots, "slots", max_new), (positions, "positions", max_new), (cu_new, "cu_new", B + 1),
-                       (counts, "counts", 3)):
-        _want_flat(t, name, i32, 1, dev)
-        if t.shape[0] < n:
+
+    def output(t, name, n):
+        if t is None:
+            t = cached_lens.new_empty(n)
+            made.append(t)
+            return t, t.data_ptr()
+        address = _flat(t, name, _I32, 1, dev)
+        if t.numel() < n:
             raise ValueError(f"{name} needs {n} elements")
-    _check(lib.moe_kv_slots(_ptr(cached_lens), _ptr(new_lens), B, _ptr(free_pages), free_pages.shape[0], page_size,
-                            _ptr(block_table), stride, block_table.shape[1], position_base, max_new, _ptr(slots),
-                            _ptr(positions), _ptr(cu_new), _ptr(counts), _stream(stream)), "moe_kv_slots")
-    _made(stream, *made)
+        return t, address
+
+    slots, s = output(slots, "slots", max_new)
+    positions, p = output(positions, "positions", max_new)
+    cu_new, c = output(cu_new, "cu_new", B + 1)
+    counts, n = output(counts, "counts", 3)
+    st = lib.moe_kv_slots(cached, new, B, free, free_pages.numel(), page_size, table, stride, blocks, position_base,
+                          max_new, s, p, c, n, _at(stream, dev, *made))
+    if st:
+        _check(st, "moe_kv_slots")
     return slots, positions, cu_new, counts
-
-
-def _cache(k_cache, v_cache, device, kv_heads: int, k_dim: int) -> KvCache:
-    _want_flat(k_cache, "k_cache", torch.bfloat16, 4, device)
-    _want_flat(v_cache, "v_cache", torch.bfloat16, 4, device)
-    if k_cache.shape[:3] != v_cache.shape[:3] or k_cache.shape[2] != kv_heads or k_cache.shape[3] != k_dim:
-        raise ValueError(f"k_cache {tuple(k_cache.shape)} / v_cache {tuple(v_cache.shape)} do not fit "
-                         f"(pages, page_size, {kv_heads}, {k_dim})")
-    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], k_cache.shape[1])
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor],
@@ -520,48 +553,49 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
     ``cos_sin`` float32 [positions, rot_dim] (cosines, then sines; None: no rotation), and with a cache the write of
     the finished keys and of v [T, Hkv, Dv] to its rows ``slots``.  -> (q_out, k_out); k_out is None with
     ``want_k=False`` (cache only).  q_out / k_out may be q / k."""
-    dev = _cuda(q, "q")
+    dev = _gpu(q, "q")
     hq = _heads(q, "q", dev)
     T, Hq, D = q.shape
-    hk = _heads(k, "k", dev, dim=D)
+    hk = _heads(k, "k", dev, tokens=T, dim=D)
     Hkv = k.shape[1]
-    f32, i32 = torch.float32, torch.int32
-    if k.shape[0] != T:
-        raise ValueError("q and k must have the same tokens")
-    rot = 0
+    rot = rows = 0
+    pos = table = qw = kw = at = None
     if cos_sin is not None:
-        _want_flat(cos_sin, "cos_sin", f32, 2, dev)
-        _want_flat(positions, "positions", i32, 1, dev)
-        if positions.shape[0] < T:
+        table, pos = _flat(cos_sin, "cos_sin", _F32, 2, dev), _flat(positions, "positions", _I32, 1, dev)
+        rows, rot = cos_sin.shape
+        if positions.numel() < T:
             raise ValueError("positions needs an entry for each token")
-        rot = cos_sin.shape[1]
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _want_flat(t, name, f32, 1, dev)
-            if t.shape[0] != D:
-                raise ValueError(f"{name} needs {D} elements")
+    if q_weight is not None:
+        qw = _flat(q_weight, "q_weight", _F32, 1, dev)
+    if k_weight is not None:
+        kw = _flat(k_weight, "k_weight", _F32, 1, dev)
+    if (qw is not None and q_weight.numel() != D) or (kw is not None and k_weight.numel() != D):
+        raise ValueError(f"q_weight and k_weight need {D} elements")
     cache = hv = None
     Dv = 0
     if k_cache is not None:
         cache = _cache(k_cache, v_cache, dev, Hkv, D)
         Dv = v_cache.shape[3]
-        hv = _heads(v, "v", dev, Hkv, Dv)
-        _want_flat(slots, "slots", i32, 1, dev)
-        if v.shape[0] != T or slots.shape[0] < T:
-            raise ValueError("v and slots need an entry for each token")
-    made = []
+        hv = _heads(v, "v", dev, T, Hkv, Dv)
+        at = _flat(slots, "slots", _I32, 1, dev)
+        if slots.numel() < T:
+            raise ValueError("slots needs an entry for each token")
+    made_q = made_k = None
     if q_out is None:
-        made.append(q_out := torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev))
-    if k_out is None and want_k:
-        made.append(k_out := torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=dev))
-    ho = _heads(q_out, "q_out", dev, Hq, D)
-    hko = None if k_out is None else _heads(k_out, "k_out", dev, Hkv, D)
-    if q_out.shape[0] != T or (k_out is not None and k_out.shape[0] != T):
-        raise ValueError("q_out and k_out need a row for each token")
-    p = RopeParams(Hq, Hkv, D, Dv, rot, int(interleaved), 0 if cos_sin is None else cos_sin.shape[0], eps)
-    _check(lib.moe_qk_norm_rope(hq, hk, hv, T, p, _ptr(positions), _ptr(cos_sin), _ptr(q_weight), _ptr(k_weight), ho, hko,
-                                cache, _ptr(slots), _stream(stream)), "moe_qk_norm_rope")
-    _made(stream, *made)
+        q_out = made_q = q.new_empty((T, Hq, D))
+        ho = Heads(q_out.data_ptr(), Hq * D, D)
+    else:
+        ho = _heads(q_out, "q_out", dev, T, Hq, D)
+    hko = None
+    if k_out is not None:
+        hko = _heads(k_out, "k_out", dev, T, Hkv, D)
+    elif want_k:
+        k_out = made_k = k.new_empty((T, Hkv, D))
+        hko = Heads(k_out.data_ptr(), Hkv * D, D)
+    st = lib.moe_qk_norm_rope(hq, hk, hv, T, RopeParams(Hq, Hkv, D, Dv, rot, interleaved, rows, eps), pos, table, qw, kw,
+                              ho, hko, cache, at, _at(stream, dev, made_q, made_k))
+    if st:
+        _check(st, "moe_qk_norm_rope")
     return q_out, k_out
 
 
@@ -571,32 +605,36 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     """Causal attention over packed prompts: q [Tq, Hq, D], k [Tk, Hkv, D], v [Tk, Hkv, Dv], offsets cu_q, cu_k int32
     [B + 1] (cu_k None: cu_q).  Query i of a sequence sees keys 0 .. i + Lk - Lq.  -> (out [Tq, Hq, Dv], lse float32
     [Tq, Hq] or None).  Rows outside the offsets' ranges are not written."""
-    dev = _cuda(q, "q")
+    dev = _gpu(q, "q")
     cu_k = cu_q if cu_k is None else cu_k
     hq = _heads(q, "q", dev)
     Tq, Hq, D = q.shape
     hk = _heads(k, "k", dev, dim=D)
     Tk, Hkv, _ = k.shape
-    hv = _heads(v, "v", dev, heads=Hkv)
+    hv = _heads(v, "v", dev, Tk, Hkv)
     Dv = v.shape[2]
-    _want_flat(cu_q, "cu_q", torch.int32, 1, dev)
-    _want_flat(cu_k, "cu_k", torch.int32, 1, dev)
-    if v.shape[0] != Tk or cu_q.shape != cu_k.shape or cu_q.shape[0] < 1:
-        raise ValueError("v needs a row for each key, cu_q and cu_k an entry for each sequence and the end")
-    made = []
+    cq, ck = _flat(cu_q, "cu_q", _I32, 1, dev), _flat(cu_k, "cu_k", _I32, 1, dev)
+    n = cu_q.numel()
+    if n < 1 or cu_k.numel() != n:
+        raise ValueError("cu_q and cu_k must have an entry for each sequence and the end")
+    made_o = made_l = None
     if out is None:
-        made.append(out := torch.empty((Tq, Hq, Dv), dtype=torch.bfloat16, device=dev))
-    if lse is None and want_lse:
-        made.append(lse := torch.empty((Tq, Hq), dtype=torch.float32, device=dev))
-    ho = _heads(out, "out", dev, Hq, Dv)
+        out = made_o = q.new_empty((Tq, Hq, Dv))
+        ho = Heads(out.data_ptr(), Hq * Dv, Dv)
+    else:
+        ho = _heads(out, "out", dev, Tq, Hq, Dv)
+    pl = None
     if lse is not None:
-        _want_flat(lse, "lse", torch.float32, 2, dev)
-    if out.shape[0] != Tq or (lse is not None and lse.shape != (Tq, Hq)):
-        raise ValueError("out and lse need a row for each query")
-    p = AttnParams(Hq, Hkv, D, Dv, D ** -0.5 if scale is None else scale)
-    _check(lib.moe_attn_prompt(hq, hk, hv, _ptr(cu_q), _ptr(cu_k), cu_q.shape[0] - 1, Tq, Tk, p, ho, _ptr(lse),
-                               _stream(stream)), "moe_attn_prompt")
-    _made(stream, *made)
+        pl = _flat(lse, "lse", _F32, 2, dev)
+        if lse.shape != (Tq, Hq):
+            raise ValueError(f"lse must be {(Tq, Hq)}")
+    elif want_lse:
+        lse = made_l = q.new_empty((Tq, Hq), dtype=_F32)
+        pl = lse.data_ptr()
+    st = lib.moe_attn_prompt(hq, hk, hv, cq, ck, n - 1, Tq, Tk, AttnParams(Hq, Hkv, D, Dv, D ** -0.5 if scale is None else scale),
+                             ho, pl, _at(stream, dev, made_o, made_l))
+    if st:
+        _check(st, "moe_attn_prompt")
     return out, lse
 
 
@@ -613,44 +651,48 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
     """One query per request, q [B, Hq, D], over the paged cache: the shared prefix (``prefix_len`` keys in the pages
     ``prefix_table``), then the request's own ``lens`` keys in its ``block_table`` pages (int32).  ``max_len``: a
     longest own length known on the host.  -> (out [B, Hq, Dv], lse float32 [B, Hq] or None)."""
-    dev = _cuda(q, "q")
+    dev = _gpu(q, "q")
     hq = _heads(q, "q", dev)
     B, Hq, D = q.shape
-    if k_cache.ndim != 4 or v_cache.ndim != 4:
+    if k_cache.dim() != 4 or v_cache.dim() != 4:
         raise ValueError("k_cache and v_cache must be [pages, page_size, heads, dim]")
     Hkv, Dv = k_cache.shape[2], v_cache.shape[3]
     cache = _cache(k_cache, v_cache, dev, Hkv, D)
-    i32 = torch.int32
-    _want(block_table, "block_table", i32, 2, dev)
-    _want_flat(lens, "lens", i32, 1, dev)
-    if lens.shape[0] < B or block_table.shape[0] < B or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("lens and block_table must have a row for each request, rows contiguous")
+    table, stride, blocks = _table(block_table, "block_table", B, dev)
+    ln = _flat(lens, "lens", _I32, 1, dev)
+    if lens.numel() < B:
+        raise ValueError("lens needs an entry for each request")
+    pt, pn = None, 0
     if prefix_table is not None:
-        _want_flat(prefix_table, "prefix_table", i32, 1, dev)
-    stride = block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
+        pt, pn = _flat(prefix_table, "prefix_table", _I32, 1, dev), prefix_table.numel()
     p = AttnParams(Hq, Hkv, D, Dv, D ** -0.5 if scale is None else scale)
-    made = []
+    made_w = made_o = made_l = ws = None
+    nbytes = 0
     if workspace is None:
-        need = int(lib.moe_attn_decode_workspace_bytes(B, prefix_len, max_len, p))
+        need = lib.moe_attn_decode_workspace_bytes(B, prefix_len, max_len, p)
         if need:
-            made.append(workspace := torch.empty(need, dtype=torch.uint8, device=dev))
-    elif not workspace.is_cuda or not workspace.is_contiguous():
+            workspace = made_w = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor")
+    if workspace is not None:
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if out is None:
-        made.append(out := torch.empty((B, Hq, Dv), dtype=torch.bfloat16, device=dev))
-    if lse is None and want_lse:
-        made.append(lse := torch.empty((B, Hq), dtype=torch.float32, device=dev))
-    ho = _heads(out, "out", dev, Hq, Dv)
+        out = made_o = q.new_empty((B, Hq, Dv))
+        ho = Heads(out.data_ptr(), Hq * Dv, Dv)
+    else:
+        ho = _heads(out, "out", dev, B, Hq, Dv)
+    pl = None
     if lse is not None:
-        _want_flat(lse, "lse", torch.float32, 2, dev)
-    if out.shape[0] != B or (lse is not None and lse.shape != (B, Hq)):
-        raise ValueError("out and lse need a row for each request")
-    _check(lib.moe_attn_decode(hq, cache, _ptr(block_table), stride, block_table.shape[1], _ptr(lens), B, max_len,
-                               _ptr(prefix_table), 0 if prefix_table is None else prefix_table.shape[0], prefix_len, p,
-                               ho, _ptr(lse), _ptr(workspace),
-                               0 if workspace is None else workspace.numel() * workspace.element_size(),
-                               _stream(stream)), "moe_attn_decode")
-    _made(stream, *made)
+        pl = _flat(lse, "lse", _F32, 2, dev)
+        if lse.shape != (B, Hq):
+            raise ValueError(f"lse must be {(B, Hq)}")
+    elif want_lse:
+        lse = made_l = q.new_empty((B, Hq), dtype=_F32)
+        pl = lse.data_ptr()
+    st = lib.moe_attn_decode(hq, cache, table, stride, blocks, ln, B, max_len, pt, pn, prefix_len, p, ho, pl, ws, nbytes,
+                             _at(stream, dev, made_w, made_o, made_l))
+    if st:
+        _check(st, "moe_attn_decode")
     return out, lse
 
 
