@@ -84,6 +84,10 @@ __device__ __forceinline__ void at_load_lds(uint32_t lds, at_rsrc r, uint32_t of
 __device__ __forceinline__ void at_load_lds(uint32_t lds, const void* from) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(from) : "memory");
 }
+// 4 bytes per lane: lane i's land at lds + 4 i
+__device__ __forceinline__ void at_load_lds4(uint32_t lds, const void* from) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" :: "s"(lds), "v"(from) : "memory");
+}
 __device__ __forceinline__ uint32_t at_lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }

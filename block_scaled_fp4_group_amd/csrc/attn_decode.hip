@@ -11,13 +11,12 @@
 //   M = max m_i,  out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 // With a single part the first kernel writes the result itself.
 //
-// Workgroups of four waves walk the keys in tiles of 64 through two LDS stages
-// that all waves fill (direct loads; every lane finds its rows through the block
-// table) while the other stage is computed on.  Who computes what:
-//   wide   (prefix, many rows): 128 rows, 32 per wave, each wave all 64 keys; the
-//          prefix's tile is read once per 128 rows.  Bound by the matrix cores.
-//   narrow (own keys, and a prefix with few rows): 64 rows, 2 blocks of 32 rows x
-//          2 halves of the keys; the halves are joined through LDS at the end.
+// Workgroups of four waves walk the keys in tiles through LDS stages that all
+// waves fill (direct loads; every lane finds its rows through the block table)
+// while another is computed on:
+//   wide   (prefix, many rows): 128 rows, 32 per wave; the prefix is read once
+//          per 128 rows.  Bound by the matrix cores.
+//   narrow (own keys, and a prefix with few rows): 64 rows, two waves per 32.
 //          Bound by reading the cache.
 // Both kinds run in one launch, their workgroups interleaved, so that the one's
 // matrix work and the other's reads share the chip.
@@ -68,113 +67,15 @@ struct DecodeItem {
   int b0, kvh, part;
 };
 
-template <int DQ, int DV, bool WIDE>
-__device__ __forceinline__ void decode_item(const DecodeArgs& a, const DecodeItem& it, uint8_t* ks, uint8_t* vs) {
-  constexpr int NB = WIDE ? 2 : 1;
-  using W = AttnWave<DQ, DV, NB>;
-  constexpr int kKeyBytes = kDecKeys * DQ * 2, kValBytes = kDecKeys * DV * 2;
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
-  const int rb = WIDE ? wv : wv >> 1, half = WIDE ? 0 : wv & 1;
-  const int G = a.q_heads / a.kv_heads;
-  const int64_t wrow = it.row0 + rb * 32;                           // this wave's first row
-  const bool active = wrow < it.rows;
-  const int64_t row = min(wrow + (lane & 31), it.rows - 1);
-  const int b = it.b0 + (int)(row / G), hq = it.kvh * G + (int)(row % G);
-  W w;
-  w.init(a.q + b * a.q_ts + hq * a.q_hs, lane);
-  // Lane l looks up the cache row of key l of a tile (past the end: the last
-  // key), one tile ahead of the loads that use it: the table entry of tile t + 2
-  // is read when the loads of tile t + 1 go out.
-  const int64_t n_keys = it.key1 - it.key0;
-  const int n_tiles = (int)((n_keys + kDecKeys - 1) / kDecKeys), n_whole = (int)(n_keys / kDecKeys);
-  auto key_of = [&](int t) { return min(it.key0 + (int64_t)t * kDecKeys + lane, it.key1 - 1); };
-  auto entry = [&](int t) { return it.table[key_of(t) >> a.page_shift]; };
-  auto slot_of = [&](int e, int t) {
-    return (int)(((int64_t)min(max(e, 0), a.num_pages - 1) << a.page_shift) +
-                 (key_of(t) & (((int64_t)1 << a.page_shift) - 1)));
-  };
-  const uint32_t k_lds = at_lds_addr(ks) + (uint32_t)wv * 1024u, v_lds = at_lds_addr(vs) + (uint32_t)wv * 1024u;
-  const uint8_t* kc = (const uint8_t*)(a.k_cache + (int64_t)it.kvh * DQ);
-  const uint8_t* vc = (const uint8_t*)(a.v_cache + (int64_t)it.kvh * DV);
-  const int64_t k_row = (int64_t)a.kv_heads * DQ * 2, v_row = (int64_t)a.kv_heads * DV * 2;
-  auto load = [&](int slot, int st) {
-#pragma unroll
-    for (int i = 0; i < kKeyBytes / 16 / kDecThreads; ++i) {
-      const int f = i * kDecThreads + threadIdx.x, r = f / (DQ / 8);
-      at_load_lds(k_lds + (uint32_t)(st * kKeyBytes + i * kDecThreads * 16),
-                  kc + (int64_t)__shfl(slot, r) * k_row + ((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16);
-    }
-#pragma unroll
-    for (int i = 0; i < kValBytes / 16 / kDecThreads; ++i) {
-      const int f = i * kDecThreads + threadIdx.x, r = f / (DV / 8);
-      at_load_lds(v_lds + (uint32_t)(st * kValBytes + i * kDecThreads * 16),
-                  vc + (int64_t)__shfl(slot, r) * v_row + ((f % (DV / 8)) ^ at_swz<DV>(r)) * 16);
-    }
-  };
-  int next = 0;
-  if (n_tiles > 0) {
-    load(slot_of(entry(0), 0), 0);
-    next = entry(1);
-  }
-  auto step = [&](auto stage, auto whole, int t) {
-    constexpr int st = decltype(stage)::value;
-    const uint8_t* k = ks + st * kKeyBytes + half * 32 * (DQ * 2);
-    const uint8_t* v = vs + st * kValBytes + half * 32 * (DV * 2);
-    // tile t has landed; everyone is done with tile t - 1, whose stage the next loads refill
-    at_wait_barrier<0>();
-    if (t + 1 < n_tiles) {
-      load(slot_of(next, t + 1), st ^ 1);
-      next = entry(t + 2);
-    }
-    if (!active) return;
-    if (decltype(whole)::value) {
-      w.tile(k, v, a.c);
-    } else {
-      const int last = (int)min(n_keys - 1 - (int64_t)t * kDecKeys - half * 32, (int64_t)kDecKeys);
-      if (last >= 0) w.tile_masked(k, v, lane, a.c, last);
-    }
-  };
-  using S0 = std::integral_constant<int, 0>;
-  using S1 = std::integral_constant<int, 1>;
-  int t = 0;
-  for (; t + 1 < n_whole; t += 2) {
-    step(S0(), std::true_type(), t);
-    step(S1(), std::true_type(), t + 1);
-  }
-  for (; t < n_tiles; t += 2) {
-    step(S0(), std::false_type(), t);
-    if (t + 1 < n_tiles) step(S1(), std::false_type(), t + 1);
-  }
-  if (!WIDE) {
-    // the second half's sums reach the first half's wave through the tiles' memory
-    // (same rows and columns in the same lanes)
-    at_wait_barrier<0>();
-    f32x4* box = (f32x4*)(ks + rb * (W::OB * 4 + 1) * 1024);
-    if (half == 1) {
-#pragma unroll
-      for (int x = 0; x < W::OB; ++x)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          box[(4 * x + i) * 64 + lane] = f32x4{w.o[x][4 * i], w.o[x][4 * i + 1], w.o[x][4 * i + 2], w.o[x][4 * i + 3]};
-      box[W::OB * 4 * 64 + lane] = f32x4{w.m, w.l, 0.0f, 0.0f};
-    }
-    at_wait_barrier<0>();
-    if (half == 1) return;
-    const f32x4 ml = box[W::OB * 4 * 64 + lane];
-    const float M = fmaxf(w.m, ml[0]), base = M == neg_inf() ? 0.0f : M;
-    const float e0 = __builtin_amdgcn_exp2f(w.m - base), e1 = __builtin_amdgcn_exp2f(ml[0] - base);
-    w.m = M;
-    w.l = w.l * e0 + ml[1] * e1;
-#pragma unroll
-    for (int x = 0; x < W::OB; ++x)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4 y = box[(4 * x + i) * 64 + lane];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w.o[x][4 * i + j] = w.o[x][4 * i + j] * e0 + y[j] * e1;
-      }
-  }
-  if (wrow + (lane & 31) >= it.rows) return;
+// The row of the cache that key `key` of an item sits in; e: its table entry.
+__device__ __forceinline__ int cache_row(const DecodeArgs& a, int e, int64_t key) {
+  return (int)(((int64_t)min(max(e, 0), a.num_pages - 1) << a.page_shift) +
+               (key & (((int64_t)1 << a.page_shift) - 1)));
+}
+
+// A wave's 32 rows finished: its part, or the result itself.
+template <class W, int DV>
+__device__ __forceinline__ void store_rows(const DecodeArgs& a, const DecodeItem& it, const W& w, int b, int hq, int h) {
   const int64_t at_row = (int64_t)b * a.q_heads + hq;
   if (a.part_o) {
     const int64_t at = (int64_t)it.part * a.num_requests * a.q_heads + at_row;
@@ -198,11 +99,201 @@ __device__ __forceinline__ void decode_item(const DecodeArgs& a, const DecodeIte
   }
 }
 
+// 128 rows, 32 per wave; tiles of 64 keys in two stages.
+template <int DQ, int DV>
+__device__ __forceinline__ void decode_wide(const DecodeArgs& a, const DecodeItem& it, uint8_t* mem) {
+  using W = AttnWave<DQ, DV, 2>;
+  constexpr int kKeys = 64;
+  uint8_t* ks = mem;
+  uint8_t* vs = mem + 2 * W::kKeyBytes;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+  const int G = a.q_heads / a.kv_heads;
+  const int64_t wrow = it.row0 + wv * 32;                           // this wave's first row
+  const bool active = wrow < it.rows;
+  const int64_t row = min(wrow + (lane & 31), it.rows - 1);
+  const int b = it.b0 + (int)(row / G), hq = it.kvh * G + (int)(row % G);
+  W w;
+  w.init(a.q + b * a.q_ts + hq * a.q_hs, lane);
+  // Lane l looks up the cache row of key l of a tile (past the end: the last
+  // key), one tile ahead of the loads that use it: the table entry of tile t + 2
+  // is read when the loads of tile t + 1 go out.
+  const int64_t n_keys = it.key1 - it.key0;
+  const int n_tiles = (int)((n_keys + kKeys - 1) / kKeys), n_whole = (int)(n_keys / kKeys);
+  auto key_of = [&](int t) { return min(it.key0 + (int64_t)t * kKeys + lane, it.key1 - 1); };
+  auto entry = [&](int t) { return it.table[key_of(t) >> a.page_shift]; };
+  const uint32_t k_lds = at_lds_addr(ks) + (uint32_t)wv * 1024u, v_lds = at_lds_addr(vs) + (uint32_t)wv * 1024u;
+  const uint8_t* kc = (const uint8_t*)(a.k_cache + (int64_t)it.kvh * DQ);
+  const uint8_t* vc = (const uint8_t*)(a.v_cache + (int64_t)it.kvh * DV);
+  const int64_t k_row = (int64_t)a.kv_heads * DQ * 2, v_row = (int64_t)a.kv_heads * DV * 2;
+  auto load = [&](int slot, int st) {
+#pragma unroll
+    for (int i = 0; i < W::kKeyBytes / 16 / kDecThreads; ++i) {
+      const int f = i * kDecThreads + threadIdx.x, r = f / (DQ / 8);
+      at_load_lds(k_lds + (uint32_t)(st * W::kKeyBytes + i * kDecThreads * 16),
+                  kc + (int64_t)__shfl(slot, r) * k_row + ((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < W::kValBytes / 16 / kDecThreads; ++i) {
+      const int f = i * kDecThreads + threadIdx.x, r = f / (DV / 8);
+      at_load_lds(v_lds + (uint32_t)(st * W::kValBytes + i * kDecThreads * 16),
+                  vc + (int64_t)__shfl(slot, r) * v_row + ((f % (DV / 8)) ^ at_swz<DV>(r)) * 16);
+    }
+  };
+  load(cache_row(a, entry(0), key_of(0)), 0);
+  int next = entry(1);
+  auto step = [&](auto stage, auto whole, int t) {
+    constexpr int st = decltype(stage)::value;
+    const uint8_t* k = ks + st * W::kKeyBytes;
+    const uint8_t* v = vs + st * W::kValBytes;
+    // tile t has landed; everyone is done with tile t - 1, whose stage the next loads refill
+    at_wait_barrier<0>();
+    if (t + 1 < n_tiles) {
+      load(cache_row(a, next, key_of(t + 1)), st ^ 1);
+      next = entry(t + 2);
+    }
+    if (!active) return;
+    if (decltype(whole)::value) w.tile(k, v, a.c);
+    else w.tile_masked(k, v, lane, a.c, (int)min(n_keys - 1 - (int64_t)t * kKeys, (int64_t)kKeys));
+  };
+  using S0 = std::integral_constant<int, 0>;
+  using S1 = std::integral_constant<int, 1>;
+  int t = 0;
+  for (; t + 1 < n_whole; t += 2) {
+    step(S0(), std::true_type(), t);
+    step(S1(), std::true_type(), t + 1);
+  }
+  for (; t < n_tiles; t += 2) {
+    step(S0(), std::false_type(), t);
+    if (t + 1 < n_tiles) step(S1(), std::false_type(), t + 1);
+  }
+  if (wrow + (lane & 31) < it.rows) store_rows<W, DV>(a, it, w, b, hq, h);
+}
+
+// 64 rows: waves 0, 1 the first 32, waves 2, 3 the others; even waves compute
+// the even tiles of 32 keys, odd waves the odd ones, and the two sums are joined
+// at the end.  The reads are what counts: NS stages, so that while one tile is
+// computed on NS - 1 are under way (at two workgroups per CU 96 KB: with 64 KB a
+// CU the reads of one 131072-key request ran at 5.6 TB/s).
+//
+// Loads in order of issue, per wave: D(t), the rows of tile t, L of them; E(t),
+// the table entries of tile t, one load, into a ring in LDS.  Step t waits for
+// D(t) and E(t + NS - 1), issues D(t + NS - 1) and E(t + 2 NS - 2): the waited-for
+// pair went out together in step t - NS + 1, so the NS - 2 pairs issued since may
+// be in flight.  Near the end fewer are.
+template <int DQ, int DV, int NS>
+__device__ __forceinline__ void decode_narrow(const DecodeArgs& a, const DecodeItem& it, uint8_t* mem) {
+  using W = AttnWave<DQ, DV, 1>;
+  constexpr int kKeys = 32, kRing = 2 * NS;                         // entries live 2 NS - 2 steps
+  constexpr int kKeyLoads = W::kKeyBytes / 16 / kDecThreads, kValLoads = W::kValBytes / 16 / kDecThreads;
+  constexpr int L = kKeyLoads + kValLoads + 1;
+  uint8_t* ks = mem;
+  uint8_t* vs = ks + NS * W::kKeyBytes;
+  const int* ring = (const int*)(vs + NS * W::kValBytes);
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+  const int rb = wv >> 1, odd = wv & 1;
+  const int G = a.q_heads / a.kv_heads;
+  const int64_t wrow = it.row0 + rb * 32;                           // this wave's first row
+  const bool active = wrow < it.rows;
+  const int64_t row = min(wrow + (lane & 31), it.rows - 1);
+  const int b = it.b0 + (int)(row / G), hq = it.kvh * G + (int)(row % G);
+  const int64_t n_keys = it.key1 - it.key0;
+  const int n_tiles = (int)((n_keys + kKeys - 1) / kKeys);
+  const uint32_t k_lds = at_lds_addr(ks) + (uint32_t)wv * 1024u, v_lds = at_lds_addr(vs) + (uint32_t)wv * 1024u;
+  const uint8_t* kc = (const uint8_t*)(a.k_cache + (int64_t)it.kvh * DQ);
+  const uint8_t* vc = (const uint8_t*)(a.v_cache + (int64_t)it.kvh * DV);
+  const int64_t k_row = (int64_t)a.kv_heads * DQ * 2, v_row = (int64_t)a.kv_heads * DV * 2;
+  auto key_of = [&](int t, int r) { return min(it.key0 + (int64_t)t * kKeys + r, it.key1 - 1); };   // past the end: the last
+  // (every wave fetches all entries itself: it then need not wait for another's)
+  auto fetch = [&](int t) {
+    at_load_lds4(at_lds_addr(ring) + (uint32_t)(t % kRing) * 256u, it.table + (key_of(t, lane & 31) >> a.page_shift));
+  };
+  auto load = [&](int t) {
+    const int st = t % NS;
+    const int* e = ring + (t % kRing) * 64;
+#pragma unroll
+    for (int i = 0; i < kKeyLoads; ++i) {
+      const int f = i * kDecThreads + threadIdx.x, r = f / (DQ / 8);
+      at_load_lds(k_lds + (uint32_t)(st * W::kKeyBytes + i * kDecThreads * 16),
+                  kc + cache_row(a, e[r], key_of(t, r)) * k_row + ((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < kValLoads; ++i) {
+      const int f = i * kDecThreads + threadIdx.x, r = f / (DV / 8);
+      at_load_lds(v_lds + (uint32_t)(st * W::kValBytes + i * kDecThreads * 16),
+                  vc + cache_row(a, e[r], key_of(t, r)) * v_row + ((f % (DV / 8)) ^ at_swz<DV>(r)) * 16);
+    }
+  };
+  W w;
+  if (n_tiles > 0)
+    for (int t = 0; t < NS - 1; ++t) fetch(t);
+  w.init(a.q + b * a.q_ts + hq * a.q_hs, lane);                     // (waits for the first entries too)
+  if (n_tiles > 0) {
+    at_wait<0>();
+    for (int t = 0; t < NS - 1; ++t) {
+      if (t < n_tiles) load(t);
+      fetch(t + NS - 1);
+    }
+  }
+  static_assert(NS == 3 || NS == 4, "the waits below");
+  auto arrive = [&](int t) {
+    // pairs issued after tile t's: NS - 2, at the end as many as tiles are left
+    const int after = min(n_tiles - 1 - t, NS - 2);
+    if (after == 0) at_wait_barrier<0>();
+    else if (after == 1) at_wait_barrier<L>();
+    else at_wait_barrier<2 * L>();
+    if (t + NS - 1 < n_tiles) {
+      load(t + NS - 1);
+      fetch(t + 2 * NS - 2);
+    }
+  };
+  const int n_whole = (int)(n_keys / kKeys);
+  for (int t = 0; t < n_whole; ++t) {
+    arrive(t);
+    if (active && (t & 1) == odd) w.tile(ks + (t % NS) * W::kKeyBytes, vs + (t % NS) * W::kValBytes, a.c);
+  }
+  if (n_tiles > n_whole) {                                          // the last one, cut
+    const int t = n_whole;
+    arrive(t);
+    if (active && (t & 1) == odd)
+      w.tile_masked(ks + (t % NS) * W::kKeyBytes, vs + (t % NS) * W::kValBytes, lane, a.c,
+                    (int)(n_keys - 1 - (int64_t)t * kKeys));
+  }
+  // The odd waves' sums reach the even ones through the tiles' memory (same rows
+  // and columns in the same lanes).
+  at_wait_barrier<0>();
+  f32x4* box = (f32x4*)(mem + rb * (W::OB * 4 + 1) * 1024);
+  if (odd) {
+#pragma unroll
+    for (int x = 0; x < W::OB; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        box[(4 * x + i) * 64 + lane] = f32x4{w.o[x][4 * i], w.o[x][4 * i + 1], w.o[x][4 * i + 2], w.o[x][4 * i + 3]};
+    box[W::OB * 4 * 64 + lane] = f32x4{w.m, w.l, 0.0f, 0.0f};
+  }
+  at_wait_barrier<0>();
+  if (odd) return;
+  const f32x4 ml = box[W::OB * 4 * 64 + lane];
+  const float M = fmaxf(w.m, ml[0]), base = M == neg_inf() ? 0.0f : M;
+  const float e0 = __builtin_amdgcn_exp2f(w.m - base), e1 = __builtin_amdgcn_exp2f(ml[0] - base);
+  w.m = M;
+  w.l = w.l * e0 + ml[1] * e1;
+#pragma unroll
+  for (int x = 0; x < W::OB; ++x)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 y = box[(4 * x + i) * 64 + lane];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w.o[x][4 * i + j] = w.o[x][4 * i + j] * e0 + y[j] * e1;
+    }
+  if (wrow + (lane & 31) < it.rows) store_rows<W, DV>(a, it, w, b, hq, h);
+}
+
 template <int DQ, int DV>
 __global__ __launch_bounds__(kDecThreads, 2) void attn_decode_kernel(DecodeArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t mem[2 * kDecKeys * (DQ + DV) * 2];
-  uint8_t* ks = mem;
-  uint8_t* vs = mem + 2 * kDecKeys * DQ * 2;
+  // stages of 32 keys and the ring of table entries; two workgroups fit a CU's 160 KB
+  constexpr int kTile = 32 * (DQ + DV) * 2, NS = 4 * kTile + 2048 <= 80 * 1024 ? 4 : 3;
+  constexpr int kNarrow = NS * kTile + 2 * NS * 256, kWide = 4 * kTile;
+  __shared__ __attribute__((aligned(16))) uint8_t mem[kNarrow > kWide ? kNarrow : kWide];
   const DecodePlan& p = a.plan;
   DecodeItem it;
   it.kvh = blockIdx.x % a.kv_heads;
@@ -218,7 +309,7 @@ __global__ __launch_bounds__(kDecThreads, 2) void attn_decode_kernel(DecodeArgs 
     it.table = a.prefix_table;
     it.key0 = (int64_t)it.part * p.chunk_p * kDecKeys;
     it.key1 = min(it.key0 + (int64_t)p.chunk_p * kDecKeys, a.prefix_len);
-    if (p.wide) return decode_item<DQ, DV, true>(a, it, ks, vs);
+    if (p.wide) return decode_wide<DQ, DV>(a, it, mem);
   } else {
     // first parts of all requests first: later ones may not exist
     int64_t is = i - ip;
@@ -238,17 +329,17 @@ __global__ __launch_bounds__(kDecThreads, 2) void attn_decode_kernel(DecodeArgs 
       it.key1 = it.key0;
     }
   }
-  decode_item<DQ, DV, false>(a, it, ks, vs);
+  decode_narrow<DQ, DV, NS>(a, it, mem);
 }
 
 // The parts of an output row joined: WPR waves per row take every WPR-th part.
 // Each wave first finds its parts' maximum (64 parts at a time, one per lane), so
 // the sums' loads follow without waiting for one another.
 template <int DV, int WPR>
-__global__ __launch_bounds__(kDecThreads) void attn_join_kernel(DecodeArgs a) {
-  constexpr int kRows = 4 / WPR;
-  __shared__ float2 red[4][64];
-  __shared__ float2 ml[4];
+__global__ __launch_bounds__(WPR <= 4 ? 256 : WPR * 64) void attn_join_kernel(DecodeArgs a) {
+  constexpr int kWaves = WPR <= 4 ? 4 : WPR, kRows = kWaves / WPR;
+  __shared__ float2 red[kWaves][64];
+  __shared__ float2 ml[kWaves];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = wv % WPR;
   const int64_t Hall = (int64_t)a.num_requests * a.q_heads;
   const int64_t at_row = (int64_t)blockIdx.x * kRows + wv / WPR;
@@ -276,16 +367,21 @@ __global__ __launch_bounds__(kDecThreads) void attn_join_kernel(DecodeArgs a) {
       M = M1;
 #pragma unroll
       for (int j = 0; j < E; ++j) o[j] *= e0;
-#pragma unroll 4
-      for (int p = 0; p < cnt; ++p) {
-        const float ep = __shfl(e, p);
-        const float* src = a.part_o + ((int64_t)(sub + (base + p) * WPR) * Hall + at_row) * DV + lane * E;
-        if (E == 2) {
-          const float2 y = *(const float2*)src;
-          o[0] = fmaf(ep, y.x, o[0]);
-          o[1] = fmaf(ep, y.y, o[1]);
-        } else {
-          o[0] = fmaf(ep, src[0], o[0]);
+      for (int p = 0; p < cnt; p += 8) {                            // 8 loads in flight
+        float y[8][2];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int q = min(p + u, cnt - 1);
+          const float* src = a.part_o + ((int64_t)(sub + (base + q) * WPR) * Hall + at_row) * DV + lane * E;
+          y[u][0] = src[0];
+          if (E == 2) y[u][1] = src[1];
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (p + u >= cnt) break;
+          const float ep = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e), p + u));
+          o[0] = fmaf(ep, y[u][0], o[0]);
+          if (E == 2) o[1] = fmaf(ep, y[u][1], o[1]);
         }
       }
     }
@@ -364,11 +460,11 @@ static void launch_decode(const DecodeArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((attn_decode_kernel<DQ, DV>), dim3(grid), dim3(kDecThreads), 0, stream, a);
   if (!a.part_o) return;
   const uint32_t rows = (uint32_t)(a.num_requests * a.q_heads);
-  // a wave per row while there are few parts; four, when a row has many
-  if (a.plan.parts_p + a.plan.parts_s <= 16)
-    hipLaunchKernelGGL((attn_join_kernel<DV, 1>), dim3((rows + 3) / 4), dim3(kDecThreads), 0, stream, a);
-  else
-    hipLaunchKernelGGL((attn_join_kernel<DV, 4>), dim3(rows), dim3(kDecThreads), 0, stream, a);
+  // waves per row: as many as leave each 8 parts or so, one round of loads
+  const int parts = a.plan.parts_p + a.plan.parts_s;
+  if (parts <= 16) hipLaunchKernelGGL((attn_join_kernel<DV, 1>), dim3((rows + 3) / 4), dim3(256), 0, stream, a);
+  else if (parts <= 48) hipLaunchKernelGGL((attn_join_kernel<DV, 4>), dim3(rows), dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((attn_join_kernel<DV, 16>), dim3(rows), dim3(1024), 0, stream, a);
 }
 
 moe_status launch_attn_decode(const moe_heads& q, const moe_kv_cache& cache, const int32_t* table,
