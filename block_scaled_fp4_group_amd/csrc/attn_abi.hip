@@ -198,6 +198,8 @@ moe_status moe_attn_decode(const moe_heads* q, const moe_kv_cache* cache, const 
   MOE_CHECK(prefix_len <= (int64_t)prefix_blocks * cache->page_size, "%s: prefix_len %lld needs more than %d pages", fn,
             (long long)prefix_len, prefix_blocks);
   MOE_CHECK(prefix_len == 0 || prefix_table, "%s: prefix_table is NULL", fn);
+  MOE_CHECK(max_len <= 0x7fffffff - 64 && prefix_len <= 0x7fffffff - 64 && num_requests * ((max_len + 31) / 32) < 0x7fffffff,
+            "%s: too many keys", fn);
   MOE_CHECK(aligned4(lse), "%s: lse not 4-byte aligned", fn);
   MOE_CHECK(attn_decode_grid(num_requests, p->q_heads, p->kv_heads, prefix_len, max_len) < ((int64_t)1 << 31) &&
                 (int64_t)num_requests * p->q_heads < ((int64_t)1 << 31),

@@ -9,7 +9,6 @@
 // a request only its G rows.  Each part leaves its unnormalised sum, maximum and
 // weight sum in float; a second kernel joins the parts of a row:
 //   M = max m_i,  out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
-// With a single part the first kernel writes the result itself.
 //
 // Workgroups of four waves walk the keys in tiles through LDS stages that all
 // waves fill (direct loads; every lane finds its rows through the block table)
@@ -18,8 +17,11 @@
 //          per 128 rows.  Bound by the matrix cores.
 //   narrow (own keys, and a prefix with few rows): 64 rows, two waves per 32.
 //          Bound by reading the cache.
-// Both kinds run in one launch, their workgroups interleaved, so that the one's
-// matrix work and the other's reads share the chip.
+// The own keys of all requests are one list of tiles, which the narrow workgroups
+// of a key head share out evenly, whatever the lengths: each takes one run of the
+// list, across as many requests as it covers, without emptying its load pipeline
+// at more than the requests' ends.  All workgroups of a launch fit the chip at
+// once, so the wide ones' matrix work and the narrow ones' reads run side by side.
 #include <algorithm>
 
 #include "attn_common.h"
@@ -27,13 +29,15 @@
 namespace moe {
 
 constexpr int kDecThreads = 256;
-constexpr int kDecKeys = 64;
+constexpr int kDecSlots = 512;                      // two workgroups on each of 256 CUs
+constexpr int kWideKeys = 64, kNarrowKeys = 32;     // per tile
 
 struct DecodePlan {
   int32_t wide;                                     // prefix workgroups are wide
-  int32_t chunk_p, chunk_s;                         // tiles per part
-  int32_t parts_p, parts_s;                         // parts of the prefix, of a request's own keys
-  int32_t blocks_p, blocks_s;                       // row blocks of B * G rows, of G rows
+  int32_t parts_p, chunk_p;                         // parts of the prefix, keys in each
+  int32_t blocks_p;                                 // row blocks of B * G rows (128 or 64)
+  int32_t blocks_s, rows_s;                         // row blocks of G rows (64), rows in each
+  int32_t runs;                                     // narrow workgroups per key head and row block
 };
 
 struct DecodeArgs {
@@ -48,288 +52,311 @@ struct DecodeArgs {
   int64_t prefix_len, max_len;
   uint16_t* out;
   float* lse;
-  float* part_o;                                    // [parts][B * Hq][DV]
-  float2* part_ml;                                  // [parts][B * Hq]: maximum (base 2), weight sum
+  // Workspace.  Prefix: part x (two per narrow workgroup, one for each of its wave
+  // pairs) of row b * Hq + h is entry x * B * Hq + row.  Own keys: run w's share of
+  // request b -- (w + b, as the runs and the requests are walked in one order, is
+  // each pair's own) -- entry own + (((head * blocks + block) * (runs + B) + w + b)
+  // * 2 + pair) * rows_s + row.
+  float* part_o;                                    // [entries][DV]
+  float2* part_ml;                                  // [entries]: maximum (base 2), weight sum
+  int32_t* first;                                   // [B + 1]: tiles of the requests before
+  int64_t own;
   int32_t num_requests, q_heads, kv_heads, num_pages, page_shift;
   float c;
   DecodePlan plan;
 };
 
-__device__ __forceinline__ int64_t own_len(const DecodeArgs& a, int b) {
-  return min(max((int64_t)a.lens[b], (int64_t)0), a.max_len);
+__device__ __forceinline__ int clamp_len(const DecodeArgs& a, int len) { return (int)min((int64_t)max(len, 0), a.max_len); }
+__device__ __forceinline__ int len_at(const DecodeArgs& a, int b) {   // b uniform: a scalar load
+  return clamp_len(a, *(const __attribute__((address_space(4))) int32_t*)(a.lens + b));
+}
+__device__ __forceinline__ int tiles_of(int keys) { return (keys + kNarrowKeys - 1) / kNarrowKeys; }
+
+// The row of the cache that key `key` sits in; e: its table entry.
+__device__ __forceinline__ int cache_row(const DecodeArgs& a, int e, int key) {
+  return (min(max(e, 0), a.num_pages - 1) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
 }
 
-// One workgroup's share: rows row0 .. of `rows` (row r is request b0 + r / G, its
-// head r % G of key head kvh) against keys key0 .. key1 - 1 of `table`.
-struct DecodeItem {
-  const int32_t* table;
-  int64_t key0, key1, row0, rows;
-  int b0, kvh, part;
-};
-
-// The row of the cache that key `key` of an item sits in; e: its table entry.
-__device__ __forceinline__ int cache_row(const DecodeArgs& a, int e, int64_t key) {
-  return (int)(((int64_t)min(max(e, 0), a.num_pages - 1) << a.page_shift) +
-               (key & (((int64_t)1 << a.page_shift) - 1)));
-}
-
-// A wave's 32 rows finished: its part, or the result itself.
+// This lane's row of a finished part.
 template <class W, int DV>
-__device__ __forceinline__ void store_rows(const DecodeArgs& a, const DecodeItem& it, const W& w, int b, int hq, int h) {
-  const int64_t at_row = (int64_t)b * a.q_heads + hq;
-  if (a.part_o) {
-    const int64_t at = (int64_t)it.part * a.num_requests * a.q_heads + at_row;
-    float* po = a.part_o + at * DV + 4 * h;
+__device__ __forceinline__ void store_part(const DecodeArgs& a, const W& w, int64_t entry, int h) {
+  float* po = a.part_o + entry * DV + 4 * h;
 #pragma unroll
-    for (int x = 0; x < W::OB; ++x)
+  for (int x = 0; x < W::OB; ++x)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *(f32x4*)(po + 32 * x + 8 * i) = f32x4{w.o[x][4 * i], w.o[x][4 * i + 1], w.o[x][4 * i + 2], w.o[x][4 * i + 3]};
-    if (h == 0) a.part_ml[at] = float2{w.m, w.l};
-  } else {
-    const float inv = w.l == 0.0f ? 0.0f : 1.0f / w.l;
-    uint16_t* op = a.out + b * a.o_ts + hq * a.o_hs + 4 * h;
-#pragma unroll
-    for (int x = 0; x < W::OB; ++x)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *(u32x2*)(op + 32 * x + 8 * i) = u32x2{cvt_bf16x2(w.o[x][4 * i] * inv, w.o[x][4 * i + 1] * inv),
-                                               cvt_bf16x2(w.o[x][4 * i + 2] * inv, w.o[x][4 * i + 3] * inv)};
-    if (a.lse && h == 0) a.lse[at_row] = w.l == 0.0f ? neg_inf() : (w.m + __builtin_amdgcn_logf(w.l)) * kLn2;
-  }
+    for (int i = 0; i < 4; ++i)
+      *(f32x4*)(po + 32 * x + 8 * i) = f32x4{w.o[x][4 * i], w.o[x][4 * i + 1], w.o[x][4 * i + 2], w.o[x][4 * i + 3]};
+  if (h == 0) a.part_ml[entry] = float2{w.m, w.l};
 }
 
-// 128 rows, 32 per wave; tiles of 64 keys in two stages.
+// Values of keys past the end (they repeat the last) become zeros in their stage:
+// their weights are 0, and 0 times an infinity would not be.
+template <int DV, int ROWS>
+__device__ __forceinline__ void clear_values(uint8_t* vs, int valid) {
+#pragma unroll
+  for (int i = 0; i < ROWS * DV * 2 / 16 / kDecThreads; ++i) {
+    const int f = i * kDecThreads + threadIdx.x;
+    if (f / (DV / 8) >= valid) *(u32x4*)(vs + f * 16) = u32x4{0u, 0u, 0u, 0u};
+  }
+  at_wait_barrier<63>();                                            // (no load is waited for)
+}
+
+// Prefix part `part`, 128 rows from row0, 32 per wave; tiles of 64 keys in two stages.
 template <int DQ, int DV>
-__device__ __forceinline__ void decode_wide(const DecodeArgs& a, const DecodeItem& it, uint8_t* mem) {
-  using W = AttnWave<DQ, DV, 2>;
-  constexpr int kKeys = 64;
+__device__ __forceinline__ void decode_wide(const DecodeArgs& a, int kvh, int part, int row0, uint8_t* mem) {
+  using W = AttnWave<DQ, DV, kWideKeys / 32>;
   uint8_t* ks = mem;
   uint8_t* vs = mem + 2 * W::kKeyBytes;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
-  const int G = a.q_heads / a.kv_heads;
-  const int64_t wrow = it.row0 + wv * 32;                           // this wave's first row
-  const bool active = wrow < it.rows;
-  const int64_t row = min(wrow + (lane & 31), it.rows - 1);
-  const int b = it.b0 + (int)(row / G), hq = it.kvh * G + (int)(row % G);
+  const int G = a.q_heads / a.kv_heads, rows = a.num_requests * G;
+  const int wrow = row0 + wv * 32;                                  // this wave's first row
+  const int row = min(wrow + (lane & 31), rows - 1);
+  const int b = row / G, hq = kvh * G + row % G;
   W w;
   w.init(a.q + b * a.q_ts + hq * a.q_hs, lane);
   // Lane l looks up the cache row of key l of a tile (past the end: the last
   // key), one tile ahead of the loads that use it: the table entry of tile t + 2
   // is read when the loads of tile t + 1 go out.
-  const int64_t n_keys = it.key1 - it.key0;
-  const int n_tiles = (int)((n_keys + kKeys - 1) / kKeys), n_whole = (int)(n_keys / kKeys);
-  auto key_of = [&](int t) { return min(it.key0 + (int64_t)t * kKeys + lane, it.key1 - 1); };
-  auto entry = [&](int t) { return it.table[key_of(t) >> a.page_shift]; };
+  const int key0 = part * a.plan.chunk_p, n_keys = (int)min((int64_t)a.plan.chunk_p, a.prefix_len - key0);
+  const int n_tiles = (n_keys + kWideKeys - 1) / kWideKeys, n_whole = n_keys / kWideKeys;
+  auto key_of = [&](int t) { return key0 + min(t * kWideKeys + lane, n_keys - 1); };
+  auto entry = [&](int t) { return a.prefix_table[key_of(t) >> a.page_shift]; };
   const uint32_t k_lds = at_lds_addr(ks) + (uint32_t)wv * 1024u, v_lds = at_lds_addr(vs) + (uint32_t)wv * 1024u;
-  const uint8_t* kc = (const uint8_t*)(a.k_cache + (int64_t)it.kvh * DQ);
-  const uint8_t* vc = (const uint8_t*)(a.v_cache + (int64_t)it.kvh * DV);
-  const int64_t k_row = (int64_t)a.kv_heads * DQ * 2, v_row = (int64_t)a.kv_heads * DV * 2;
+  const uint8_t* kc = (const uint8_t*)(a.k_cache + (int64_t)kvh * DQ);
+  const uint8_t* vc = (const uint8_t*)(a.v_cache + (int64_t)kvh * DV);
+  const uint32_t k_row = (uint32_t)a.kv_heads * DQ * 2, v_row = (uint32_t)a.kv_heads * DV * 2;
   auto load = [&](int slot, int st) {
 #pragma unroll
     for (int i = 0; i < W::kKeyBytes / 16 / kDecThreads; ++i) {
       const int f = i * kDecThreads + threadIdx.x, r = f / (DQ / 8);
       at_load_lds(k_lds + (uint32_t)(st * W::kKeyBytes + i * kDecThreads * 16),
-                  kc + (int64_t)__shfl(slot, r) * k_row + ((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16);
+                  kc + (uint64_t)(uint32_t)__shfl(slot, r) * k_row + ((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16);
     }
 #pragma unroll
     for (int i = 0; i < W::kValBytes / 16 / kDecThreads; ++i) {
       const int f = i * kDecThreads + threadIdx.x, r = f / (DV / 8);
       at_load_lds(v_lds + (uint32_t)(st * W::kValBytes + i * kDecThreads * 16),
-                  vc + (int64_t)__shfl(slot, r) * v_row + ((f % (DV / 8)) ^ at_swz<DV>(r)) * 16);
+                  vc + (uint64_t)(uint32_t)__shfl(slot, r) * v_row + ((f % (DV / 8)) ^ at_swz<DV>(r)) * 16);
     }
   };
   load(cache_row(a, entry(0), key_of(0)), 0);
   int next = entry(1);
-  auto step = [&](auto stage, auto whole, int t) {
+  auto step = [&](auto stage, int t) {
     constexpr int st = decltype(stage)::value;
-    const uint8_t* k = ks + st * W::kKeyBytes;
-    const uint8_t* v = vs + st * W::kValBytes;
     // tile t has landed; everyone is done with tile t - 1, whose stage the next loads refill
     at_wait_barrier<0>();
     if (t + 1 < n_tiles) {
       load(cache_row(a, next, key_of(t + 1)), st ^ 1);
       next = entry(t + 2);
     }
-    if (!active) return;
-    if (decltype(whole)::value) w.tile(k, v, a.c);
-    else w.tile_masked(k, v, lane, a.c, (int)min(n_keys - 1 - (int64_t)t * kKeys, (int64_t)kKeys));
+    const bool cut = t >= n_whole;
+    if (cut) clear_values<DV, kWideKeys>(vs + st * W::kValBytes, n_keys - t * kWideKeys);
+    if (wrow >= rows) return;
+    w.scores(ks + st * W::kKeyBytes);
+    if (cut) w.mask(lane, n_keys - 1 - t * kWideKeys);
+    w.weights(a.c);
+    w.values(vs + st * W::kValBytes);
   };
-  using S0 = std::integral_constant<int, 0>;
-  using S1 = std::integral_constant<int, 1>;
-  int t = 0;
-  for (; t + 1 < n_whole; t += 2) {
-    step(S0(), std::true_type(), t);
-    step(S1(), std::true_type(), t + 1);
+  for (int t = 0; t < n_tiles; t += 2) {
+    step(std::integral_constant<int, 0>(), t);
+    if (t + 1 < n_tiles) step(std::integral_constant<int, 1>(), t + 1);
   }
-  for (; t < n_tiles; t += 2) {
-    step(S0(), std::false_type(), t);
-    if (t + 1 < n_tiles) step(S1(), std::false_type(), t + 1);
-  }
-  if (wrow + (lane & 31) < it.rows) store_rows<W, DV>(a, it, w, b, hq, h);
+  if (wrow + (lane & 31) < rows)
+    store_part<W, DV>(a, w, (int64_t)part * a.num_requests * a.q_heads + (int64_t)b * a.q_heads + hq, h);
 }
 
-// 64 rows: waves 0, 1 the first 32, waves 2, 3 the others; even waves compute
-// the even tiles of 32 keys, odd waves the odd ones, and the two sums are joined
-// at the end.  The reads are what counts: NS stages, so that while one tile is
-// computed on NS - 1 are under way (at two workgroups per CU 96 KB: with 64 KB a
-// CU the reads of one 131072-key request ran at 5.6 TB/s).
+// Where a narrow workgroup is in its run of tiles: tile `tile` of request b, which
+// has len keys from key0 on.  PREFIX: one request, the prefix's part.
+template <bool PREFIX>
+struct Cursor {
+  int b, tile, tiles, len, key0;
+  const int32_t* table;
+  __device__ __forceinline__ void next(const DecodeArgs& a) {
+    if (++tile < tiles || PREFIX) return;
+    do {
+      ++b;
+      len = len_at(a, b);
+    } while (len == 0);
+    tiles = tiles_of(len);
+    tile = 0;
+    table = a.table + b * a.table_stride;
+  }
+  __device__ __forceinline__ int key(int r) const { return key0 + min(tile * kNarrowKeys + r, len - 1); }   // past the end: the last
+};
+
+// n_tiles tiles from `at` on for 64 rows: waves 0, 1 the first 32, waves 2, 3 the
+// others; even waves compute every other tile, odd waves those between, and the
+// two leave parts of their own.  The reads are what counts: NS stages, so that
+// while one tile is computed on NS - 1 are under way.
 //
-// Loads in order of issue, per wave: D(t), the rows of tile t, L of them; E(t),
-// the table entries of tile t, one load, into a ring in LDS.  Step t waits for
-// D(t) and E(t + NS - 1), issues D(t + NS - 1) and E(t + 2 NS - 2): the waited-for
-// pair went out together in step t - NS + 1, so the NS - 2 pairs issued since may
-// be in flight.  Near the end fewer are.
-template <int DQ, int DV, int NS>
-__device__ __forceinline__ void decode_narrow(const DecodeArgs& a, const DecodeItem& it, uint8_t* mem) {
+// Loads in order of issue, per wave: D(t), the rows of tile t, and E(t), the table
+// entries of tile t, one load, into a ring in LDS; L loads in a pair.  Step t waits
+// for D(t) and E(t + NS - 1), issues D(t + NS - 1) and E(t + 2 NS - 2): the
+// waited-for pair went out together in step t - NS + 1, so the NS - 2 pairs issued
+// since may be in flight.  Near the end fewer are.
+template <int DQ, int DV, int NS, bool PREFIX>
+__device__ __forceinline__ void decode_narrow(const DecodeArgs& a, int kvh, Cursor<PREFIX> at, int n_tiles, int row0, int rows,
+                                              int64_t entry0, uint8_t* mem) {
   using W = AttnWave<DQ, DV, 1>;
-  constexpr int kKeys = 32, kRing = 2 * NS;                         // entries live 2 NS - 2 steps
+  constexpr int kRing = 2 * NS;                                     // entries live 2 NS - 2 steps
   constexpr int kKeyLoads = W::kKeyBytes / 16 / kDecThreads, kValLoads = W::kValBytes / 16 / kDecThreads;
   constexpr int L = kKeyLoads + kValLoads + 1;
+  static_assert(NS == 3 || NS == 4, "the waits below");
   uint8_t* ks = mem;
   uint8_t* vs = ks + NS * W::kKeyBytes;
   const int* ring = (const int*)(vs + NS * W::kValBytes);
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
-  const int rb = wv >> 1, odd = wv & 1;
-  const int G = a.q_heads / a.kv_heads;
-  const int64_t wrow = it.row0 + rb * 32;                           // this wave's first row
-  const bool active = wrow < it.rows;
-  const int64_t row = min(wrow + (lane & 31), it.rows - 1);
-  const int b = it.b0 + (int)(row / G), hq = it.kvh * G + (int)(row % G);
-  const int64_t n_keys = it.key1 - it.key0;
-  const int n_tiles = (int)((n_keys + kKeys - 1) / kKeys);
+  const int odd = wv & 1, G = a.q_heads / a.kv_heads;
+  const int wrow = row0 + (wv >> 1) * 32;                           // this wave's first row
+  const int row = min(wrow + (lane & 31), rows - 1);
   const uint32_t k_lds = at_lds_addr(ks) + (uint32_t)wv * 1024u, v_lds = at_lds_addr(vs) + (uint32_t)wv * 1024u;
-  const uint8_t* kc = (const uint8_t*)(a.k_cache + (int64_t)it.kvh * DQ);
-  const uint8_t* vc = (const uint8_t*)(a.v_cache + (int64_t)it.kvh * DV);
-  const int64_t k_row = (int64_t)a.kv_heads * DQ * 2, v_row = (int64_t)a.kv_heads * DV * 2;
-  auto key_of = [&](int t, int r) { return min(it.key0 + (int64_t)t * kKeys + r, it.key1 - 1); };   // past the end: the last
-  // (every wave fetches all entries itself: it then need not wait for another's)
-  auto fetch = [&](int t) {
-    at_load_lds4(at_lds_addr(ring) + (uint32_t)(t % kRing) * 256u, it.table + (key_of(t, lane & 31) >> a.page_shift));
+  const uint8_t* kc = (const uint8_t*)(a.k_cache + (int64_t)kvh * DQ);
+  const uint8_t* vc = (const uint8_t*)(a.v_cache + (int64_t)kvh * DV);
+  const uint32_t k_row = (uint32_t)a.kv_heads * DQ * 2, v_row = (uint32_t)a.kv_heads * DV * 2;
+  Cursor<PREFIX> ahead = at, behind = at;                           // of the entries; of the computation (`at`: of the rows)
+  int fetched = 0, loaded = 0;                                      // tiles, also their places in ring and stages
+  // (every wave fetches all entries itself: it then need not wait for another's;
+  // past the run's end it fetches the last again, unread)
+  auto fetch = [&]() {
+    at_load_lds4(at_lds_addr(ring) + (uint32_t)(fetched % kRing) * 256u, ahead.table + (ahead.key(lane & 31) >> a.page_shift));
+    if (++fetched < n_tiles) ahead.next(a);
   };
-  auto load = [&](int t) {
-    const int st = t % NS;
-    const int* e = ring + (t % kRing) * 64;
+  auto load = [&]() {
+    const int st = loaded % NS;
+    const int* e = ring + (loaded % kRing) * 64;
 #pragma unroll
     for (int i = 0; i < kKeyLoads; ++i) {
       const int f = i * kDecThreads + threadIdx.x, r = f / (DQ / 8);
       at_load_lds(k_lds + (uint32_t)(st * W::kKeyBytes + i * kDecThreads * 16),
-                  kc + cache_row(a, e[r], key_of(t, r)) * k_row + ((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16);
+                  kc + (uint64_t)(uint32_t)cache_row(a, e[r], at.key(r)) * k_row + ((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16);
     }
 #pragma unroll
     for (int i = 0; i < kValLoads; ++i) {
       const int f = i * kDecThreads + threadIdx.x, r = f / (DV / 8);
       at_load_lds(v_lds + (uint32_t)(st * W::kValBytes + i * kDecThreads * 16),
-                  vc + cache_row(a, e[r], key_of(t, r)) * v_row + ((f % (DV / 8)) ^ at_swz<DV>(r)) * 16);
+                  vc + (uint64_t)(uint32_t)cache_row(a, e[r], at.key(r)) * v_row + ((f % (DV / 8)) ^ at_swz<DV>(r)) * 16);
     }
+    if (++loaded < n_tiles) at.next(a);
   };
   W w;
-  if (n_tiles > 0)
-    for (int t = 0; t < NS - 1; ++t) fetch(t);
-  w.init(a.q + b * a.q_ts + hq * a.q_hs, lane);                     // (waits for the first entries too)
-  if (n_tiles > 0) {
-    at_wait<0>();
-    for (int t = 0; t < NS - 1; ++t) {
-      if (t < n_tiles) load(t);
-      fetch(t + NS - 1);
-    }
+  auto begin = [&]() {                                              // the rows of the computation's request
+    const int b = PREFIX ? row / G : behind.b, hq = kvh * G + (PREFIX ? row % G : row);
+    w.init(a.q + b * a.q_ts + hq * a.q_hs, lane);
+    at_wait<0>();                                                   // nothing of before is counted below
+  };
+  for (int t = 0; t < NS - 1; ++t) fetch();
+  begin();
+  for (int t = 0; t < NS - 1; ++t) {
+    if (t < n_tiles) load();
+    fetch();
   }
-  static_assert(NS == 3 || NS == 4, "the waits below");
-  auto arrive = [&](int t) {
+  for (int t = 0; t < n_tiles; ++t) {
     // pairs issued after tile t's: NS - 2, at the end as many as tiles are left
     const int after = min(n_tiles - 1 - t, NS - 2);
     if (after == 0) at_wait_barrier<0>();
     else if (after == 1) at_wait_barrier<L>();
     else at_wait_barrier<2 * L>();
     if (t + NS - 1 < n_tiles) {
-      load(t + NS - 1);
-      fetch(t + 2 * NS - 2);
+      load();
+      fetch();
     }
-  };
-  const int n_whole = (int)(n_keys / kKeys);
-  for (int t = 0; t < n_whole; ++t) {
-    arrive(t);
-    if (active && (t & 1) == odd) w.tile(ks + (t % NS) * W::kKeyBytes, vs + (t % NS) * W::kValBytes, a.c);
-  }
-  if (n_tiles > n_whole) {                                          // the last one, cut
-    const int t = n_whole;
-    arrive(t);
-    if (active && (t & 1) == odd)
-      w.tile_masked(ks + (t % NS) * W::kKeyBytes, vs + (t % NS) * W::kValBytes, lane, a.c,
-                    (int)(n_keys - 1 - (int64_t)t * kKeys));
-  }
-  // The odd waves' sums reach the even ones through the tiles' memory (same rows
-  // and columns in the same lanes).
-  at_wait_barrier<0>();
-  f32x4* box = (f32x4*)(mem + rb * (W::OB * 4 + 1) * 1024);
-  if (odd) {
-#pragma unroll
-    for (int x = 0; x < W::OB; ++x)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        box[(4 * x + i) * 64 + lane] = f32x4{w.o[x][4 * i], w.o[x][4 * i + 1], w.o[x][4 * i + 2], w.o[x][4 * i + 3]};
-    box[W::OB * 4 * 64 + lane] = f32x4{w.m, w.l, 0.0f, 0.0f};
-  }
-  at_wait_barrier<0>();
-  if (odd) return;
-  const f32x4 ml = box[W::OB * 4 * 64 + lane];
-  const float M = fmaxf(w.m, ml[0]), base = M == neg_inf() ? 0.0f : M;
-  const float e0 = __builtin_amdgcn_exp2f(w.m - base), e1 = __builtin_amdgcn_exp2f(ml[0] - base);
-  w.m = M;
-  w.l = w.l * e0 + ml[1] * e1;
-#pragma unroll
-  for (int x = 0; x < W::OB; ++x)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f32x4 y = box[(4 * x + i) * 64 + lane];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w.o[x][4 * i + j] = w.o[x][4 * i + j] * e0 + y[j] * e1;
+    const int last = behind.len - 1 - behind.tile * kNarrowKeys;
+    const uint8_t* k = ks + (t % NS) * W::kKeyBytes;
+    uint8_t* v = vs + (t % NS) * W::kValBytes;
+    if (last < kNarrowKeys - 1) clear_values<DV, kNarrowKeys>(v, last + 1);
+    if (wrow < rows && (t & 1) == odd) {
+      w.scores(k);
+      if (last < kNarrowKeys - 1) w.mask(lane, last);
+      w.weights(a.c);
+      w.values(v);
     }
-  if (wrow + (lane & 31) < it.rows) store_rows<W, DV>(a, it, w, b, hq, h);
+    const bool end = t + 1 == n_tiles;
+    if (end || behind.tile + 1 == behind.tiles) {
+      if (wrow + (lane & 31) < rows) {
+        const int64_t entry = PREFIX ? entry0 + (int64_t)odd * a.num_requests * a.q_heads + (int64_t)(row / G) * a.q_heads + kvh * G + row % G
+                                     : entry0 + ((int64_t)behind.b * 2 + odd) * a.plan.rows_s + row - row0;
+        store_part<W, DV>(a, w, entry, h);
+      }
+      if (end) break;
+      behind.next(a);
+      begin();
+    } else {
+      behind.next(a);
+    }
+  }
 }
 
 template <int DQ, int DV>
 __global__ __launch_bounds__(kDecThreads, 2) void attn_decode_kernel(DecodeArgs a) {
-  // stages of 32 keys and the ring of table entries; two workgroups fit a CU's 160 KB
-  constexpr int kTile = 32 * (DQ + DV) * 2, NS = 4 * kTile + 2048 <= 80 * 1024 ? 4 : 3;
-  constexpr int kNarrow = NS * kTile + 2 * NS * 256, kWide = 4 * kTile;
+  // narrow: stages of 32 keys and the ring of table entries; two workgroups fit a CU's 160 KB
+  constexpr int kTile = kNarrowKeys * (DQ + DV) * 2, NS = 4 * kTile + 2048 <= 80 * 1024 ? 4 : 3;
+  constexpr int kNarrow = NS * kTile + 2 * NS * 256, kWide = 2 * kWideKeys * (DQ + DV) * 2;
   __shared__ __attribute__((aligned(16))) uint8_t mem[kNarrow > kWide ? kNarrow : kWide];
   const DecodePlan& p = a.plan;
-  DecodeItem it;
-  it.kvh = blockIdx.x % a.kv_heads;
-  const int64_t i = blockIdx.x / (uint32_t)a.kv_heads;
-  const int64_t np = (int64_t)p.parts_p * p.blocks_p, n = np + (int64_t)a.num_requests * p.blocks_s * p.parts_s;
-  const int64_t ip = i * np / n;                                    // prefix items spread evenly over the launch
-  if ((i + 1) * np / n != ip) {
+  const int kvh = blockIdx.x % a.kv_heads, lane = threadIdx.x & 63;
+  int item = blockIdx.x / (uint32_t)a.kv_heads;
+  if (item < p.parts_p * p.blocks_p) {
     // row blocks of one part side by side: they share the part's keys in L2
-    it.part = (int)(ip / p.blocks_p);
-    it.row0 = (ip % p.blocks_p) * (p.wide ? 128 : 64);
-    it.rows = (int64_t)a.num_requests * (a.q_heads / a.kv_heads);
-    it.b0 = 0;
-    it.table = a.prefix_table;
-    it.key0 = (int64_t)it.part * p.chunk_p * kDecKeys;
-    it.key1 = min(it.key0 + (int64_t)p.chunk_p * kDecKeys, a.prefix_len);
-    if (p.wide) return decode_wide<DQ, DV>(a, it, mem);
-  } else {
-    // first parts of all requests first: later ones may not exist
-    int64_t is = i - ip;
-    const int s = (int)(is / ((int64_t)a.num_requests * p.blocks_s));
-    is %= (int64_t)a.num_requests * p.blocks_s;
-    it.row0 = (is % p.blocks_s) * 64;
-    it.b0 = (int)(is / p.blocks_s);
-    it.rows = a.q_heads / a.kv_heads;
-    it.part = p.parts_p + s;
-    it.table = a.table + it.b0 * a.table_stride;
-    it.key0 = (int64_t)s * p.chunk_s * kDecKeys;
-    it.key1 = min(it.key0 + (int64_t)p.chunk_s * kDecKeys, own_len(a, it.b0));
-    // nothing here: the joining kernel skips the part (a single part of a request
-    // without keys still writes its empty row)
-    if (it.key1 <= it.key0) {
-      if (a.part_o) return;
-      it.key1 = it.key0;
-    }
+    const int part = item / p.blocks_p, block = item % p.blocks_p;
+    if (p.wide) return decode_wide<DQ, DV>(a, kvh, part, block * 128, mem);
+    Cursor<true> at;
+    at.b = at.tile = 0;
+    at.key0 = part * p.chunk_p;
+    at.len = (int)min((int64_t)p.chunk_p, a.prefix_len - at.key0);
+    at.tiles = tiles_of(at.len);
+    at.table = a.prefix_table;
+    return decode_narrow<DQ, DV, NS, true>(a, kvh, at, at.tiles, block * 64, a.num_requests * (a.q_heads / a.kv_heads),
+                                           (int64_t)part * 2 * a.num_requests * a.q_heads, mem);
   }
-  decode_narrow<DQ, DV, NS>(a, it, mem);
+  item -= p.parts_p * p.blocks_p;
+  const int run = item / p.blocks_s, block = item % p.blocks_s;
+  // tiles of all requests; the first workgroup writes down where each request's begin
+  const int B = a.num_requests;
+  int total = 0;
+  for (int b0 = 0; b0 < B; b0 += 64) {
+    const int n = b0 + lane < B ? tiles_of(clamp_len(a, a.lens[b0 + lane])) : 0;
+    int sum = n;                                                    // inclusive over the lanes
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(sum, d);
+      if (lane >= d) sum += up;
+    }
+    if (blockIdx.x == (uint32_t)(p.parts_p * p.blocks_p * a.kv_heads) && threadIdx.x < 64 && b0 + lane < B)
+      a.first[b0 + lane] = total + sum - n;
+    total += __builtin_amdgcn_readlane(sum, 63);
+  }
+  if (blockIdx.x == (uint32_t)(p.parts_p * p.blocks_p * a.kv_heads) && threadIdx.x == 0) a.first[B] = total;
+  const int each = (total + p.runs - 1) / p.runs, begin = run * each, end = min(begin + each, total);
+  if (begin >= end) return;
+  // the request that tile `begin` belongs to: the last whose tiles begin at or before it
+  Cursor<false> at;
+  int before = 0, b = 0;
+  for (int b0 = 0, sofar = 0; b0 < B; b0 += 64) {
+    const int n = b0 + lane < B ? tiles_of(clamp_len(a, a.lens[b0 + lane])) : 0;
+    int sum = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(sum, d);
+      if (lane >= d) sum += up;
+    }
+    const uint64_t le = __ballot(sofar + sum - n <= begin && n > 0);
+    if (le) {
+      const int l = 63 - __builtin_clzll(le);
+      b = b0 + l;
+      before = sofar + __builtin_amdgcn_readlane(sum - n, l);
+    }
+    sofar += __builtin_amdgcn_readlane(sum, 63);
+    if (sofar > begin) break;
+  }
+  at.b = b;
+  at.tile = begin - before;
+  at.len = len_at(a, at.b);
+  at.tiles = tiles_of(at.len);
+  at.key0 = 0;
+  at.table = a.table + at.b * a.table_stride;
+  const int row0 = block * p.rows_s, rows = min(row0 + p.rows_s, a.q_heads / a.kv_heads);
+  const int64_t entry0 = a.own + ((int64_t)(kvh * p.blocks_s + block) * (p.runs + B) + run) * 2 * p.rows_s;
+  decode_narrow<DQ, DV, NS, false>(a, kvh, at, end - begin, row0, rows, entry0, mem);
 }
 
 // The parts of an output row joined: WPR waves per row take every WPR-th part.
@@ -341,20 +368,33 @@ __global__ __launch_bounds__(WPR <= 4 ? 256 : WPR * 64) void attn_join_kernel(De
   __shared__ float2 red[kWaves][64];
   __shared__ float2 ml[kWaves];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = wv % WPR;
-  const int64_t Hall = (int64_t)a.num_requests * a.q_heads;
-  const int64_t at_row = (int64_t)blockIdx.x * kRows + wv / WPR;
+  const int Hall = a.num_requests * a.q_heads;
+  const int at_row = blockIdx.x * kRows + wv / WPR;
   const bool live = at_row < Hall;                                  // whole waves; a row's waves agree
+  const int b = min(at_row, Hall - 1) / a.q_heads, hq = min(at_row, Hall - 1) % a.q_heads;
   constexpr int E = DV / 64;                                        // values per lane
   float M = neg_inf(), L = 0.0f, o[2] = {0.0f, 0.0f};
   if (live) {
-    const int b = (int)(at_row / a.q_heads);
-    const int64_t chunk = (int64_t)a.plan.chunk_s * kDecKeys;
-    const int n = a.plan.parts_p + (int)((own_len(a, b) + chunk - 1) / chunk);
+    const DecodePlan& p = a.plan;
+    // own parts: two for each run that the request's tiles lie in
+    const int np = p.parts_p * (p.wide ? 1 : 2);
+    int n = np, run0 = 0;
+    if (p.runs > 0) {
+      const int t0 = a.first[b], t1 = a.first[b + 1], each = (a.first[a.num_requests] + p.runs - 1) / p.runs;
+      if (t1 > t0) {
+        run0 = t0 / each;
+        n += 2 * ((t1 - 1) / each - run0 + 1);
+      }
+    }
+    const int G = a.q_heads / a.kv_heads, kvh = hq / G, g = hq % G, block = g / p.rows_s;
+    const int64_t own = a.own + ((int64_t)(kvh * p.blocks_s + block) * (p.runs + a.num_requests) + run0 + b) * 2 * p.rows_s +
+                        g - block * p.rows_s;
+    auto entry = [&](int x) { return x < np ? (int64_t)x * Hall + at_row : own + (int64_t)(x - np) * p.rows_s; };
     const int mine = (n - sub + WPR - 1) / WPR;                     // parts sub, sub + WPR, ...
     for (int base = 0; base < mine; base += 64) {
       const int cnt = min(64, mine - base);
       float2 x = float2{neg_inf(), 0.0f};
-      if (lane < cnt) x = a.part_ml[(int64_t)(sub + (base + lane) * WPR) * Hall + at_row];
+      if (lane < cnt) x = a.part_ml[entry(sub + (base + lane) * WPR)];
       float mx = x.x;
 #pragma unroll
       for (int d = 32; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
@@ -367,19 +407,18 @@ __global__ __launch_bounds__(WPR <= 4 ? 256 : WPR * 64) void attn_join_kernel(De
       M = M1;
 #pragma unroll
       for (int j = 0; j < E; ++j) o[j] *= e0;
-      for (int p = 0; p < cnt; p += 8) {                            // 8 loads in flight
+      for (int q0 = 0; q0 < cnt; q0 += 8) {                         // 8 loads in flight
         float y[8][2];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const int q = min(p + u, cnt - 1);
-          const float* src = a.part_o + ((int64_t)(sub + (base + q) * WPR) * Hall + at_row) * DV + lane * E;
+          const float* src = a.part_o + entry(sub + (base + min(q0 + u, cnt - 1)) * WPR) * DV + lane * E;
           y[u][0] = src[0];
           if (E == 2) y[u][1] = src[1];
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          if (p + u >= cnt) break;
-          const float ep = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e), p + u));
+          if (q0 + u >= cnt) break;
+          const float ep = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e), q0 + u));
           o[0] = fmaf(ep, y[u][0], o[0]);
           if (E == 2) o[1] = fmaf(ep, y[u][1], o[1]);
         }
@@ -410,7 +449,6 @@ __global__ __launch_bounds__(WPR <= 4 ? 256 : WPR * 64) void attn_join_kernel(De
     M = M1;
   }
   if (!live) return;
-  const int b = (int)(at_row / a.q_heads), hq = (int)(at_row % a.q_heads);
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   uint16_t* dst = a.out + b * a.o_ts + hq * a.o_hs + lane * E;
   if (E == 2) *(uint32_t*)dst = cvt_bf16x2(o[0] * inv, o[1] * inv);
@@ -425,43 +463,58 @@ static DecodePlan decode_plan(int64_t B, int q_heads, int kv_heads, int64_t pref
   p.wide = rows > 64;
   p.blocks_p = (int32_t)up(rows, p.wide ? 128 : 64);
   p.blocks_s = (int32_t)up(G, 64);
-  // Two workgroups run on each of the 256 CUs, and a tile takes about as long in
-  // either kind (2.1 us of matrix work, 2.6 us of its share of the reads): parts
-  // of tiles / 512 tiles each fill the chip once.  Own keys go in finer parts
-  // (their lengths differ; max_len is only a bound), at least 2 tiles.
-  const int64_t tiles_p = up(prefix_len, kDecKeys), tiles_s = up(max_len, kDecKeys);
-  const int64_t work = kv_heads * (tiles_p * p.blocks_p + tiles_s * B * p.blocks_s);
-  const int64_t fill = std::max<int64_t>(2, up(work, 512));
-  p.parts_p = (int32_t)up(tiles_p, fill);
-  p.chunk_p = (int32_t)std::max<int64_t>(1, up(tiles_p, std::max(p.parts_p, 1)));
-  p.chunk_s = (int32_t)std::max<int64_t>(2, up(fill, 2));
-  p.parts_s = (int32_t)up(tiles_s, p.chunk_s);
-  if (p.parts_p + p.parts_s == 0) p.parts_s = 1;      // no key anywhere: the single part writes the empty rows
+  p.rows_s = (int32_t)std::min<int64_t>(G, 64);
+  // The workgroups that the chip holds at once, shared by the two kinds after
+  // their work: 64 keys take either kind about as long (2.1 us of matrix work for
+  // 128 rows, 2.6 us of a workgroup's share of the reads).  The own lengths are
+  // not known here: half of the bound is counted.
+  const int64_t tiles_p = up(prefix_len, 64), tiles_s = up(max_len, 64);
+  const int64_t work_p = kv_heads * p.blocks_p * tiles_p, work_s = up(kv_heads * p.blocks_s * B * tiles_s, 2);
+  const int64_t per_part = kv_heads * p.blocks_p;
+  const int64_t share = work_p == 0 ? 0 : kDecSlots * work_p / (work_p + work_s);
+  // parts of the prefix: at least two tiles in each
+  int64_t parts = tiles_p == 0 ? 0 : std::max<int64_t>(1, std::min(share / per_part, up(tiles_p, 2)));
+  p.chunk_p = tiles_p == 0 ? 0 : (int32_t)(up(tiles_p, parts) * 64);
+  p.parts_p = tiles_p == 0 ? 0 : (int32_t)up(prefix_len, p.chunk_p);
+  // runs of the own keys: the rest of the chip, at least two narrow tiles in each
+  const int64_t left = std::max<int64_t>(kDecSlots - p.parts_p * per_part, kDecSlots / 4) / (kv_heads * p.blocks_s);
+  p.runs = max_len == 0 ? 0 : (int32_t)std::max<int64_t>(1, std::min(left, up(B * up(max_len, kNarrowKeys), 2)));
   return p;
+}
+
+// entries of the two kinds of parts; the workspace holds their sums, their maxima
+// and weight sums, and the requests' first tiles
+static int64_t prefix_entries(const DecodePlan& p, int64_t B, int q_heads) {
+  return p.parts_p * (p.wide ? 1 : 2) * B * q_heads;
+}
+static int64_t plan_entries(const DecodePlan& p, int64_t B, int q_heads, int kv_heads) {
+  return prefix_entries(p, B, q_heads) +
+         (p.runs > 0 ? (int64_t)kv_heads * p.blocks_s * (p.runs + B) * 2 * p.rows_s : 0);
 }
 
 size_t attn_decode_ws_bytes(int64_t B, int q_heads, int kv_heads, int v_dim, int64_t prefix_len, int64_t max_len) {
   const DecodePlan p = decode_plan(B, q_heads, kv_heads, prefix_len, max_len);
-  const size_t parts = (size_t)p.parts_p + (size_t)p.parts_s;
-  return parts <= 1 ? 0 : parts * (size_t)B * (size_t)q_heads * ((size_t)v_dim * 4 + 8);
+  const int64_t entries = plan_entries(p, B, q_heads, kv_heads);
+  return entries == 0 ? 0 : (size_t)entries * ((size_t)v_dim * 4 + 8) + ((size_t)B + 1) * 4;
 }
 
-static int64_t plan_grid(const DecodePlan& p, int64_t B, int kv_heads) {
-  return ((int64_t)p.parts_p * p.blocks_p + B * p.blocks_s * p.parts_s) * kv_heads;
+static int64_t plan_grid(const DecodePlan& p, int kv_heads) {
+  return ((int64_t)p.parts_p * p.blocks_p + (int64_t)p.runs * p.blocks_s) * kv_heads;
 }
 
 int64_t attn_decode_grid(int64_t B, int q_heads, int kv_heads, int64_t prefix_len, int64_t max_len) {
-  return plan_grid(decode_plan(B, q_heads, kv_heads, prefix_len, max_len), B, kv_heads);
+  return plan_grid(decode_plan(B, q_heads, kv_heads, prefix_len, max_len), kv_heads);
 }
 
 template <int DQ, int DV>
 static void launch_decode(const DecodeArgs& a, hipStream_t stream) {
-  const uint32_t grid = (uint32_t)plan_grid(a.plan, a.num_requests, a.kv_heads);
-  hipLaunchKernelGGL((attn_decode_kernel<DQ, DV>), dim3(grid), dim3(kDecThreads), 0, stream, a);
-  if (!a.part_o) return;
+  const uint32_t grid = (uint32_t)plan_grid(a.plan, a.kv_heads);
+  if (grid > 0)
+    hipLaunchKernelGGL((attn_decode_kernel<DQ, DV>), dim3(grid), dim3(kDecThreads), 0, stream, a);
   const uint32_t rows = (uint32_t)(a.num_requests * a.q_heads);
-  // waves per row: as many as leave each 8 parts or so, one round of loads
-  const int parts = a.plan.parts_p + a.plan.parts_s;
+  // waves per row: as many as leave each 8 parts or so, one round of loads (a
+  // request's own parts: two per run it lies in, on average runs / B of them)
+  const int parts = a.plan.parts_p * (a.plan.wide ? 1 : 2) + 2 * (1 + a.plan.runs / a.num_requests);
   if (parts <= 16) hipLaunchKernelGGL((attn_join_kernel<DV, 1>), dim3((rows + 3) / 4), dim3(256), 0, stream, a);
   else if (parts <= 48) hipLaunchKernelGGL((attn_join_kernel<DV, 4>), dim3(rows), dim3(256), 0, stream, a);
   else hipLaunchKernelGGL((attn_join_kernel<DV, 16>), dim3(rows), dim3(1024), 0, stream, a);
@@ -494,10 +547,11 @@ moe_status launch_attn_decode(const moe_heads& q, const moe_kv_cache& cache, con
   a.page_shift = __builtin_ctz((unsigned)cache.page_size);
   a.c = p.scale * kLog2e;
   a.plan = decode_plan(B, p.q_heads, p.kv_heads, prefix_len, max_len);
-  const int64_t parts = (int64_t)a.plan.parts_p + a.plan.parts_s;
-  // (the sums first: they keep their 16-byte alignment)
-  a.part_o = parts > 1 ? (float*)ws : nullptr;
-  a.part_ml = parts > 1 ? (float2*)(a.part_o + parts * B * p.q_heads * p.v_dim) : nullptr;
+  const int64_t entries = plan_entries(a.plan, B, p.q_heads, p.kv_heads);
+  a.part_o = (float*)ws;                            // (the sums first: they need 16-byte alignment)
+  a.part_ml = (float2*)(a.part_o + entries * p.v_dim);
+  a.first = (int32_t*)(a.part_ml + entries);
+  a.own = prefix_entries(a.plan, B, p.q_heads);
   if (p.k_dim == 64) launch_decode<64, 64>(a, stream);
   else if (p.k_dim == 128) launch_decode<128, 128>(a, stream);
   else launch_decode<192, 128>(a, stream);
