@@ -80,9 +80,14 @@ __device__ __forceinline__ void at_load_lds(uint32_t lds, at_rsrc r, uint32_t of
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "s"(lds), "v"(off), "s"(r) : "memory");
 }
-// the same from a 64-bit address per lane
+// The same from a 64-bit address per lane.  ONCE: data that nothing reads again
+// (non-temporal cache policy).
+template <bool ONCE>
 __device__ __forceinline__ void at_load_lds(uint32_t lds, const void* from) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(from) : "memory");
+  if (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" :: "s"(lds), "v"(from) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(from) : "memory");
 }
 // 4 bytes per lane: lane i's land at lds + 4 i
 __device__ __forceinline__ void at_load_lds4(uint32_t lds, const void* from) {
@@ -359,6 +364,122 @@ struct AttnWave {
     weights(c);
     if (not_finite(vs)) values_careful(vs, lane, last);
     else values(vs);
+  }
+};
+
+// The same for few query rows: RB blocks of 16 rows against 32 keys, on 16x16x32
+// MFMAs.  Lane l holds row l % 16 of each block and, g = l / 16, the scores of
+// keys 4 g + i and 16 + 4 g + i (i < 4); in that order they are the second
+// product's operand, and V's rows 4 g .. 4 g + 3 and 16 + 4 g .. come by one
+// transposing read each.  Half the matrix work and half the softmax of the 32-row
+// form where at most 16 rows are real.
+__device__ __forceinline__ float quarter_max(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float quarter_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+template <int DQ, int DV, int RB>
+struct AttnWave16 {
+  static constexpr int KQ = DQ / 32, OB = DV / 16, KA = DQ == 192 ? 2 : KQ;
+  static constexpr int kKeyBytes = 32 * DQ * 2, kValBytes = 32 * DV * 2;
+  bf16x8 q[RB][KQ];
+  f32x4 o[RB][OB], s[RB][2];
+  bf16x8 p[RB];
+  float m[RB], l[RB];
+  uint32_t ka[KA], va[OB];                                          // this lane's offsets in a tile; the rest are constants
+
+  __device__ __forceinline__ void offsets(int lane) {
+    const int r = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int k = 0; k < KA; ++k) ka[k] = (uint32_t)(r * (DQ * 2) + ((4 * k + g) ^ at_swz<DQ>(r)) * 16);
+#pragma unroll
+    for (int b = 0; b < OB; ++b) {
+      const int row = 4 * g + (r >> 2);                             // at_swz repeats every 16 rows
+      va[b] = (uint32_t)(row * (DV * 2) + ((2 * b + ((r & 3) >> 1)) ^ at_swz<DV>(row)) * 16 + 8 * (r & 1));
+    }
+  }
+  // row: this lane's query row of block rb; all blocks' rows are loaded before settle()
+  __device__ __forceinline__ void init(int rb, const uint16_t* row, int lane) {
+#pragma unroll
+    for (int k = 0; k < KQ; ++k) q[rb][k] = __builtin_bit_cast(bf16x8, *(const u32x4*)(row + 32 * k + 8 * (lane >> 4)));
+#pragma unroll
+    for (int b = 0; b < OB; ++b) o[rb][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    m[rb] = neg_inf();
+    l[rb] = 0.0f;
+  }
+  __device__ __forceinline__ void settle() {                        // waits for the rows, see AttnWave::init
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int k = 0; k < KQ; ++k) asm volatile("" : "+v"(q[rb][k]));
+  }
+  __device__ __forceinline__ void scores(const uint8_t* ks) {
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) s[rb][0] = s[rb][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < KQ; ++k)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const bf16x8 kf = *(const bf16x8*)(ks + ka[k % KA] + (16 * b * (DQ * 2) + (k / KA) * (KA * 64)));
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) s[rb][b] = mfma16(kf, q[rb][k], s[rb][b]);
+      }
+  }
+  // keys past `last` are not there
+  __device__ __forceinline__ void mask(int lane, int last) {
+    const int seen = last - 4 * (lane >> 4);
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[rb][b][i] = 16 * b + i <= seen ? s[rb][b][i] : neg_inf();
+  }
+  // as AttnWave::weights
+  __device__ __forceinline__ void weights(float c) {
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      float mx = neg_inf();
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[rb][b][i]);
+      mx = quarter_max(mx) * c;
+      const bool grown = mx > m[rb] + 8.0f;
+      if (__any(grown)) {
+        const float alpha = grown ? __builtin_amdgcn_exp2f(m[rb] - mx) : 1.0f;
+        m[rb] = grown ? mx : m[rb];
+        l[rb] *= alpha;
+#pragma unroll
+        for (int b = 0; b < OB; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[rb][b][i] *= alpha;
+      }
+      const float base = m[rb] == neg_inf() ? 0.0f : m[rb];
+      float w[8], sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        w[j] = __builtin_amdgcn_exp2f(fmaf(s[rb][j / 4][j % 4], c, -base));
+        sum += w[j];
+      }
+      p[rb] = __builtin_bit_cast(
+          bf16x8, u32x4{cvt_bf16x2(w[0], w[1]), cvt_bf16x2(w[2], w[3]), cvt_bf16x2(w[4], w[5]), cvt_bf16x2(w[6], w[7])});
+      l[rb] += quarter_sum(sum);
+    }
+  }
+  __device__ __forceinline__ void values(const uint8_t* vs) {
+#pragma unroll
+    for (int b = 0; b < OB; ++b) {
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at_lds_s16x4*)(vs + va[b]));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at_lds_s16x4*)(vs + va[b] + 16 * (DV * 2)));
+      const bf16x8 vf = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) o[rb][b] = mfma16(vf, p[rb], o[rb][b]);
+    }
   }
 };
 

@@ -15,7 +15,7 @@
 // while another is computed on:
 //   wide   (prefix, many rows): 128 rows, 32 per wave; the prefix is read once
 //          per 128 rows.  Bound by the matrix cores.
-//   narrow (own keys, and a prefix with few rows): 64 rows, two waves per 32.
+//   narrow (own keys, and a prefix with few rows): 32 or 64 rows.
 //          Bound by reading the cache.
 // The own keys of all requests are one list of tiles, which the narrow workgroups
 // of a key head share out evenly, whatever the lengths: each takes one run of the
@@ -35,8 +35,9 @@ constexpr int kWideKeys = 64, kNarrowKeys = 32;     // per tile
 struct DecodePlan {
   int32_t wide;                                     // prefix workgroups are wide
   int32_t parts_p, chunk_p;                         // parts of the prefix, keys in each
-  int32_t blocks_p;                                 // row blocks of B * G rows (128 or 64)
-  int32_t blocks_s, rows_s;                         // row blocks of G rows (64), rows in each
+  int32_t blocks_p;                                 // row blocks of B * G rows (wide 128, narrow 32 rb)
+  int32_t rb;                                       // narrow workgroups take 32 rb rows
+  int32_t blocks_s, rows_s;                         // row blocks of G rows, rows in each
   int32_t runs;                                     // narrow workgroups per key head and row block
 };
 
@@ -129,13 +130,13 @@ __device__ __forceinline__ void decode_wide(const DecodeArgs& a, int kvh, int pa
 #pragma unroll
     for (int i = 0; i < W::kKeyBytes / 16 / kDecThreads; ++i) {
       const int f = i * kDecThreads + threadIdx.x, r = f / (DQ / 8);
-      at_load_lds(k_lds + (uint32_t)(st * W::kKeyBytes + i * kDecThreads * 16),
+      at_load_lds<false>(k_lds + (uint32_t)(st * W::kKeyBytes + i * kDecThreads * 16),
                   kc + (uint64_t)(uint32_t)__shfl(slot, r) * k_row + ((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16);
     }
 #pragma unroll
     for (int i = 0; i < W::kValBytes / 16 / kDecThreads; ++i) {
       const int f = i * kDecThreads + threadIdx.x, r = f / (DV / 8);
-      at_load_lds(v_lds + (uint32_t)(st * W::kValBytes + i * kDecThreads * 16),
+      at_load_lds<false>(v_lds + (uint32_t)(st * W::kValBytes + i * kDecThreads * 16),
                   vc + (uint64_t)(uint32_t)__shfl(slot, r) * v_row + ((f % (DV / 8)) ^ at_swz<DV>(r)) * 16);
     }
   };
@@ -184,8 +185,8 @@ struct Cursor {
   __device__ __forceinline__ int key(int r) const { return key0 + min(tile * kNarrowKeys + r, len - 1); }   // past the end: the last
 };
 
-// n_tiles tiles from `at` on for 64 rows: waves 0, 1 the first 32, waves 2, 3 the
-// others; even waves compute every other tile, odd waves those between, and the
+// n_tiles tiles from `at` on for 32 RB rows: waves 0, 1 the first 16 RB, waves 2, 3
+// the others; even waves compute every other tile, odd waves those between, and the
 // two leave parts of their own.  The reads are what counts: NS stages, so that
 // while one tile is computed on NS - 1 are under way.
 //
@@ -194,10 +195,10 @@ struct Cursor {
 // for D(t) and E(t + NS - 1), issues D(t + NS - 1) and E(t + 2 NS - 2): the
 // waited-for pair went out together in step t - NS + 1, so the NS - 2 pairs issued
 // since may be in flight.  Near the end fewer are.
-template <int DQ, int DV, int NS, bool PREFIX>
+template <int DQ, int DV, int NS, int RB, bool PREFIX>
 __device__ __forceinline__ void decode_narrow(const DecodeArgs& a, int kvh, Cursor<PREFIX> at, int n_tiles, int row0, int rows,
                                               int64_t entry0, uint8_t* mem) {
-  using W = AttnWave<DQ, DV, 1>;
+  using W = AttnWave16<DQ, DV, RB>;
   constexpr int kRing = 2 * NS;                                     // entries live 2 NS - 2 steps
   constexpr int kKeyLoads = W::kKeyBytes / 16 / kDecThreads, kValLoads = W::kValBytes / 16 / kDecThreads;
   constexpr int L = kKeyLoads + kValLoads + 1;
@@ -205,10 +206,9 @@ __device__ __forceinline__ void decode_narrow(const DecodeArgs& a, int kvh, Curs
   uint8_t* ks = mem;
   uint8_t* vs = ks + NS * W::kKeyBytes;
   const int* ring = (const int*)(vs + NS * W::kValBytes);
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int odd = wv & 1, G = a.q_heads / a.kv_heads;
-  const int wrow = row0 + (wv >> 1) * 32;                           // this wave's first row
-  const int row = min(wrow + (lane & 31), rows - 1);
+  const int wrow = row0 + (wv >> 1) * 16 * RB;                      // this wave's first row
   const uint32_t k_lds = at_lds_addr(ks) + (uint32_t)wv * 1024u, v_lds = at_lds_addr(vs) + (uint32_t)wv * 1024u;
   const uint8_t* kc = (const uint8_t*)(a.k_cache + (int64_t)kvh * DQ);
   const uint8_t* vc = (const uint8_t*)(a.v_cache + (int64_t)kvh * DV);
@@ -227,21 +227,27 @@ __device__ __forceinline__ void decode_narrow(const DecodeArgs& a, int kvh, Curs
 #pragma unroll
     for (int i = 0; i < kKeyLoads; ++i) {
       const int f = i * kDecThreads + threadIdx.x, r = f / (DQ / 8);
-      at_load_lds(k_lds + (uint32_t)(st * W::kKeyBytes + i * kDecThreads * 16),
+      at_load_lds<!PREFIX>(k_lds + (uint32_t)(st * W::kKeyBytes + i * kDecThreads * 16),
                   kc + (uint64_t)(uint32_t)cache_row(a, e[r], at.key(r)) * k_row + ((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16);
     }
 #pragma unroll
     for (int i = 0; i < kValLoads; ++i) {
       const int f = i * kDecThreads + threadIdx.x, r = f / (DV / 8);
-      at_load_lds(v_lds + (uint32_t)(st * W::kValBytes + i * kDecThreads * 16),
+      at_load_lds<!PREFIX>(v_lds + (uint32_t)(st * W::kValBytes + i * kDecThreads * 16),
                   vc + (uint64_t)(uint32_t)cache_row(a, e[r], at.key(r)) * v_row + ((f % (DV / 8)) ^ at_swz<DV>(r)) * 16);
     }
     if (++loaded < n_tiles) at.next(a);
   };
   W w;
+  w.offsets(lane);
   auto begin = [&]() {                                              // the rows of the computation's request
-    const int b = PREFIX ? row / G : behind.b, hq = kvh * G + (PREFIX ? row % G : row);
-    w.init(a.q + b * a.q_ts + hq * a.q_hs, lane);
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const int row = min(wrow + 16 * rb + (lane & 15), rows - 1);
+      const int b = PREFIX ? row / G : behind.b, hq = kvh * G + (PREFIX ? row % G : row);
+      w.init(rb, a.q + b * a.q_ts + hq * a.q_hs, lane);
+    }
+    w.settle();
     at_wait<0>();                                                   // nothing of before is counted below
   };
   for (int t = 0; t < NS - 1; ++t) fetch();
@@ -272,10 +278,15 @@ __device__ __forceinline__ void decode_narrow(const DecodeArgs& a, int kvh, Curs
     }
     const bool end = t + 1 == n_tiles;
     if (end || behind.tile + 1 == behind.tiles) {
-      if (wrow + (lane & 31) < rows) {
-        const int64_t entry = PREFIX ? entry0 + (int64_t)odd * a.num_requests * a.q_heads + (int64_t)(row / G) * a.q_heads + kvh * G + row % G
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) {
+        const int row = wrow + 16 * rb + (lane & 15);
+        if (row >= rows) continue;
+        const int64_t entry = PREFIX ? entry0 + ((int64_t)odd * a.num_requests + row / G) * a.q_heads + kvh * G + row % G
                                      : entry0 + ((int64_t)behind.b * 2 + odd) * a.plan.rows_s + row - row0;
-        store_part<W, DV>(a, w, entry, h);
+#pragma unroll
+        for (int x = 0; x < W::OB; ++x) *(f32x4*)(a.part_o + entry * DV + 16 * x + 4 * (lane >> 4)) = w.o[rb][x];
+        if (lane < 16) a.part_ml[entry] = float2{w.m[rb], w.l[rb]};
       }
       if (end) break;
       behind.next(a);
@@ -286,7 +297,7 @@ __device__ __forceinline__ void decode_narrow(const DecodeArgs& a, int kvh, Curs
   }
 }
 
-template <int DQ, int DV>
+template <int DQ, int DV, int RB>
 __global__ __launch_bounds__(kDecThreads, 2) void attn_decode_kernel(DecodeArgs a) {
   // narrow: stages of 32 keys and the ring of table entries; two workgroups fit a CU's 160 KB
   constexpr int kTile = kNarrowKeys * (DQ + DV) * 2, NS = 4 * kTile + 2048 <= 80 * 1024 ? 4 : 3;
@@ -305,7 +316,7 @@ __global__ __launch_bounds__(kDecThreads, 2) void attn_decode_kernel(DecodeArgs 
     at.len = (int)min((int64_t)p.chunk_p, a.prefix_len - at.key0);
     at.tiles = tiles_of(at.len);
     at.table = a.prefix_table;
-    return decode_narrow<DQ, DV, NS, true>(a, kvh, at, at.tiles, block * 64, a.num_requests * (a.q_heads / a.kv_heads),
+    return decode_narrow<DQ, DV, NS, RB, true>(a, kvh, at, at.tiles, block * 32 * RB, a.num_requests * (a.q_heads / a.kv_heads),
                                            (int64_t)part * 2 * a.num_requests * a.q_heads, mem);
   }
   item -= p.parts_p * p.blocks_p;
@@ -356,7 +367,7 @@ __global__ __launch_bounds__(kDecThreads, 2) void attn_decode_kernel(DecodeArgs 
   at.table = a.table + at.b * a.table_stride;
   const int row0 = block * p.rows_s, rows = min(row0 + p.rows_s, a.q_heads / a.kv_heads);
   const int64_t entry0 = a.own + ((int64_t)(kvh * p.blocks_s + block) * (p.runs + B) + run) * 2 * p.rows_s;
-  decode_narrow<DQ, DV, NS, false>(a, kvh, at, end - begin, row0, rows, entry0, mem);
+  decode_narrow<DQ, DV, NS, RB, false>(a, kvh, at, end - begin, row0, rows, entry0, mem);
 }
 
 // The parts of an output row joined: WPR waves per row take every WPR-th part.
@@ -461,9 +472,10 @@ static DecodePlan decode_plan(int64_t B, int q_heads, int kv_heads, int64_t pref
   const int64_t G = q_heads / kv_heads, rows = B * G;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
   p.wide = rows > 64;
-  p.blocks_p = (int32_t)up(rows, p.wide ? 128 : 64);
-  p.blocks_s = (int32_t)up(G, 64);
-  p.rows_s = (int32_t)std::min<int64_t>(G, 64);
+  p.rb = G > 32 || (!p.wide && rows > 32) ? 2 : 1;
+  p.blocks_p = (int32_t)up(rows, p.wide ? 128 : 32 * p.rb);
+  p.blocks_s = (int32_t)up(G, 32 * p.rb);
+  p.rows_s = (int32_t)std::min<int64_t>(G, 32 * p.rb);
   // The workgroups that the chip holds at once, shared by the two kinds after
   // their work: 64 keys take either kind about as long (2.1 us of matrix work for
   // 128 rows, 2.6 us of a workgroup's share of the reads).  The own lengths are
@@ -509,8 +521,10 @@ int64_t attn_decode_grid(int64_t B, int q_heads, int kv_heads, int64_t prefix_le
 template <int DQ, int DV>
 static void launch_decode(const DecodeArgs& a, hipStream_t stream) {
   const uint32_t grid = (uint32_t)plan_grid(a.plan, a.kv_heads);
-  if (grid > 0)
-    hipLaunchKernelGGL((attn_decode_kernel<DQ, DV>), dim3(grid), dim3(kDecThreads), 0, stream, a);
+  if (grid > 0) {
+    if (a.plan.rb == 1) hipLaunchKernelGGL((attn_decode_kernel<DQ, DV, 1>), dim3(grid), dim3(kDecThreads), 0, stream, a);
+    else hipLaunchKernelGGL((attn_decode_kernel<DQ, DV, 2>), dim3(grid), dim3(kDecThreads), 0, stream, a);
+  }
   const uint32_t rows = (uint32_t)(a.num_requests * a.q_heads);
   // waves per row: as many as leave each 8 parts or so, one round of loads (a
   // request's own parts: two per run it lies in, on average runs / B of them)
