@@ -5,8 +5,12 @@
 // keys 0 .. i + Lk - Lq (the last query sees every key; with Lk < Lq the first
 // rows see none and give 0).
 //
-// A workgroup takes kPromptRows consecutive queries of one sequence and one head, 32
-// per wave (attn_common.h), and walks the keys in tiles of 64 through LDS.
+// The G query heads of a key head see the same keys, so a sequence's rows are
+// taken token by token with the G heads of each token side by side: row m is head
+// m % G of token m / G.  A workgroup takes 128 such rows, 32 per wave
+// (attn_common.h), and walks the keys in tiles of 64 through LDS.  Its rows span
+// only 128 / G tokens: all waves end at about the same key, and little is computed
+// beyond the diagonal (against 128 tokens of one head: see the figures below).
 #include "attn_common.h"
 
 namespace moe {
@@ -31,22 +35,23 @@ struct PromptArgs {
 
 struct PromptTile {
   int64_t q0, k0;     // the sequence's first query and key
-  int lq, lk, row0;   // its lengths; the tile's first row
+  int lq, lk;         // its lengths
+  int64_t row0, rows; // the tile's first row, the sequence's rows (lq * G)
 };
 
 // Row tiles without a plan made beforehand: sequence b owns the virtual tiles
-// from cu_q[b] / rows + b on, at least as many as it needs, so a tile's
+// from cu_q[b] * G / 128 + b on, at least as many as it needs, so a tile's
 // sequence is found by searching cu_q itself (64 probes at a time), and
-// total_q / rows + num_seqs workgroups per head cover any lengths.  Tiles past
-// a sequence's end have row0 >= lq.  Within a sequence the last tile (the one
-// that sees most keys) comes first.
-__device__ __forceinline__ PromptTile prompt_tile(const PromptArgs& a, int64_t vt, int rows, int lane) {
+// total_q * G / 128 + num_seqs workgroups per key head cover any lengths.  Tiles
+// past a sequence's end have row0 >= rows.  Within a sequence the last tile (the
+// one that sees most keys) comes first.
+__device__ __forceinline__ PromptTile prompt_tile(const PromptArgs& a, int vt, int G, int lane) {
   auto cu = [&](const int32_t* p, int i, int64_t total) { return min(max((int64_t)p[i], (int64_t)0), total); };
   int lo = 0, n = a.num_seqs;
   while (n > 1) {
     const int stride = (n + 63) >> 6;
     const int off = lane * stride;
-    const bool le = off < n && cu(a.cu_q, lo + off, a.total_q) / rows + lo + off <= vt;
+    const bool le = off < n && cu(a.cu_q, lo + off, a.total_q) * G / kPromptRows + lo + off <= vt;
     const uint64_t mask = __ballot(le) | 1;
     const int seg = (63 - __builtin_clzll(mask)) * stride;
     lo += seg;
@@ -58,8 +63,9 @@ __device__ __forceinline__ PromptTile prompt_tile(const PromptArgs& a, int64_t v
   t.lq = (int)(max(cu(a.cu_q, b + 1, a.total_q), t.q0) - t.q0);
   t.k0 = cu(a.cu_k, b, a.total_k);
   t.lk = (int)(max(cu(a.cu_k, b + 1, a.total_k), t.k0) - t.k0);
-  const int64_t idx = vt - (t.q0 / rows + b), need = (t.lq + rows - 1) / rows;
-  t.row0 = idx < 0 || idx >= need ? t.lq : (int)((need - 1 - idx) * rows);
+  t.rows = (int64_t)t.lq * G;
+  const int64_t idx = vt - (t.q0 * G / kPromptRows + b), need = (t.rows + kPromptRows - 1) / kPromptRows;
+  t.row0 = idx < 0 || idx >= need ? t.rows : (need - 1 - idx) * kPromptRows;
   return t;
 }
 
@@ -70,24 +76,22 @@ __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptAr
   __shared__ __attribute__((aligned(16))) uint8_t ks[2 * W::kKeyBytes];
   __shared__ __attribute__((aligned(16))) uint8_t vs[2 * W::kValBytes];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
-  // the key head varies fastest (workgroups go to the XCDs in turn, so one
-  // key head's workgroups meet in few L2s), then the heads that share it
+  // the key head varies fastest: workgroups go to the XCDs in turn, so one key
+  // head's workgroups meet in few L2s
   const int G = a.q_heads / a.kv_heads;
   const int kvh = blockIdx.x % a.kv_heads;
-  const int g = (blockIdx.x / a.kv_heads) % G;
-  const int64_t vt = blockIdx.x / (uint32_t)a.q_heads;
-  const PromptTile T = prompt_tile(a, vt, kPromptRows, lane);
-  if (T.row0 >= T.lq) return;
-  const int hq = kvh * G + g;
-  const int wrow = T.row0 + wv * 32;                                // this wave's rows
-  const int row = min(wrow + (lane & 31), T.lq - 1);                // rows past the end repeat the last
+  const PromptTile T = prompt_tile(a, (int)(blockIdx.x / (uint32_t)a.kv_heads), G, lane);
+  if (T.row0 >= T.rows) return;
+  const int64_t wrow = T.row0 + wv * 32, m = min(wrow + (lane & 31), T.rows - 1);   // rows past the end repeat the last
+  const int row = (int)(m / G), hq = kvh * G + (int)(m % G);
   const int pos = row + T.lk - T.lq;                                // last key this row sees
   W w;
   w.init(a.q + (T.q0 + row) * a.q_ts + hq * a.q_hs, lane);
-  // the workgroup's keys, and the last that a row of this wave sees
-  const int last_row = min(T.row0 + kPromptRows, T.lq) - 1;
-  const int n_keys = max(0, min(T.lk, last_row + T.lk - T.lq + 1));
-  const int wave_last = min(wrow + 31, T.lq - 1) + T.lk - T.lq;
+  // the last key that a row of the workgroup sees, and one of this wave; keys that
+  // all its rows see
+  auto key_of = [&](int64_t r) { return (int)(min(r, T.rows - 1) / G) + T.lk - T.lq; };
+  const int n_keys = max(0, key_of(T.row0 + kPromptRows - 1) + 1);
+  const int wave_last = key_of(wrow + 31), all_see = key_of(T.row0) + 1;
   const uint16_t* kp = a.k + T.k0 * a.k_ts + kvh * a.k_hs;
   const uint16_t* vp = a.v + T.k0 * a.v_ts + kvh * a.v_hs;
   // Each lane's share of a tile: 16-byte chunk i * threads + thread of the
@@ -128,7 +132,7 @@ __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptAr
   const int n_tiles = (n_keys + kPromptKeys - 1) / kPromptKeys;
   // tiles that every row of the workgroup sees whole come first; for the others
   // (around the diagonal) each wave looks whether it sees any of it at all
-  const int n_whole = max(0, min(n_tiles, (T.row0 + T.lk - T.lq + 1) / kPromptKeys));
+  const int n_whole = max(0, min(n_tiles, all_see / kPromptKeys));
   auto seen = [&](int t) { return t * kPromptKeys <= wave_last; };
   if (n_tiles > 0) load(0, 0);
   auto step = [&](auto stage, auto whole, int t) {
@@ -139,6 +143,7 @@ __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptAr
     // done with tile t - 1, whose stage the next loads refill
     at_wait_barrier<0>();
     if (t + 1 < n_tiles) load(t + 1, st ^ 1);
+    if (wrow >= T.rows) return;                                     // no row of this wave is real
     if (decltype(whole)::value) w.tile(k, v, a.c);
     else if (seen(t)) w.tile_masked(k, v, lane, a.c, pos - t * kPromptKeys);
   };
@@ -154,7 +159,7 @@ __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptAr
     step(S0(), std::false_type(), t);
     if (t + 1 < n_tiles) step(S1(), std::false_type(), t + 1);
   }
-  if (wrow + (lane & 31) >= T.lq) return;
+  if (wrow + (lane & 31) >= T.rows) return;
   const float inv = w.l == 0.0f ? 0.0f : 1.0f / w.l;
   uint16_t* op = a.out + (T.q0 + row) * a.o_ts + hq * a.o_hs;
 #pragma unroll
@@ -171,8 +176,8 @@ __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptAr
 
 template <int DQ, int DV>
 static void launch_prompt(const PromptArgs& a, hipStream_t stream) {
-  const int64_t tiles = a.total_q / kPromptRows + a.num_seqs;
-  hipLaunchKernelGGL((attn_prompt_kernel<DQ, DV>), dim3((uint32_t)(tiles * a.q_heads)), dim3(kPromptThreads), 0, stream, a);
+  const int64_t tiles = a.total_q * (a.q_heads / a.kv_heads) / kPromptRows + a.num_seqs;
+  hipLaunchKernelGGL((attn_prompt_kernel<DQ, DV>), dim3((uint32_t)(tiles * a.kv_heads)), dim3(kPromptThreads), 0, stream, a);
 }
 
 moe_status launch_attn_prompt(const moe_heads& q, const moe_heads& k, const moe_heads& v, const int32_t* cu_q,
