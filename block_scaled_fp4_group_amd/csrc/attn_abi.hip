@@ -162,7 +162,10 @@ moe_status moe_attn_prompt(const moe_heads* q, const moe_heads* k, const moe_hea
     set_error("%s: token strides of k and v over 2^23 elements are not supported", fn);
     return MOE_ERR_UNSUPPORTED;
   }
-  MOE_CHECK((total_q / 32 + num_seqs) * (int64_t)p->q_heads < ((int64_t)1 << 31), "%s: too many rows", fn);
+  // rows (queries x heads of a key head), their tiles and the grid in 31 bits
+  MOE_CHECK(total_q * (p->q_heads / p->kv_heads) <= 0x7fffffff - 1024 - num_seqs &&
+                (total_q * p->q_heads / 128 + (int64_t)num_seqs * p->kv_heads) < ((int64_t)1 << 31),
+            "%s: too many rows", fn);
   static const moe_heads none = {nullptr, 0, 0};
   return launch_attn_prompt(*q, total_k > 0 ? *k : none, total_k > 0 ? *v : none, cu_q, cu_k, num_seqs, total_q, total_k,
                             *p, *out, lse, stream);

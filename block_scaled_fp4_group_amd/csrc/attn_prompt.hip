@@ -28,15 +28,15 @@ struct PromptArgs {
   int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;
   const int32_t* cu_q;
   const int32_t* cu_k;
-  int64_t total_q, total_k;
+  int32_t total_q, total_k;
   int32_t num_seqs, q_heads, kv_heads;
   float c;            // scale * log2(e)
 };
 
 struct PromptTile {
-  int64_t q0, k0;     // the sequence's first query and key
+  int q0, k0;         // the sequence's first query and key
   int lq, lk;         // its lengths
-  int64_t row0, rows; // the tile's first row, the sequence's rows (lq * G)
+  int row0, rows;     // the tile's first row, the sequence's rows (lq * G)
 };
 
 // Row tiles without a plan made beforehand: sequence b owns the virtual tiles
@@ -45,26 +45,41 @@ struct PromptTile {
 // total_q * G / 128 + num_seqs workgroups per key head cover any lengths.  Tiles
 // past a sequence's end have row0 >= rows.  Within a sequence the last tile (the
 // one that sees most keys) comes first.
+// (total_q * G < 2^31, checked on the host.)
 __device__ __forceinline__ PromptTile prompt_tile(const PromptArgs& a, int vt, int G, int lane) {
-  auto cu = [&](const int32_t* p, int i, int64_t total) { return min(max((int64_t)p[i], (int64_t)0), total); };
-  int lo = 0, n = a.num_seqs;
-  while (n > 1) {
-    const int stride = (n + 63) >> 6;
-    const int off = lane * stride;
-    const bool le = off < n && cu(a.cu_q, lo + off, a.total_q) * G / kPromptRows + lo + off <= vt;
-    const uint64_t mask = __ballot(le) | 1;
-    const int seg = (63 - __builtin_clzll(mask)) * stride;
-    lo += seg;
-    n = min(stride, n - seg);
-  }
-  const int b = __builtin_amdgcn_readfirstlane(lo);
+  auto cu = [&](const int32_t* p, int i, int total) { return min(max(p[i], 0), total); };
   PromptTile t;
-  t.q0 = cu(a.cu_q, b, a.total_q);
-  t.lq = (int)(max(cu(a.cu_q, b + 1, a.total_q), t.q0) - t.q0);
-  t.k0 = cu(a.cu_k, b, a.total_k);
-  t.lk = (int)(max(cu(a.cu_k, b + 1, a.total_k), t.k0) - t.k0);
-  t.rows = (int64_t)t.lq * G;
-  const int64_t idx = vt - (t.q0 * G / kPromptRows + b), need = (t.rows + kPromptRows - 1) / kPromptRows;
+  int b;
+  if (a.num_seqs <= 64) {
+    // lane b holds sequence b: one round of loads
+    const int at = min(lane, a.num_seqs - 1);
+    const int q0 = cu(a.cu_q, at, a.total_q), q1 = cu(a.cu_q, at + 1, a.total_q);
+    const int k0 = cu(a.cu_k, at, a.total_k), k1 = cu(a.cu_k, at + 1, a.total_k);
+    const uint64_t mask = __ballot(lane < a.num_seqs && q0 * G / kPromptRows + lane <= vt) | 1;
+    b = 63 - __builtin_clzll(mask);
+    t.q0 = __builtin_amdgcn_readlane(q0, b);
+    t.lq = __builtin_amdgcn_readlane(q1, b) - t.q0;
+    t.k0 = __builtin_amdgcn_readlane(k0, b);
+    t.lk = __builtin_amdgcn_readlane(k1, b) - t.k0;
+  } else {
+    int lo = 0, n = a.num_seqs;
+    while (n > 1) {
+      const int stride = (n + 63) >> 6, off = lane * stride;
+      const bool le = off < n && cu(a.cu_q, lo + off, a.total_q) * G / kPromptRows + lo + off <= vt;
+      const int seg = (63 - __builtin_clzll(__ballot(le) | 1)) * stride;
+      lo += seg;
+      n = min(stride, n - seg);
+    }
+    b = __builtin_amdgcn_readfirstlane(lo);
+    t.q0 = cu(a.cu_q, b, a.total_q);
+    t.lq = cu(a.cu_q, b + 1, a.total_q) - t.q0;
+    t.k0 = cu(a.cu_k, b, a.total_k);
+    t.lk = cu(a.cu_k, b + 1, a.total_k) - t.k0;
+  }
+  t.lq = max(t.lq, 0);
+  t.lk = max(t.lk, 0);
+  t.rows = t.lq * G;
+  const int idx = vt - (t.q0 * G / kPromptRows + b), need = (t.rows + kPromptRows - 1) / kPromptRows;
   t.row0 = idx < 0 || idx >= need ? t.rows : (need - 1 - idx) * kPromptRows;
   return t;
 }
@@ -82,18 +97,16 @@ __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptAr
   const int kvh = blockIdx.x % a.kv_heads;
   const PromptTile T = prompt_tile(a, (int)(blockIdx.x / (uint32_t)a.kv_heads), G, lane);
   if (T.row0 >= T.rows) return;
-  const int64_t wrow = T.row0 + wv * 32, m = min(wrow + (lane & 31), T.rows - 1);   // rows past the end repeat the last
-  const int row = (int)(m / G), hq = kvh * G + (int)(m % G);
+  const int wrow = T.row0 + wv * 32, m = min(wrow + (lane & 31), T.rows - 1);       // rows past the end repeat the last
+  const int row = m / G, hq = kvh * G + m % G;
   const int pos = row + T.lk - T.lq;                                // last key this row sees
-  W w;
-  w.init(a.q + (T.q0 + row) * a.q_ts + hq * a.q_hs, lane);
   // the last key that a row of the workgroup sees, and one of this wave; keys that
   // all its rows see
-  auto key_of = [&](int64_t r) { return (int)(min(r, T.rows - 1) / G) + T.lk - T.lq; };
+  auto key_of = [&](int r) { return min(r, T.rows - 1) / G + T.lk - T.lq; };
   const int n_keys = max(0, key_of(T.row0 + kPromptRows - 1) + 1);
   const int wave_last = key_of(wrow + 31), all_see = key_of(T.row0) + 1;
-  const uint16_t* kp = a.k + T.k0 * a.k_ts + kvh * a.k_hs;
-  const uint16_t* vp = a.v + T.k0 * a.v_ts + kvh * a.v_hs;
+  const uint16_t* kp = a.k + (int64_t)T.k0 * a.k_ts + kvh * a.k_hs;
+  const uint16_t* vp = a.v + (int64_t)T.k0 * a.v_ts + kvh * a.v_hs;
   // Each lane's share of a tile: 16-byte chunk i * threads + thread of the
   // swizzled tile, i.e. of row r the chunk that belongs there; its offset from
   // the tile's first row in memory.  Rows past the last key repeat it.
@@ -134,7 +147,9 @@ __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptAr
   // (around the diagonal) each wave looks whether it sees any of it at all
   const int n_whole = max(0, min(n_tiles, all_see / kPromptKeys));
   auto seen = [&](int t) { return t * kPromptKeys <= wave_last; };
-  if (n_tiles > 0) load(0, 0);
+  if (n_tiles > 0) load(0, 0);                                      // under way while the queries are read
+  W w;
+  w.init(a.q + (int64_t)(T.q0 + row) * a.q_ts + hq * a.q_hs, lane);
   auto step = [&](auto stage, auto whole, int t) {
     constexpr int st = decltype(stage)::value;
     const uint8_t* k = ks + st * W::kKeyBytes;
@@ -161,7 +176,7 @@ __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptAr
   }
   if (wrow + (lane & 31) >= T.rows) return;
   const float inv = w.l == 0.0f ? 0.0f : 1.0f / w.l;
-  uint16_t* op = a.out + (T.q0 + row) * a.o_ts + hq * a.o_hs;
+  uint16_t* op = a.out + (int64_t)(T.q0 + row) * a.o_ts + hq * a.o_hs;
 #pragma unroll
   for (int b = 0; b < W::OB; ++b)
 #pragma unroll
@@ -171,12 +186,12 @@ __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptAr
       *(u32x2*)(op + 32 * b + 8 * i + 4 * h) = v;
     }
   if (a.lse && h == 0)
-    a.lse[(T.q0 + row) * a.q_heads + hq] = w.l == 0.0f ? neg_inf() : (w.m + __builtin_amdgcn_logf(w.l)) * kLn2;
+    a.lse[(int64_t)(T.q0 + row) * a.q_heads + hq] = w.l == 0.0f ? neg_inf() : (w.m + __builtin_amdgcn_logf(w.l)) * kLn2;
 }
 
 template <int DQ, int DV>
 static void launch_prompt(const PromptArgs& a, hipStream_t stream) {
-  const int64_t tiles = a.total_q * (a.q_heads / a.kv_heads) / kPromptRows + a.num_seqs;
+  const int64_t tiles = (int64_t)a.total_q * (a.q_heads / a.kv_heads) / kPromptRows + a.num_seqs;
   hipLaunchKernelGGL((attn_prompt_kernel<DQ, DV>), dim3((uint32_t)(tiles * a.kv_heads)), dim3(kPromptThreads), 0, stream, a);
 }
 
@@ -200,8 +215,8 @@ moe_status launch_attn_prompt(const moe_heads& q, const moe_heads& k, const moe_
   a.cu_q = cu_q;
   a.cu_k = cu_k;
   a.num_seqs = num_seqs;
-  a.total_q = total_q;
-  a.total_k = total_k;
+  a.total_q = (int32_t)total_q;
+  a.total_k = (int32_t)total_k;
   a.q_heads = p.q_heads;
   a.kv_heads = p.kv_heads;
   a.c = p.scale * kLog2e;
