@@ -66,11 +66,11 @@ __device__ __forceinline__ SlotRequest slot_request(const SlotArgs& a, int b) {
 
 __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotArgs a) {
   __shared__ int64_t tok[kSlotMaxRequests + 1], page[kSlotMaxRequests + 1];   // exclusive prefix sums
-  __shared__ int64_t part[2][kSlotThreads];
-  __shared__ int64_t lost_part[kSlotThreads];
-  const int B = a.num_requests, tid = threadIdx.x;
-  // each thread sums its run of consecutive requests, the 256 sums are scanned,
-  // and the runs are written out from their starts
+  __shared__ int64_t part[3][kSlotThreads / 64];
+  const int B = a.num_requests, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  // each thread sums its run of consecutive requests, the 256 sums are scanned
+  // (each wave its own, then the waves' totals), and the runs are written out from
+  // their starts
   const int per = (B + kSlotThreads - 1) / kSlotThreads;
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
   int64_t nt = 0, np = 0;
@@ -79,17 +79,30 @@ __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotArgs a) {
     nt += r.fresh;
     np += r.need;
   }
-  part[0][tid] = nt;
-  part[1][tid] = np;
-  __syncthreads();
-  for (int w = 1; w < kSlotThreads; w <<= 1) {
-    const int64_t x = tid >= w ? part[0][tid - w] : 0, y = tid >= w ? part[1][tid - w] : 0;
-    __syncthreads();
-    part[0][tid] += x;
-    part[1][tid] += y;
-    __syncthreads();
+  int64_t st = nt, sp = np;                                         // inclusive
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t x = __shfl_up(st, d), y = __shfl_up(sp, d);
+    if (lane >= d) {
+      st += x;
+      sp += y;
+    }
   }
-  int64_t t0 = part[0][tid] - nt, p0 = part[1][tid] - np, lost = 0;
+  if (lane == 63) {
+    part[0][wv] = st;
+    part[1][wv] = sp;
+  }
+  __syncthreads();
+  int64_t t0 = st - nt, p0 = sp - np, lost = 0, total = 0, pages = 0;
+#pragma unroll
+  for (int w = 0; w < kSlotThreads / 64; ++w) {
+    if (w < wv) {
+      t0 += part[0][w];
+      p0 += part[1][w];
+    }
+    total += part[0][w];
+    pages += part[1][w];
+  }
   for (int b = b0; b < b1; ++b) {
     const SlotRequest r = slot_request(a, b);
     tok[b] = t0;
@@ -102,23 +115,25 @@ __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotArgs a) {
     t0 += r.fresh;
     p0 += r.need;
   }
-  if (tid == kSlotThreads - 1) {
-    tok[B] = part[0][tid];
-    page[B] = part[1][tid];
+  if (tid == 0) {
+    tok[B] = total;
+    page[B] = pages;
   }
-  lost_part[tid] = lost;
+  if (blockIdx.x == 0) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) lost += __shfl_xor(lost, d);
+    if (lane == 0) part[2][wv] = lost;
+  }
   __syncthreads();
-  const int64_t total = tok[B], pages = page[B];
   if (blockIdx.x == 0) {
     for (int b = tid; b <= B; b += kSlotThreads) a.cu_new[b] = (int32_t)min(tok[b], (int64_t)0x7fffffff);
-    for (int w = kSlotThreads / 2; w > 0; w >>= 1) {
-      if (tid < w) lost_part[tid] += lost_part[tid + w];
-      __syncthreads();
-    }
     if (tid == 0) {
+      lost = 0;
+#pragma unroll
+      for (int w = 0; w < kSlotThreads / 64; ++w) lost += part[2][w];
       a.counts[0] = (int32_t)min(min(pages, a.num_free), (int64_t)0x7fffffff);
       a.counts[1] = (int32_t)min(pages, (int64_t)0x7fffffff);
-      a.counts[2] = (int32_t)min(lost_part[0], (int64_t)0x7fffffff);
+      a.counts[2] = (int32_t)min(lost, (int64_t)0x7fffffff);
     }
   }
   const int64_t step = (int64_t)gridDim.x * kSlotThreads, at = (int64_t)blockIdx.x * kSlotThreads + tid;
