@@ -697,3 +697,4 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
 
 
 from .layer import MoELayer, LayerWeights  # noqa: E402  (composition of the calls above)
+from .attention import AttentionLayer, AttentionWeights  # noqa: E402
