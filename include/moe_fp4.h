@@ -518,6 +518,7 @@ typedef struct {
  *   cu_q, cu_k int32 [num_seqs + 1], not descending, from 0 to total_q / total_k
  *   (rows outside the ranges keep their values; entries are clamped to them);
  *   lse float [total_q, q_heads] or NULL.
+ * Token strides of k and v up to 2^23 elements (else MOE_ERR_UNSUPPORTED).
  * num_seqs == 0 or total_q == 0 is a no-op.  One launch.
  */
 moe_status moe_attn_prompt(const moe_heads* q, const moe_heads* k, const moe_heads* v, const int32_t* cu_q,

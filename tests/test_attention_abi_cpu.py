@@ -74,6 +74,7 @@ def test_attn_prompt_refuses():
         refuses(prompt(**kw), INVALID)
     for D, Dv in ((96, 96), (128, 64), (192, 192), (256, 256)):
         refuses(prompt(D=D, Dv=Dv), UNSUPPORTED)
+    refuses(prompt(k=heads(2, 128, ts=(1 << 23) + 8)), UNSUPPORTED)
     refuses(prompt(seqs=0), OK)
     refuses(prompt(tq=0), OK)
 

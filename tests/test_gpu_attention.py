@@ -533,3 +533,111 @@ def test_attn_decode_same_bits_other_stream_and_graph():
         eager, el = moe.attn_decode(*args, prefix_table=pt, prefix_len=600, want_lse=True)
         torch.cuda.synchronize()
         assert torch.equal(out, eager) and torch.equal(lse, el), i
+
+
+# ----------------------------------------------- variants chosen by size, and other streams
+@pytest.mark.parametrize("D,inter,heads", [(64, False, 216), (128, True, 108), (192, False, 72)])
+def test_qk_norm_rope_large_equals_small(D, inter, heads):
+    """Outputs over 128 MiB take the stores that bypass the cache: the bits of the same tokens in small calls."""
+    Hkv, T, page = 4, 5200, 16
+    Hq = heads - 2 * Hkv
+    say(f"qk_norm_rope {T} x {Hq}/{Hkv} x {D}")
+    assert T * heads * D * 2 > 128 << 20
+    g = torch.Generator(device="cuda").manual_seed(D)
+    rows = torch.randn((T, heads, D), generator=g, device="cuda").to(torch.bfloat16)
+    q, k, v = rows[:, :Hq], rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:]
+    pos = torch.randint(0, 300, (T,), generator=g, device="cuda", dtype=torch.int32)
+    cs, w = torch.randn((300, D), generator=g, device="cuda"), torch.rand(D, generator=g, device="cuda")
+    pages = T // page + 4
+    slots = torch.randperm(pages * page, generator=g, device="cuda")[:T].to(torch.int32)
+    caches = [torch.zeros((pages, page, Hkv, D), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    ql, kl = moe.qk_norm_rope(q, k, pos, cs, w, w, 1e-6, inter, v, *caches[:2], slots, want_k=True)
+    for i in range(0, T, 1300):
+        s = slice(i, i + 1300)
+        qs, ks = moe.qk_norm_rope(q[s], k[s], pos[s], cs, w, w, 1e-6, inter, v[s], *caches[2:], slots[s], want_k=True)
+        torch.cuda.synchronize()
+        assert torch.equal(qs, ql[s]) and torch.equal(ks, kl[s]), i
+    assert torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
+    assert torch.equal(caches[1].view(-1, Hkv, D)[slots.long()], v)
+
+
+@pytest.mark.parametrize("lens,prefix,Hq,Hkv", [([5, 40], 70, 70, 1), ([33], 0, 130, 1), ([1, 0, 65], 64, 132, 2)])
+def test_attn_decode_many_heads_per_key_head(lens, prefix, Hq, Hkv):
+    """More than 64 query heads of a key head: several row blocks of the own keys."""
+    what = f"attn_decode lens={lens} prefix={prefix} heads {Hq}/{Hkv}"
+    say(what)
+    *_, ref, _, _ = run_decode(Hq + prefix, lens, prefix, 16, Hq, Hkv, 128, 128)
+    check_decode(*ref, what)
+
+
+@pytest.mark.parametrize("D,Dv", HEADS)
+@pytest.mark.parametrize("B", [2, 3, 20])
+def test_attn_decode_places_past_the_end(D, Dv, B):
+    """Few and many rows (32, 48 and 320 to a key head): the last page's unused rows hold infinities that nothing sees;
+    an infinity in the last key's value is seen by exactly the rows that read it."""
+    say(f"attn_decode {D}/{Dv}: infinities behind the last key, {B} requests")
+    lens, prefix = [40 + b for b in range(B)], 75
+    kb, vb, table, ptab, blocks = paged(80 + B, lens, prefix, 16, 1, D, Dv)
+    q = dev_bf16(synth.random_bf16(81, (B, 16, D)))
+    v, k = dev_bf16(vb), dev_bf16(kb)
+    args = (dev_i32(table), dev_i32(np.array(lens)), max(lens), dev_i32(ptab), prefix)
+    ref, rl = moe.attn_decode(q, k, v, *args, want_lse=True)
+    dirt = torch.isnan(v)
+    assert dirt.any() and torch.isfinite(ref.float()).all()
+    for value in (float("inf"), -float("inf")):
+        k2, v2 = k.clone(), v.clone()
+        k2[torch.isnan(k)], v2[dirt] = value, value
+        out, lse = moe.attn_decode(q, k2, v2, *args, want_lse=True)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref) and torch.equal(lse, rl), value
+    v[ptab[74 // 16], 74 % 16, 0, 7] = float("inf")
+    last = lens[-1] - 1
+    v[table[B - 1][last // 16], last % 16, 0, 21] = -float("inf")
+    out, lse = moe.attn_decode(q, k, v, *args, want_lse=True)
+    torch.cuda.synchronize()
+    assert (out[:, :, 7] == float("inf")).all() and (out[-1, :, 21] == -float("inf")).all()
+    rest = [i for i in range(Dv) if i not in (7, 21)]
+    assert torch.equal(out[..., rest], ref[..., rest]) and torch.equal(out[:-1, :, 21], ref[:-1, :, 21])
+    assert torch.equal(lse, rl)
+
+
+def test_slots_and_rope_other_stream_and_graph():
+    """The tables of a step that are built and used on another stream, and in a graph: the bits of the eager calls."""
+    say("kv_slots + qk_norm_rope: another stream, a graph")
+    B, page, Hq, Hkv, D = 5, 16, 4, 2, 64
+    rng = np.random.default_rng(4)
+    new, cached = dev_i32(rng.integers(0, 20, B)), dev_i32(rng.integers(0, 20, B))
+    free, cs = dev_i32(rng.permutation(40)), torch.randn((64, D), device="cuda")
+    rows = dev_bf16(synth.random_bf16(9, (100, Hq + 2 * Hkv, D)))
+
+    def step(table, kc, vc, out, **kw):
+        s, p, cu, n = moe.kv_slots(cached, new, free, table, page, 100, 0, *out, **kw)
+        return moe.qk_norm_rope(rows[:, :Hq], rows[:, Hq:Hq + Hkv], p, cs, v=rows[:, Hq + Hkv:], k_cache=kc, v_cache=vc,
+                                slots=s, want_k=True, **kw)
+
+    def fresh():
+        caches = [torch.zeros((40, page, Hkv, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        outs = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (100, 100, B + 1, 3)]
+        return torch.full((B, 4), -1, dtype=torch.int32, device="cuda"), *caches, outs
+
+    a, b, c = fresh(), fresh(), fresh()
+    qa, ka = step(*a)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    qb, kb = step(*b, stream=s)
+    s.synchronize()
+    assert torch.equal(qa, qb) and torch.equal(ka, kb) and all(torch.equal(x, y) for x, y in zip(a[:3], b[:3]))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qc, kc = step(*c)
+    for i in range(3):
+        for t in c[:3]:
+            t.fill_(-1 if t.dtype == torch.int32 else 0)
+        d = fresh()
+        new.copy_(dev_i32(rng.integers(0, 20, B)))
+        g.replay()
+        qd, kd = step(*d)
+        torch.cuda.synchronize()
+        assert torch.equal(qc, qd) and torch.equal(kc, kd), i
+        assert all(torch.equal(x, y) for x, y in zip(c[:3], d[:3])) and all(torch.equal(x, y) for x, y in zip(c[3], d[3])), i
