@@ -279,28 +279,6 @@ struct AttnWave {
     l += half_sum(sum);
   }
 
-  // Whether some value of the tile is infinite or NaN: zero times it is not zero.
-  __device__ __forceinline__ bool not_finite(const uint8_t* vs) const {
-    f32x16 z;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = 0.0f;
-    const bf16x8 zero = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
-    bf16x8 f[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = operand(nullptr, vs, kScoreOps + i);
-#pragma unroll
-    for (int i = 0; i < kValueOps; ++i) {
-      __builtin_amdgcn_sched_barrier(0);
-      z = mfma32(f[i % 4], zero, z);
-      if (i + 4 < kValueOps) f[i % 4] = operand(nullptr, vs, kScoreOps + i + 4);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) bad |= z[i] != 0.0f;
-    return __any(bad);
-  }
-
   // values() of a tile with masked places and values that are not all finite.  A
   // weight of 0 times an infinite or NaN value is NaN, so a value that is masked
   // for a row would reach it.  So the product runs on the finite values, and
@@ -352,18 +330,26 @@ struct AttnWave {
     }
   }
 
-  // a whole tile that every row sees; one with masked places, see mask()
+  // a whole tile that every row sees
   __device__ __forceinline__ void tile(const uint8_t* ks, const uint8_t* vs, float c) {
     scores(ks);
     weights(c);
     values(vs);
   }
+  // One with masked places, see mask().  All values that a row does not see have
+  // weight 0; an infinity or a NaN among them makes the row's o NaN all the same,
+  // which the caller has to notice and do again with tile_careful().
   __device__ __forceinline__ void tile_masked(const uint8_t* ks, const uint8_t* vs, int lane, float c, int last) {
     scores(ks);
     mask(lane, last);
     weights(c);
-    if (not_finite(vs)) values_careful(vs, lane, last);
-    else values(vs);
+    values(vs);
+  }
+  __device__ __forceinline__ void tile_careful(const uint8_t* ks, const uint8_t* vs, int lane, float c, int last) {
+    scores(ks);
+    mask(lane, last);
+    weights(c);
+    values_careful(vs, lane, last);
   }
 };
 

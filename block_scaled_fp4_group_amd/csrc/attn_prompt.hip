@@ -30,8 +30,17 @@ struct PromptArgs {
   const int32_t* cu_k;
   int32_t total_q, total_k;
   int32_t num_seqs, q_heads, kv_heads;
+  uint32_t g_mul;     // n / G = n * g_mul >> 32 + g_shift, see div_g
+  int32_t g_shift;
   float c;            // scale * log2(e)
 };
+
+// n / G for 0 <= n < 2^31: with 2^(s - 1) < G <= 2^s and g_mul = ceil(2^(31 + s) / G),
+// n * g_mul exceeds n * 2^(31 + s) / G by less than n < 2^31 ulps of the last
+// place before the shift, 1 / G of which is less than 1 / G of the quotient's unit.
+__device__ __forceinline__ int div_g(const PromptArgs& a, int n) {
+  return a.g_shift < 0 ? n : (int)(__umulhi((uint32_t)n, a.g_mul) >> a.g_shift);
+}
 
 struct PromptTile {
   int q0, k0;         // the sequence's first query and key
@@ -84,25 +93,26 @@ __device__ __forceinline__ PromptTile prompt_tile(const PromptArgs& a, int vt, i
   return t;
 }
 
-template <int DQ, int DV>
-__global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptArgs a) {
+// The rows of workgroup `block`, this is its thread `thread`.  Whether some result
+// is not finite; in that case the workgroup's rows have to be done again,
+// CAREFUL: a value that is infinite or NaN reaches the rows that see it only.
+template <int DQ, int DV, bool CAREFUL>
+__device__ __forceinline__ bool prompt_rows(const PromptArgs& a, uint32_t block, uint32_t thread, uint8_t* ks, uint8_t* vs) {
   using W = AttnWave<DQ, DV, kPromptKeys / 32>;
   constexpr int kThreads = kPromptThreads;
-  __shared__ __attribute__((aligned(16))) uint8_t ks[2 * W::kKeyBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t vs[2 * W::kValBytes];
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+  const int lane = thread & 63, wv = __builtin_amdgcn_readfirstlane(thread >> 6), h = lane >> 5;
   // the key head varies fastest: workgroups go to the XCDs in turn, so one key
   // head's workgroups meet in few L2s
   const int G = a.q_heads / a.kv_heads;
-  const int kvh = blockIdx.x % a.kv_heads;
-  const PromptTile T = prompt_tile(a, (int)(blockIdx.x / (uint32_t)a.kv_heads), G, lane);
-  if (T.row0 >= T.rows) return;
+  const int kvh = block % (uint32_t)a.kv_heads;
+  const PromptTile T = prompt_tile(a, (int)(block / (uint32_t)a.kv_heads), G, lane);
+  if (T.row0 >= T.rows) return false;
   const int wrow = T.row0 + wv * 32, m = min(wrow + (lane & 31), T.rows - 1);       // rows past the end repeat the last
-  const int row = m / G, hq = kvh * G + m % G;
+  const int row = div_g(a, m), hq = kvh * G + m - row * G;
   const int pos = row + T.lk - T.lq;                                // last key this row sees
   // the last key that a row of the workgroup sees, and one of this wave; keys that
   // all its rows see
-  auto key_of = [&](int r) { return min(r, T.rows - 1) / G + T.lk - T.lq; };
+  auto key_of = [&](int r) { return div_g(a, min(r, T.rows - 1)) + T.lk - T.lq; };
   const int n_keys = max(0, key_of(T.row0 + kPromptRows - 1) + 1);
   const int wave_last = key_of(wrow + 31), all_see = key_of(T.row0) + 1;
   const uint16_t* kp = a.k + (int64_t)T.k0 * a.k_ts + kvh * a.k_hs;
@@ -113,11 +123,11 @@ __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptAr
   constexpr int kKeyLoads = W::kKeyBytes / 16 / kThreads, kValLoads = W::kValBytes / 16 / kThreads;
   const uint32_t k_row = (uint32_t)(a.k_ts * 2), v_row = (uint32_t)(a.v_ts * 2);   // bytes; a tile spans < 2 GiB (host)
   auto k_off = [&](int i, int end) {
-    const int f = i * kThreads + threadIdx.x, r = f / (DQ / 8);
+    const int f = i * kThreads + (int)thread, r = f / (DQ / 8);
     return (uint32_t)min(r, end) * k_row + (uint32_t)((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16u;
   };
   auto v_off = [&](int i, int end) {
-    const int f = i * kThreads + threadIdx.x, r = f / (DV / 8);
+    const int f = i * kThreads + (int)thread, r = f / (DV / 8);
     return (uint32_t)min(r, end) * v_row + (uint32_t)((f % (DV / 8)) ^ at_swz<DV>(r)) * 16u;
   };
   uint32_t koff[kKeyLoads], voff[kValLoads];
@@ -150,43 +160,99 @@ __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptAr
   if (n_tiles > 0) load(0, 0);                                      // under way while the queries are read
   W w;
   w.init(a.q + (int64_t)(T.q0 + row) * a.q_ts + hq * a.q_hs, lane);
-  auto step = [&](auto stage, auto whole, int t) {
-    constexpr int st = decltype(stage)::value;
-    const uint8_t* k = ks + st * W::kKeyBytes;
-    const uint8_t* v = vs + st * W::kValBytes;
-    // this wave's part of tile t has landed, then everyone's; and everyone is
-    // done with tile t - 1, whose stage the next loads refill
+  // tile t has landed, and everyone is done with tile t - 1, whose stage the next
+  // loads refill
+  auto begin = [&](int t, int st) {
     at_wait_barrier<0>();
     if (t + 1 < n_tiles) load(t + 1, st ^ 1);
-    if (wrow >= T.rows) return;                                     // no row of this wave is real
-    if (decltype(whole)::value) w.tile(k, v, a.c);
-    else if (seen(t)) w.tile_masked(k, v, lane, a.c, pos - t * kPromptKeys);
   };
-  using S0 = std::integral_constant<int, 0>;
-  using S1 = std::integral_constant<int, 1>;
+  const bool real = wrow < T.rows;                                  // some row of this wave is
   int t = 0;
-  for (; t + 1 < n_whole; t += 2) {
-    step(S0(), std::true_type(), t);
-    step(S1(), std::true_type(), t + 1);
+  if (!CAREFUL) {
+    auto step = [&](auto stage, int tile) {
+      constexpr int st = decltype(stage)::value;
+      begin(tile, st);
+      if (real) w.tile(ks + st * W::kKeyBytes, vs + st * W::kValBytes, a.c);
+    };
+    for (; t + 1 < n_whole; t += 2) {
+      step(std::integral_constant<int, 0>(), t);
+      step(std::integral_constant<int, 1>(), t + 1);
+    }
   }
   // (a last odd whole tile goes with the others)
-  for (; t < n_tiles; t += 2) {
-    step(S0(), std::false_type(), t);
-    if (t + 1 < n_tiles) step(S1(), std::false_type(), t + 1);
+#pragma unroll 1
+  for (; t < n_tiles; ++t) {
+    const int st = t & 1;
+    begin(t, st);
+    if (!real || !seen(t)) continue;
+    const uint8_t* k = ks + st * W::kKeyBytes;
+    const uint8_t* v = vs + st * W::kValBytes;
+    if (CAREFUL) w.tile_careful(k, v, lane, a.c, pos - t * kPromptKeys);
+    else w.tile_masked(k, v, lane, a.c, pos - t * kPromptKeys);
   }
-  if (wrow + (lane & 31) >= T.rows) return;
+  // The results go through LDS, so that stores write whole rows: 16-byte chunk c
+  // of row r lies at chunk c ^ r of the stage that is not the last tile's (everyone
+  // is done with it and no load is under way there), a quarter per wave.
+  constexpr int CH = DV / 8;
+  const int idle = n_tiles & 1;
+  uint8_t* rows = (wv < 2 ? ks + idle * W::kKeyBytes : vs + idle * W::kValBytes) + (wv & 1) * (32 * DV * 2);
   const float inv = w.l == 0.0f ? 0.0f : 1.0f / w.l;
-  uint16_t* op = a.out + (int64_t)(T.q0 + row) * a.o_ts + hq * a.o_hs;
+  float odd = 0.0f;                                                 // NaN once some result is not finite
 #pragma unroll
   for (int b = 0; b < W::OB; ++b)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const u32x2 v = {cvt_bf16x2(w.o[b][4 * i] * inv, w.o[b][4 * i + 1] * inv),
-                       cvt_bf16x2(w.o[b][4 * i + 2] * inv, w.o[b][4 * i + 3] * inv)};
-      *(u32x2*)(op + 32 * b + 8 * i + 4 * h) = v;
+    for (int i = 0; i < 4; i += 2) {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        y[j] = w.o[b][4 * i + j] * inv;
+        if (!CAREFUL) odd = fmaf(y[j], 0.0f, odd);
+      }
+      u32x4 v;
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        // the halves of the wave hold 4 columns each of groups i and i + 1 of 8; each gets one group
+        const auto x = __builtin_amdgcn_permlane32_swap(cvt_bf16x2(y[j], y[j + 1]), cvt_bf16x2(y[4 + j], y[5 + j]), false, false);
+        v[j / 2] = x[0];
+        v[2 + j / 2] = x[1];
+      }
+      const int r = lane & 31, c = 4 * b + i + h;
+      *(u32x4*)(rows + r * (DV * 2) + ((c ^ (r & (CH - 1))) * 16)) = v;
     }
-  if (a.lse && h == 0)
+  asm volatile("" ::: "memory");                                    // (a wave's own LDS accesses stay in order)
+  const int64_t at = (int64_t)(T.q0 + row) * a.o_ts + hq * a.o_hs;
+#pragma unroll
+  for (int i = 0; i < 32 * CH / 64; ++i) {
+    const int r = (i * 64 + lane) / CH, c = lane % CH;
+    const u32x4 v = *(const u32x4*)(rows + r * (DV * 2) + ((c ^ (r & (CH - 1))) * 16));
+    const int64_t to = (int64_t)__shfl((long long)at, r);
+    if (wrow + r < T.rows) *(u32x4*)(a.out + to + c * 8) = v;
+  }
+  if (a.lse && h == 0 && wrow + (lane & 31) < T.rows)
     a.lse[(int64_t)(T.q0 + row) * a.q_heads + hq] = w.l == 0.0f ? neg_inf() : (w.m + __builtin_amdgcn_logf(w.l)) * kLn2;
+  if (CAREFUL) return false;
+  // each wave's word, in its quarter of the idle stage
+  if (lane == 0) *(int*)rows = 0;
+  if (odd != odd) *(int*)rows = 1;
+  at_wait_barrier<63>();                                            // (the stores are not waited for)
+  int any = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) any |= *(const int*)((i < 2 ? ks + idle * W::kKeyBytes : vs + idle * W::kValBytes) + (i & 1) * (32 * DV * 2));
+  return any != 0;
+}
+
+template <int DQ, int DV>
+__global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptArgs a) {
+  using W = AttnWave<DQ, DV, kPromptKeys / 32>;
+  __shared__ __attribute__((aligned(16))) uint8_t ks[2 * W::kKeyBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t vs[2 * W::kValBytes];
+  uint32_t block = blockIdx.x, thread = threadIdx.x;
+  if (!prompt_rows<DQ, DV, false>(a, block, thread, ks, vs)) return;
+  // (opaque copies: nothing of the first run is kept in registers for this one)
+  asm volatile("" : "+s"(block));
+  asm volatile("" : "+v"(thread));
+  at_wait_barrier<0>();                                             // everyone has read the words; their stage is refilled
+  prompt_rows<DQ, DV, true>(a, block, thread, ks, vs);
 }
 
 template <int DQ, int DV>
@@ -219,6 +285,10 @@ moe_status launch_attn_prompt(const moe_heads& q, const moe_heads& k, const moe_
   a.total_k = (int32_t)total_k;
   a.q_heads = p.q_heads;
   a.kv_heads = p.kv_heads;
+  const uint32_t G = (uint32_t)(p.q_heads / p.kv_heads);
+  const int bits = G == 1 ? 0 : 32 - __builtin_clz(G - 1);          // 2^(bits - 1) < G <= 2^bits
+  a.g_shift = bits - 1;
+  a.g_mul = G == 1 ? 0 : (uint32_t)((((uint64_t)1 << (31 + bits)) + G - 1) / G);
   a.c = p.scale * kLog2e;
   if (p.k_dim == 64) launch_prompt<64, 64>(a, stream);
   else if (p.k_dim == 128) launch_prompt<128, 128>(a, stream);
