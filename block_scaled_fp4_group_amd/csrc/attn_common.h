@@ -134,10 +134,6 @@ struct AttnWave {
     const int h = lane >> 5, r = lane & 31, g = lane >> 4, i16 = lane & 15;
 #pragma unroll
     for (int i = 0; i < KQ; ++i) q[i] = __builtin_bit_cast(bf16x8, *(const u32x4*)(row + 16 * i + 8 * h));
-    // the loads are waited for here, not by the first use in the key loop (whose
-    // wait would take the direct loads in flight with it, tile after tile)
-#pragma unroll
-    for (int i = 0; i < KQ; ++i) asm volatile("" : "+v"(q[i]));
 #pragma unroll
     for (int k = 0; k < KA; ++k) ka[k] = (uint32_t)(r * (DQ * 2) + ((2 * k + h) ^ at_swz<DQ>(r)) * 16);
 #pragma unroll
@@ -154,6 +150,15 @@ struct AttnWave {
       for (int i = 0; i < 16; ++i) o[b][i] = 0.0f;
     m = neg_inf();
     l = 0.0f;
+    // The loads are waited for here, not by the first use in the key loop (whose
+    // wait would take the direct loads in flight with it, tile after tile); all
+    // the rest is done while they are under way.
+#pragma unroll
+    for (int k = 0; k < KA; ++k) asm volatile("" : "+v"(ka[k]));
+#pragma unroll
+    for (int b = 0; b < OB; ++b) asm volatile("" : "+v"(va[b][0]), "+v"(va[b][1]), "+v"(o[b]));
+#pragma unroll
+    for (int i = 0; i < KQ; ++i) asm volatile("" : "+v"(q[i]));
   }
 
   // operand of keys 32 b .. 32 b + 31, columns 16 k .. 16 k + 15

@@ -103,7 +103,10 @@ __device__ __forceinline__ void clear_values(uint8_t* vs, int valid) {
 }
 
 // Prefix part `part`, 128 rows from row0, 32 per wave; tiles of 64 keys in two stages.
-template <int DQ, int DV>
+// PAGED: pages hold 64 rows or more, so a tile's rows follow one another (rows past
+// the end are the page's own and masked); a lane's offsets in a tile are constant
+// then.  Otherwise each lane finds its rows.
+template <int DQ, int DV, bool PAGED>
 __device__ __forceinline__ void decode_wide(const DecodeArgs& a, int kvh, int part, int row0, uint8_t* mem) {
   using W = AttnWave<DQ, DV, kWideKeys / 32>;
   uint8_t* ks = mem;
@@ -120,24 +123,48 @@ __device__ __forceinline__ void decode_wide(const DecodeArgs& a, int kvh, int pa
   // is read when the loads of tile t + 1 go out.
   const int key0 = part * a.plan.chunk_p, n_keys = (int)min((int64_t)a.plan.chunk_p, a.prefix_len - key0);
   const int n_tiles = (n_keys + kWideKeys - 1) / kWideKeys, n_whole = n_keys / kWideKeys;
-  auto key_of = [&](int t) { return key0 + min(t * kWideKeys + lane, n_keys - 1); };
+  auto key_of = [&](int t) { return key0 + min(t * kWideKeys + (PAGED ? 0 : lane), n_keys - 1); };
   auto entry = [&](int t) { return a.prefix_table[key_of(t) >> a.page_shift]; };
   const uint32_t k_lds = at_lds_addr(ks) + (uint32_t)wv * 1024u, v_lds = at_lds_addr(vs) + (uint32_t)wv * 1024u;
   const uint8_t* kc = (const uint8_t*)(a.k_cache + (int64_t)kvh * DQ);
   const uint8_t* vc = (const uint8_t*)(a.v_cache + (int64_t)kvh * DV);
   const uint32_t k_row = (uint32_t)a.kv_heads * DQ * 2, v_row = (uint32_t)a.kv_heads * DV * 2;
-  auto load = [&](int slot, int st) {
+  constexpr int kKeyLoads = W::kKeyBytes / 16 / kDecThreads, kValLoads = W::kValBytes / 16 / kDecThreads;
+  uint32_t koff[PAGED ? kKeyLoads : 1], voff[PAGED ? kValLoads : 1];
+  if (PAGED) {
 #pragma unroll
-    for (int i = 0; i < W::kKeyBytes / 16 / kDecThreads; ++i) {
+    for (int i = 0; i < kKeyLoads; ++i) {
       const int f = i * kDecThreads + threadIdx.x, r = f / (DQ / 8);
-      at_load_lds<false>(k_lds + (uint32_t)(st * W::kKeyBytes + i * kDecThreads * 16),
-                  kc + (uint64_t)(uint32_t)__shfl(slot, r) * k_row + ((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16);
+      koff[i] = (uint32_t)r * k_row + (uint32_t)((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16u;   // < 2^31: 63 rows of 65536 heads
     }
 #pragma unroll
-    for (int i = 0; i < W::kValBytes / 16 / kDecThreads; ++i) {
+    for (int i = 0; i < kValLoads; ++i) {
       const int f = i * kDecThreads + threadIdx.x, r = f / (DV / 8);
-      at_load_lds<false>(v_lds + (uint32_t)(st * W::kValBytes + i * kDecThreads * 16),
-                  vc + (uint64_t)(uint32_t)__shfl(slot, r) * v_row + ((f % (DV / 8)) ^ at_swz<DV>(r)) * 16);
+      voff[i] = (uint32_t)r * v_row + (uint32_t)((f % (DV / 8)) ^ at_swz<DV>(r)) * 16u;
+    }
+  }
+  auto load = [&](int slot, int st) {
+    const uint32_t kt = k_lds + (uint32_t)(st * W::kKeyBytes), vt = v_lds + (uint32_t)(st * W::kValBytes);
+    if (PAGED) {
+      const uint32_t row = (uint32_t)__builtin_amdgcn_readfirstlane(slot);
+      const at_rsrc kr = at_make_rsrc(kc + (uint64_t)row * k_row), vr = at_make_rsrc(vc + (uint64_t)row * v_row);
+#pragma unroll
+      for (int i = 0; i < kKeyLoads; ++i) at_load_lds(kt + i * kDecThreads * 16, kr, koff[i]);
+#pragma unroll
+      for (int i = 0; i < kValLoads; ++i) at_load_lds(vt + i * kDecThreads * 16, vr, voff[i]);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < kKeyLoads; ++i) {
+      const int f = i * kDecThreads + threadIdx.x, r = f / (DQ / 8);
+      at_load_lds<false>(kt + i * kDecThreads * 16,
+                         kc + (uint64_t)(uint32_t)__shfl(slot, r) * k_row + ((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < kValLoads; ++i) {
+      const int f = i * kDecThreads + threadIdx.x, r = f / (DV / 8);
+      at_load_lds<false>(vt + i * kDecThreads * 16,
+                         vc + (uint64_t)(uint32_t)__shfl(slot, r) * v_row + ((f % (DV / 8)) ^ at_swz<DV>(r)) * 16);
     }
   };
   load(cache_row(a, entry(0), key_of(0)), 0);
@@ -309,7 +336,8 @@ __global__ __launch_bounds__(kDecThreads, 2) void attn_decode_kernel(DecodeArgs 
   if (item < p.parts_p * p.blocks_p) {
     // row blocks of one part side by side: they share the part's keys in L2
     const int part = item / p.blocks_p, block = item % p.blocks_p;
-    if (p.wide) return decode_wide<DQ, DV>(a, kvh, part, block * 128, mem);
+    if (p.wide && a.page_shift >= 6) return decode_wide<DQ, DV, true>(a, kvh, part, block * 128, mem);
+    if (p.wide) return decode_wide<DQ, DV, false>(a, kvh, part, block * 128, mem);
     Cursor<true> at;
     at.b = at.tile = 0;
     at.key0 = part * p.chunk_p;
