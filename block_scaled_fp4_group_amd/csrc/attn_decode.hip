@@ -504,20 +504,29 @@ static DecodePlan decode_plan(int64_t B, int q_heads, int kv_heads, int64_t pref
   p.blocks_p = (int32_t)up(rows, p.wide ? 128 : 32 * p.rb);
   p.blocks_s = (int32_t)up(G, 32 * p.rb);
   p.rows_s = (int32_t)std::min<int64_t>(G, 32 * p.rb);
-  // The workgroups that the chip holds at once, shared by the two kinds after
-  // their work: 64 keys take either kind about as long (2.1 us of matrix work for
-  // 128 rows, 2.6 us of a workgroup's share of the reads).  The own lengths are
-  // not known here: half of the bound is counted.
-  const int64_t tiles_p = up(prefix_len, 64), tiles_s = up(max_len, 64);
-  const int64_t work_p = kv_heads * p.blocks_p * tiles_p, work_s = up(kv_heads * p.blocks_s * B * tiles_s, 2);
-  const int64_t per_part = kv_heads * p.blocks_p;
-  const int64_t share = work_p == 0 ? 0 : kDecSlots * work_p / (work_p + work_s);
-  // parts of the prefix: at least two tiles in each
-  int64_t parts = tiles_p == 0 ? 0 : std::max<int64_t>(1, std::min(share / per_part, up(tiles_p, 2)));
+  // The workgroups that the chip holds at once are shared by the two kinds so that
+  // both end at about the same time.  64 keys of a prefix take a wide workgroup 3
+  // units where they take a narrow one 5 (1.5 us of matrix work for 128 rows, 2.7 us
+  // of its share of the reads; 128-wide heads).  The own lengths are not known here:
+  // half of the bound is counted, and each request once more for starting on it.
+  // (64 requests behind 8192 tokens: 79 us with shares by keys alone, of which the
+  // prefix's workgroups worked 39.)
+  const int64_t tiles_p = up(prefix_len, 64), tiles_s = max_len == 0 ? 0 : up(B * up(max_len, 64), 2) + B;
+  const int64_t cost_p = p.wide ? 3 : 5, cost_s = 5;
+  const int64_t per_part = kv_heads * p.blocks_p, per_run = kv_heads * p.blocks_s;
+  const int64_t work_p = per_part * tiles_p * cost_p, work_s = per_run * tiles_s * cost_s;
+  int64_t parts = 0;
+  if (tiles_p > 0) {
+    // parts of the prefix, at least two tiles in each: the share rounded down or up
+    const int64_t most = up(tiles_p, 2), room = max_len == 0 ? kDecSlots : kDecSlots - per_run;
+    parts = std::max<int64_t>(1, std::min(most, kDecSlots * work_p / (work_p + work_s) / per_part));
+    auto time = [&](int64_t n) { return std::max(up(tiles_p, n) * cost_p, work_s / std::max<int64_t>(1, kDecSlots - n * per_part)); };
+    if (parts < most && (parts + 1) * per_part <= room && time(parts + 1) < time(parts)) ++parts;
+  }
   p.chunk_p = tiles_p == 0 ? 0 : (int32_t)(up(tiles_p, parts) * 64);
   p.parts_p = tiles_p == 0 ? 0 : (int32_t)up(prefix_len, p.chunk_p);
   // runs of the own keys: the rest of the chip, at least two narrow tiles in each
-  const int64_t left = std::max<int64_t>(kDecSlots - p.parts_p * per_part, kDecSlots / 4) / (kv_heads * p.blocks_s);
+  const int64_t left = (kDecSlots - p.parts_p * per_part) / per_run;
   p.runs = max_len == 0 ? 0 : (int32_t)std::max<int64_t>(1, std::min(left, up(B * up(max_len, kNarrowKeys), 2)));
   return p;
 }
