@@ -13,8 +13,8 @@ moe_status launch_qk_norm_rope(const moe_heads&, const moe_heads&, const moe_hea
                                const moe_heads*, const moe_kv_cache*, const int32_t*, hipStream_t);
 moe_status launch_attn_prompt(const moe_heads&, const moe_heads&, const moe_heads&, const int32_t*, const int32_t*, int,
                               int64_t, int64_t, const moe_attn_params&, const moe_heads&, float*, hipStream_t);
-size_t attn_decode_ws_bytes(int64_t, int, int, int, int64_t, int64_t);
-int64_t attn_decode_grid(int64_t, int, int, int64_t, int64_t);
+size_t attn_decode_ws_bytes(int64_t, int, int, int, int, int64_t, int64_t);
+int64_t attn_decode_grid(int64_t, int, int, int, int, int64_t, int64_t);
 moe_status launch_attn_decode(const moe_heads&, const moe_kv_cache&, const int32_t*, int64_t, const int32_t*, int64_t,
                               int64_t, const int32_t*, int64_t, const moe_attn_params&, const moe_heads&, float*, void*,
                               hipStream_t);
@@ -174,9 +174,9 @@ moe_status moe_attn_prompt(const moe_heads* q, const moe_heads* k, const moe_hea
 size_t moe_attn_decode_workspace_bytes(int32_t num_requests, int64_t prefix_len, int64_t max_len,
                                        const moe_attn_params* p) {
   if (!p || num_requests <= 0 || prefix_len < 0 || max_len < 0 || p->kv_heads < 1 || p->q_heads < p->kv_heads ||
-      p->q_heads % p->kv_heads != 0 || p->v_dim < 1)
+      p->q_heads % p->kv_heads != 0 || p->k_dim < 1 || p->v_dim < 1)
     return 0;
-  return attn_decode_ws_bytes(num_requests, p->q_heads, p->kv_heads, p->v_dim, prefix_len, max_len);
+  return attn_decode_ws_bytes(num_requests, p->q_heads, p->kv_heads, p->k_dim, p->v_dim, prefix_len, max_len);
 }
 
 moe_status moe_attn_decode(const moe_heads* q, const moe_kv_cache* cache, const int32_t* block_table,
@@ -204,10 +204,10 @@ moe_status moe_attn_decode(const moe_heads* q, const moe_kv_cache* cache, const 
   MOE_CHECK(max_len <= 0x7fffffff - 64 && prefix_len <= 0x7fffffff - 64 && num_requests * ((max_len + 31) / 32) < 0x7fffffff,
             "%s: too many keys", fn);
   MOE_CHECK(aligned4(lse), "%s: lse not 4-byte aligned", fn);
-  MOE_CHECK(attn_decode_grid(num_requests, p->q_heads, p->kv_heads, prefix_len, max_len) < ((int64_t)1 << 31) &&
+  MOE_CHECK(attn_decode_grid(num_requests, p->q_heads, p->kv_heads, p->k_dim, p->v_dim, prefix_len, max_len) < ((int64_t)1 << 31) &&
                 (int64_t)num_requests * p->q_heads < ((int64_t)1 << 31),
             "%s: too many rows", fn);
-  const size_t need = attn_decode_ws_bytes(num_requests, p->q_heads, p->kv_heads, p->v_dim, prefix_len, max_len);
+  const size_t need = attn_decode_ws_bytes(num_requests, p->q_heads, p->kv_heads, p->k_dim, p->v_dim, prefix_len, max_len);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))) {
     set_error("%s: workspace %zu bytes < %zu (or NULL / unaligned)", fn, workspace_bytes, need);
     return MOE_ERR_WORKSPACE;

@@ -47,6 +47,7 @@ __device__ __forceinline__ void take_turns(int t) {
 }
 
 struct DecodePlan {
+  int32_t small;                                    // no parts, the rest is 0
   int32_t wide;                                     // prefix workgroups are wide
   int32_t parts_p, chunk_p;                         // parts of the prefix, keys in each
   int32_t blocks_p;                                 // row blocks of B * G rows (wide 128, narrow 32 rb)
@@ -511,10 +512,136 @@ __global__ __launch_bounds__(WPR <= 4 ? 256 : WPR * 64) void attn_join_kernel(De
   if (a.lse && lane == 0) a.lse[at_row] = L == 0.0f ? neg_inf() : (M + __builtin_amdgcn_logf(L)) * kLn2;
 }
 
-static DecodePlan decode_plan(int64_t B, int q_heads, int kv_heads, int64_t prefix_len, int64_t max_len) {
-  DecodePlan p;
+// Few keys: a workgroup per request and key head answers alone, without parts and
+// a second launch.  Its eight waves take every eighth tile of 32 keys, prefix first,
+// each through registers into its own LDS, the next tile's loads under way while
+// one is computed on; then the waves' sums are joined.  Every request reads the
+// prefix for itself (from L2 after the first).  At most 16 heads of a key head.
+constexpr int kSmallWaves = 8;
+
+template <int DQ, int DV>
+__global__ __launch_bounds__(kSmallWaves * 64) void attn_decode_small_kernel(DecodeArgs a) {
+  using W = AttnWave16<DQ, DV, 1>;
+  constexpr int kRegion = W::kKeyBytes + W::kValBytes, kOut = DV + 4;             // floats of a row of sums (padded: banks)
+  constexpr int kKeyLoads = W::kKeyBytes / 1024, kValLoads = W::kValBytes / 1024;  // 16 bytes per lane
+  static_assert(16 * kOut * 4 + 16 * 8 <= kRegion, "a wave's sums fit its region");
+  __shared__ __attribute__((aligned(16))) uint8_t mem[kSmallWaves * kRegion];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kvh = blockIdx.x % (uint32_t)a.kv_heads, b = blockIdx.x / (uint32_t)a.kv_heads, G = a.q_heads / a.kv_heads;
+  const int len = len_at(a, b), prefix = (int)a.prefix_len;
+  const int tiles_p = tiles_of(prefix), n_tiles = tiles_p + tiles_of(len);
+  const int32_t* own = a.table + b * a.table_stride;
+  auto base_of = [&](int t) { return (t < tiles_p ? t : t - tiles_p) * kNarrowKeys; };
+  auto end_of = [&](int t) { return t < tiles_p ? prefix : len; };
+  // lane's row of tile t (past the end: the last key's)
+  auto slot_of = [&](int t) {
+    const int key = min(base_of(t) + (lane & 31), end_of(t) - 1);
+    return cache_row(a, (t < tiles_p ? a.prefix_table : own)[key >> a.page_shift], key);
+  };
+  const uint8_t* kc = (const uint8_t*)(a.k_cache + (int64_t)kvh * DQ);
+  const uint8_t* vc = (const uint8_t*)(a.v_cache + (int64_t)kvh * DV);
+  const uint32_t k_row = (uint32_t)a.kv_heads * DQ * 2, v_row = (uint32_t)a.kv_heads * DV * 2;
+  u32x4 kr[kKeyLoads], vr[kValLoads];
+  auto load = [&](int slot) {
+#pragma unroll
+    for (int i = 0; i < kKeyLoads; ++i) {
+      const int f = i * 64 + lane, r = f / (DQ / 8);
+      kr[i] = *(const u32x4*)(kc + (uint64_t)(uint32_t)__shfl(slot, r) * k_row + ((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < kValLoads; ++i) {
+      const int f = i * 64 + lane, r = f / (DV / 8);
+      vr[i] = *(const u32x4*)(vc + (uint64_t)(uint32_t)__shfl(slot, r) * v_row + ((f % (DV / 8)) ^ at_swz<DV>(r)) * 16);
+    }
+  };
+  uint8_t* ks = mem + wv * kRegion;
+  uint8_t* vs = ks + W::kKeyBytes;
+  int t = wv, next = 0;
+  W w;
+  w.init(0, a.q + b * a.q_ts + (int64_t)(kvh * G + min(lane & 15, G - 1)) * a.q_hs, lane);
+  if (t < n_tiles) {
+    const int slot = slot_of(t);
+    if (t + kSmallWaves < n_tiles) next = slot_of(t + kSmallWaves);
+    load(slot);
+  }
+  w.offsets(lane);
+  for (; t < n_tiles; t += kSmallWaves) {
+    const int last = end_of(t) - 1 - base_of(t);
+#pragma unroll
+    for (int i = 0; i < kKeyLoads; ++i) *(u32x4*)(ks + (i * 64 + lane) * 16) = kr[i];
+#pragma unroll
+    for (int i = 0; i < kValLoads; ++i) {
+      // (a weight of 0 times an infinity past the end would not be 0)
+      const bool there = (i * 64 + lane) / (DV / 8) <= last;
+      *(u32x4*)(vs + (i * 64 + lane) * 16) = there ? vr[i] : u32x4{0u, 0u, 0u, 0u};
+    }
+    asm volatile("" ::: "memory");                                  // (a wave's own LDS accesses stay in order)
+    if (t + kSmallWaves < n_tiles) {
+      load(next);
+      if (t + 2 * kSmallWaves < n_tiles) next = slot_of(t + 2 * kSmallWaves);
+    }
+    w.scores(ks);
+    if (last < kNarrowKeys - 1) w.mask(lane, last);
+    w.weights(a.c);
+    w.values(vs);
+    asm volatile("" ::: "memory");
+  }
+  // each wave's sums, maxima and weight sums into its region; joined by 4 columns per thread
+  float* po = (float*)ks;
+#pragma unroll
+  for (int x = 0; x < W::OB; ++x) *(f32x4*)(po + (lane & 15) * kOut + 16 * x + 4 * (lane >> 4)) = w.o[0][x];
+  if (lane < 16) ((float2*)(po + 16 * kOut))[lane] = float2{w.m[0], w.l[0]};
+  __syncthreads();
+  const int row = threadIdx.x / (DV / 4), col = threadIdx.x % (DV / 4) * 4;
+  if (row >= G) return;
+  float2 ml[kSmallWaves];
+  float M = neg_inf(), L = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kSmallWaves; ++i) {
+    ml[i] = ((const float2*)((const float*)(mem + i * kRegion) + 16 * kOut))[row];
+    M = fmaxf(M, ml[i].x);
+  }
+  const float ref = M == neg_inf() ? 0.0f : M;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kSmallWaves; ++i) {
+    const float e = __builtin_amdgcn_exp2f(ml[i].x - ref);
+    const f32x4 o = *(const f32x4*)((const float*)(mem + i * kRegion) + row * kOut + col);
+    L = fmaf(e, ml[i].y, L);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] = fmaf(e, o[j], sum[j]);
+  }
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  const int hq = kvh * G + row;
+  *(u32x2*)(a.out + b * a.o_ts + hq * a.o_hs + col) =
+      u32x2{cvt_bf16x2(sum[0] * inv, sum[1] * inv), cvt_bf16x2(sum[2] * inv, sum[3] * inv)};
+  if (a.lse && col == 0) a.lse[(int64_t)b * a.q_heads + hq] = L == 0.0f ? neg_inf() : (M + __builtin_amdgcn_logf(L)) * kLn2;
+}
+
+// Whether one workgroup per request and key head is sooner done than parts and
+// their join, in nanoseconds as measured (128-wide heads; others by their bytes).
+// Small: 3500, and 220 for each tile of 32 keys of the longest request, prefix
+// included, in as many rounds as the chip needs at a workgroup per CU; or the
+// reading of the own keys (half of the bound) at a little under the parts' rate.
+// Parts: 10000 for two launches, and the reading of all keys once.
+// Own keys up to 512, 32 requests of 8 key heads: 8 us for 16; 2000 behind a prefix
+// of 2000: 33 for 24.  Within 5% of the better one in 9 of 10 of 216 sizes tried, 1
+// to 96 requests with 16 to 2048 own keys.
+static bool small_is_sooner(int64_t B, int64_t G, int64_t kv_heads, int64_t prefix_len, int64_t max_len, int64_t dims) {
+  if (G > 16) return false;
+  const int64_t tiles_p = (prefix_len + 31) / 32, tiles_s = (max_len + 31) / 32, rounds = (B * kv_heads + 255) / 256;
+  if (tiles_p + tiles_s > 1024) return false;                       // (the products below stay small)
+  const int64_t own = 3 * kv_heads * B * tiles_s / 2 * dims / 256, prefix = 3 * kv_heads * tiles_p * dims / 256;
+  const int64_t small = 3500 + std::max(220 * (tiles_p + tiles_s) * rounds * dims / 256, own + own / 7);
+  return small < 10000 + own + prefix;
+}
+
+static DecodePlan decode_plan(int64_t B, int q_heads, int kv_heads, int64_t prefix_len, int64_t max_len, int dims) {
+  DecodePlan p = {};
   const int64_t G = q_heads / kv_heads, rows = B * G;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  p.small = small_is_sooner(B, G, kv_heads, prefix_len, max_len, dims);
+  if (p.small) return p;
   p.wide = rows > 64;
   p.rb = G > 32 || (!p.wide && rows > 32) ? 2 : 1;
   p.blocks_p = (int32_t)up(rows, p.wide ? 128 : 32 * p.rb);
@@ -557,8 +684,8 @@ static int64_t plan_entries(const DecodePlan& p, int64_t B, int q_heads, int kv_
          (p.runs > 0 ? (int64_t)kv_heads * p.blocks_s * (p.runs + B) * 2 * p.rows_s : 0);
 }
 
-size_t attn_decode_ws_bytes(int64_t B, int q_heads, int kv_heads, int v_dim, int64_t prefix_len, int64_t max_len) {
-  const DecodePlan p = decode_plan(B, q_heads, kv_heads, prefix_len, max_len);
+size_t attn_decode_ws_bytes(int64_t B, int q_heads, int kv_heads, int k_dim, int v_dim, int64_t prefix_len, int64_t max_len) {
+  const DecodePlan p = decode_plan(B, q_heads, kv_heads, prefix_len, max_len, k_dim + v_dim);
   const int64_t entries = plan_entries(p, B, q_heads, kv_heads);
   return entries == 0 ? 0 : (size_t)entries * ((size_t)v_dim * 4 + 8) + ((size_t)B + 1) * 4;
 }
@@ -567,12 +694,18 @@ static int64_t plan_grid(const DecodePlan& p, int kv_heads) {
   return ((int64_t)p.parts_p * p.blocks_p + (int64_t)p.runs * p.blocks_s) * kv_heads;
 }
 
-int64_t attn_decode_grid(int64_t B, int q_heads, int kv_heads, int64_t prefix_len, int64_t max_len) {
-  return plan_grid(decode_plan(B, q_heads, kv_heads, prefix_len, max_len), kv_heads);
+int64_t attn_decode_grid(int64_t B, int q_heads, int kv_heads, int k_dim, int v_dim, int64_t prefix_len, int64_t max_len) {
+  const DecodePlan p = decode_plan(B, q_heads, kv_heads, prefix_len, max_len, k_dim + v_dim);
+  return p.small ? B * kv_heads : plan_grid(p, kv_heads);
 }
 
 template <int DQ, int DV>
 static void launch_decode(const DecodeArgs& a, hipStream_t stream) {
+  if (a.plan.small) {
+    hipLaunchKernelGGL((attn_decode_small_kernel<DQ, DV>), dim3((uint32_t)(a.num_requests * a.kv_heads)), dim3(kSmallWaves * 64), 0,
+                       stream, a);
+    return;
+  }
   const uint32_t grid = (uint32_t)plan_grid(a.plan, a.kv_heads);
   if (grid > 0) {
     if (a.plan.rb == 1) hipLaunchKernelGGL((attn_decode_kernel<DQ, DV, 1>), dim3(grid), dim3(kDecThreads), 0, stream, a);
@@ -613,7 +746,7 @@ moe_status launch_attn_decode(const moe_heads& q, const moe_kv_cache& cache, con
   a.num_pages = (int32_t)cache.num_pages;
   a.page_shift = __builtin_ctz((unsigned)cache.page_size);
   a.c = p.scale * kLog2e;
-  a.plan = decode_plan(B, p.q_heads, p.kv_heads, prefix_len, max_len);
+  a.plan = decode_plan(B, p.q_heads, p.kv_heads, prefix_len, max_len, p.k_dim + p.v_dim);
   const int64_t entries = plan_entries(a.plan, B, p.q_heads, p.kv_heads);
   a.part_o = (float*)ws;                            // (the sums first: they need 16-byte alignment)
   a.part_ml = (float2*)(a.part_o + entries * p.v_dim);

@@ -94,10 +94,11 @@ def test_attn_decode_refuses():
                dict(out=heads(8, 128, hs=64)), dict(lse=ctypes.c_void_p(0x10001))):
         refuses(decode(**kw), INVALID)
     refuses(decode(D=192, Dv=192), UNSUPPORTED)
-    need = moe.attn_decode_workspace_bytes(4, 40, 100, 8, 2, 128, 128)
+    assert moe.attn_decode_workspace_bytes(4, 40, 100, 8, 2, 128, 128) == 0     # few keys: no parts to join
+    need = moe.attn_decode_workspace_bytes(4, 40, 4000, 8, 2, 128, 128)
     assert need > 0
     for kw in (dict(ws=None), dict(nbytes=need - 1), dict(ws=ODD)):
-        refuses(decode(**kw), WORKSPACE)
+        refuses(decode(most=4000, blocks=256, stride=256, **kw), WORKSPACE)
     refuses(decode(B=0), OK)
 
 

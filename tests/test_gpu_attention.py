@@ -641,3 +641,106 @@ def test_slots_and_rope_other_stream_and_graph():
         torch.cuda.synchronize()
         assert torch.equal(qc, qd) and torch.equal(kc, kd), i
         assert all(torch.equal(x, y) for x, y in zip(c[:3], d[:3])) and all(torch.equal(x, y) for x, y in zip(c[3], d[3])), i
+
+
+# ----------------------------------------------- many keys: parts that are joined
+def makes_parts(lens, prefix, Hq, Hkv, D, Dv):
+    return moe.attn_decode_workspace_bytes(len(lens), prefix, max(lens), Hq, Hkv, D, Dv) > 0
+
+
+@pytest.mark.parametrize("D,Dv", HEADS)
+@pytest.mark.parametrize("lens,prefix,page,Hq,Hkv", [
+    ([5, 0, 33], 2901, 16, 4, 2), ([0, 0], 2985, 4, 8, 2), ([17] * 9, 3000, 16, 16, 2), ([70, 9], 2930, 128, 40, 1),
+    ([2] * 40, 2857, 64, 2, 2), ([130, 2, 0], 2945, 64, 5, 1), ([700, 1, 513], 2900, 16, 2, 1), ([3500, 0, 33, 1], 0, 32, 8, 2),
+    ([2900, 3100, 2999], 0, 1024, 4, 4), ([64] * 12, 2816, 64, 12, 2), ([31] * 12, 2823, 32, 12, 2)])
+def test_attn_decode_parts(D, Dv, lens, prefix, page, Hq, Hkv):
+    """Parts and runs that end inside a tile, a page or a request; few rows and many, small pages and large."""
+    what = f"attn_decode {D}/{Dv} lens={lens[:4]} prefix={prefix} page={page} heads {Hq}/{Hkv}"
+    say(what)
+    assert makes_parts(lens, prefix, Hq, Hkv, D, Dv)
+    *_, ref, _, _ = run_decode(len(lens) * 17 + prefix + D, lens, prefix, page, Hq, Hkv, D, Dv)
+    check_decode(*ref, what)
+
+
+@pytest.mark.parametrize("B,page", [(2, 16), (3, 64), (20, 16), (20, 64)])
+def test_attn_decode_parts_past_the_end(B, page):
+    """As test_attn_decode_places_past_the_end, where parts are joined."""
+    say(f"attn_decode parts: infinities behind the last key, {B} requests, pages of {page}")
+    D, lens, prefix = 128, [40 + b for b in range(B)], 3075
+    assert makes_parts(lens, prefix, 16, 1, D, D)
+    kb, vb, table, ptab, blocks = paged(90 + B, lens, prefix, page, 1, D, D)
+    q = dev_bf16(synth.random_bf16(81, (B, 16, D)))
+    v, k = dev_bf16(vb), dev_bf16(kb)
+    args = (dev_i32(table), dev_i32(np.array(lens)), max(lens), dev_i32(ptab), prefix)
+    ref, rl = moe.attn_decode(q, k, v, *args, want_lse=True)
+    k2, v2 = k.clone(), v.clone()
+    k2[torch.isnan(k)], v2[torch.isnan(v)] = float("inf"), float("inf")
+    out, lse = moe.attn_decode(q, k2, v2, *args, want_lse=True)
+    torch.cuda.synchronize()
+    assert torch.isfinite(ref.float()).all() and torch.equal(out, ref) and torch.equal(lse, rl)
+    v[ptab[(prefix - 1) // page], (prefix - 1) % page, 0, 7] = float("inf")
+    last = lens[-1] - 1
+    v[table[B - 1][last // page], last % page, 0, 21] = -float("inf")
+    out, lse = moe.attn_decode(q, k, v, *args, want_lse=True)
+    torch.cuda.synchronize()
+    assert (out[:, :, 7] == float("inf")).all() and (out[-1, :, 21] == -float("inf")).all()
+    rest = [i for i in range(D) if i not in (7, 21)]
+    assert torch.equal(out[..., rest], ref[..., rest]) and torch.equal(out[:-1, :, 21], ref[:-1, :, 21])
+    assert torch.equal(lse, rl)
+
+
+def test_attn_decode_parts_bounds_and_bad_entries():
+    """max_len over and under the lengths, and table entries outside the cache, where parts are joined."""
+    lens = [3100, 0, 2037]
+    _, _, ref, _, _ = run_decode(9, lens, 20, 16, 4, 2, 128, 128, max_len=194 * 16)
+    check_decode(*ref, "attn_decode max_len over the lengths, parts")
+    args, pt, _, out, _ = run_decode(9, lens, 20, 16, 4, 2, 128, 128)
+    assert makes_parts([2837] * 3, 20, 4, 2, 128, 128)
+    short, _ = moe.attn_decode(*args[:5], 2837, prefix_table=pt, prefix_len=20)
+    cut, _ = moe.attn_decode(*args[:4], dev_i32(np.array([2837, 0, 2037])), 2837, prefix_table=pt, prefix_len=20)
+    t = args[3].clone()
+    t[0, 5], t[0, 150] = 1 << 30, -(1 << 30)
+    bad, _ = moe.attn_decode(*args[:3], t, *args[4:], prefix_table=pt, prefix_len=20)
+    torch.cuda.synchronize()
+    assert torch.equal(short, cut) and torch.equal(bad[2], out[2])
+
+
+def test_attn_decode_parts_far_rows():
+    """As test_attn_decode_far_rows with every page many times, so that parts are joined."""
+    page, Hkv, D, times = 64, 8, 128, 30
+    pages = (1 << 32) // (page * Hkv * D * 2) + 40
+    say("attn_decode parts: rows past 2^32 bytes")
+    k = torch.empty((pages, page, Hkv, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty((pages, page, Hkv, D), dtype=torch.bfloat16, device="cuda")
+    far = [pages - 1, pages - 7, pages - 20, 3]
+    kb, vb = synth.random_bf16(50, (4, page, Hkv, D)), synth.random_bf16(51, (4, page, Hkv, D))
+    for i, p in enumerate(far):
+        k[p], v[p] = dev_bf16(kb[i]), dev_bf16(vb[i])
+    for B in (1, 40):                                                # few rows and many to a key head
+        q = dev_bf16(synth.random_bf16(52, (B, 16, D)))
+        n = 3 * page * times - 42
+        rows = lambda t: dev_i32(np.array([t * times] * B))  # noqa: E731
+        lens = dev_i32(np.array([n] * B))
+        assert moe.attn_decode_workspace_bytes(B, 4 * page * times - 14, n, 16, Hkv, D, D) > 0
+        a, _ = moe.attn_decode(q, k, v, rows(far[1:]), lens, n, dev_i32(np.array(far * times)), 4 * page * times - 14)
+        b, _ = moe.attn_decode(q, dev_bf16(kb), dev_bf16(vb), rows([1, 2, 3]), lens, n,
+                               dev_i32(np.array([0, 1, 2, 3] * times)), 4 * page * times - 14)
+        torch.cuda.synchronize()
+        assert torch.equal(a, b), B
+
+
+def test_attn_decode_alone_equals_parts():
+    """A request's answer where one workgroup gives it and where parts are joined: the rounding of the weights apart."""
+    say("attn_decode: one workgroup against parts")
+    lens, prefix = [300, 7, 120], 200
+    args, pt, _, small, sl = run_decode(33, lens, prefix, 16, 8, 2, 128, 128)
+    assert not makes_parts(lens, prefix, 8, 2, 128, 128)
+    # the same requests among others that need parts
+    wide = torch.zeros((3, 200), dtype=torch.int32, device="cuda")
+    wide[:, :args[3].shape[1]] = args[3]
+    assert moe.attn_decode_workspace_bytes(3, prefix, 3200, 8, 2, 128, 128) > 0
+    parts, pl = moe.attn_decode(*args[:3], wide, args[4], 3200, prefix_table=pt, prefix_len=prefix, want_lse=True)
+    torch.cuda.synchronize()
+    np.testing.assert_allclose(host(sl), host(pl), rtol=0, atol=2e-6)
+    big = args[2][~torch.isnan(args[2])].float().abs().max()
+    assert (small.float() - parts.float()).abs().max() <= 4 * R * big
