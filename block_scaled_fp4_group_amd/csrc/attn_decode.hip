@@ -10,6 +10,9 @@
 // weight sum in float; a second kernel joins the parts of a row:
 //   M = max m_i,  out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 //
+// With few keys one workgroup per request and key head does it all instead
+// (attn_decode_small_kernel below).
+//
 // Workgroups of four waves walk the keys in tiles through LDS stages that all
 // waves fill (direct loads; every lane finds its rows through the block table)
 // while another is computed on:
@@ -22,6 +25,11 @@
 // list, across as many requests as it covers, without emptying its load pipeline
 // at more than the requests' ends.  All workgroups of a launch fit the chip at
 // once, so the wide ones' matrix work and the narrow ones' reads run side by side.
+//
+// Measured: one request with 131072 own keys x 32/8 heads x 128: 83 us and 6 for the
+// join, 6.5 TB/s of the 6.9 that contiguous reads reach; 96 requests behind 32768
+// keys x 64/4 x 192: 145 to 150 us in all, 0.88 PFLOP/s; 64 behind 8192 with 69511
+// own keys x 64/8 x 128: 71 to 73 us, 318 MB at 4.4 TB/s beside 17 GFLOP of prefix.
 #include <algorithm>
 
 #include "attn_common.h"

@@ -10,7 +10,17 @@
 // m % G of token m / G.  A workgroup takes 128 such rows, 32 per wave
 // (attn_common.h), and walks the keys in tiles of 64 through LDS.  Its rows span
 // only 128 / G tokens: all waves end at about the same key, and little is computed
-// beyond the diagonal (against 128 tokens of one head: see the figures below).
+// beyond the diagonal (against 128 tokens of one head: 32 prompts of 21 to 2048 tokens
+// 195 -> 188 us, 3 of up to 3500 with context 448 -> 425 us).
+//
+// Bound by the matrix cores' power budget where the keys are many: 16384 tokens x
+// 32/4 heads x 128 take 1.98 to 2.02 ms = 1.1 PFLOP/s, matrix units busy 61% of the
+// cycles at the 1.7 GHz that the chip then runs at (a library's 8192^3 product
+// reaches 1.25 PFLOP/s).  With two tile loops per CU in opposite phases the cycles
+// fell by a tenth, and the clock with them.  Where the keys are few a workgroup
+// costs 7 us beside its 1.7 us per tile -- 0.7 to find its rows, 3 until the first
+// tile is there, 1.7 to store, 2 until the next one starts --, which the two on a
+// CU hide in part: the 32 prompts above take 170 us, 740 TFLOP/s.
 #include "attn_common.h"
 
 namespace moe {
@@ -96,6 +106,7 @@ __device__ __forceinline__ PromptTile prompt_tile(const PromptArgs& a, int vt, i
 // The rows of workgroup `block`, this is its thread `thread`.  Whether some result
 // is not finite; in that case the workgroup's rows have to be done again,
 // CAREFUL: a value that is infinite or NaN reaches the rows that see it only.
+// (Testing the values of each masked tile beforehand took half as long as the tile.)
 template <int DQ, int DV, bool CAREFUL>
 __device__ __forceinline__ bool prompt_rows(const PromptArgs& a, uint32_t block, uint32_t thread, uint8_t* ks, uint8_t* vs) {
   using W = AttnWave<DQ, DV, kPromptKeys / 32>;
@@ -190,7 +201,8 @@ __device__ __forceinline__ bool prompt_rows(const PromptArgs& a, uint32_t block,
     if (CAREFUL) w.tile_careful(k, v, lane, a.c, pos - t * kPromptKeys);
     else w.tile_masked(k, v, lane, a.c, pos - t * kPromptKeys);
   }
-  // The results go through LDS, so that stores write whole rows: 16-byte chunk c
+  // The results go through LDS, so that stores write whole rows (2.6 us of a
+  // workgroup's time as 8-byte pieces, 1.6 us so): 16-byte chunk c
   // of row r lies at chunk c ^ r of the stage that is not the last tile's (everyone
   // is done with it and no load is under way there), a quarter per wave.
   constexpr int CH = DV / 8;

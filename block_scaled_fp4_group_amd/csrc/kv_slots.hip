@@ -13,6 +13,9 @@
 // waits for another.  A new page is looked up in the free list, never read back
 // from the table, and the table's old entries are never written, so the update
 // in place needs no order between workgroups.
+//
+// Bound by latency: 64 requests of one token take 4.0 us, 1500 requests with
+// 140792 new tokens 8.7 us (1.2 MB written); an empty launch takes about 2.
 #include "common.h"
 
 namespace moe {

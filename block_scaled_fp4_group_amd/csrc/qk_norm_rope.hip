@@ -7,7 +7,9 @@
 // values also go to their cache rows.  Everything is float until the one
 // rounding to bf16 of each output.
 //
-// Memory traffic is all there is (a few operations per value).  A lane owns the
+// Memory traffic is all there is (a few operations per value): 8191 tokens x 64/4
+// heads x 192 read and write 459 MB in 96 us, 4.8 TB/s where a large copy reaches
+// 5.1; 64 tokens x 32/8 x 128 take 3.5 us, a launch's latency.  A lane owns the
 // 8 elements at e and the 8 at e + half of the rotated part (or of the rest), so
 // both members of every pair of either kind sit in one lane, loads and stores
 // are 16 bytes, and only the sum of squares crosses lanes.

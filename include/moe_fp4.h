@@ -540,7 +540,8 @@ moe_status moe_attn_prompt(const moe_heads* q, const moe_heads* k, const moe_hea
  *   reaches and that is not one of them gives an unspecified result).
  * workspace: moe_attn_decode_workspace_bytes() bytes for the same sizes, 16-byte
  * aligned (may be NULL when that is 0); calls that share one must not overlap.
- * One or two launches.  num_requests == 0 is a no-op.
+ * One launch with few keys (the workspace is 0 bytes then), else one or two.
+ * num_requests == 0 is a no-op.
  */
 size_t moe_attn_decode_workspace_bytes(int32_t num_requests, int64_t prefix_len, int64_t max_len,
                                        const moe_attn_params* p);
