@@ -28,7 +28,8 @@ EXPORTS = ("moe_status_string", "moe_last_error", "moe_version", "moe_route", "m
            "moe_permute", "moe_route_permute", "moe_fp4_grouped_gemm", "moe_combine", "fp4_transcode_mx_to_nv", "moe_quantize_nvfp4",
            "moe_fp4_tile_weights", "moe_route_permute_noalloc", "moe_quantize_mxfp8", "moe_quantize_nvfp4_planes",
            "moe_route_gemv_workspace_bytes", "moe_route_gemv", "moe_reap_saliency_accumulate", "moe_fp4_compact_mx",
-           "moe_kv_slots", "moe_qk_norm_rope", "moe_attn_prompt", "moe_attn_decode_workspace_bytes", "moe_attn_decode")
+           "moe_kv_slots", "moe_qk_norm_rope", "moe_attn_prompt_workspace_bytes",
+           "moe_attn_prompt", "moe_attn_decode_workspace_bytes", "moe_attn_decode")
 
 
 class RouteParams(ctypes.Structure):
@@ -124,7 +125,10 @@ def _load() -> ctypes.CDLL:
     lib.moe_qk_norm_rope.argtypes = [heads, heads, heads, i64, ctypes.POINTER(RopeParams), vp, vp, vp, vp, heads, heads,
                                      cache, vp, vp]
     lib.moe_attn_prompt.restype = i32
-    lib.moe_attn_prompt.argtypes = [heads, heads, heads, vp, vp, i32, i64, i64, ctypes.POINTER(AttnParams), heads, vp, vp]
+    lib.moe_attn_prompt.argtypes = [heads, heads, heads, vp, vp, i32, i64, i64, ctypes.POINTER(AttnParams), heads, vp, vp,
+                                    ctypes.c_size_t, vp]
+    lib.moe_attn_prompt_workspace_bytes.restype = ctypes.c_size_t
+    lib.moe_attn_prompt_workspace_bytes.argtypes = [i32, i64, i64, ctypes.POINTER(AttnParams)]
     lib.moe_attn_decode_workspace_bytes.restype = sz
     lib.moe_attn_decode_workspace_bytes.argtypes = [i32, i64, i64, ctypes.POINTER(AttnParams)]
     lib.moe_attn_decode.restype = i32
@@ -497,6 +501,19 @@ def _cache(k_cache, v_cache, index: int, kv_heads: int, k_dim: int) -> KvCache:
     return KvCache(k, v, pages, page)
 
 
+def _workspace(workspace, like, index: int, query, *sizes):
+    """(tensor, the tensor if it was made here, its address, its bytes) of a workspace that was given or is needed."""
+    made = None
+    if workspace is None:
+        need = query(*sizes)
+        if not need:
+            return None, None, None, 0
+        workspace = made = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor")
+    return workspace, made, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _at(stream, index: int, *made) -> int:
     """The stream to launch on.  Tensors made here belong to the current stream; their use on another one has to be
     known to the allocator."""
@@ -601,7 +618,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
 
 def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
                 cu_k: Optional[torch.Tensor] = None, scale: Optional[float] = None, out=None, lse=None,
-                want_lse: bool = False, stream=None):
+                want_lse: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
     """Causal attention over packed prompts: q [Tq, Hq, D], k [Tk, Hkv, D], v [Tk, Hkv, Dv], offsets cu_q, cu_k int32
     [B + 1] (cu_k None: cu_q).  Query i of a sequence sees keys 0 .. i + Lk - Lq.  -> (out [Tq, Hq, Dv], lse float32
     [Tq, Hq] or None).  Rows outside the offsets' ranges are not written."""
@@ -617,6 +634,9 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     n = cu_q.numel()
     if n < 1 or cu_k.numel() != n:
         raise ValueError("cu_q and cu_k must have an entry for each sequence and the end")
+    p = AttnParams(Hq, Hkv, D, Dv, D ** -0.5 if scale is None else scale)
+    workspace, made_w, ws, nbytes = _workspace(workspace, q, dev, lib.moe_attn_prompt_workspace_bytes, n - 1, Tq, Tk, p) \
+        if workspace is not None or Tk >= 512 * (n - 1) else (None, None, None, 0)     # (0 bytes with fewer keys)
     made_o = made_l = None
     if out is None:
         out = made_o = q.new_empty((Tq, Hq, Dv))
@@ -631,11 +651,17 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     elif want_lse:
         lse = made_l = q.new_empty((Tq, Hq), dtype=_F32)
         pl = lse.data_ptr()
-    st = lib.moe_attn_prompt(hq, hk, hv, cq, ck, n - 1, Tq, Tk, AttnParams(Hq, Hkv, D, Dv, D ** -0.5 if scale is None else scale),
-                             ho, pl, _at(stream, dev, made_o, made_l))
+    st = lib.moe_attn_prompt(hq, hk, hv, cq, ck, n - 1, Tq, Tk, p, ho, pl, ws, nbytes,
+                             _at(stream, dev, made_w, made_o, made_l))
     if st:
         _check(st, "moe_attn_prompt")
     return out, lse
+
+
+def attn_prompt_workspace_bytes(num_seqs: int, total_q: int, total_k: int, q_heads: int, kv_heads: int, k_dim: int,
+                                v_dim: int) -> int:
+    p = AttnParams(q_heads, kv_heads, k_dim, v_dim, 1.0)
+    return int(lib.moe_attn_prompt_workspace_bytes(num_seqs, total_q, total_k, p))
 
 
 def attn_decode_workspace_bytes(num_requests: int, prefix_len: int, max_len: int, q_heads: int, kv_heads: int, k_dim: int,
@@ -666,16 +692,8 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
     if prefix_table is not None:
         pt, pn = _flat(prefix_table, "prefix_table", _I32, 1, dev), prefix_table.numel()
     p = AttnParams(Hq, Hkv, D, Dv, D ** -0.5 if scale is None else scale)
-    made_w = made_o = made_l = ws = None
-    nbytes = 0
-    if workspace is None:
-        need = lib.moe_attn_decode_workspace_bytes(B, prefix_len, max_len, p)
-        if need:
-            workspace = made_w = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous GPU tensor")
-    if workspace is not None:
-        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    workspace, made_w, ws, nbytes = _workspace(workspace, q, dev, lib.moe_attn_decode_workspace_bytes, B, prefix_len, max_len, p)
+    made_o = made_l = None
     if out is None:
         out = made_o = q.new_empty((B, Hq, Dv))
         ho = Heads(out.data_ptr(), Hq * Dv, Dv)

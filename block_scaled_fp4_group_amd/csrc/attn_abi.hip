@@ -12,7 +12,8 @@ moe_status launch_qk_norm_rope(const moe_heads&, const moe_heads&, const moe_hea
                                const int32_t*, const float*, const float*, const float*, const moe_heads&,
                                const moe_heads*, const moe_kv_cache*, const int32_t*, hipStream_t);
 moe_status launch_attn_prompt(const moe_heads&, const moe_heads&, const moe_heads&, const int32_t*, const int32_t*, int,
-                              int64_t, int64_t, const moe_attn_params&, const moe_heads&, float*, hipStream_t);
+                              int64_t, int64_t, const moe_attn_params&, const moe_heads&, float*, void*, hipStream_t);
+size_t attn_prompt_ws_bytes(int64_t, int64_t, int64_t, const moe_attn_params&);
 size_t attn_decode_ws_bytes(int64_t, int, int, int, int, int64_t, int64_t);
 int64_t attn_decode_grid(int64_t, int, int, int, int, int64_t, int64_t);
 moe_status launch_attn_decode(const moe_heads&, const moe_kv_cache&, const int32_t*, int64_t, const int32_t*, int64_t,
@@ -140,9 +141,21 @@ moe_status moe_qk_norm_rope(const moe_heads* q, const moe_heads* k, const moe_he
                              stream);
 }
 
+// what both workspace queries need of the parameters
+static bool sizes_of_heads(const moe_attn_params* p) {
+  return p && p->kv_heads >= 1 && p->q_heads >= p->kv_heads && p->q_heads <= 65536 && p->q_heads % p->kv_heads == 0 &&
+         p->k_dim >= 1 && p->k_dim <= 1024 && p->v_dim >= 1 && p->v_dim <= 1024;
+}
+
+size_t moe_attn_prompt_workspace_bytes(int32_t num_seqs, int64_t total_q, int64_t total_k, const moe_attn_params* p) {
+  if (!sizes_of_heads(p) || num_seqs <= 0 || total_q <= 0 || total_k <= 0 || total_q > 0x7fffffff || total_k > 0x7fffffff) return 0;
+  return attn_prompt_ws_bytes(total_q, total_k, num_seqs, *p);
+}
+
 moe_status moe_attn_prompt(const moe_heads* q, const moe_heads* k, const moe_heads* v, const int32_t* cu_q,
                            const int32_t* cu_k, int32_t num_seqs, int64_t total_q, int64_t total_k,
-                           const moe_attn_params* p, const moe_heads* out, float* lse, hipStream_t stream) {
+                           const moe_attn_params* p, const moe_heads* out, float* lse, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
   const char* fn = "moe_attn_prompt";
   set_error("");
   MOE_PASS(check_attn(fn, p));
@@ -166,15 +179,19 @@ moe_status moe_attn_prompt(const moe_heads* q, const moe_heads* k, const moe_hea
   MOE_CHECK(total_q * (p->q_heads / p->kv_heads) <= 0x7fffffff - 1024 - num_seqs &&
                 (total_q * p->q_heads / 128 + (int64_t)num_seqs * p->kv_heads) < ((int64_t)1 << 31),
             "%s: too many rows", fn);
+  const size_t need = attn_prompt_ws_bytes(total_q, total_k, num_seqs, *p);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))) {
+    set_error("%s: workspace %zu bytes < %zu (or NULL / unaligned)", fn, workspace_bytes, need);
+    return MOE_ERR_WORKSPACE;
+  }
   static const moe_heads none = {nullptr, 0, 0};
   return launch_attn_prompt(*q, total_k > 0 ? *k : none, total_k > 0 ? *v : none, cu_q, cu_k, num_seqs, total_q, total_k,
-                            *p, *out, lse, stream);
+                            *p, *out, lse, workspace, stream);
 }
 
 size_t moe_attn_decode_workspace_bytes(int32_t num_requests, int64_t prefix_len, int64_t max_len,
                                        const moe_attn_params* p) {
-  if (!p || num_requests <= 0 || prefix_len < 0 || max_len < 0 || p->kv_heads < 1 || p->q_heads < p->kv_heads ||
-      p->q_heads % p->kv_heads != 0 || p->k_dim < 1 || p->v_dim < 1)
+  if (!sizes_of_heads(p) || num_requests <= 0 || prefix_len < 0 || max_len < 0 || prefix_len > 0x7fffffff || max_len > 0x7fffffff)
     return 0;
   return attn_decode_ws_bytes(num_requests, p->q_heads, p->kv_heads, p->k_dim, p->v_dim, prefix_len, max_len);
 }

@@ -21,6 +21,12 @@
 // costs 7 us beside its 1.7 us per tile -- 0.7 to find its rows, 3 until the first
 // tile is there, 1.7 to store, 2 until the next one starts --, which the two on a
 // CU hide in part: the 32 prompts above take 170 us, 740 TFLOP/s.
+//
+// Few rows with many keys (a short addition to a long context) would leave most of
+// the chip idle: their keys are split over several workgroups, whose float sums,
+// maxima and weight sums a second launch joins (prompt_splits).
+#include <algorithm>
+
 #include "attn_common.h"
 
 namespace moe {
@@ -43,6 +49,10 @@ struct PromptArgs {
   uint32_t g_mul;     // n / G = n * g_mul >> 32 + g_shift, see div_g
   int32_t g_shift;
   float c;            // scale * log2(e)
+  // SPLIT: part s of row r (token * q_heads + head) is entry r * splits + s
+  float* part_o;      // [entries][DV]
+  float2* part_ml;    // [entries]: maximum (base 2), weight sum
+  int32_t splits;
 };
 
 // n / G for 0 <= n < 2^31: with 2^(s - 1) < G <= 2^s and g_mul = ceil(2^(31 + s) / G),
@@ -107,7 +117,9 @@ __device__ __forceinline__ PromptTile prompt_tile(const PromptArgs& a, int vt, i
 // is not finite; in that case the workgroup's rows have to be done again,
 // CAREFUL: a value that is infinite or NaN reaches the rows that see it only.
 // (Testing the values of each masked tile beforehand took half as long as the tile.)
-template <int DQ, int DV, bool CAREFUL>
+// SPLIT: one of `splits` workgroups for the same rows, an equal run of their tiles
+// of keys each.
+template <int DQ, int DV, bool CAREFUL, bool SPLIT>
 __device__ __forceinline__ bool prompt_rows(const PromptArgs& a, uint32_t block, uint32_t thread, uint8_t* ks, uint8_t* vs) {
   using W = AttnWave<DQ, DV, kPromptKeys / 32>;
   constexpr int kThreads = kPromptThreads;
@@ -116,7 +128,9 @@ __device__ __forceinline__ bool prompt_rows(const PromptArgs& a, uint32_t block,
   // head's workgroups meet in few L2s
   const int G = a.q_heads / a.kv_heads;
   const int kvh = block % (uint32_t)a.kv_heads;
-  const PromptTile T = prompt_tile(a, (int)(block / (uint32_t)a.kv_heads), G, lane);
+  const uint32_t item = block / (uint32_t)a.kv_heads;
+  const int part = SPLIT ? (int)(item % (uint32_t)a.splits) : 0;
+  const PromptTile T = prompt_tile(a, (int)(SPLIT ? item / (uint32_t)a.splits : item), G, lane);
   if (T.row0 >= T.rows) return false;
   const int wrow = T.row0 + wv * 32, m = min(wrow + (lane & 31), T.rows - 1);       // rows past the end repeat the last
   const int row = div_g(a, m), hq = kvh * G + m - row * G;
@@ -163,12 +177,14 @@ __device__ __forceinline__ bool prompt_rows(const PromptArgs& a, uint32_t block,
       for (int i = 0; i < kValLoads; ++i) at_load_lds(vt + i * kThreads * 16, vr, v_off(i, end));
     }
   };
-  const int n_tiles = (n_keys + kPromptKeys - 1) / kPromptKeys;
+  const int all_tiles = (n_keys + kPromptKeys - 1) / kPromptKeys;
+  const int run = SPLIT ? (all_tiles + a.splits - 1) / a.splits : all_tiles;
+  const int t0 = SPLIT ? min(part * run, all_tiles) : 0, n_tiles = SPLIT ? min(t0 + run, all_tiles) : all_tiles;
   // tiles that every row of the workgroup sees whole come first; for the others
   // (around the diagonal) each wave looks whether it sees any of it at all
   const int n_whole = max(0, min(n_tiles, all_see / kPromptKeys));
   auto seen = [&](int t) { return t * kPromptKeys <= wave_last; };
-  if (n_tiles > 0) load(0, 0);                                      // under way while the queries are read
+  if (n_tiles > t0) load(t0, 0);                                    // under way while the queries are read
   W w;
   w.init(a.q + (int64_t)(T.q0 + row) * a.q_ts + hq * a.q_hs, lane);
   // tile t has landed, and everyone is done with tile t - 1, whose stage the next
@@ -178,7 +194,7 @@ __device__ __forceinline__ bool prompt_rows(const PromptArgs& a, uint32_t block,
     if (t + 1 < n_tiles) load(t + 1, st ^ 1);
   };
   const bool real = wrow < T.rows;                                  // some row of this wave is
-  int t = 0;
+  int t = t0;
   if (!CAREFUL) {
     auto step = [&](auto stage, int tile) {
       constexpr int st = decltype(stage)::value;
@@ -193,7 +209,7 @@ __device__ __forceinline__ bool prompt_rows(const PromptArgs& a, uint32_t block,
   // (a last odd whole tile goes with the others)
 #pragma unroll 1
   for (; t < n_tiles; ++t) {
-    const int st = t & 1;
+    const int st = (t - t0) & 1;
     begin(t, st);
     if (!real || !seen(t)) continue;
     const uint8_t* k = ks + st * W::kKeyBytes;
@@ -206,42 +222,61 @@ __device__ __forceinline__ bool prompt_rows(const PromptArgs& a, uint32_t block,
   // of row r lies at chunk c ^ r of the stage that is not the last tile's (everyone
   // is done with it and no load is under way there), a quarter per wave.
   constexpr int CH = DV / 8;
-  const int idle = n_tiles & 1;
+  const int idle = (n_tiles - t0) & 1;
   uint8_t* rows = (wv < 2 ? ks + idle * W::kKeyBytes : vs + idle * W::kValBytes) + (wv & 1) * (32 * DV * 2);
-  const float inv = w.l == 0.0f ? 0.0f : 1.0f / w.l;
   float odd = 0.0f;                                                 // NaN once some result is not finite
+  if (SPLIT) {
+    if (wrow + (lane & 31) < T.rows) {
+      const int64_t entry = ((int64_t)(T.q0 + row) * a.q_heads + hq) * a.splits + part;
+      float* po = a.part_o + entry * DV + 4 * h;
 #pragma unroll
-  for (int b = 0; b < W::OB; ++b)
+      for (int b = 0; b < W::OB; ++b)
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      float y[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        y[j] = w.o[b][4 * i + j] * inv;
-        if (!CAREFUL) odd = fmaf(y[j], 0.0f, odd);
-      }
-      u32x4 v;
-#pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        // the halves of the wave hold 4 columns each of groups i and i + 1 of 8; each gets one group
-        const auto x = __builtin_amdgcn_permlane32_swap(cvt_bf16x2(y[j], y[j + 1]), cvt_bf16x2(y[4 + j], y[5 + j]), false, false);
-        v[j / 2] = x[0];
-        v[2 + j / 2] = x[1];
-      }
-      const int r = lane & 31, c = 4 * b + i + h;
-      *(u32x4*)(rows + r * (DV * 2) + ((c ^ (r & (CH - 1))) * 16)) = v;
+        for (int i = 0; i < 4; ++i)
+          *(f32x4*)(po + 32 * b + 8 * i) = f32x4{w.o[b][4 * i], w.o[b][4 * i + 1], w.o[b][4 * i + 2], w.o[b][4 * i + 3]};
+      if (h == 0) a.part_ml[entry] = float2{w.m, w.l};
     }
-  asm volatile("" ::: "memory");                                    // (a wave's own LDS accesses stay in order)
-  const int64_t at = (int64_t)(T.q0 + row) * a.o_ts + hq * a.o_hs;
+    if (!CAREFUL) {
 #pragma unroll
-  for (int i = 0; i < 32 * CH / 64; ++i) {
-    const int r = (i * 64 + lane) / CH, c = lane % CH;
-    const u32x4 v = *(const u32x4*)(rows + r * (DV * 2) + ((c ^ (r & (CH - 1))) * 16));
-    const int64_t to = (int64_t)__shfl((long long)at, r);
-    if (wrow + r < T.rows) *(u32x4*)(a.out + to + c * 8) = v;
+      for (int b = 0; b < W::OB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) odd = fmaf(w.o[b][i], 0.0f, odd);
+    }
+  } else {
+    const float inv = w.l == 0.0f ? 0.0f : 1.0f / w.l;
+#pragma unroll
+    for (int b = 0; b < W::OB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          y[j] = w.o[b][4 * i + j] * inv;
+          if (!CAREFUL) odd = fmaf(y[j], 0.0f, odd);
+        }
+        u32x4 v;
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          // the halves of the wave hold 4 columns each of groups i and i + 1 of 8; each gets one group
+          const auto x = __builtin_amdgcn_permlane32_swap(cvt_bf16x2(y[j], y[j + 1]), cvt_bf16x2(y[4 + j], y[5 + j]), false, false);
+          v[j / 2] = x[0];
+          v[2 + j / 2] = x[1];
+        }
+        const int r = lane & 31, c = 4 * b + i + h;
+        *(u32x4*)(rows + r * (DV * 2) + ((c ^ (r & (CH - 1))) * 16)) = v;
+      }
+    asm volatile("" ::: "memory");                                    // (a wave's own LDS accesses stay in order)
+    const int64_t at = (int64_t)(T.q0 + row) * a.o_ts + hq * a.o_hs;
+#pragma unroll
+    for (int i = 0; i < 32 * CH / 64; ++i) {
+      const int r = (i * 64 + lane) / CH, c = lane % CH;
+      const u32x4 v = *(const u32x4*)(rows + r * (DV * 2) + ((c ^ (r & (CH - 1))) * 16));
+      const int64_t to = (int64_t)__shfl((long long)at, r);
+      if (wrow + r < T.rows) *(u32x4*)(a.out + to + c * 8) = v;
+    }
+    if (a.lse && h == 0 && wrow + (lane & 31) < T.rows)
+      a.lse[(int64_t)(T.q0 + row) * a.q_heads + hq] = w.l == 0.0f ? neg_inf() : (w.m + __builtin_amdgcn_logf(w.l)) * kLn2;
   }
-  if (a.lse && h == 0 && wrow + (lane & 31) < T.rows)
-    a.lse[(int64_t)(T.q0 + row) * a.q_heads + hq] = w.l == 0.0f ? neg_inf() : (w.m + __builtin_amdgcn_logf(w.l)) * kLn2;
   if (CAREFUL) return false;
   // each wave's word, in its quarter of the idle stage
   if (lane == 0) *(int*)rows = 0;
@@ -253,30 +288,116 @@ __device__ __forceinline__ bool prompt_rows(const PromptArgs& a, uint32_t block,
   return any != 0;
 }
 
-template <int DQ, int DV>
+template <int DQ, int DV, bool SPLIT>
 __global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptArgs a) {
   using W = AttnWave<DQ, DV, kPromptKeys / 32>;
   __shared__ __attribute__((aligned(16))) uint8_t ks[2 * W::kKeyBytes];
   __shared__ __attribute__((aligned(16))) uint8_t vs[2 * W::kValBytes];
   uint32_t block = blockIdx.x, thread = threadIdx.x;
-  if (!prompt_rows<DQ, DV, false>(a, block, thread, ks, vs)) return;
+  if (!prompt_rows<DQ, DV, false, SPLIT>(a, block, thread, ks, vs)) return;
   // (opaque copies: nothing of the first run is kept in registers for this one)
   asm volatile("" : "+s"(block));
   asm volatile("" : "+v"(thread));
   at_wait_barrier<0>();                                             // everyone has read the words; their stage is refilled
-  prompt_rows<DQ, DV, true>(a, block, thread, ks, vs);
+  prompt_rows<DQ, DV, true, SPLIT>(a, block, thread, ks, vs);
+}
+
+// The parts of the rows joined, a wave per row: M = max m_s, then
+// out = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s.  At most 64 parts, lane s weighs
+// part s.  Rows outside the sequences are left alone.
+template <int DV>
+__global__ __launch_bounds__(256) void attn_prompt_join_kernel(PromptArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t r = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t token = r / a.q_heads;
+  const int hq = (int)(r % a.q_heads);
+  if (token < min(max(a.cu_q[0], 0), a.total_q) || token >= min(max(a.cu_q[a.num_seqs], 0), a.total_q)) return;
+  constexpr int E = DV / 64;                                        // values per lane
+  float2 x = float2{neg_inf(), 0.0f};
+  if (lane < a.splits) x = a.part_ml[r * a.splits + lane];
+  float M = x.x;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor(M, d));
+  const float e = __builtin_amdgcn_exp2f(x.x - (M == neg_inf() ? 0.0f : M));
+  float L = x.y * e, o[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) L += __shfl_xor(L, d);
+  const float* src = a.part_o + r * a.splits * DV + lane * E;
+  for (int s0 = 0; s0 < a.splits; s0 += 8) {                        // 8 loads in flight
+    float y[8][2];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float* p = src + (int64_t)min(s0 + u, a.splits - 1) * DV;
+      y[u][0] = p[0];
+      if (E == 2) y[u][1] = p[1];
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (s0 + u >= a.splits) break;
+      const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e), s0 + u));
+      o[0] = fmaf(w, y[u][0], o[0]);
+      if (E == 2) o[1] = fmaf(w, y[u][1], o[1]);
+    }
+  }
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  uint16_t* dst = a.out + token * a.o_ts + hq * a.o_hs + lane * E;
+  if (E == 2) *(uint32_t*)dst = cvt_bf16x2(o[0] * inv, o[1] * inv);
+  else *dst = (uint16_t)f32_to_bf16_bits(o[0] * inv);
+  if (a.lse && lane == 0) a.lse[r] = L == 0.0f ? neg_inf() : (M + __builtin_amdgcn_logf(L)) * kLn2;
+}
+
+static int64_t prompt_tiles(int64_t total_q, int64_t G, int64_t num_seqs) { return total_q * G / kPromptRows + num_seqs; }
+
+// Workgroups that share a tile of rows.  The lengths are not known here: the average
+// number of keys counts, in tiles.  A tile takes 1.0 us (128-wide heads) while there
+// is a workgroup per CU at most and 1.7 with two; parts cost 6 us for the second
+// launch and their floats written and read at 4 TB/s.  16 tokens on 4096 keys x 32/8
+// x 128: 14 us for 71 unsplit; 128 on 8192: 39 for 135; 512 on 8192: 93 for 140.
+// Never with less than 512 keys on average, which the callers may rely on.
+static int prompt_splits(int64_t total_q, int64_t total_k, int64_t num_seqs, int64_t q_heads, int64_t kv_heads, int64_t k_dim,
+                         int64_t v_dim) {
+  if (num_seqs <= 0 || total_q <= 0 || total_k < 512 * num_seqs) return 1;
+  const int64_t groups = prompt_tiles(total_q, q_heads / kv_heads, num_seqs) * kv_heads;
+  if (groups > 256) return 1;
+  const int64_t n = (total_k / num_seqs + kPromptKeys - 1) / kPromptKeys, unit = (k_dim + v_dim) * 1000 / 256;   // ns
+  const int64_t part = total_q * q_heads * (v_dim * 4 + 8) / 2000;   // ns
+  int best = 1;
+  int64_t least = unit * n;
+  const int64_t most = std::min<int64_t>(std::min<int64_t>(64, 512 / groups), n / 2);
+  for (int64_t s = 2; s <= most; ++s) {
+    const int64_t time = (groups * s <= 256 ? unit : unit * 17 / 10) * ((n + s - 1) / s) + 6000 + s * part;
+    if (time < least) {
+      least = time;
+      best = (int)s;
+    }
+  }
+  return best;
+}
+
+size_t attn_prompt_ws_bytes(int64_t total_q, int64_t total_k, int64_t num_seqs, const moe_attn_params& p) {
+  const int s = prompt_splits(total_q, total_k, num_seqs, p.q_heads, p.kv_heads, p.k_dim, p.v_dim);
+  return s == 1 ? 0 : (size_t)(total_q * p.q_heads * s) * ((size_t)p.v_dim * 4 + 8);
 }
 
 template <int DQ, int DV>
 static void launch_prompt(const PromptArgs& a, hipStream_t stream) {
-  const int64_t tiles = (int64_t)a.total_q * (a.q_heads / a.kv_heads) / kPromptRows + a.num_seqs;
-  hipLaunchKernelGGL((attn_prompt_kernel<DQ, DV>), dim3((uint32_t)(tiles * a.kv_heads)), dim3(kPromptThreads), 0, stream, a);
+  const int64_t groups = prompt_tiles(a.total_q, a.q_heads / a.kv_heads, a.num_seqs) * a.kv_heads;
+  if (a.splits == 1) {
+    hipLaunchKernelGGL((attn_prompt_kernel<DQ, DV, false>), dim3((uint32_t)groups), dim3(kPromptThreads), 0, stream, a);
+    return;
+  }
+  hipLaunchKernelGGL((attn_prompt_kernel<DQ, DV, true>), dim3((uint32_t)(groups * a.splits)), dim3(kPromptThreads), 0, stream, a);
+  hipLaunchKernelGGL((attn_prompt_join_kernel<DV>), dim3((uint32_t)(((int64_t)a.total_q * a.q_heads + 3) / 4)), dim3(256), 0,
+                     stream, a);
 }
 
 moe_status launch_attn_prompt(const moe_heads& q, const moe_heads& k, const moe_heads& v, const int32_t* cu_q,
                               const int32_t* cu_k, int num_seqs, int64_t total_q, int64_t total_k,
-                              const moe_attn_params& p, const moe_heads& out, float* lse, hipStream_t stream) {
+                              const moe_attn_params& p, const moe_heads& out, float* lse, void* ws, hipStream_t stream) {
   PromptArgs a;
+  a.splits = prompt_splits(total_q, total_k, num_seqs, p.q_heads, p.kv_heads, p.k_dim, p.v_dim);
+  a.part_o = (float*)ws;
+  a.part_ml = (float2*)(a.part_o + total_q * p.q_heads * a.splits * p.v_dim);
   a.q = (const uint16_t*)q.data;
   a.q_ts = q.token_stride;
   a.q_hs = q.head_stride;

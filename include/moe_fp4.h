@@ -519,11 +519,16 @@ typedef struct {
  *   (rows outside the ranges keep their values; entries are clamped to them);
  *   lse float [total_q, q_heads] or NULL.
  * Token strides of k and v up to 2^23 elements (else MOE_ERR_UNSUPPORTED).
- * num_seqs == 0 or total_q == 0 is a no-op.  One launch.
+ * workspace: moe_attn_prompt_workspace_bytes() bytes for the same sizes, 16-byte
+ * aligned (may be NULL when that is 0, as it is whenever total_k < 512 * num_seqs);
+ * calls that share one must not overlap.
+ * num_seqs == 0 or total_q == 0 is a no-op.  One launch; two with a workspace.
  */
+size_t moe_attn_prompt_workspace_bytes(int32_t num_seqs, int64_t total_q, int64_t total_k, const moe_attn_params* p);
 moe_status moe_attn_prompt(const moe_heads* q, const moe_heads* k, const moe_heads* v, const int32_t* cu_q,
                            const int32_t* cu_k, int32_t num_seqs, int64_t total_q, int64_t total_k,
-                           const moe_attn_params* p, const moe_heads* out, float* lse, hipStream_t stream);
+                           const moe_attn_params* p, const moe_heads* out, float* lse, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------ attention of single tokens, shared prefix
  * One query per request over a paged cache (row b of q and out: request b).

@@ -60,10 +60,11 @@ def test_qk_norm_rope_refuses():
     refuses(rope(T=0), OK)
 
 
-def prompt(seqs=2, tq=8, tk=8, q=None, k=None, out=None, cu=P, lse=None, hq=4, hkv=2, D=128, Dv=128, scale=0.1):
+def prompt(seqs=2, tq=8, tk=8, q=None, k=None, out=None, cu=P, lse=None, hq=4, hkv=2, D=128, Dv=128, scale=0.1,
+           ws=None, nbytes=0):
     p = moe.AttnParams(hq, hkv, D, Dv, scale)
     return moe.lib.moe_attn_prompt(heads(hq, D) if q is None else q, heads(hkv, D) if k is None else k, heads(hkv, Dv), cu, P,
-                                   seqs, tq, tk, p, heads(hq, Dv) if out is None else out, lse, None)
+                                   seqs, tq, tk, p, heads(hq, Dv) if out is None else out, lse, ws, nbytes, None)
 
 
 def test_attn_prompt_refuses():
@@ -75,6 +76,10 @@ def test_attn_prompt_refuses():
     for D, Dv in ((96, 96), (128, 64), (192, 192), (256, 256)):
         refuses(prompt(D=D, Dv=Dv), UNSUPPORTED)
     refuses(prompt(k=heads(2, 128, ts=(1 << 23) + 8)), UNSUPPORTED)
+    need = moe.attn_prompt_workspace_bytes(2, 8, 8000, 4, 2, 128, 128)
+    assert need > 0                                                  # few rows, many keys: parts to join
+    for kw in (dict(), dict(ws=P, nbytes=need - 1), dict(ws=ODD, nbytes=need)):
+        refuses(prompt(tk=8000, **kw), WORKSPACE)
     refuses(prompt(seqs=0), OK)
     refuses(prompt(tq=0), OK)
 
@@ -107,6 +112,10 @@ def test_workspace_size():
     assert f(0, 40, 100, 8, 2, 128, 128) == 0 and f(4, -1, 100, 8, 2, 128, 128) == 0 and f(4, 40, 100, 7, 2, 128, 128) == 0
     assert f(1, 0, 0, 8, 2, 128, 128) == 0                          # nothing to join
     assert f(1, 0, 131072, 32, 8, 128, 128) > 0
+    g = moe.attn_prompt_workspace_bytes
+    assert g(0, 8, 8000, 4, 2, 128, 128) == 0 and g(2, 8, 8000, 5, 2, 128, 128) == 0 and g(2, 0, 8000, 4, 2, 128, 128) == 0
+    assert g(16, 64, 512 * 16 - 1, 4, 2, 128, 128) == 0             # under 512 keys each: never
+    assert g(1, 16384, 16384, 32, 4, 128, 128) == 0                 # rows for the whole chip
 
 
 def test_python_wrappers_refuse_before_the_library():

@@ -744,3 +744,79 @@ def test_attn_decode_alone_equals_parts():
     np.testing.assert_allclose(host(sl), host(pl), rtol=0, atol=2e-6)
     big = args[2][~torch.isnan(args[2])].float().abs().max()
     assert (small.float() - parts.float()).abs().max() <= 4 * R * big
+
+
+# ----------------------------------------------- prompts of few rows and many keys: keys split, parts joined
+@pytest.mark.parametrize("D,Dv", HEADS)
+@pytest.mark.parametrize("lq,lk,Hq,Hkv", [
+    ([1], [1500], 1, 1), ([16], [2100], 4, 2), ([3, 0, 40], [2000, 700, 1345], 4, 1), ([33, 2], [65, 3900], 5, 1),
+    ([200], [1999], 2, 2), ([1, 1, 1, 1], [700, 3000, 0, 1], 8, 2), ([64], [4097], 3, 1), ([50, 9], [40, 2500], 2, 1)])
+def test_attn_prompt_split_keys(D, Dv, lq, lk, Hq, Hkv):
+    """Runs of keys that end before the diagonal, in it, or see nothing; rows without keys."""
+    what = f"attn_prompt {D}/{Dv} lq={lq} lk={lk} heads {Hq}/{Hkv}, split"
+    say(what)
+    # (3701 keys of four sequences are too few on average to split for the smallest heads)
+    assert moe.attn_prompt_workspace_bytes(len(lq), sum(lq), sum(lk), Hq, Hkv, D, Dv) > 0 or (D == 64 and len(lq) == 4)
+    r = run_prompt(len(lq) * 37 + lq[0] + D, lq, lk, Hq, Hkv, D, Dv)
+    check_prompt(*r[:5], D ** -0.5, *r[5:], what)
+
+
+def test_attn_prompt_split_masked_places_and_other_rows():
+    """Infinities and NaN in values and keys reach the rows that see them alone; rows outside the sequences stay."""
+    say("attn_prompt split: not finite values, rows outside")
+    cu_q, cu_k = np.array([3, 40, 60]), np.array([0, 1800, 3100])
+    qb, kb, vb = synth.random_bf16(70, (70, 4, 128)), synth.random_bf16(71, (3100, 2, 128)), synth.random_bf16(72, (3100, 2, 128))
+    q, k, v = dev_bf16(qb), dev_bf16(kb), dev_bf16(vb)
+    args = (dev_i32(cu_q), dev_i32(cu_k))
+    assert moe.attn_prompt_workspace_bytes(2, 70, 3100, 4, 2, 128, 128) > 0
+
+    def call(q, k, v):
+        out = torch.full((70, 4, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((70, 4), 5.0, device="cuda")
+        moe.attn_prompt(q, k, v, *args, out=out, lse=lse)
+        torch.cuda.synchronize()
+        return out, lse
+
+    ref, rl = call(q, k, v)
+    assert (ref[:3] == 3).all() and (ref[60:] == 3).all() and (rl[:3] == 5).all() and (rl[60:] == 5).all()
+    assert torch.isfinite(ref.float()).all() and torch.isfinite(rl).all()
+    where = 1780                                                     # rows 20 .. 36 of the first sequence see it
+    for which, value in ((1, float("nan")), (2, float("nan")), (2, float("inf")), (2, -float("inf"))):
+        t = [q, k.clone(), v.clone()]
+        t[which][where, 1, 5] = value
+        out, lse = call(*t)
+        row = 3 + where - (1800 - 37)
+        same = lambda a, b: torch.equal(a.contiguous().view(torch.int16), b.contiguous().view(torch.int16))  # noqa: E731
+        assert same(out[:row], ref[:row]) and same(out[40:], ref[40:]) and same(out[:, :2], ref[:, :2]), (which, value)
+        if which == 2:
+            hit = out[row:40, 2:, 5].float()
+            assert (torch.isnan(hit) if value != value else hit == value).all()
+            rest = [i for i in range(128) if i != 5]
+            assert same(out[..., rest], ref[..., rest]) and torch.equal(lse, rl)
+        else:
+            assert torch.isnan(out[row:40, 2:].float()).all()
+
+
+def test_attn_prompt_split_stream_graph_and_workspace():
+    say("attn_prompt split: repeated, on another stream, in a graph, with a workspace that is given")
+    cu_q, cu_k = dev_i32(np.array([0, 20, 33])), dev_i32(np.array([0, 2500, 4000]))
+    q, k, v = (dev_bf16(synth.random_bf16(60 + i, (n, h, 128))) for i, (n, h) in enumerate(((33, 8), (4000, 2), (4000, 2))))
+    ref, rl = moe.attn_prompt(q, k, v, cu_q, cu_k, want_lse=True)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out, lse = moe.attn_prompt(q, k, v, cu_q, cu_k, want_lse=True, stream=s)
+    s.synchronize()
+    assert torch.equal(out, ref) and torch.equal(lse, rl)
+    ws = torch.full((moe.attn_prompt_workspace_bytes(2, 33, 4000, 8, 2, 128, 128),), 0xFF, dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.attn_prompt(q, k, v, cu_q, cu_k, out=out, lse=lse, workspace=ws)
+    for i in range(3):
+        out.zero_()
+        ws.fill_(0xFF)
+        q.mul_(1.5 if i else 1.0)
+        g.replay()
+        eager, el = moe.attn_prompt(q, k, v, cu_q, cu_k, want_lse=True)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager) and torch.equal(lse, el), i
