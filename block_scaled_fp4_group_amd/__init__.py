@@ -1,7 +1,9 @@
 """Python binding of the gfx950 MoE-FP4 C ABI (``include/moe_fp4.h``).
 
 Argument marshalling only: every step of the layer runs in the HIP library
-``libmoefp4.so``; torch provides device memory and the current stream.  If the
+``libmoefp4.so``; torch provides device memory and the current stream.  The
+routed layer's calls go through ctypes, the attention calls through the
+extension ``_calls``.  If the
 library is missing the import fails loudly -- there is no CPU fallback.
 """
 from __future__ import annotations
@@ -430,13 +432,8 @@ def quantize_nvfp4_planes(x: torch.Tensor, input_scale: float = 1.0, planes=None
 
 
 # ----------------------------------------------------------------- attention
-# (The decode step's calls run in a few microseconds on the GPU, so the checks
-# here are written to cost little: a wrong argument is described in the slow path.)
-_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
+# kv_slots, qk_norm_rope, attn_prompt and attn_decode are in _calls (csrc/calls.cpp):
+# their kernels run in a few microseconds, and so do their checks there.
 def _bad(t, name: str, dtype, ndim: int, index: int):
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
@@ -444,218 +441,6 @@ def _bad(t, name: str, dtype, ndim: int, index: int):
         raise ValueError(f"{name} must be a GPU tensor")
     raise ValueError(f"{name} must be a {ndim}-d {dtype} tensor on cuda:{index}, its last dimension contiguous (got "
                      f"{tuple(t.shape)}, strides {t.stride()}, {t.dtype}, {t.device})")
-
-
-def _gpu(t, name: str) -> int:
-    """The tensor's device index."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    return t.get_device()
-
-
-def _flat(t, name: str, dtype, ndim: int, index: int) -> int:
-    """Address of a contiguous tensor."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index or t.dim() != ndim \
-            or not t.is_contiguous():
-        _bad(t, name, dtype, ndim, index)
-    return t.data_ptr()
-
-
-def _table(t, name: str, rows: int, index: int):
-    """(address, row stride, columns) of an int32 table whose rows are contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.get_device() != index or t.dim() != 2:
-        _bad(t, name, _I32, 2, index)
-    n, cols = t.shape
-    if n < rows:
-        raise ValueError(f"{name} needs a row for each of {rows} requests")
-    rs, cs = t.stride()
-    if cols > 1 and cs != 1:
-        _bad(t, name, _I32, 2, index)
-    return t.data_ptr(), rs if n > 1 else cols, cols
-
-
-def _heads(t, name: str, index: int, tokens=None, heads=None, dim=None) -> Heads:
-    """bf16 [tokens, heads, dim], any token and head strides, dim contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != index or t.dim() != 3:
-        _bad(t, name, _BF16, 3, index)
-    T, H, D = t.shape
-    ts, hs, ds = t.stride()
-    if ds != 1 and D > 1:
-        _bad(t, name, _BF16, 3, index)
-    if (tokens is not None and T != tokens) or (heads is not None and H != heads) or (dim is not None and D != dim):
-        raise ValueError(f"{name}: shape {(T, H, D)} does not fit (tokens {tokens}, heads {heads}, dim {dim})")
-    # the strides of dimensions of one element say nothing
-    if H == 1:
-        hs = D
-    if T == 1:
-        ts = (H - 1) * hs + D
-    return Heads(t.data_ptr(), ts, hs)
-
-
-def _cache(k_cache, v_cache, index: int, kv_heads: int, k_dim: int) -> KvCache:
-    k, v = _flat(k_cache, "k_cache", _BF16, 4, index), _flat(v_cache, "v_cache", _BF16, 4, index)
-    pages, page, heads, dim = k_cache.shape
-    if heads != kv_heads or dim != k_dim or v_cache.shape[:3] != (pages, page, heads):
-        raise ValueError(f"k_cache {tuple(k_cache.shape)} / v_cache {tuple(v_cache.shape)} do not fit "
-                         f"(pages, page_size, {kv_heads}, {k_dim})")
-    return KvCache(k, v, pages, page)
-
-
-def _workspace(workspace, like, index: int, query, *sizes):
-    """(tensor, the tensor if it was made here, its address, its bytes) of a workspace that was given or is needed."""
-    made = None
-    if workspace is None:
-        need = query(*sizes)
-        if not need:
-            return None, None, None, 0
-        workspace = made = torch.empty(need, dtype=torch.uint8, device=like.device)
-    elif workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous GPU tensor")
-    return workspace, made, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def _at(stream, index: int, *made) -> int:
-    """The stream to launch on.  Tensors made here belong to the current stream; their use on another one has to be
-    known to the allocator."""
-    if stream is None:
-        return _raw_stream(index)
-    for t in made:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream
-
-
-def kv_slots(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
-             page_size: int, max_new: int, position_base: int = 0, slots=None, positions=None, cu_new=None, counts=None,
-             stream=None):
-    """Cache slots of a step's new tokens.  int32 tensors: cached_lens, new_lens [B], free_pages [F], block_table
-    [B, blocks] (new pages are entered in place).  -> (slots [max_new], positions [max_new], cu_new [B + 1],
-    counts [3]: pages taken, pages needed, tokens without a slot).  ``position_base``: length of a shared prefix."""
-    dev = _gpu(cached_lens, "cached_lens")
-    cached, new = _flat(cached_lens, "cached_lens", _I32, 1, dev), _flat(new_lens, "new_lens", _I32, 1, dev)
-    free = _flat(free_pages, "free_pages", _I32, 1, dev)
-    B = cached_lens.numel()
-    if new_lens.numel() != B:
-        raise ValueError("cached_lens and new_lens must have an entry for each request")
-    table, stride, blocks = _table(block_table, "block_table", B, dev)
-    made = []
-
-    def output(t, name, n):
-        if t is None:
-            t = cached_lens.new_empty(n)
-            made.append(t)
-            return t, t.data_ptr()
-        address = _flat(t, name, _I32, 1, dev)
-        if t.numel() < n:
-            raise ValueError(f"{name} needs {n} elements")
-        return t, address
-
-    slots, s = output(slots, "slots", max_new)
-    positions, p = output(positions, "positions", max_new)
-    cu_new, c = output(cu_new, "cu_new", B + 1)
-    counts, n = output(counts, "counts", 3)
-    st = lib.moe_kv_slots(cached, new, B, free, free_pages.numel(), page_size, table, stride, blocks, position_base,
-                          max_new, s, p, c, n, _at(stream, dev, *made))
-    if st:
-        _check(st, "moe_kv_slots")
-    return slots, positions, cu_new, counts
-
-
-def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor],
-                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
-                 interleaved: bool = False, v: Optional[torch.Tensor] = None, k_cache: Optional[torch.Tensor] = None,
-                 v_cache: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None, want_k: bool = True,
-                 q_out=None, k_out=None, stream=None):
-    """RMS norm of each head of q [T, Hq, D] and k [T, Hkv, D] (weights float32 [D]; None: no norm), the rotation by
-    ``cos_sin`` float32 [positions, rot_dim] (cosines, then sines; None: no rotation), and with a cache the write of
-    the finished keys and of v [T, Hkv, Dv] to its rows ``slots``.  -> (q_out, k_out); k_out is None with
-    ``want_k=False`` (cache only).  q_out / k_out may be q / k."""
-    dev = _gpu(q, "q")
-    hq = _heads(q, "q", dev)
-    T, Hq, D = q.shape
-    hk = _heads(k, "k", dev, tokens=T, dim=D)
-    Hkv = k.shape[1]
-    rot = rows = 0
-    pos = table = qw = kw = at = None
-    if cos_sin is not None:
-        table, pos = _flat(cos_sin, "cos_sin", _F32, 2, dev), _flat(positions, "positions", _I32, 1, dev)
-        rows, rot = cos_sin.shape
-        if positions.numel() < T:
-            raise ValueError("positions needs an entry for each token")
-    if q_weight is not None:
-        qw = _flat(q_weight, "q_weight", _F32, 1, dev)
-    if k_weight is not None:
-        kw = _flat(k_weight, "k_weight", _F32, 1, dev)
-    if (qw is not None and q_weight.numel() != D) or (kw is not None and k_weight.numel() != D):
-        raise ValueError(f"q_weight and k_weight need {D} elements")
-    cache = hv = None
-    Dv = 0
-    if k_cache is not None:
-        cache = _cache(k_cache, v_cache, dev, Hkv, D)
-        Dv = v_cache.shape[3]
-        hv = _heads(v, "v", dev, T, Hkv, Dv)
-        at = _flat(slots, "slots", _I32, 1, dev)
-        if slots.numel() < T:
-            raise ValueError("slots needs an entry for each token")
-    made_q = made_k = None
-    if q_out is None:
-        q_out = made_q = q.new_empty((T, Hq, D))
-        ho = Heads(q_out.data_ptr(), Hq * D, D)
-    else:
-        ho = _heads(q_out, "q_out", dev, T, Hq, D)
-    hko = None
-    if k_out is not None:
-        hko = _heads(k_out, "k_out", dev, T, Hkv, D)
-    elif want_k:
-        k_out = made_k = k.new_empty((T, Hkv, D))
-        hko = Heads(k_out.data_ptr(), Hkv * D, D)
-    st = lib.moe_qk_norm_rope(hq, hk, hv, T, RopeParams(Hq, Hkv, D, Dv, rot, interleaved, rows, eps), pos, table, qw, kw,
-                              ho, hko, cache, at, _at(stream, dev, made_q, made_k))
-    if st:
-        _check(st, "moe_qk_norm_rope")
-    return q_out, k_out
-
-
-def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
-                cu_k: Optional[torch.Tensor] = None, scale: Optional[float] = None, out=None, lse=None,
-                want_lse: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
-    """Causal attention over packed prompts: q [Tq, Hq, D], k [Tk, Hkv, D], v [Tk, Hkv, Dv], offsets cu_q, cu_k int32
-    [B + 1] (cu_k None: cu_q).  Query i of a sequence sees keys 0 .. i + Lk - Lq.  -> (out [Tq, Hq, Dv], lse float32
-    [Tq, Hq] or None).  Rows outside the offsets' ranges are not written."""
-    dev = _gpu(q, "q")
-    cu_k = cu_q if cu_k is None else cu_k
-    hq = _heads(q, "q", dev)
-    Tq, Hq, D = q.shape
-    hk = _heads(k, "k", dev, dim=D)
-    Tk, Hkv, _ = k.shape
-    hv = _heads(v, "v", dev, Tk, Hkv)
-    Dv = v.shape[2]
-    cq, ck = _flat(cu_q, "cu_q", _I32, 1, dev), _flat(cu_k, "cu_k", _I32, 1, dev)
-    n = cu_q.numel()
-    if n < 1 or cu_k.numel() != n:
-        raise ValueError("cu_q and cu_k must have an entry for each sequence and the end")
-    p = AttnParams(Hq, Hkv, D, Dv, D ** -0.5 if scale is None else scale)
-    workspace, made_w, ws, nbytes = _workspace(workspace, q, dev, lib.moe_attn_prompt_workspace_bytes, n - 1, Tq, Tk, p) \
-        if workspace is not None or Tk >= 512 * (n - 1) else (None, None, None, 0)     # (0 bytes with fewer keys)
-    made_o = made_l = None
-    if out is None:
-        out = made_o = q.new_empty((Tq, Hq, Dv))
-        ho = Heads(out.data_ptr(), Hq * Dv, Dv)
-    else:
-        ho = _heads(out, "out", dev, Tq, Hq, Dv)
-    pl = None
-    if lse is not None:
-        pl = _flat(lse, "lse", _F32, 2, dev)
-        if lse.shape != (Tq, Hq):
-            raise ValueError(f"lse must be {(Tq, Hq)}")
-    elif want_lse:
-        lse = made_l = q.new_empty((Tq, Hq), dtype=_F32)
-        pl = lse.data_ptr()
-    st = lib.moe_attn_prompt(hq, hk, hv, cq, ck, n - 1, Tq, Tk, p, ho, pl, ws, nbytes,
-                             _at(stream, dev, made_w, made_o, made_l))
-    if st:
-        _check(st, "moe_attn_prompt")
-    return out, lse
 
 
 def attn_prompt_workspace_bytes(num_seqs: int, total_q: int, total_k: int, q_heads: int, kv_heads: int, k_dim: int,
@@ -670,49 +455,20 @@ def attn_decode_workspace_bytes(num_requests: int, prefix_len: int, max_len: int
     return int(lib.moe_attn_decode_workspace_bytes(num_requests, prefix_len, max_len, p))
 
 
-def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
-                lens: torch.Tensor, max_len: int, prefix_table: Optional[torch.Tensor] = None, prefix_len: int = 0,
-                scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None, out=None, lse=None,
-                want_lse: bool = False, stream=None):
-    """One query per request, q [B, Hq, D], over the paged cache: the shared prefix (``prefix_len`` keys in the pages
-    ``prefix_table``), then the request's own ``lens`` keys in its ``block_table`` pages (int32).  ``max_len``: a
-    longest own length known on the host.  -> (out [B, Hq, Dv], lse float32 [B, Hq] or None)."""
-    dev = _gpu(q, "q")
-    hq = _heads(q, "q", dev)
-    B, Hq, D = q.shape
-    if k_cache.dim() != 4 or v_cache.dim() != 4:
-        raise ValueError("k_cache and v_cache must be [pages, page_size, heads, dim]")
-    Hkv, Dv = k_cache.shape[2], v_cache.shape[3]
-    cache = _cache(k_cache, v_cache, dev, Hkv, D)
-    table, stride, blocks = _table(block_table, "block_table", B, dev)
-    ln = _flat(lens, "lens", _I32, 1, dev)
-    if lens.numel() < B:
-        raise ValueError("lens needs an entry for each request")
-    pt, pn = None, 0
-    if prefix_table is not None:
-        pt, pn = _flat(prefix_table, "prefix_table", _I32, 1, dev), prefix_table.numel()
-    p = AttnParams(Hq, Hkv, D, Dv, D ** -0.5 if scale is None else scale)
-    workspace, made_w, ws, nbytes = _workspace(workspace, q, dev, lib.moe_attn_decode_workspace_bytes, B, prefix_len, max_len, p)
-    made_o = made_l = None
-    if out is None:
-        out = made_o = q.new_empty((B, Hq, Dv))
-        ho = Heads(out.data_ptr(), Hq * Dv, Dv)
-    else:
-        ho = _heads(out, "out", dev, B, Hq, Dv)
-    pl = None
-    if lse is not None:
-        pl = _flat(lse, "lse", _F32, 2, dev)
-        if lse.shape != (B, Hq):
-            raise ValueError(f"lse must be {(B, Hq)}")
-    elif want_lse:
-        lse = made_l = q.new_empty((B, Hq), dtype=_F32)
-        pl = lse.data_ptr()
-    st = lib.moe_attn_decode(hq, cache, table, stride, blocks, ln, B, max_len, pt, pn, prefix_len, p, ho, pl, ws, nbytes,
-                             _at(stream, dev, made_w, made_o, made_l))
-    if st:
-        _check(st, "moe_attn_decode")
-    return out, lse
+def _setup_calls():
+    path = os.path.join(_PKG, "_calls.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is not built; run `python block_scaled_fp4_group_amd/build.py`")
+    from . import _calls
+    raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _calls.setup(torch.Tensor, torch.bfloat16, torch.int32, torch.float32, torch.uint8, raw_stream, _check, _bad)
+    return _calls
 
+
+_calls = _setup_calls()
+kv_slots, qk_norm_rope, attn_prompt, attn_decode = (
+    _calls.kv_slots, _calls.qk_norm_rope, _calls.attn_prompt, _calls.attn_decode)
 
 from .layer import MoELayer, LayerWeights  # noqa: E402  (composition of the calls above)
 from .attention import AttentionLayer, AttentionWeights  # noqa: E402

@@ -80,8 +80,8 @@ class AttentionLayer:
         """Projection, slots, norm + rotation + cache write of the step's tokens: requests first .. of the table bring
         ``new`` tokens each.  -> (q, k, v) of the step."""
         T, n = x.shape[0], len(new)
-        if T != sum(new) or T > self.max_tokens:
-            raise ValueError(f"{T} tokens for requests that bring {sum(new)} (at most {self.max_tokens})")
+        if T < 1 or T != sum(new) or T > self.max_tokens:
+            raise ValueError(f"{T} tokens for requests that bring {sum(new)} (1 to {self.max_tokens})")
         page = self.page_size
         old = self.host_lens[first:first + n]
         if any(c + m > self.blocks * page for c, m in zip(old, new)):
@@ -130,8 +130,8 @@ class AttentionLayer:
     def decode(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None) -> torch.Tensor:
         """One token of each of requests 0 .. B - 1: x bf16 [B, hidden]."""
         B = x.shape[0]
-        if B > self.max_requests:
-            raise ValueError(f"{B} requests, at most {self.max_requests}")
+        if not 1 <= B <= self.max_requests:
+            raise ValueError(f"{B} requests, at least 1 and at most {self.max_requests}")
         self.new[:B].fill_(1)
         q, _, _ = self._tokens(x, [1] * B, 0, self.prefix_len)
         longest, prefix = max(self.host_lens[:B], default=0), self.prefix_len

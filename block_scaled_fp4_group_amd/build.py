@@ -5,7 +5,9 @@
 (run as a script: importing the package itself needs the built library)
 
 Each HIP source compiles to its own object in parallel (the GEMM files hold
-many kernel instantiations), then one link step writes libmoefp4.so.
+many kernel instantiations), then one link step writes libmoefp4.so.  The
+Python side of the attention calls (csrc/calls.cpp, plain CPython) becomes
+_calls.so, linked to it.
 """
 from __future__ import annotations
 
@@ -14,10 +16,12 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libmoefp4.so")
+CALLS = os.path.join(PKG, "_calls.so")
 OBJ_DIR = os.path.join(PKG, "_build")
 ARCH = "gfx950"
 
@@ -42,6 +46,14 @@ def compile_command(src: str, obj: str) -> list:
 
 def link_command(objs: list, out: str) -> list:
     return [hipcc(), f"--offload-arch={ARCH}", "-fPIC", "-shared", *objs, "-o", out]
+
+
+def calls_command(out: str) -> list:
+    """Host code only: the system's compiler (the HIP header gives the stream's type)."""
+    rocm = os.path.dirname(os.path.dirname(hipcc())) if os.path.sep in hipcc() else "/opt/rocm"
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(rocm, "include"), "-I", os.path.join(ROOT, "include"),
+            os.path.join(PKG, "csrc", "calls.cpp"), "-o", out, "-L", PKG, "-lmoefp4", "-Wl,-rpath,$ORIGIN"]
 
 
 def _run(cmd: list) -> tuple:
@@ -78,8 +90,14 @@ def build(verbose: bool = True, jobs: int = 0) -> str:
     if stubs:
         raise RuntimeError("kernel launch stubs left undefined (host-side instantiation failed): " + ", ".join(stubs[:4]))
     os.replace(tmp, LIB)
+    tmp = CALLS + ".tmp"
+    rc, msgs = _run(calls_command(tmp))
+    if rc != 0:
+        sys.stderr.write("\n".join(msgs) + "\n")
+        raise RuntimeError(f"the compiler failed on calls.cpp with exit code {rc}")
+    os.replace(tmp, CALLS)
     if verbose:
-        print(f"built {LIB} from {len(srcs)} sources", flush=True)
+        print(f"built {LIB} from {len(srcs)} sources, {CALLS}", flush=True)
     return LIB
 
 

@@ -129,3 +129,21 @@ def test_python_wrappers_refuse_before_the_library():
         moe.qk_norm_rope(x, x, None, None)
     with pytest.raises(ValueError, match="GPU tensor"):
         moe.kv_slots(i, i, i, i[None], 16, 1)
+
+
+def test_calls_parse_like_python_functions():
+    x = torch.zeros((2, 2, 128), dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="missing required argument 'cu_q'"):
+        moe.attn_prompt(x, x, x)
+    with pytest.raises(TypeError, match="unexpected keyword argument 'cuq'"):
+        moe.attn_prompt(x, x, x, x, cuq=x)
+    with pytest.raises(TypeError, match="multiple values for argument 'q'"):
+        moe.attn_prompt(x, x, x, x, q=x)
+    with pytest.raises(TypeError, match="at most 12"):
+        moe.kv_slots(*[x] * 13)
+    with pytest.raises(ValueError, match="q must be a GPU tensor"):
+        moe.attn_decode(None, x, x, x, x, 1)
+    import inspect
+    assert list(inspect.signature(moe.attn_decode).parameters)[:4] == ["q", "k_cache", "v_cache", "block_table"]
+    assert inspect.signature(moe.qk_norm_rope).parameters["eps"].default == 1e-6
+    assert "paged cache" in moe.attn_decode.__doc__

@@ -820,3 +820,67 @@ def test_attn_prompt_split_stream_graph_and_workspace():
         eager, el = moe.attn_prompt(q, k, v, cu_q, cu_k, want_lse=True)
         torch.cuda.synchronize()
         assert torch.equal(out, eager) and torch.equal(lse, el), i
+
+
+# ----------------------------------------------- the Python side
+def test_calls_refuse_and_keep_no_references():
+    """Wrong tensors are named; refused and finished calls leave every argument's reference count as it was."""
+    import gc
+    import sys
+    say("attention calls: refusals from Python, reference counts")
+    z = lambda *s, d=torch.bfloat16: torch.zeros(s, dtype=d, device="cuda")  # noqa: E731
+    q, k, v, cu = z(8, 4, 128), z(8, 2, 128), z(8, 2, 128), dev_i32(np.array([0, 8]))
+    kc, vc, tb, ln = z(4, 16, 2, 128), z(4, 16, 2, 128), dev_i32(np.zeros((8, 2))), dev_i32(np.full(8, 5))
+    f = torch.zeros(128, device="cuda")
+    cases = [
+        (ValueError, "q must be a 3-d", lambda: moe.attn_prompt(q.float(), k, v, cu)),
+        (ValueError, "k must be a 3-d", lambda: moe.attn_prompt(q, k[..., ::2], v, cu)),
+        (ValueError, "k: shape", lambda: moe.attn_prompt(q, k[..., :64], v, cu)),
+        (ValueError, "v: shape", lambda: moe.attn_prompt(q, k, v[:4], cu)),
+        (ValueError, "cu_q must be a 1-d", lambda: moe.attn_prompt(q, k, v, cu.long())),
+        (ValueError, "entry for each sequence", lambda: moe.attn_prompt(q, k, v, cu, dev_i32(np.zeros(3)))),
+        (ValueError, "out: shape", lambda: moe.attn_prompt(q, k, v, cu, out=k)),
+        (ValueError, "lse must be", lambda: moe.attn_prompt(q, k, v, cu, lse=z(8, 2, d=torch.float32))),
+        (ValueError, "workspace must be", lambda: moe.attn_prompt(q, k, v, cu, workspace=torch.zeros(8))),
+        (TypeError, None, lambda: moe.attn_prompt(q, k, v, cu, scale="x")),
+        (moe.MoeError, "scale", lambda: moe.attn_prompt(q, k, v, cu, scale=-1.0)),
+        (ValueError, "k_cache must be", lambda: moe.attn_decode(q, kc[0], vc, tb, ln, 5)),
+        (ValueError, "do not fit", lambda: moe.attn_decode(q, kc, vc[:2], tb, ln, 5)),
+        (ValueError, "block_table needs", lambda: moe.attn_decode(q, kc, vc, tb[:3], ln, 5)),
+        (ValueError, "lens needs", lambda: moe.attn_decode(q, kc, vc, tb, ln[:3], 5)),
+        (moe.MoeError, "max_len", lambda: moe.attn_decode(q, kc, vc, tb, ln, 50)),
+        (TypeError, None, lambda: moe.attn_decode(q, kc, vc, tb, ln, None)),
+        (ValueError, "positions must be", lambda: moe.qk_norm_rope(q, k, None, z(4, 64, d=torch.float32))),
+        (ValueError, "positions needs", lambda: moe.qk_norm_rope(q, k, cu, z(4, 64, d=torch.float32))),
+        (ValueError, "need 128", lambda: moe.qk_norm_rope(q, k, None, None, f[:64])),
+        (ValueError, "slots needs", lambda: moe.qk_norm_rope(q, k, None, None, v=v, k_cache=kc, v_cache=vc, slots=cu)),
+        (moe.MoeError, "nowhere", lambda: moe.qk_norm_rope(q, k, None, None, want_k=False)),
+        (ValueError, "entry for each request", lambda: moe.kv_slots(ln, cu, cu, tb, 16, 4)),
+        (ValueError, "slots needs 4", lambda: moe.kv_slots(ln, ln, cu, tb, 16, 4, slots=cu)),
+        (ValueError, "32-bit", lambda: moe.kv_slots(ln, ln, cu, tb, 1 << 40, 4)),
+        (moe.MoeError, "page_size", lambda: moe.kv_slots(ln, ln, cu, tb, 24, 4)),
+    ]
+    fine = [lambda: moe.attn_prompt(q, k, v, cu, want_lse=True), lambda: moe.attn_prompt(q, k, v, cu, cu, 0.1, out=q.clone()),
+            lambda: moe.attn_decode(q, kc, vc, tb, ln, 5, tb[0], 7, want_lse=True),
+            lambda: moe.qk_norm_rope(q, k, None, None, f, f, v=v, k_cache=kc, v_cache=vc, slots=ln),
+            lambda: moe.kv_slots(ln, ln, cu, tb.clone(), 16, 4), lambda: moe.kv_slots(ln, ln, cu, tb.clone(), 16, 4, counts=ln)]
+    watched = [q, k, v, cu, kc, vc, tb, ln, f, None]
+    count = lambda: [sys.getrefcount(x) for x in watched[:-1]]  # noqa: E731
+    before = None
+    for turn in range(3):
+        for kind, match, call in cases:
+            with pytest.raises(kind, match=match):
+                call()
+        for call in fine:
+            call()
+        gc.collect()
+        assert before is None or count() == before, turn
+        before = count()
+    torch.cuda.synchronize()
+    held = torch.cuda.memory_allocated()
+    for _ in range(50):
+        for call in fine:
+            call()
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() == held
+    assert [tuple(t.shape) for t in fine[4]()] == [(4,), (4,), (9,), (3,)]
