@@ -80,9 +80,10 @@ __device__ __forceinline__ at_rsrc at_make_rsrc(const void* base) {
   const uint64_t b = (uint64_t)base;
   return at_rsrc{(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, 0x7fffffffu, 0x00020000u};
 }
-__device__ __forceinline__ void at_load_lds(uint32_t lds, at_rsrc r, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(lds), "v"(off), "s"(r) : "memory");
+// (off per lane, uniform on top of it)
+__device__ __forceinline__ void at_load_lds(uint32_t lds, at_rsrc r, uint32_t off, uint32_t uniform) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :: "s"(lds), "v"(off), "s"(r), "s"(uniform) : "memory");
 }
 // The same from a 64-bit address per lane.  ONCE: data that nothing reads again
 // (non-temporal cache policy).
@@ -126,28 +127,25 @@ struct AttnWave {
   f32x16 s[NB];
   bf16x8 p[2 * NB];
   float m, l;
-  // This lane's byte offsets within a tile: of its operand chunk of key row
-  // l % 32 (chunks repeat their swizzle every KA steps), and of its 8 bytes of
-  // the transposing reads of value block b, lower and upper 8 keys.  All other
-  // offsets are constants added to these.
+  // This lane's byte offsets within a tile: of its first operand chunk of key row
+  // l % 32, and of its 8 bytes of the transposing reads of value block 0, lower and
+  // upper 8 keys.  The others differ by constants, xored in within the span of the
+  // swizzle (KA steps of the keys) and added beyond it.
   static constexpr int KA = DQ == 192 ? 4 : KQ;
-  uint32_t ka[KA], va[OB][2];
+  uint32_t k0, v0[2];
 
   // q: this lane's query row (16-byte aligned)
   __device__ __forceinline__ void init(const uint16_t* row, int lane) {
     const int h = lane >> 5, r = lane & 31, g = lane >> 4, i16 = lane & 15;
 #pragma unroll
     for (int i = 0; i < KQ; ++i) q[i] = __builtin_bit_cast(bf16x8, *(const u32x4*)(row + 16 * i + 8 * h));
+    k0 = (uint32_t)(r * (DQ * 2) + (h ^ at_swz<DQ>(r)) * 16);
 #pragma unroll
-    for (int k = 0; k < KA; ++k) ka[k] = (uint32_t)(r * (DQ * 2) + ((2 * k + h) ^ at_swz<DQ>(r)) * 16);
-#pragma unroll
-    for (int b = 0; b < OB; ++b)
-#pragma unroll
-      for (int jj = 0; jj < 2; ++jj) {
-        const int row16 = 8 * jj + 4 * h + (i16 >> 2);              // at_swz repeats every 16 rows
-        const int chunk = (4 * b + 2 * (g & 1) + ((i16 & 3) >> 1)) ^ at_swz<DV>(row16);
-        va[b][jj] = (uint32_t)(row16 * (DV * 2) + chunk * 16 + 8 * (i16 & 1));
-      }
+    for (int jj = 0; jj < 2; ++jj) {
+      const int row16 = 8 * jj + 4 * h + (i16 >> 2);                // at_swz repeats every 16 rows
+      const int chunk = (2 * (g & 1) + ((i16 & 3) >> 1)) ^ at_swz<DV>(row16);
+      v0[jj] = (uint32_t)(row16 * (DV * 2) + chunk * 16 + 8 * (i16 & 1));
+    }
 #pragma unroll
     for (int b = 0; b < OB; ++b)
 #pragma unroll
@@ -157,24 +155,21 @@ struct AttnWave {
     // The loads are waited for here, not by the first use in the key loop (whose
     // wait would take the direct loads in flight with it, tile after tile); all
     // the rest is done while they are under way.
-#pragma unroll
-    for (int k = 0; k < KA; ++k) asm volatile("" : "+v"(ka[k]));
-#pragma unroll
-    for (int b = 0; b < OB; ++b) asm volatile("" : "+v"(va[b][0]), "+v"(va[b][1]), "+v"(o[b]));
+    asm volatile("" : "+v"(k0), "+v"(v0[0]), "+v"(v0[1]));
 #pragma unroll
     for (int i = 0; i < KQ; ++i) asm volatile("" : "+v"(q[i]));
   }
 
   // operand of keys 32 b .. 32 b + 31, columns 16 k .. 16 k + 15
   __device__ __forceinline__ bf16x8 read_k(const uint8_t* ks, int b, int k) const {
-    return *(const bf16x8*)(ks + ka[k % KA] + (32 * b * (DQ * 2) + (k / KA) * (KA * 32)));
+    return *(const bf16x8*)(ks + (k0 ^ ((k % KA) * 32)) + (32 * b * (DQ * 2) + (k / KA) * (KA * 32)));
   }
   // operand of value columns 32 b .. 32 b + 31, keys 16 st .. 16 st + 15
   __device__ __forceinline__ bf16x8 read_v(const uint8_t* vs, int st, int b) const {
     s16x4 part[2];
 #pragma unroll
     for (int jj = 0; jj < 2; ++jj)
-      part[jj] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at_lds_s16x4*)(vs + va[b][jj] + 16 * st * (DV * 2)));
+      part[jj] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at_lds_s16x4*)(vs + (v0[jj] ^ (b * 64)) + 16 * st * (DV * 2)));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7));
   }
 
@@ -337,28 +332,6 @@ struct AttnWave {
         for (int i = 0; i < 16; ++i) o[b][i] += z[i] > 0.0f ? value : 0.0f;
       }
     }
-  }
-
-  // a whole tile that every row sees
-  __device__ __forceinline__ void tile(const uint8_t* ks, const uint8_t* vs, float c) {
-    scores(ks);
-    weights(c);
-    values(vs);
-  }
-  // One with masked places, see mask().  All values that a row does not see have
-  // weight 0; an infinity or a NaN among them makes the row's o NaN all the same,
-  // which the caller has to notice and do again with tile_careful().
-  __device__ __forceinline__ void tile_masked(const uint8_t* ks, const uint8_t* vs, int lane, float c, int last) {
-    scores(ks);
-    mask(lane, last);
-    weights(c);
-    values(vs);
-  }
-  __device__ __forceinline__ void tile_careful(const uint8_t* ks, const uint8_t* vs, int lane, float c, int last) {
-    scores(ks);
-    mask(lane, last);
-    weights(c);
-    values_careful(vs, lane, last);
   }
 };
 

@@ -172,9 +172,9 @@ __device__ __forceinline__ void decode_wide(const DecodeArgs& a, int kvh, int pa
       const uint32_t row = (uint32_t)__builtin_amdgcn_readfirstlane(slot);
       const at_rsrc kr = at_make_rsrc(kc + (uint64_t)row * k_row), vr = at_make_rsrc(vc + (uint64_t)row * v_row);
 #pragma unroll
-      for (int i = 0; i < kKeyLoads; ++i) at_load_lds(kt + i * kDecThreads * 16, kr, koff[i]);
+      for (int i = 0; i < kKeyLoads; ++i) at_load_lds(kt + i * kDecThreads * 16, kr, koff[i], 0);
 #pragma unroll
-      for (int i = 0; i < kValLoads; ++i) at_load_lds(vt + i * kDecThreads * 16, vr, voff[i]);
+      for (int i = 0; i < kValLoads; ++i) at_load_lds(vt + i * kDecThreads * 16, vr, voff[i], 0);
       return;
     }
 #pragma unroll

@@ -14,13 +14,12 @@
 // 195 -> 188 us, 3 of up to 3500 with context 448 -> 425 us).
 //
 // Bound by the matrix cores' power budget where the keys are many: 16384 tokens x
-// 32/4 heads x 128 take 1.98 to 2.02 ms = 1.1 PFLOP/s, matrix units busy 61% of the
-// cycles at the 1.7 GHz that the chip then runs at (a library's 8192^3 product
-// reaches 1.25 PFLOP/s).  With two tile loops per CU in opposite phases the cycles
-// fell by a tenth, and the clock with them.  Where the keys are few a workgroup
-// costs 7 us beside its 1.7 us per tile -- 0.7 to find its rows, 3 until the first
-// tile is there, 1.7 to store, 2 until the next one starts --, which the two on a
-// CU hide in part: the 32 prompts above take 170 us, 740 TFLOP/s.
+// 32/4 heads x 128 take 1.85 to 1.95 ms = 1.13 to 1.19 PFLOP/s by the box (a
+// library's 8192^3 product reaches 1.25 PFLOP/s).  Where the keys are few a
+// workgroup costs 7 us beside its tiles (1 us each alone on a CU, 1.7 beside
+// another): 0.7 to find its rows, 3 until the first tile is there, 1.7 to store, 2
+// until the next one starts, which the others on its CU hide in part: the 32 prompts
+// above take 160 to 163 us, 780 TFLOP/s.
 //
 // Few rows with many keys (a short addition to a long context) would leave most of
 // the chip idle: their keys are split over several workgroups, whose float sums,
@@ -34,6 +33,17 @@ namespace moe {
 constexpr int kPromptThreads = 256;
 constexpr int kPromptRows = kPromptThreads / 64 * 32;
 constexpr int kPromptKeys = 64;
+
+// What a CU holds at once.  128-wide heads: three workgroups, by keeping a wave at
+// 168 registers and the values in one LDS stage (48 KB), loaded while their tile's
+// weights are formed -- against two with two stages, on two boxes: 16384 tokens x 32/4
+// 2.01 -> 1.95 and 1.96 -> 1.85 ms, the 32 prompts above 171 -> 163 and 168 -> 160 us,
+// 4096 x 32/8 150 -> 138 us, and 2% slower where a workgroup has a CU to itself.  64-wide heads fit four with two
+// stages (one: 64 us for 60 at 4096 x 16/16); 192-wide ones fit two either way.
+template <int DQ>
+constexpr int kPromptPerSimd = DQ == 64 ? 4 : (DQ == 128 ? 3 : 2);
+template <int DQ>
+constexpr int kPromptValStages = DQ == 128 ? 1 : 2;
 
 struct PromptArgs {
   const uint16_t* q;
@@ -113,117 +123,22 @@ __device__ __forceinline__ PromptTile prompt_tile(const PromptArgs& a, int vt, i
   return t;
 }
 
-// The rows of workgroup `block`, this is its thread `thread`.  Whether some result
-// is not finite; in that case the workgroup's rows have to be done again,
-// CAREFUL: a value that is infinite or NaN reaches the rows that see it only.
-// (Testing the values of each masked tile beforehand took half as long as the tile.)
-// SPLIT: one of `splits` workgroups for the same rows, an equal run of their tiles
-// of keys each.
-template <int DQ, int DV, bool CAREFUL, bool SPLIT>
-__device__ __forceinline__ bool prompt_rows(const PromptArgs& a, uint32_t block, uint32_t thread, uint8_t* ks, uint8_t* vs) {
-  using W = AttnWave<DQ, DV, kPromptKeys / 32>;
-  constexpr int kThreads = kPromptThreads;
-  const int lane = thread & 63, wv = __builtin_amdgcn_readfirstlane(thread >> 6), h = lane >> 5;
-  // the key head varies fastest: workgroups go to the XCDs in turn, so one key
-  // head's workgroups meet in few L2s
-  const int G = a.q_heads / a.kv_heads;
-  const int kvh = block % (uint32_t)a.kv_heads;
-  const uint32_t item = block / (uint32_t)a.kv_heads;
-  const int part = SPLIT ? (int)(item % (uint32_t)a.splits) : 0;
-  const PromptTile T = prompt_tile(a, (int)(SPLIT ? item / (uint32_t)a.splits : item), G, lane);
-  if (T.row0 >= T.rows) return false;
-  const int wrow = T.row0 + wv * 32, m = min(wrow + (lane & 31), T.rows - 1);       // rows past the end repeat the last
-  const int row = div_g(a, m), hq = kvh * G + m - row * G;
-  const int pos = row + T.lk - T.lq;                                // last key this row sees
-  // the last key that a row of the workgroup sees, and one of this wave; keys that
-  // all its rows see
-  auto key_of = [&](int r) { return div_g(a, min(r, T.rows - 1)) + T.lk - T.lq; };
-  const int n_keys = max(0, key_of(T.row0 + kPromptRows - 1) + 1);
-  const int wave_last = key_of(wrow + 31), all_see = key_of(T.row0) + 1;
-  const uint16_t* kp = a.k + (int64_t)T.k0 * a.k_ts + kvh * a.k_hs;
-  const uint16_t* vp = a.v + (int64_t)T.k0 * a.v_ts + kvh * a.v_hs;
-  // Each lane's share of a tile: 16-byte chunk i * threads + thread of the
-  // swizzled tile, i.e. of row r the chunk that belongs there; its offset from
-  // the tile's first row in memory.  Rows past the last key repeat it.
-  constexpr int kKeyLoads = W::kKeyBytes / 16 / kThreads, kValLoads = W::kValBytes / 16 / kThreads;
-  const uint32_t k_row = (uint32_t)(a.k_ts * 2), v_row = (uint32_t)(a.v_ts * 2);   // bytes; a tile spans < 2 GiB (host)
-  auto k_off = [&](int i, int end) {
-    const int f = i * kThreads + (int)thread, r = f / (DQ / 8);
-    return (uint32_t)min(r, end) * k_row + (uint32_t)((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16u;
-  };
-  auto v_off = [&](int i, int end) {
-    const int f = i * kThreads + (int)thread, r = f / (DV / 8);
-    return (uint32_t)min(r, end) * v_row + (uint32_t)((f % (DV / 8)) ^ at_swz<DV>(r)) * 16u;
-  };
-  uint32_t koff[kKeyLoads], voff[kValLoads];
-#pragma unroll
-  for (int i = 0; i < kKeyLoads; ++i) koff[i] = k_off(i, kPromptKeys - 1);
-#pragma unroll
-  for (int i = 0; i < kValLoads; ++i) voff[i] = v_off(i, kPromptKeys - 1);
-  const uint32_t k_lds = at_lds_addr(ks) + (uint32_t)wv * 1024u, v_lds = at_lds_addr(vs) + (uint32_t)wv * 1024u;
-  auto load = [&](int t, int st) {
-    const int key0 = t * kPromptKeys, end = T.lk - 1 - key0;
-    const at_rsrc kr = at_make_rsrc(kp + key0 * a.k_ts), vr = at_make_rsrc(vp + key0 * a.v_ts);
-    const uint32_t kt = k_lds + (uint32_t)(st * W::kKeyBytes), vt = v_lds + (uint32_t)(st * W::kValBytes);
-    if (end >= kPromptKeys - 1) {
-#pragma unroll
-      for (int i = 0; i < kKeyLoads; ++i) at_load_lds(kt + i * kThreads * 16, kr, koff[i]);
-#pragma unroll
-      for (int i = 0; i < kValLoads; ++i) at_load_lds(vt + i * kThreads * 16, vr, voff[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kKeyLoads; ++i) at_load_lds(kt + i * kThreads * 16, kr, k_off(i, end));
-#pragma unroll
-      for (int i = 0; i < kValLoads; ++i) at_load_lds(vt + i * kThreads * 16, vr, v_off(i, end));
-    }
-  };
-  const int all_tiles = (n_keys + kPromptKeys - 1) / kPromptKeys;
-  const int run = SPLIT ? (all_tiles + a.splits - 1) / a.splits : all_tiles;
-  const int t0 = SPLIT ? min(part * run, all_tiles) : 0, n_tiles = SPLIT ? min(t0 + run, all_tiles) : all_tiles;
-  // tiles that every row of the workgroup sees whole come first; for the others
-  // (around the diagonal) each wave looks whether it sees any of it at all
-  const int n_whole = max(0, min(n_tiles, all_see / kPromptKeys));
-  auto seen = [&](int t) { return t * kPromptKeys <= wave_last; };
-  if (n_tiles > t0) load(t0, 0);                                    // under way while the queries are read
-  W w;
-  w.init(a.q + (int64_t)(T.q0 + row) * a.q_ts + hq * a.q_hs, lane);
-  // tile t has landed, and everyone is done with tile t - 1, whose stage the next
-  // loads refill
-  auto begin = [&](int t, int st) {
-    at_wait_barrier<0>();
-    if (t + 1 < n_tiles) load(t + 1, st ^ 1);
-  };
-  const bool real = wrow < T.rows;                                  // some row of this wave is
-  int t = t0;
-  if (!CAREFUL) {
-    auto step = [&](auto stage, int tile) {
-      constexpr int st = decltype(stage)::value;
-      begin(tile, st);
-      if (real) w.tile(ks + st * W::kKeyBytes, vs + st * W::kValBytes, a.c);
-    };
-    for (; t + 1 < n_whole; t += 2) {
-      step(std::integral_constant<int, 0>(), t);
-      step(std::integral_constant<int, 1>(), t + 1);
-    }
-  }
-  // (a last odd whole tile goes with the others)
-#pragma unroll 1
-  for (; t < n_tiles; ++t) {
-    const int st = (t - t0) & 1;
-    begin(t, st);
-    if (!real || !seen(t)) continue;
-    const uint8_t* k = ks + st * W::kKeyBytes;
-    const uint8_t* v = vs + st * W::kValBytes;
-    if (CAREFUL) w.tile_careful(k, v, lane, a.c, pos - t * kPromptKeys);
-    else w.tile_masked(k, v, lane, a.c, pos - t * kPromptKeys);
-  }
+// The wave's results from the accumulators to memory, or as a part to the workspace.
+// Whether some of the workgroup's is not finite (never with CAREFUL).
+template <int DQ, int DV, bool CAREFUL, bool SPLIT, class W, class Row>
+__device__ __forceinline__ bool prompt_store(const PromptArgs& a, const W& w, uint32_t thread, int wrow, int wv, int part,
+                                             const PromptTile& T, const Row& row_of, uint8_t* ks) {
+  asm volatile("" : "+v"(thread));                                  // (nothing of this is held in registers before)
+  const int lane = thread & 63, h = lane >> 5;
+  int row, hq;
+  row_of(lane, row, hq);
+  at_wait_barrier<0>();                                             // everyone is done with the stages
   // The results go through LDS, so that stores write whole rows (2.6 us of a
-  // workgroup's time as 8-byte pieces, 1.6 us so): 16-byte chunk c
-  // of row r lies at chunk c ^ r of the stage that is not the last tile's (everyone
-  // is done with it and no load is under way there), a quarter per wave.
+  // workgroup's time as 8-byte pieces, 1.6 us so): 16-byte chunk c of row r lies at
+  // chunk c ^ r of the keys' stages, a quarter per wave.
   constexpr int CH = DV / 8;
-  const int idle = (n_tiles - t0) & 1;
-  uint8_t* rows = (wv < 2 ? ks + idle * W::kKeyBytes : vs + idle * W::kValBytes) + (wv & 1) * (32 * DV * 2);
+  static_assert(4 * 32 * DV * 2 <= 2 * W::kKeyBytes, "");
+  uint8_t* rows = ks + wv * (32 * DV * 2);
   float odd = 0.0f;                                                 // NaN once some result is not finite
   if (SPLIT) {
     if (wrow + (lane & 31) < T.rows) {
@@ -278,27 +193,190 @@ __device__ __forceinline__ bool prompt_rows(const PromptArgs& a, uint32_t block,
       a.lse[(int64_t)(T.q0 + row) * a.q_heads + hq] = w.l == 0.0f ? neg_inf() : (w.m + __builtin_amdgcn_logf(w.l)) * kLn2;
   }
   if (CAREFUL) return false;
-  // each wave's word, in its quarter of the idle stage
+  // each wave's word, in its quarter
   if (lane == 0) *(int*)rows = 0;
   if (odd != odd) *(int*)rows = 1;
   at_wait_barrier<63>();                                            // (the stores are not waited for)
   int any = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) any |= *(const int*)((i < 2 ? ks + idle * W::kKeyBytes : vs + idle * W::kValBytes) + (i & 1) * (32 * DV * 2));
+  for (int i = 0; i < 4; ++i) any |= *(const int*)(ks + i * (32 * DV * 2));
   return any != 0;
 }
 
+// The rows of workgroup `block`, this is its thread `thread`.  Whether some result
+// is not finite; in that case the workgroup's rows have to be done again,
+// CAREFUL: a value that is infinite or NaN reaches the rows that see it only.
+// (Testing the values of each masked tile beforehand took half as long as the tile.)
+// SPLIT: one of `splits` workgroups for the same rows, an equal run of their tiles
+// of keys each.
+template <int DQ, int DV, bool CAREFUL, bool SPLIT>
+__device__ __forceinline__ bool prompt_rows(const PromptArgs& a, uint32_t block, uint32_t thread, uint8_t* ks, uint8_t* vs) {
+  using W = AttnWave<DQ, DV, kPromptKeys / 32>;
+  constexpr int kThreads = kPromptThreads;
+  constexpr int VS = kPromptValStages<DQ>;
+  const int lane = thread & 63, wv = __builtin_amdgcn_readfirstlane(thread >> 6);
+  // the key head varies fastest: workgroups go to the XCDs in turn, so one key
+  // head's workgroups meet in few L2s
+  const int G = a.q_heads / a.kv_heads;
+  const int kvh = block % (uint32_t)a.kv_heads;
+  const uint32_t item = block / (uint32_t)a.kv_heads;
+  const int part = SPLIT ? (int)(item % (uint32_t)a.splits) : 0;
+  const PromptTile T = prompt_tile(a, (int)(SPLIT ? item / (uint32_t)a.splits : item), G, lane);
+  if (T.row0 >= T.rows) return false;
+  const int wrow = T.row0 + wv * 32;
+  // this lane's row: its token and head (rows past the end repeat the last)
+  auto row_of = [&](int l, int& row, int& hq) {
+    const int m = min(wrow + (l & 31), T.rows - 1);
+    row = div_g(a, m);
+    hq = kvh * G + m - row * G;
+  };
+  int row, hq;
+  row_of(lane, row, hq);
+  const int pos = row + T.lk - T.lq;                                // last key this row sees
+  // the last key that a row of the workgroup sees, and one of this wave; keys that
+  // all its rows see
+  auto key_of = [&](int r) { return div_g(a, min(r, T.rows - 1)) + T.lk - T.lq; };
+  const int n_keys = max(0, key_of(T.row0 + kPromptRows - 1) + 1);
+  const int wave_last = key_of(wrow + 31), all_see = key_of(T.row0) + 1;
+  const uint16_t* kp = a.k + (int64_t)T.k0 * a.k_ts + kvh * a.k_hs;
+  const uint16_t* vp = a.v + (int64_t)T.k0 * a.v_ts + kvh * a.v_hs;
+  // Each lane's share of a tile: 16-byte chunk i * threads + thread of the
+  // swizzled tile, i.e. of row r the chunk that belongs there; its offset from
+  // the tile's first row in memory.  Rows past the last key repeat it.
+  constexpr int kKeyLoads = W::kKeyBytes / 16 / kThreads, kValLoads = W::kValBytes / 16 / kThreads;
+  const uint32_t k_row = (uint32_t)(a.k_ts * 2), v_row = (uint32_t)(a.v_ts * 2);   // bytes; a tile spans < 2 GiB (host)
+  auto k_off = [&](int i, int end, uint32_t th) {
+    const int f = i * kThreads + (int)th, r = f / (DQ / 8);
+    return (uint32_t)min(r, end) * k_row + (uint32_t)((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16u;
+  };
+  auto v_off = [&](int i, int end, uint32_t th) {
+    const int f = i * kThreads + (int)th, r = f / (DV / 8);
+    return (uint32_t)min(r, end) * v_row + (uint32_t)((f % (DV / 8)) ^ at_swz<DV>(r)) * 16u;
+  };
+  // Where a tile's share is whole rows, load i is load 0 further on by a uniform
+  // number of rows (a multiple of 16, after which the swizzle repeats).
+  constexpr bool kUniK = kThreads % (DQ / 8) == 0;
+  static_assert(kThreads % (DV / 8) == 0, "");
+  const uint32_t k_step = kThreads / (DQ / 8) * k_row, v_step = kThreads / (DV / 8) * v_row;
+  uint32_t koff[kUniK ? 1 : kKeyLoads], voff = v_off(0, kPromptKeys - 1, thread);
+  asm volatile("" : "+v"(voff));                                    // (kept as 32 bits, not as the product it came from)
+#pragma unroll
+  for (int i = 0; i < (kUniK ? 1 : kKeyLoads); ++i) {
+    koff[i] = k_off(i, kPromptKeys - 1, thread);
+    asm volatile("" : "+v"(koff[i]));
+  }
+  const uint32_t k_lds = at_lds_addr(ks) + (uint32_t)wv * 1024u, v_lds = at_lds_addr(vs) + (uint32_t)wv * 1024u;
+  // (the last tile's own offsets are formed where they are used, from an opaque copy
+  // of the thread's number: nothing of them is held in registers meanwhile)
+  auto load_k = [&](int t, int st) {
+    const int key0 = t * kPromptKeys, end = T.lk - 1 - key0;
+    const at_rsrc kr = at_make_rsrc(kp + key0 * a.k_ts);
+    const uint32_t kt = k_lds + (uint32_t)(st * W::kKeyBytes);
+    if (end >= kPromptKeys - 1) {
+#pragma unroll
+      for (int i = 0; i < kKeyLoads; ++i) at_load_lds(kt + i * kThreads * 16, kr, koff[kUniK ? 0 : i], kUniK ? i * k_step : 0);
+    } else {
+      uint32_t th = thread;
+      asm volatile("" : "+v"(th));
+#pragma unroll
+      for (int i = 0; i < kKeyLoads; ++i) at_load_lds(kt + i * kThreads * 16, kr, k_off(i, end, th), 0);
+    }
+  };
+  auto load_v = [&](int t, int st) {
+    const int key0 = t * kPromptKeys, end = T.lk - 1 - key0;
+    const at_rsrc vr = at_make_rsrc(vp + key0 * a.v_ts);
+    const uint32_t vt = v_lds + (uint32_t)(st * W::kValBytes);
+    if (end >= kPromptKeys - 1) {
+#pragma unroll
+      for (int i = 0; i < kValLoads; ++i) at_load_lds(vt + i * kThreads * 16, vr, voff, i * v_step);
+    } else {
+      uint32_t th = thread;
+      asm volatile("" : "+v"(th));
+#pragma unroll
+      for (int i = 0; i < kValLoads; ++i) at_load_lds(vt + i * kThreads * 16, vr, v_off(i, end, th), 0);
+    }
+  };
+  const int all_tiles = (n_keys + kPromptKeys - 1) / kPromptKeys;
+  const int run = SPLIT ? (all_tiles + a.splits - 1) / a.splits : all_tiles;
+  const int t0 = SPLIT ? min(part * run, all_tiles) : 0, n_tiles = SPLIT ? min(t0 + run, all_tiles) : all_tiles;
+  // tiles that every row of the workgroup sees whole come first; for the others
+  // (around the diagonal) each wave looks whether it sees any of it at all
+  const int n_whole = max(0, min(n_tiles, all_see / kPromptKeys));
+  auto seen = [&](int t) { return t * kPromptKeys <= wave_last; };
+  if (n_tiles > t0) {                                               // under way while the queries are read
+    load_k(t0, 0);
+    if (VS == 2) load_v(t0, 0);
+  }
+  W w;
+  w.init(a.q + (int64_t)(T.q0 + row) * a.q_ts + hq * a.q_hs, lane);
+  // Keys of tile t (with two stages its values too) have landed, and everyone is
+  // done with tile t - 1, whose stages the next loads refill.
+  auto begin = [&](int t, int st) {
+    at_wait_barrier<0>();
+    if (VS == 1) load_v(t, 0);
+    if (t + 1 < n_tiles) {
+      load_k(t + 1, st ^ 1);
+      if (VS == 2) load_v(t + 1, st ^ 1);
+    }
+  };
+  // before the values are used: with one stage they are still under way, and the
+  // next tile's keys behind them
+  auto landed = [&](int t) {
+    if (VS == 2) return;
+    if (t + 1 < n_tiles) at_wait_barrier<kKeyLoads>();
+    else at_wait_barrier<0>();
+  };
+  const bool real = wrow < T.rows;                                  // some row of this wave is
+  int t = t0;
+  if (!CAREFUL) {
+    auto step = [&](auto stage, int tile) {
+      constexpr int st = decltype(stage)::value;
+      begin(tile, st);
+      if (real) {
+        w.scores(ks + st * W::kKeyBytes);
+        w.weights(a.c);
+      }
+      landed(tile);
+      if (real) w.values(vs + (VS == 2 ? st : 0) * W::kValBytes);
+    };
+    for (; t + 1 < n_whole; t += 2) {
+      step(std::integral_constant<int, 0>(), t);
+      step(std::integral_constant<int, 1>(), t + 1);
+    }
+  }
+  // (a last odd whole tile goes with the others)
+#pragma unroll 1
+  for (; t < n_tiles; ++t) {
+    const int st = (t - t0) & 1;
+    begin(t, st);
+    const bool now = real && seen(t);
+    if (now) {
+      w.scores(ks + st * W::kKeyBytes);
+      w.mask(lane, pos - t * kPromptKeys);
+      w.weights(a.c);
+    }
+    landed(t);
+    if (!now) continue;
+    // A value that a row does not see has weight 0; an infinity or a NaN among them
+    // makes the row's result NaN all the same, which the end notices.
+    const uint8_t* v = vs + (VS == 2 ? st : 0) * W::kValBytes;
+    if (CAREFUL) w.values_careful(v, lane, pos - t * kPromptKeys);
+    else w.values(v);
+  }
+  return prompt_store<DQ, DV, CAREFUL, SPLIT>(a, w, thread, wrow, wv, part, T, row_of, ks);
+}
+
 template <int DQ, int DV, bool SPLIT>
-__global__ __launch_bounds__(kPromptThreads, 2) void attn_prompt_kernel(PromptArgs a) {
+__global__ __launch_bounds__(kPromptThreads, kPromptPerSimd<DQ>) void attn_prompt_kernel(PromptArgs a) {
   using W = AttnWave<DQ, DV, kPromptKeys / 32>;
   __shared__ __attribute__((aligned(16))) uint8_t ks[2 * W::kKeyBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t vs[2 * W::kValBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t vs[kPromptValStages<DQ> * W::kValBytes];
   uint32_t block = blockIdx.x, thread = threadIdx.x;
   if (!prompt_rows<DQ, DV, false, SPLIT>(a, block, thread, ks, vs)) return;
   // (opaque copies: nothing of the first run is kept in registers for this one)
   asm volatile("" : "+s"(block));
   asm volatile("" : "+v"(thread));
-  at_wait_barrier<0>();                                             // everyone has read the words; their stage is refilled
+  at_wait_barrier<0>();                                             // everyone has read the words; the stages are refilled
   prompt_rows<DQ, DV, true, SPLIT>(a, block, thread, ks, vs);
 }
 
