@@ -428,7 +428,7 @@ static int64_t prompt_tiles(int64_t total_q, int64_t G, int64_t num_seqs) { retu
 
 // Workgroups that share a tile of rows.  The lengths are not known here: the average
 // number of keys counts, in tiles.  A tile takes 1.0 us (128-wide heads) while there
-// is a workgroup per CU at most and 1.7 with two; parts cost 6 us for the second
+// is a workgroup per CU at most, 1.7 with two, 2.3 with three; parts cost 6 us for the second
 // launch and their floats written and read at 4 TB/s.  16 tokens on 4096 keys x 32/8
 // x 128: 14 us for 71 unsplit; 128 on 8192: 39 for 135; 512 on 8192: 93 for 140.
 // Never with less than 512 keys on average, which the callers may rely on.
@@ -441,9 +441,11 @@ static int prompt_splits(int64_t total_q, int64_t total_k, int64_t num_seqs, int
   const int64_t part = total_q * q_heads * (v_dim * 4 + 8) / 2000;   // ns
   int best = 1;
   int64_t least = unit * n;
-  const int64_t most = std::min<int64_t>(std::min<int64_t>(64, 512 / groups), n / 2);
+  const int64_t per_cu = k_dim == 64 ? kPromptPerSimd<64> : (k_dim == 128 ? kPromptPerSimd<128> : kPromptPerSimd<192>);
+  const int64_t most = std::min<int64_t>(std::min<int64_t>(64, 256 * per_cu / groups), n / 2);
+  const int64_t slower[4] = {10, 17, 23, 30};                       // by workgroups on a CU, tenths
   for (int64_t s = 2; s <= most; ++s) {
-    const int64_t time = (groups * s <= 256 ? unit : unit * 17 / 10) * ((n + s - 1) / s) + 6000 + s * part;
+    const int64_t time = unit * slower[(groups * s - 1) / 256] / 10 * ((n + s - 1) / s) + 6000 + s * part;
     if (time < least) {
       least = time;
       best = (int)s;
