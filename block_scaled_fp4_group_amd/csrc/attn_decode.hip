@@ -525,9 +525,13 @@ __global__ __launch_bounds__(WPR <= 4 ? 256 : WPR * 64) void attn_join_kernel(De
 // each through registers into its own LDS, the next tile's loads under way while
 // one is computed on; then the waves' sums are joined.  Every request reads the
 // prefix for itself (from L2 after the first).  At most 16 heads of a key head.
+// PAGED: pages hold 8 rows or more, so the whole rows of one load (4 of 128 columns,
+// 8 of 64) follow one another: one row is looked up for all lanes (8 requests behind
+// 777 tokens 10.8 -> 10.4 us; keys of 192 columns do not come in whole rows and gain
+// nothing).
 constexpr int kSmallWaves = 8;
 
-template <int DQ, int DV>
+template <int DQ, int DV, bool PAGED>
 __global__ __launch_bounds__(kSmallWaves * 64) void attn_decode_small_kernel(DecodeArgs a) {
   using W = AttnWave16<DQ, DV, 1>;
   constexpr int kRegion = W::kKeyBytes + W::kValBytes, kOut = DV + 4;             // floats of a row of sums (padded: banks)
@@ -550,15 +554,28 @@ __global__ __launch_bounds__(kSmallWaves * 64) void attn_decode_small_kernel(Dec
   const uint8_t* vc = (const uint8_t*)(a.v_cache + (int64_t)kvh * DV);
   const uint32_t k_row = (uint32_t)a.kv_heads * DQ * 2, v_row = (uint32_t)a.kv_heads * DV * 2;
   u32x4 kr[kKeyLoads], vr[kValLoads];
+  static_assert(!PAGED || DQ != 192, "");
+  constexpr int kRowsK = 512 / DQ, kRowsV = 512 / DV;               // whole rows of a load
   auto load = [&](int slot) {
 #pragma unroll
     for (int i = 0; i < kKeyLoads; ++i) {
       const int f = i * 64 + lane, r = f / (DQ / 8);
+      if (PAGED) {
+        // (rows past the end: those of the last key's group, its page's own)
+        const uint32_t row = (uint32_t)__builtin_amdgcn_readlane(slot, i * kRowsK) & ~(uint32_t)(kRowsK - 1);
+        kr[i] = *(const u32x4*)(kc + (uint64_t)row * k_row + ((uint32_t)(r - i * kRowsK) * k_row + ((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16u));
+        continue;
+      }
       kr[i] = *(const u32x4*)(kc + (uint64_t)(uint32_t)__shfl(slot, r) * k_row + ((f % (DQ / 8)) ^ at_swz<DQ>(r)) * 16);
     }
 #pragma unroll
     for (int i = 0; i < kValLoads; ++i) {
       const int f = i * 64 + lane, r = f / (DV / 8);
+      if (PAGED) {
+        const uint32_t row = (uint32_t)__builtin_amdgcn_readlane(slot, i * kRowsV) & ~(uint32_t)(kRowsV - 1);
+        vr[i] = *(const u32x4*)(vc + (uint64_t)row * v_row + ((uint32_t)(r - i * kRowsV) * v_row + ((f % (DV / 8)) ^ at_swz<DV>(r)) * 16u));
+        continue;
+      }
       vr[i] = *(const u32x4*)(vc + (uint64_t)(uint32_t)__shfl(slot, r) * v_row + ((f % (DV / 8)) ^ at_swz<DV>(r)) * 16);
     }
   };
@@ -710,8 +727,10 @@ int64_t attn_decode_grid(int64_t B, int q_heads, int kv_heads, int k_dim, int v_
 template <int DQ, int DV>
 static void launch_decode(const DecodeArgs& a, hipStream_t stream) {
   if (a.plan.small) {
-    hipLaunchKernelGGL((attn_decode_small_kernel<DQ, DV>), dim3((uint32_t)(a.num_requests * a.kv_heads)), dim3(kSmallWaves * 64), 0,
-                       stream, a);
+    const dim3 grid((uint32_t)(a.num_requests * a.kv_heads)), threads(kSmallWaves * 64);
+    constexpr bool kWhole = DQ != 192;
+    if (kWhole && a.page_shift >= 3) hipLaunchKernelGGL((attn_decode_small_kernel<DQ, DV, kWhole>), grid, threads, 0, stream, a);
+    else hipLaunchKernelGGL((attn_decode_small_kernel<DQ, DV, false>), grid, threads, 0, stream, a);
     return;
   }
   const uint32_t grid = (uint32_t)plan_grid(a.plan, a.kv_heads);
