@@ -14,12 +14,13 @@
 // 195 -> 188 us, 3 of up to 3500 with context 448 -> 425 us).
 //
 // Bound by the matrix cores' power budget where the keys are many: 16384 tokens x
-// 32/4 heads x 128 take 1.85 to 1.95 ms = 1.13 to 1.19 PFLOP/s by the box (a
-// library's 8192^3 product reaches 1.25 PFLOP/s).  Where the keys are few a
+// 32/4 heads x 128 take 1.83 to 1.95 ms = 1.13 to 1.2 PFLOP/s by the box, matrix
+// units busy 70% of the cycles at the 1.64 GHz that the chip then runs at (a library's
+// 8192^3 product reaches 1.25 PFLOP/s).  Where the keys are few a
 // workgroup costs 7 us beside its tiles (1 us each alone on a CU, 1.7 beside
 // another): 0.7 to find its rows, 3 until the first tile is there, 1.7 to store, 2
 // until the next one starts, which the others on its CU hide in part: the 32 prompts
-// above take 160 to 163 us, 780 TFLOP/s.
+// above take 156 to 163 us, 790 TFLOP/s.
 //
 // Few rows with many keys (a short addition to a long context) would leave most of
 // the chip idle: their keys are split over several workgroups, whose float sums,
