@@ -673,14 +673,16 @@ static DecodePlan decode_plan(int64_t B, int q_heads, int kv_heads, int64_t pref
   p.blocks_s = (int32_t)up(G, 32 * p.rb);
   p.rows_s = (int32_t)std::min<int64_t>(G, 32 * p.rb);
   // The workgroups that the chip holds at once are shared by the two kinds so that
-  // both end at about the same time.  64 keys of a prefix take a wide workgroup 3
-  // units where they take a narrow one 5 (1.5 us of matrix work for 128 rows, 2.7 us
-  // of its share of the reads; 128-wide heads).  The own lengths are not known here:
-  // half of the bound is counted, and each request once more for starting on it.
+  // both end at about the same time.  64 keys of a prefix take a wide workgroup 6
+  // units, a narrow one 7, and own keys a narrow one 10 (1.5 us of matrix work for 128
+  // rows, 2.7 us of its share of the reads; 128-wide heads).  The own lengths are not
+  // known here: one is counted at the bound, the others at half, and each request once
+  // more for starting on it.  (One request with 7647 keys behind 12490, 32/8 heads: 31
+  // us with half of the bound and equal units for the narrow ones, 24 us so.)
   // (64 requests behind 8192 tokens: 79 us with shares by keys alone, of which the
   // prefix's workgroups worked 39.)
-  const int64_t tiles_p = up(prefix_len, 64), tiles_s = max_len == 0 ? 0 : up(B * up(max_len, 64), 2) + B;
-  const int64_t cost_p = p.wide ? 3 : 5, cost_s = 5;
+  const int64_t tiles_p = up(prefix_len, 64), tiles_s = max_len == 0 ? 0 : up((B + 1) * up(max_len, 64), 2) + B;
+  const int64_t cost_p = p.wide ? 6 : 7, cost_s = 10;
   const int64_t per_part = kv_heads * p.blocks_p, per_run = kv_heads * p.blocks_s;
   const int64_t work_p = per_part * tiles_p * cost_p, work_s = per_run * tiles_s * cost_s;
   int64_t parts = 0;
