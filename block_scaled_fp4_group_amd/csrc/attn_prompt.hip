@@ -66,9 +66,9 @@ struct PromptArgs {
   int32_t splits;
 };
 
-// n / G for 0 <= n < 2^31: with 2^(s - 1) < G <= 2^s and g_mul = ceil(2^(31 + s) / G),
-// n * g_mul exceeds n * 2^(31 + s) / G by less than n < 2^31 ulps of the last
-// place before the shift, 1 / G of which is less than 1 / G of the quotient's unit.
+// n / G for 0 <= n < 2^31: with 2^(s - 1) < G <= 2^s and p = 31 + s, g_mul =
+// ceil(2^p / G) = (2^p + e) / G, 0 <= e < G, so n * g_mul / 2^p = n / G + n e / (G 2^p),
+// and n e < 2^p: less than 1 / G too much, which never reaches the next whole number.
 __device__ __forceinline__ int div_g(const PromptArgs& a, int n) {
   return a.g_shift < 0 ? n : (int)(__umulhi((uint32_t)n, a.g_mul) >> a.g_shift);
 }
@@ -431,7 +431,7 @@ static int64_t prompt_tiles(int64_t total_q, int64_t G, int64_t num_seqs) { retu
 // number of keys counts, in tiles.  A tile takes 1.0 us (128-wide heads) while there
 // is a workgroup per CU at most, 1.7 with two, 2.3 with three; parts cost 6 us for the second
 // launch and their floats written and read at 4 TB/s.  16 tokens on 4096 keys x 32/8
-// x 128: 14 us for 71 unsplit; 128 on 8192: 39 for 135; 512 on 8192: 93 for 140.
+// x 128: 14 us for 71 unsplit; 128 on 8192: 39 for 135; 512 on 8192: 88 for 140.
 // Never with less than 512 keys on average, which the callers may rely on.
 static int prompt_splits(int64_t total_q, int64_t total_k, int64_t num_seqs, int64_t q_heads, int64_t kv_heads, int64_t k_dim,
                          int64_t v_dim) {
