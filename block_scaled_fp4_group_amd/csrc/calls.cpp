@@ -18,11 +18,11 @@ namespace {
 
 // set once by setup()
 PyTypeObject* g_tensor;
-PyObject *g_bf16, *g_i32, *g_f32, *g_u8, *g_raw_stream, *g_check, *g_describe;
+PyObject *g_bf16, *g_i32, *g_f32, *g_u8, *g_raw_stream, *g_check, *g_describe, *g_current_stream, *g_under_stream;
 
 struct Names {
   PyObject *dtype, *shape, *stride, *data_ptr, *get_device, *is_contiguous, *new_empty, *record_stream, *cuda_stream,
-      *element_size, *numel, *split;
+      *element_size, *numel, *split, *enter, *exit;
 } n_;
 
 // An owned reference.
@@ -255,23 +255,52 @@ PyObject* make(PyObject* like, int ndim, const int64_t* d, PyObject* dtype, void
   return t.give();
 }
 
-// The stream to launch on.  Tensors made here belong to the current stream; their
-// use on another one has to be known to the allocator.
-bool stream_of(PyObject* stream, int index, PyObject* const* made, int n, hipStream_t* out) {
-  if (!given(stream)) {
+// A stream that the caller names is the current one while the call makes its tensors:
+// their memory is then free in that stream's own order.  (A block from another
+// stream's pool may still be written by what is queued there.)  The outputs are made
+// known to the stream that was current before, where the caller may read them.
+class Placed {
+ public:
+  ~Placed() {
+    if (context_) {
+      PyObject *type, *value, *trace;
+      PyErr_Fetch(&type, &value, &trace);
+      PyObject* a[4] = {context_, Py_None, Py_None, Py_None};
+      Ref r(PyObject_VectorcallMethod(n_.exit, a, 4, nullptr));
+      if (!r.p) PyErr_WriteUnraisable(context_);
+      PyErr_Restore(type, value, trace);
+      Py_DECREF(context_);
+    }
+    Py_XDECREF(outer_);
+  }
+  bool enter(PyObject* stream, int index) {
+    if (!given(stream)) return true;
     Ref i(PyLong_FromLong(index));
-    Ref s(i.p ? PyObject_CallOneArg(g_raw_stream, i.p) : nullptr);
-    if (!s.p) return false;
-    *out = (hipStream_t)(uintptr_t)PyLong_AsUnsignedLongLongMask(s.p);
-    return !PyErr_Occurred();
-  }
-  for (int k = 0; k < n; ++k) {
-    if (!made[k]) continue;
-    PyObject* a[2] = {made[k], stream};
-    Ref r(PyObject_VectorcallMethod(n_.record_stream, a, 2, nullptr));
+    outer_ = i.p ? PyObject_CallOneArg(g_current_stream, i.p) : nullptr;
+    Ref c(outer_ ? PyObject_CallOneArg(g_under_stream, stream) : nullptr);
+    Ref r(c.p ? PyObject_CallMethodNoArgs(c.p, n_.enter) : nullptr);
     if (!r.p) return false;
+    context_ = c.give();
+    return true;
   }
-  Ref s(PyObject_GetAttr(stream, n_.cuda_stream));
+  bool known(PyObject* const* made, int n) const {
+    for (int k = 0; k < n && outer_; ++k) {
+      if (!made[k]) continue;
+      PyObject* a[2] = {made[k], outer_};
+      Ref r(PyObject_VectorcallMethod(n_.record_stream, a, 2, nullptr));
+      if (!r.p) return false;
+    }
+    return true;
+  }
+
+ private:
+  PyObject *context_ = nullptr, *outer_ = nullptr;
+};
+
+// The stream to launch on.
+bool stream_of(PyObject* stream, int index, hipStream_t* out) {
+  Ref i(given(stream) ? nullptr : PyLong_FromLong(index));
+  Ref s(given(stream) ? PyObject_GetAttr(stream, n_.cuda_stream) : (i.p ? PyObject_CallOneArg(g_raw_stream, i.p) : nullptr));
   if (!s.p) return false;
   *out = (hipStream_t)(uintptr_t)PyLong_AsUnsignedLongLongMask(s.p);
   return !PyErr_Occurred();
@@ -366,11 +395,12 @@ PyObject* kv_slots(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject*
         "positions", "cu_new", "counts", "stream");
   if (!parse("kv_slots", args, nargs, kwnames, names, N, 6, a)) return nullptr;
   int dev;
+  Placed placed;
   void *cached, *fresh, *pool, *tab, *p[4];
   Shape cs, ns, fs;
   int64_t stride, blocks, most;
   int32_t page, base = 0;
-  if (!gpu(a[0], "cached_lens", &dev) || !flat(a[0], "cached_lens", g_i32, 1, dev, &cached, &cs) ||
+  if (!gpu(a[0], "cached_lens", &dev) || !placed.enter(a[11], dev) || !flat(a[0], "cached_lens", g_i32, 1, dev, &cached, &cs) ||
       !flat(a[1], "new_lens", g_i32, 1, dev, &fresh, &ns) || !flat(a[2], "free_pages", g_i32, 1, dev, &pool, &fs))
     return nullptr;
   const int64_t B = cs.d[0];
@@ -422,7 +452,7 @@ PyObject* kv_slots(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject*
     own[i] = made[i].p;
   }
   hipStream_t stream;
-  if (!stream_of(a[11], dev, own, 4, &stream)) return nullptr;
+  if (!stream_of(a[11], dev, &stream) || !placed.known(own, 4)) return nullptr;
   if (!check(moe_kv_slots((const int32_t*)cached, (const int32_t*)fresh, (int32_t)B, (const int32_t*)pool, fs.d[0], page,
                           (int32_t*)tab, stride, (int32_t)blocks, base, most, (int32_t*)p[0], (int32_t*)p[1],
                           (int32_t*)p[2], (int32_t*)p[3], stream),
@@ -436,9 +466,10 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObj
         "want_k", "q_out", "k_out", "stream");
   if (!parse("qk_norm_rope", args, nargs, kwnames, names, N, 4, a)) return nullptr;
   int dev;
+  Placed placed;
   moe_heads hq, hk, hv, ho, hko;
   Shape qs, ks, s;
-  if (!gpu(a[0], "q", &dev) || !heads(a[0], "q", dev, Shape{{-1, -1, -1, 0}}, &hq, &qs)) return nullptr;
+  if (!gpu(a[0], "q", &dev) || !placed.enter(a[15], dev) || !heads(a[0], "q", dev, Shape{{-1, -1, -1, 0}}, &hq, &qs)) return nullptr;
   const int64_t T = qs.d[0], D = qs.d[2];
   if (!heads(a[1], "k", dev, Shape{{T, -1, D, 0}}, &hk, &ks)) return nullptr;
   const int64_t Hkv = ks.d[1];
@@ -490,7 +521,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObj
   if (write_k && !output_heads(a[14], "k_out", a[1], dev, T, Hkv, D, &mk, &k_out, &hko)) return nullptr;
   PyObject* own[2] = {mq.p, mk.p};
   hipStream_t stream;
-  if (!stream_of(a[15], dev, own, 2, &stream)) return nullptr;
+  if (!stream_of(a[15], dev, &stream) || !placed.known(own, 2)) return nullptr;
   if (!check(moe_qk_norm_rope(&hq, &hk, cached ? &hv : nullptr, T, &prm, (const int32_t*)pos, (const float*)cs,
                               (const float*)w[0], (const float*)w[1], &ho, write_k ? &hko : nullptr, cached ? &c : nullptr,
                               (const int32_t*)slots, stream),
@@ -503,10 +534,11 @@ PyObject* attn_prompt(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObje
   NAMES("q", "k", "v", "cu_q", "cu_k", "scale", "out", "lse", "want_lse", "workspace", "stream");
   if (!parse("attn_prompt", args, nargs, kwnames, names, N, 4, a)) return nullptr;
   int dev;
+  Placed placed;
   moe_heads hq, hk, hv, ho;
   Shape qs, ks, vs, cq, ck;
   void *pq, *pk, *pl, *ws;
-  if (!gpu(a[0], "q", &dev) || !heads(a[0], "q", dev, Shape{{-1, -1, -1, 0}}, &hq, &qs) ||
+  if (!gpu(a[0], "q", &dev) || !placed.enter(a[10], dev) || !heads(a[0], "q", dev, Shape{{-1, -1, -1, 0}}, &hq, &qs) ||
       !heads(a[1], "k", dev, Shape{{-1, -1, qs.d[2], 0}}, &hk, &ks) ||
       !heads(a[2], "v", dev, Shape{{ks.d[0], ks.d[1], -1, 0}}, &hv, &vs) || !flat(a[3], "cu_q", g_i32, 1, dev, &pq, &cq))
     return nullptr;
@@ -527,9 +559,9 @@ PyObject* attn_prompt(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObje
       !output_heads(a[6], "out", a[0], dev, T, H, vs.d[2], &mo, &out, &ho) ||
       !output_lse(a[7], a[8], a[0], dev, T, H, &ml, &lse, &pl))
     return nullptr;
-  PyObject* own[3] = {mw.p, mo.p, ml.p};
+  PyObject* own[2] = {mo.p, ml.p};
   hipStream_t stream;
-  if (!stream_of(a[10], dev, own, 3, &stream)) return nullptr;
+  if (!stream_of(a[10], dev, &stream) || !placed.known(own, 2)) return nullptr;
   if (!check(moe_attn_prompt(&hq, &hk, &hv, (const int32_t*)pq, (const int32_t*)pk, (int32_t)seqs, T, ks.d[0], &prm, &ho,
                              (float*)pl, ws, bytes, stream),
              "moe_attn_prompt"))
@@ -542,12 +574,14 @@ PyObject* attn_decode(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObje
         "out", "lse", "want_lse", "stream");
   if (!parse("attn_decode", args, nargs, kwnames, names, N, 6, a)) return nullptr;
   int dev;
+  Placed placed;
   moe_heads hq, ho;
   moe_kv_cache c;
   Shape qs, s;
   void *tab, *lens, *prefix = nullptr, *pl, *ws;
   int64_t stride, blocks, most, prefix_blocks = 0, prefix_len = 0, v_dim;
-  if (!gpu(a[0], "q", &dev) || !heads(a[0], "q", dev, Shape{{-1, -1, -1, 0}}, &hq, &qs)) return nullptr;
+  if (!gpu(a[0], "q", &dev) || !placed.enter(a[13], dev) || !heads(a[0], "q", dev, Shape{{-1, -1, -1, 0}}, &hq, &qs))
+    return nullptr;
   const int64_t B = qs.d[0], H = qs.d[1];
   Shape ks;
   if (!cache(a[1], a[2], dev, -1, qs.d[2], &c, &v_dim) || !shape_of(a[1], 4, &ks) ||
@@ -570,9 +604,9 @@ PyObject* attn_decode(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObje
       !output_heads(a[10], "out", a[0], dev, B, H, v_dim, &mo, &out, &ho) ||
       !output_lse(a[11], a[12], a[0], dev, B, H, &ml, &lse, &pl))
     return nullptr;
-  PyObject* own[3] = {mw.p, mo.p, ml.p};
+  PyObject* own[2] = {mo.p, ml.p};
   hipStream_t stream;
-  if (!stream_of(a[13], dev, own, 3, &stream)) return nullptr;
+  if (!stream_of(a[13], dev, &stream) || !placed.known(own, 2)) return nullptr;
   if (!check(moe_attn_decode(&hq, &c, (const int32_t*)tab, stride, (int32_t)blocks, (const int32_t*)lens, (int32_t)B, most,
                              (const int32_t*)prefix, (int32_t)prefix_blocks, prefix_len, &prm, &ho, (float*)pl, ws, bytes,
                              stream),
@@ -582,13 +616,14 @@ PyObject* attn_decode(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObje
 }
 
 PyObject* setup(PyObject*, PyObject* args) {
-  PyObject *tensor, *bf16, *i32, *f32, *u8, *raw, *chk, *desc;
-  if (!PyArg_ParseTuple(args, "OOOOOOOO", &tensor, &bf16, &i32, &f32, &u8, &raw, &chk, &desc)) return nullptr;
+  PyObject *tensor, *bf16, *i32, *f32, *u8, *raw, *chk, *desc, *current, *under;
+  if (!PyArg_ParseTuple(args, "OOOOOOOOOO", &tensor, &bf16, &i32, &f32, &u8, &raw, &chk, &desc, &current, &under))
+    return nullptr;
   if (!PyType_Check(tensor)) {
     PyErr_SetString(PyExc_TypeError, "the tensor type is no type");
     return nullptr;
   }
-  for (PyObject* x : {tensor, bf16, i32, f32, u8, raw, chk, desc}) Py_INCREF(x);   // for good
+  for (PyObject* x : {tensor, bf16, i32, f32, u8, raw, chk, desc, current, under}) Py_INCREF(x);   // for good
   g_tensor = (PyTypeObject*)tensor;
   g_bf16 = bf16;
   g_i32 = i32;
@@ -597,10 +632,15 @@ PyObject* setup(PyObject*, PyObject* args) {
   g_raw_stream = raw;
   g_check = chk;
   g_describe = desc;
+  g_current_stream = current;
+  g_under_stream = under;
   Py_RETURN_NONE;
 }
 
 #define CALL(name, doc) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL | METH_KEYWORDS, doc}
+#define STREAM_DOC                                                                                             \
+  "``stream``: where the call runs, the current stream if None.  It has to come after what makes the arguments;\n" \
+  "new outputs are made on it, and a reader on another stream has to wait for it."
 PyMethodDef methods[] = {
     {"setup", setup, METH_VARARGS, "Names what the calls need of torch and of the package."},
     CALL(kv_slots,
@@ -608,26 +648,27 @@ PyMethodDef methods[] = {
          "positions=None, cu_new=None, counts=None, stream=None)\n--\n\n"
          "Cache slots of a step's new tokens.  int32 tensors: cached_lens, new_lens [B], free_pages [F], block_table\n"
          "[B, blocks] (new pages are entered in place).  -> (slots [max_new], positions [max_new], cu_new [B + 1],\n"
-         "counts [3]: pages taken, pages needed, tokens without a slot).  ``position_base``: length of a shared prefix."),
+         "counts [3]: pages taken, pages needed, tokens without a slot).  ``position_base``: length of a shared prefix.\n"
+         STREAM_DOC),
     CALL(qk_norm_rope,
          "qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-06, interleaved=False, v=None, "
          "k_cache=None, v_cache=None, slots=None, want_k=True, q_out=None, k_out=None, stream=None)\n--\n\n"
          "RMS norm of each head of q [T, Hq, D] and k [T, Hkv, D] (weights float32 [D]; None: no norm), the rotation by\n"
          "``cos_sin`` float32 [positions, rot_dim] (cosines, then sines; None: no rotation), and with a cache the write of\n"
          "the finished keys and of v [T, Hkv, Dv] to its rows ``slots``.  -> (q_out, k_out); k_out is None with\n"
-         "``want_k=False`` (cache only).  q_out / k_out may be q / k."),
+         "``want_k=False`` (cache only).  q_out / k_out may be q / k.\n" STREAM_DOC),
     CALL(attn_prompt,
          "attn_prompt(q, k, v, cu_q, cu_k=None, scale=None, out=None, lse=None, want_lse=False, workspace=None, "
          "stream=None)\n--\n\n"
          "Causal attention over packed prompts: q [Tq, Hq, D], k [Tk, Hkv, D], v [Tk, Hkv, Dv], offsets cu_q, cu_k int32\n"
          "[B + 1] (cu_k None: cu_q).  Query i of a sequence sees keys 0 .. i + Lk - Lq.  -> (out [Tq, Hq, Dv], lse float32\n"
-         "[Tq, Hq] or None).  Rows outside the offsets' ranges are not written."),
+         "[Tq, Hq] or None).  Rows outside the offsets' ranges are not written.\n" STREAM_DOC),
     CALL(attn_decode,
          "attn_decode(q, k_cache, v_cache, block_table, lens, max_len, prefix_table=None, prefix_len=0, scale=None, "
          "workspace=None, out=None, lse=None, want_lse=False, stream=None)\n--\n\n"
          "One query per request, q [B, Hq, D], over the paged cache: the shared prefix (``prefix_len`` keys in the pages\n"
          "``prefix_table``), then the request's own ``lens`` keys in its ``block_table`` pages (int32).  ``max_len``: a\n"
-         "longest own length known on the host.  -> (out [B, Hq, Dv], lse float32 [B, Hq] or None)."),
+         "longest own length known on the host.  -> (out [B, Hq, Dv], lse float32 [B, Hq] or None).\n" STREAM_DOC),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "Argument checks and marshalling of the attention calls.", -1, methods,
@@ -640,7 +681,8 @@ PyMODINIT_FUNC PyInit__calls(void) {
   if (!name(&n_.dtype, "dtype") || !name(&n_.shape, "shape") || !name(&n_.stride, "stride") ||
       !name(&n_.data_ptr, "data_ptr") || !name(&n_.get_device, "get_device") || !name(&n_.is_contiguous, "is_contiguous") ||
       !name(&n_.new_empty, "new_empty") || !name(&n_.record_stream, "record_stream") ||
-      !name(&n_.cuda_stream, "cuda_stream") || !name(&n_.element_size, "element_size") || !name(&n_.numel, "numel") || !name(&n_.split, "unsafe_split_with_sizes"))
+      !name(&n_.cuda_stream, "cuda_stream") || !name(&n_.element_size, "element_size") || !name(&n_.numel, "numel") || !name(&n_.split, "unsafe_split_with_sizes") ||
+      !name(&n_.enter, "__enter__") || !name(&n_.exit, "__exit__"))
     return nullptr;
   return PyModule_Create(&module);
 }

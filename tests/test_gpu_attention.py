@@ -884,3 +884,67 @@ def test_calls_refuse_and_keep_no_references():
     torch.cuda.synchronize()
     assert torch.cuda.memory_allocated() == held
     assert [tuple(t.shape) for t in fine[4]()] == [(4,), (4,), (9,), (3,)]
+
+
+# ----------------------------------------------- memory of two streams
+def stream_calls():
+    """Each call on inputs of its own, with outputs (and a workspace where there is one) made by the call."""
+    z = lambda i, *s: dev_bf16(synth.random_bf16(900 + i, s))  # noqa: E731
+    q, k, v, cs = z(0, 64, 8, 128), z(1, 64, 2, 128), z(2, 64, 2, 128), torch.randn((64, 128), device="cuda")
+    kc, vc = z(3, 300, 16, 2, 128), z(4, 300, 16, 2, 128)
+    kl, vl = z(5, 4000, 2, 128), z(6, 4000, 2, 128)
+    i = lambda a: dev_i32(np.asarray(a))  # noqa: E731
+    ints = [i(np.full(40, 9)), i(np.full(40, 30)), i(np.arange(200)), i(np.zeros((40, 4)))]
+    pos, cu_q, cu_k, tb, ln, pt = i(np.arange(64)), i([0, 64]), i([0, 4000]), i(np.arange(128).reshape(64, 2)), i(np.full(64, 20)), i(np.arange(250))
+    assert moe.attn_prompt_workspace_bytes(1, 64, 4000, 8, 2, 128, 128) > 0 and makes_parts([20] * 64, 4000, 8, 2, 128, 128)
+    return {
+        "kv_slots": lambda **kw: moe.kv_slots(*ints, 16, 1300, **kw),
+        "qk_norm_rope": lambda **kw: moe.qk_norm_rope(q, k, pos, cs, **kw),
+        "attn_prompt": lambda **kw: moe.attn_prompt(q, kl, vl, cu_q, cu_k, want_lse=True, **kw),
+        "attn_decode": lambda **kw: moe.attn_decode(q, kc, vc, tb, ln, 20, pt, 4000, want_lse=True, **kw)}
+
+
+SIZES = [1 << b for b in range(9, 24)]                              # of freed blocks: each call finds one that fits
+
+
+@pytest.mark.parametrize("name", ["kv_slots", "qk_norm_rope", "attn_prompt", "attn_decode"])
+def test_outputs_do_not_lie_in_memory_that_queued_work_writes(name):
+    """Blocks freed while work on them is queued belong to the current stream's order; a call on another stream runs
+    before that work does."""
+    say(f"{name}: freed blocks of the current stream, still written")
+    call = stream_calls()[name]
+    want = [t.clone() for t in call() if t is not None]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    junk = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in SIZES for _ in range(2)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(30_000_000)
+    for t in junk:
+        t.fill_(0xFF)
+    del junk, t
+    got = call(stream=s)
+    assert torch.cuda.current_stream() != s
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("name", ["kv_slots", "qk_norm_rope", "attn_prompt", "attn_decode"])
+def test_outputs_of_another_stream_outlive_their_readers(name):
+    """An output read on the current stream and freed there: the next call on its own stream gets other memory until
+    the reader is done."""
+    say(f"{name}: outputs read on the current stream after they are freed")
+    call = stream_calls()[name]
+    want = [t.clone() for t in call() if t is not None]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = call(stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda._sleep(30_000_000)
+    read = [t.clone() for t in got]
+    del got
+    with torch.cuda.stream(s):
+        junk = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in SIZES for _ in range(2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(read, want))
+    del junk
