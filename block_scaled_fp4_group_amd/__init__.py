@@ -463,7 +463,8 @@ def _setup_calls():
     raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
     _calls.setup(torch.Tensor, torch.bfloat16, torch.int32, torch.float32, torch.uint8, raw_stream, _check, _bad,
-                 torch.cuda.current_stream, torch.cuda.stream)
+                 torch.cuda.current_stream, torch.cuda.stream,
+                 getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), torch.cuda.device)
     return _calls
 
 

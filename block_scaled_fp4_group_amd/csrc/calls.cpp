@@ -18,11 +18,12 @@ namespace {
 
 // set once by setup()
 PyTypeObject* g_tensor;
-PyObject *g_bf16, *g_i32, *g_f32, *g_u8, *g_raw_stream, *g_check, *g_describe, *g_current_stream, *g_under_stream;
+PyObject *g_bf16, *g_i32, *g_f32, *g_u8, *g_raw_stream, *g_check, *g_describe, *g_current_stream, *g_under_stream, *g_get_device,
+    *g_under_device;
 
 struct Names {
   PyObject *dtype, *shape, *stride, *data_ptr, *get_device, *is_contiguous, *new_empty, *record_stream, *cuda_stream,
-      *element_size, *numel, *split, *enter, *exit;
+      *element_size, *numel, *split, *enter, *exit, *device_index;
 } n_;
 
 // An owned reference.
@@ -255,6 +256,8 @@ PyObject* make(PyObject* like, int ndim, const int64_t* d, PyObject* dtype, void
   return t.give();
 }
 
+// The arguments' device is the current one while the call runs (every device's default
+// stream has the same handle: launched from another device it would be that one's).
 // A stream that the caller names is the current one while the call makes its tensors:
 // their memory is then free in that stream's own order.  (A block from another
 // stream's pool may still be written by what is queued there.)  The outputs are made
@@ -274,10 +277,25 @@ class Placed {
     Py_XDECREF(outer_);
   }
   bool enter(PyObject* stream, int index) {
-    if (!given(stream)) return true;
-    Ref i(PyLong_FromLong(index));
-    outer_ = i.p ? PyObject_CallOneArg(g_current_stream, i.p) : nullptr;
-    Ref c(outer_ ? PyObject_CallOneArg(g_under_stream, stream) : nullptr);
+    Ref i(nullptr), c(nullptr);
+    if (!given(stream)) {
+      Ref now(PyObject_CallNoArgs(g_get_device));
+      const long at = now.p ? PyLong_AsLong(now.p) : -1;
+      if (at == index || PyErr_Occurred()) return !PyErr_Occurred();
+      i.set(PyLong_FromLong(index));
+      c.set(i.p ? PyObject_CallOneArg(g_under_device, i.p) : nullptr);
+    } else {
+      Ref of(PyObject_GetAttr(stream, n_.device_index));
+      const long at = of.p ? PyLong_AsLong(of.p) : -1;
+      if (PyErr_Occurred()) return false;
+      if (at != index) {
+        PyErr_Format(PyExc_ValueError, "stream of cuda:%ld, the arguments are on cuda:%d", at, index);
+        return false;
+      }
+      i.set(PyLong_FromLong(index));
+      outer_ = i.p ? PyObject_CallOneArg(g_current_stream, i.p) : nullptr;
+      c.set(outer_ ? PyObject_CallOneArg(g_under_stream, stream) : nullptr);
+    }
     Ref r(c.p ? PyObject_CallMethodNoArgs(c.p, n_.enter) : nullptr);
     if (!r.p) return false;
     context_ = c.give();
@@ -616,14 +634,14 @@ PyObject* attn_decode(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObje
 }
 
 PyObject* setup(PyObject*, PyObject* args) {
-  PyObject *tensor, *bf16, *i32, *f32, *u8, *raw, *chk, *desc, *current, *under;
-  if (!PyArg_ParseTuple(args, "OOOOOOOOOO", &tensor, &bf16, &i32, &f32, &u8, &raw, &chk, &desc, &current, &under))
+  PyObject *tensor, *bf16, *i32, *f32, *u8, *raw, *chk, *desc, *current, *under, *get, *device;
+  if (!PyArg_ParseTuple(args, "OOOOOOOOOOOO", &tensor, &bf16, &i32, &f32, &u8, &raw, &chk, &desc, &current, &under, &get, &device))
     return nullptr;
   if (!PyType_Check(tensor)) {
     PyErr_SetString(PyExc_TypeError, "the tensor type is no type");
     return nullptr;
   }
-  for (PyObject* x : {tensor, bf16, i32, f32, u8, raw, chk, desc, current, under}) Py_INCREF(x);   // for good
+  for (PyObject* x : {tensor, bf16, i32, f32, u8, raw, chk, desc, current, under, get, device}) Py_INCREF(x);   // for good
   g_tensor = (PyTypeObject*)tensor;
   g_bf16 = bf16;
   g_i32 = i32;
@@ -634,6 +652,8 @@ PyObject* setup(PyObject*, PyObject* args) {
   g_describe = desc;
   g_current_stream = current;
   g_under_stream = under;
+  g_get_device = get;
+  g_under_device = device;
   Py_RETURN_NONE;
 }
 
@@ -682,7 +702,7 @@ PyMODINIT_FUNC PyInit__calls(void) {
       !name(&n_.data_ptr, "data_ptr") || !name(&n_.get_device, "get_device") || !name(&n_.is_contiguous, "is_contiguous") ||
       !name(&n_.new_empty, "new_empty") || !name(&n_.record_stream, "record_stream") ||
       !name(&n_.cuda_stream, "cuda_stream") || !name(&n_.element_size, "element_size") || !name(&n_.numel, "numel") || !name(&n_.split, "unsafe_split_with_sizes") ||
-      !name(&n_.enter, "__enter__") || !name(&n_.exit, "__exit__"))
+      !name(&n_.enter, "__enter__") || !name(&n_.exit, "__exit__") || !name(&n_.device_index, "device_index"))
     return nullptr;
   return PyModule_Create(&module);
 }
