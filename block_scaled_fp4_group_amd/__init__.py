@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
+import inspect
 import os
 from typing import Optional
 
@@ -165,6 +167,36 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _known(made, stream):
+    """Tells the allocator that ``stream`` reads what a call made."""
+    if isinstance(made, torch.Tensor):
+        made.record_stream(stream)
+    elif isinstance(made, (tuple, list)):
+        for t in made:
+            _known(t, stream)
+    elif isinstance(made, Weights):
+        _known((made.packed, made.scale, made.global_scale), stream)
+
+
+def _placed(call):
+    """A stream that the caller names is the current one while the call makes its tensors: their memory is then free in
+    that stream's own order (a block from another stream's pool may still be written by what is queued there).  What it
+    returns is made known to the stream that was current before, where the caller may read it."""
+    at = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def placed(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return call(*args, **kw)
+        outer = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            made = call(*args, **kw)
+        _known(made, outer)
+        return made
+    return placed
+
+
 def _dev(t: torch.Tensor, name: str):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
@@ -173,6 +205,7 @@ def _dev(t: torch.Tensor, name: str):
 
 
 # --------------------------------------------------------------------- calls
+@_placed
 def route(logits: torch.Tensor, bias: Optional[torch.Tensor], num_experts: int, n_group: int, topk_group: int,
           top_k: int, routed_scaling_factor: float, norm_topk_prob: bool = True, ids=None, weights=None, stream=None):
     _dev(logits, "logits")
@@ -189,6 +222,7 @@ def route_gemv_workspace_bytes(T: int, num_experts: int) -> int:
     return int(lib.moe_route_gemv_workspace_bytes(T, num_experts))
 
 
+@_placed
 def route_gemv(x: torch.Tensor, gate_weight: torch.Tensor, bias: Optional[torch.Tensor], num_experts: int,
                n_group: int, topk_group: int, top_k: int, routed_scaling_factor: float, workspace: torch.Tensor,
                norm_topk_prob: bool = True, ids=None, weights=None, stream=None):
@@ -211,6 +245,7 @@ def permute_workspace_bytes(T: int, top_k: int, num_experts: int) -> int:
     return int(lib.moe_permute_workspace_bytes(T, top_k, num_experts))
 
 
+@_placed
 def permute(ids: torch.Tensor, num_experts: int, workspace: Optional[torch.Tensor] = None, offsets=None,
             sorted_slots=None, slot_rows=None, stream=None):
     _dev(ids, "ids")
@@ -227,6 +262,7 @@ def permute(ids: torch.Tensor, num_experts: int, workspace: Optional[torch.Tenso
     return offsets, sorted_slots, slot_rows
 
 
+@_placed
 def route_permute(logits: torch.Tensor, bias: Optional[torch.Tensor], num_experts: int, n_group: int,
                   topk_group: int, top_k: int, routed_scaling_factor: float, counter: torch.Tensor,
                   norm_topk_prob: bool = True, ids=None, weights=None, workspace: Optional[torch.Tensor] = None,
@@ -255,6 +291,7 @@ def route_permute(logits: torch.Tensor, bias: Optional[torch.Tensor], num_expert
     return ids, weights, offsets, sorted_slots, slot_rows
 
 
+@_placed
 def route_permute_noalloc(logits: torch.Tensor, bias: Optional[torch.Tensor], num_experts: int, n_group: int,
                           topk_group: int, top_k: int, routed_scaling_factor: float, ids: torch.Tensor,
                           weights: torch.Tensor, offsets: torch.Tensor, sorted_slots: torch.Tensor,
@@ -299,6 +336,7 @@ _ACT_MODES = {"bf16": MOE_ACT_BF16, "nvfp4": MOE_ACT_NVFP4, "mxfp8": MOE_ACT_MXF
 _OUT_FORMATS = {"nvfp4": MOE_OUT_NVFP4, "mxfp8": MOE_OUT_MXFP8, "planes": MOE_OUT_NVFP4_PLANES}
 
 
+@_placed
 def grouped_gemm(a: torch.Tensor, w0: Weights, w1: Optional[Weights], offsets: torch.Tensor, rows: int,
                  gather: Optional[torch.Tensor] = None, gather_div: int = 1, a_scales: Optional[torch.Tensor] = None,
                  input_scale: float = 1.0, out: Optional[torch.Tensor] = None, out_codes: Optional[torch.Tensor] = None,
@@ -331,6 +369,7 @@ def grouped_gemm(a: torch.Tensor, w0: Weights, w1: Optional[Weights], offsets: t
     return out
 
 
+@_placed
 def combine(expert_out: torch.Tensor, slot_rows: torch.Tensor, topk_weights: torch.Tensor,
             residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, stream=None):
     T, top_k = topk_weights.shape
@@ -341,6 +380,7 @@ def combine(expert_out: torch.Tensor, slot_rows: torch.Tensor, topk_weights: tor
     return y
 
 
+@_placed
 def transcode_mx_to_nv(mx_scale: torch.Tensor, packed: torch.Tensor, nv=None, g=None, cnt=None, stream=None):
     """mx_scale u8 [M, n, k/32], packed u8 [M, n, k/2] -> (nv_scale, global f32 [M], counters i64 [4])
     (written into ``nv``, ``g``, ``cnt`` when given)."""
@@ -355,6 +395,7 @@ def transcode_mx_to_nv(mx_scale: torch.Tensor, packed: torch.Tensor, nv=None, g=
     return nv, g, cnt
 
 
+@_placed
 def tile_weights(w: Weights, stream=None) -> Weights:
     """Copy of ``w`` in the tiled layout (same values; shapes unchanged, flag MOE_FP4_TILED)."""
     if w.tiled:
@@ -367,6 +408,7 @@ def tile_weights(w: Weights, stream=None) -> Weights:
     return Weights(packed, scale, w.global_scale, w.scales_pow2, tiled=True, mx_exact=w.mx_exact, compact=w.compact)
 
 
+@_placed
 def compact_mx(mx_scale: torch.Tensor, packed: torch.Tensor, codes=None, base=None, cnt=None, stream=None):
     """mx_scale u8 [M, n, k/32], packed u8 [M, n, k/2] -> (exponent codes u8 [M, n, k/64],
     base f32 [M], counters i64 [4]: blocks, all-zero below the window, re-rounded, NaN)."""
@@ -381,14 +423,16 @@ def compact_mx(mx_scale: torch.Tensor, packed: torch.Tensor, codes=None, base=No
     return codes, base, cnt
 
 
+@_placed
 def compact_weights(w: Weights, stream=None):
     """Compact copy of row-major MXFP4 weights (codes shared) -> (Weights, counters i64 [4])."""
     if w.format != MOE_FP4_MX or w.tiled:
         raise ValueError("compact_weights takes row-major MXFP4 weights")
-    codes, base, cnt = compact_mx(w.scale, w.packed, stream=stream)
+    codes, base, cnt = compact_mx(w.scale, w.packed)   # (on `stream`: it is the current one here)
     return Weights(w.packed, codes, base, compact=True), cnt
 
 
+@_placed
 def quantize_nvfp4(x: torch.Tensor, input_scale: float = 1.0, codes=None, scales=None, dequant=None, stream=None):
     """-> (codes u8 [rows, k/2], scales u8 [rows, k/16]); ``dequant`` (bf16 [rows, k]) optionally
     receives the NVFP4 values themselves."""
@@ -400,6 +444,7 @@ def quantize_nvfp4(x: torch.Tensor, input_scale: float = 1.0, codes=None, scales
     return codes, scales
 
 
+@_placed
 def reap_saliency_accumulate(row_sumsq: torch.Tensor, offsets: torch.Tensor, sorted_slots: torch.Tensor,
                              topk_weights: torch.Tensor, sums: torch.Tensor, counts: torch.Tensor, rows: int,
                              stream=None):
@@ -411,6 +456,7 @@ def reap_saliency_accumulate(row_sumsq: torch.Tensor, offsets: torch.Tensor, sor
     return sums, counts
 
 
+@_placed
 def quantize_mxfp8(x: torch.Tensor, codes=None, scales=None, stream=None):
     """bf16 [rows, k] -> (E4M3 codes u8 [rows, k], E8M0 scales u8 [rows, k/32])."""
     rows, k = x.shape
@@ -420,6 +466,7 @@ def quantize_mxfp8(x: torch.Tensor, codes=None, scales=None, stream=None):
     return codes, scales
 
 
+@_placed
 def quantize_nvfp4_planes(x: torch.Tensor, input_scale: float = 1.0, planes=None, scales=None, stream=None):
     """bf16 [rows, k] -> (E4M3 planes u8 [rows, 2k], E8M0 scales u8 [rows, k/16]): the NVFP4
     quantisation of x in the block-scaled MFMA's operand form."""
