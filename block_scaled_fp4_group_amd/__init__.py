@@ -178,17 +178,38 @@ def _known(made, stream):
         _known((made.packed, made.scale, made.global_scale), stream)
 
 
+Tensor = torch.Tensor
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _device(args, kw) -> int:
+    """Index of the first tensor's device (-1: none on a GPU)."""
+    for a in (*args, *kw.values()):
+        a = a.packed if isinstance(a, Weights) else a
+        if isinstance(a, torch.Tensor):
+            return a.get_device()
+    return -1
+
+
 def _placed(call):
-    """A stream that the caller names is the current one while the call makes its tensors: their memory is then free in
-    that stream's own order (a block from another stream's pool may still be written by what is queued there).  What it
-    returns is made known to the stream that was current before, where the caller may read it."""
+    """The arguments' device is the current one while the call runs (every device's default stream has the same handle:
+    launched from another device it would be that one's).  A stream that the caller names is the current one while the
+    call makes its tensors: their memory is then free in that stream's own order (a block from another stream's pool may
+    still be written by what is queued there).  What it returns is made known to the stream that was current before,
+    where the caller may read it."""
     at = list(inspect.signature(call).parameters).index("stream")
 
     @functools.wraps(call)
     def placed(*args, **kw):
-        stream = args[at] if len(args) > at else kw.get("stream")
+        stream = kw.get("stream") if len(args) <= at else args[at]
+        index = args[0].get_device() if args and type(args[0]) is Tensor else _device(args, kw)
         if stream is None:
-            return call(*args, **kw)
+            if index < 0 or index == _get_device():
+                return call(*args, **kw)
+            with torch.cuda.device(index):
+                return call(*args, **kw)
+        if index >= 0 and stream.device_index != index:
+            raise ValueError(f"stream of cuda:{stream.device_index}, the arguments are on cuda:{index}")
         outer = torch.cuda.current_stream(stream.device)
         with torch.cuda.stream(stream):
             made = call(*args, **kw)

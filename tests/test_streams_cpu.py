@@ -23,11 +23,12 @@ class Library:
 
 
 class World:
-    log, streams = [], []
+    log, streams, device, devices = [], [], 0, []
 
     @staticmethod
     def launch(name, args):
         if not name.endswith("_bytes"):
+            World.devices.append(World.device)
             World.log.append(("launched", World.streams[-1].name, args[-1].value))
             return 0
         return 64
@@ -45,9 +46,21 @@ class Under:
         World.streams.pop()
 
 
+class OnDevice:
+    """Stands in for torch.cuda.device()."""
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        self.before, World.device = World.device, self.index
+
+    def __exit__(self, *a):
+        World.device = self.before
+
+
 @pytest.fixture
 def world(monkeypatch):
-    World.log, World.streams = [], [Stream("current", 0x10)]
+    World.log, World.streams, World.device, World.devices = [], [Stream("current", 0x10)], 0, []
     empty, like = torch.empty, torch.empty_like
     for name, f in (("empty", empty), ("empty_like", like)):
         def made(*a, f=f, **kw):
@@ -59,8 +72,10 @@ def world(monkeypatch):
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: World.log.append(("known to", s.name)))
     monkeypatch.setattr(moe, "lib", Library())
     monkeypatch.setattr(moe, "_dev", lambda t, name: None)
+    monkeypatch.setattr(torch.cuda, "device", OnDevice)
+    monkeypatch.setattr(moe, "_get_device", lambda: World.device)
     yield World
-    assert [s.name for s in World.streams] == ["current"]
+    assert [s.name for s in World.streams] == ["current"] and World.device == 0
 
 
 def routed_calls():
@@ -120,3 +135,15 @@ def test_an_error_leaves_the_current_stream(world):
 
 def routed_weights():
     return torch.zeros((2, 64, 32), dtype=U8), torch.zeros((2, 64, 2), dtype=U8)
+
+
+@pytest.mark.parametrize("name", sorted(routed_calls()))
+@pytest.mark.parametrize("device", [0, 1])
+def test_calls_run_on_the_device_of_their_arguments(world, monkeypatch, name, device):
+    """The default stream has one handle on all devices: the current device decides where a launch goes."""
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: device)
+    routed_calls()[name]()
+    assert world.devices == [device]
+    if device == 1:
+        with pytest.raises(ValueError, match="stream of cuda:0, the arguments are on cuda:1"):
+            routed_calls()[name](stream=Stream("s", 0x20))
