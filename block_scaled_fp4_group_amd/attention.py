@@ -121,6 +121,8 @@ class AttentionLayer:
             raise ValueError("prompt() takes the first tokens of at most max_requests requests")
         if not prefix and self.prefix_len:
             raise ValueError("prompt() of requests behind a prefix: use decode()")
+        if prefix and any(self.host_lens):
+            raise ValueError("the prefix comes before the first tokens of any request: theirs are rotated without it")
         self.new[first:first + len(lens)] = torch.tensor(list(lens), dtype=torch.int32).to(self.new.device)
         q, k, v = self._tokens(x, lens, first, 0)
         cu = self.cu[:len(lens) + 1]

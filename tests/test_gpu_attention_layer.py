@@ -139,3 +139,15 @@ def test_decoder_layer_example():
     import decoder_layer
     y = decoder_layer.main()
     assert y.shape == (8, 512) and torch.isfinite(y.float()).all()
+
+
+def test_prefix_after_requests_is_refused():
+    """The requests' keys in the cache are rotated to positions from 0 on; a prefix would come to lie on the same ones."""
+    for start in ("prompt", "decode"):
+        layer, _ = make_layer(requests=2, context=32)
+        x = dev_bf16(synth.random_bf16(1, (20, H)))
+        layer.prompt(x[:3], [0, 3]) if start == "prompt" else layer.decode(x[:1])
+        held = list(layer.host_lens)
+        with pytest.raises(ValueError, match="before the first tokens"):
+            layer.prompt(x, [20], prefix=True)
+        assert layer.host_lens == held and layer.prefix_len == 0
