@@ -36,8 +36,9 @@ class AttentionLayer:
     def __init__(self, weights: AttentionWeights, q_heads: int, kv_heads: int, k_dim: int, v_dim: int,
                  cos_sin: torch.Tensor, num_pages: int, page_size: int, max_requests: int, max_context: int,
                  max_tokens: int, interleaved: bool = False, eps: float = 1e-6, device="cuda"):
-        """``cos_sin``: float32 [positions, rotated dims] (cosines, then sines).  ``max_context``: most tokens of a
-        request, the prefix not counted (and most of the prefix); ``max_tokens``: most tokens of one step."""
+        """``cos_sin``: float32 [positions, rotated dims] (cosines, then sines), a row for each position that a token
+        takes: the prefix's length and the longest request's own together.  ``max_context``: most tokens of a request,
+        the prefix not counted (and most of the prefix); ``max_tokens``: most tokens of one step."""
         self.w, self.cos_sin, self.interleaved, self.eps = weights, cos_sin, interleaved, eps
         self.q_heads, self.kv_heads, self.k_dim, self.v_dim = q_heads, kv_heads, k_dim, v_dim
         self.page_size, self.max_requests, self.max_tokens = page_size, max_requests, max_tokens
@@ -86,6 +87,8 @@ class AttentionLayer:
         old = self.host_lens[first:first + n]
         if any(c + m > self.blocks * page for c, m in zip(old, new)):
             raise ValueError("a request grows over max_context")
+        if self.cos_sin is not None and base + max(c + m for c, m in zip(old, new)) > self.cos_sin.shape[0]:
+            raise ValueError(f"a token's position is past the {self.cos_sin.shape[0]} rows of cos_sin")
         need = sum(-(-(c + m) // page) - -(-c // page) for c, m in zip(old, new))
         if self.taken + need > self.free.numel():
             raise ValueError(f"{need} pages needed, {self.free.numel() - self.taken} free")

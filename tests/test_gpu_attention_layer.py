@@ -151,3 +151,20 @@ def test_prefix_after_requests_is_refused():
         with pytest.raises(ValueError, match="before the first tokens"):
             layer.prompt(x, [20], prefix=True)
         assert layer.host_lens == held and layer.prefix_len == 0
+
+
+def test_positions_past_the_table_are_refused():
+    """Past the last row every position would be turned by the same angle.  Prefix and own tokens count together."""
+    layer, _ = make_layer(requests=2, context=32)
+    x = dev_bf16(synth.random_bf16(1, (40, H)))
+    layer.cos_sin = layer.cos_sin[:22].contiguous()
+    with pytest.raises(ValueError, match="22 rows"):
+        layer.prompt(x[:24], [1, 23])
+    layer.prompt(x[:20], [20], prefix=True)
+    layer.decode(x[:2])
+    layer.decode(x[:1])                                               # position 21, the last
+    with pytest.raises(ValueError, match="22 rows"):
+        layer.decode(x[:1])
+    with pytest.raises(ValueError, match="22 rows"):
+        layer.decode(x[:2])
+    assert layer.host_lens == [2, 1, 20]
