@@ -81,7 +81,7 @@ class AttentionLayer:
         """Projection, slots, norm + rotation + cache write of the step's tokens: requests first .. of the table bring
         ``new`` tokens each.  -> (q, k, v) of the step."""
         T, n = x.shape[0], len(new)
-        if T < 1 or T != sum(new) or T > self.max_tokens:
+        if T < 1 or T != sum(new) or min(new) < 0 or T > self.max_tokens:
             raise ValueError(f"{T} tokens for requests that bring {sum(new)} (1 to {self.max_tokens})")
         page = self.page_size
         old = self.host_lens[first:first + n]

@@ -168,3 +168,15 @@ def test_positions_past_the_table_are_refused():
     with pytest.raises(ValueError, match="22 rows"):
         layer.decode(x[:2])
     assert layer.host_lens == [2, 1, 20]
+
+
+def test_negative_lengths_are_refused():
+    """Even where the sum fits: the host's lengths would differ from the GPU's, which counts a negative one as 0."""
+    layer, _ = make_layer(requests=2, context=32)
+    x = dev_bf16(synth.random_bf16(1, (4, H)))
+    for lens in ([5, -1], [-1, 5]):
+        with pytest.raises(ValueError, match="bring"):
+            layer.prompt(x, lens)
+    with pytest.raises(ValueError):
+        layer.prompt(x[:0], [])
+    assert layer.host_lens == [0, 0, 0] and layer.taken == 0
