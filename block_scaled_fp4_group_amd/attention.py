@@ -77,6 +77,16 @@ class AttentionLayer:
             self.offsets[T] = torch.tensor([0, T], dtype=torch.int32, device=self.free.device)
         return self.offsets[T]
 
+    def _check_rows(self, **rows: Optional[torch.Tensor]):
+        """The step's rows are read and written whole: bf16 [tokens, hidden], contiguous, on the layer's device.  Looked
+        at before anything of the step is done."""
+        T = rows["x"].shape[0]
+        for name, t in rows.items():
+            if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (T, self.o.shape[1])
+                                  or not t.is_contiguous() or t.device != self.o.device):
+                raise ValueError(f"{name} must be a contiguous bfloat16 tensor ({T}, {self.o.shape[1]}) on "
+                                 f"{self.o.device} (got {tuple(t.shape)}, {t.dtype}, {t.device})")
+
     def _tokens(self, x: torch.Tensor, new: Sequence[int], first: int, base: int):
         """Projection, slots, norm + rotation + cache write of the step's tokens: requests first .. of the table bring
         ``new`` tokens each.  -> (q, k, v) of the step."""
@@ -119,6 +129,7 @@ class AttentionLayer:
                y: Optional[torch.Tensor] = None) -> torch.Tensor:
         """First tokens of requests 0 .. len(lens) - 1, packed: x bf16 [sum(lens), hidden].  ``prefix``: of the shared
         prefix instead (one length).  Behind a prefix a request starts with ``decode`` steps."""
+        self._check_rows(x=x, residual=residual, y=y)
         first = self.max_requests if prefix else 0
         if len(lens) > (1 if prefix else self.max_requests) or any(self.host_lens[first:first + len(lens)]):
             raise ValueError("prompt() takes the first tokens of at most max_requests requests")
@@ -134,6 +145,7 @@ class AttentionLayer:
 
     def decode(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None) -> torch.Tensor:
         """One token of each of requests 0 .. B - 1: x bf16 [B, hidden]."""
+        self._check_rows(x=x, residual=residual, y=y)
         B = x.shape[0]
         if not 1 <= B <= self.max_requests:
             raise ValueError(f"{B} requests, at least 1 and at most {self.max_requests}")
