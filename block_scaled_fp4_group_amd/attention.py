@@ -120,10 +120,11 @@ class AttentionLayer:
 
     def _finish(self, x: torch.Tensor, residual: Optional[torch.Tensor], y: Optional[torch.Tensor]):
         T = x.shape[0]
-        grouped_gemm(self.a[:T].flatten(1), self.w.out, None, self._one(T), T, out=self.o[:T])
+        o = self.o[:T] if residual is not None or y is None else y
+        grouped_gemm(self.a[:T].flatten(1), self.w.out, None, self._one(T), T, out=o)
         if residual is None:
-            return self.o[:T]
-        return combine(self.o[:T], self.rows[:T], self.ones[:T], residual, y=self.y[:T] if y is None else y)
+            return o
+        return combine(o, self.rows[:T], self.ones[:T], residual, y=self.y[:T] if y is None else y)
 
     def prompt(self, x: torch.Tensor, lens: Sequence[int], residual: Optional[torch.Tensor] = None, prefix: bool = False,
                y: Optional[torch.Tensor] = None) -> torch.Tensor:

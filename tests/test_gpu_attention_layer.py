@@ -180,3 +180,14 @@ def test_negative_lengths_are_refused():
     with pytest.raises(ValueError):
         layer.prompt(x[:0], [])
     assert layer.host_lens == [0, 0, 0] and layer.taken == 0
+
+
+def test_results_go_to_y():
+    """With and without a residual: the result is written to y and returned."""
+    xb = dev_bf16(synth.random_bf16(1, (9, H)))
+    a, b = make_layer(requests=2, context=32)[0], make_layer(requests=2, context=32)[0]
+    for step in (lambda l, **kw: l.prompt(xb, [4, 5], **kw), lambda l, **kw: l.decode(xb[:2], **kw),
+                 lambda l, **kw: l.decode(xb[:2], residual=xb[:2], **kw)):
+        want = step(a).clone()
+        y = torch.full_like(want, float("nan"))
+        assert step(b, y=y) is y and torch.equal(y, want)
