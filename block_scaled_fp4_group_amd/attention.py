@@ -78,13 +78,13 @@ class AttentionLayer:
         return self.offsets[T]
 
     def _check_rows(self, **rows: Optional[torch.Tensor]):
-        """The step's rows are read and written whole: bf16 [tokens, hidden], contiguous, on the layer's device.  Looked
-        at before anything of the step is done."""
+        """The step's rows are read and written whole: bf16 [tokens, hidden], contiguous, 16-byte aligned, on the
+        layer's device.  Looked at before anything of the step is done."""
         T = rows["x"].shape[0]
         for name, t in rows.items():
             if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (T, self.o.shape[1])
-                                  or not t.is_contiguous() or t.device != self.o.device):
-                raise ValueError(f"{name} must be a contiguous bfloat16 tensor ({T}, {self.o.shape[1]}) on "
+                                  or not t.is_contiguous() or t.device != self.o.device or t.data_ptr() % 16):
+                raise ValueError(f"{name} must be a contiguous bfloat16 tensor, 16-byte aligned, ({T}, {self.o.shape[1]}) on "
                                  f"{self.o.device} (got {tuple(t.shape)}, {t.dtype}, {t.device})")
 
     def _tokens(self, x: torch.Tensor, new: Sequence[int], first: int, base: int):

@@ -40,6 +40,16 @@ def test_rows_that_do_not_fit_are_refused(layer, bad):
     assert layer.host_lens == [0, 0, 0] and layer.taken == 0
 
 
+@pytest.mark.parametrize("name", ["x", "residual", "y"])
+def test_rows_off_a_16_byte_boundary_are_refused(layer, name):
+    """Refused by a kernel's check, they would leave the cache a token ahead."""
+    off = torch.zeros(2 * H + 1, dtype=torch.bfloat16)[1:].view(2, H)
+    assert off.is_contiguous()
+    with pytest.raises(ValueError, match="16-byte aligned"):
+        layer.decode(**{"x": rows(2), name: off})
+    assert layer.host_lens == [0, 0, 0]
+
+
 def test_rows_that_fit_reach_the_step(layer):
     with pytest.raises(AssertionError, match="launched"):
         layer.decode(rows(2), residual=rows(2), y=rows(2))
