@@ -14,8 +14,9 @@
 // from the table, and the table's old entries are never written, so the update
 // in place needs no order between workgroups.
 //
-// Bound by latency: 64 requests of one token take 4.0 us, 1500 requests with
-// 140792 new tokens 8.7 us (1.2 MB written); an empty launch takes about 2.
+// Bound by latency: 64 requests of one token take 3.5 us, 1500 requests with
+// 140792 new tokens 7.7 us (1.2 MB written), launch after launch in a graph; an empty
+// launch takes about 2.
 #include "common.h"
 
 namespace moe {
@@ -67,16 +68,37 @@ __device__ __forceinline__ SlotRequest slot_request(const SlotArgs& a, int b) {
   return r;
 }
 
+// The last workgroup writes the offsets and the counts, the others the pages and the
+// tokens: what it reads for the counts is not waited for by theirs.
 __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotArgs a) {
   __shared__ int64_t tok[kSlotMaxRequests + 1], page[kSlotMaxRequests + 1];   // exclusive prefix sums
   __shared__ int64_t part[3][kSlotThreads / 64];
   const int B = a.num_requests, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const bool counts = blockIdx.x == gridDim.x - 1;
   // each thread sums its run of consecutive requests, the 256 sums are scanned
   // (each wave its own, then the waves' totals), and the runs are written out from
   // their starts
   const int per = (B + kSlotThreads - 1) / kSlotThreads;
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
-  int64_t nt = 0, np = 0;
+  int64_t nt = 0, np = 0, lost = 0;
+  if (counts) {
+    // Tokens that go into a page entered as -1 before: only the last page held has room
+    // for any.  (Without room some entry is read and not used.)  Eight requests' loads
+    // are under way at once.
+    for (int first = tid; first < B; first += 8 * kSlotThreads) {
+      SlotRequest r[8];
+      int32_t pg[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[i] = slot_request(a, min(first + i * kSlotThreads, B - 1));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        pg[i] = a.table[min(first + i * kSlotThreads, B - 1) * a.table_stride + max(r[i].held - 1, (int64_t)0)];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (first + i * kSlotThreads < B && !(pg[i] >= 0 && pg[i] < a.max_pages))
+          lost += min(r[i].fresh, (r[i].held << a.page_shift) - r[i].cached);
+    }
+  }
   for (int b = b0; b < b1; ++b) {
     const SlotRequest r = slot_request(a, b);
     nt += r.fresh;
@@ -96,7 +118,7 @@ __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotArgs a) {
     part[1][wv] = sp;
   }
   __syncthreads();
-  int64_t t0 = st - nt, p0 = sp - np, lost = 0, total = 0, pages = 0;
+  int64_t t0 = st - nt, p0 = sp - np, total = 0, pages = 0;
 #pragma unroll
   for (int w = 0; w < kSlotThreads / 64; ++w) {
     if (w < wv) {
@@ -122,13 +144,13 @@ __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotArgs a) {
     tok[B] = total;
     page[B] = pages;
   }
-  if (blockIdx.x == 0) {
+  if (counts) {
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) lost += __shfl_xor(lost, d);
     if (lane == 0) part[2][wv] = lost;
   }
   __syncthreads();
-  if (blockIdx.x == 0) {
+  if (counts) {
     for (int b = tid; b <= B; b += kSlotThreads) a.cu_new[b] = (int32_t)min(tok[b], (int64_t)0x7fffffff);
     if (tid == 0) {
       lost = 0;
@@ -138,8 +160,9 @@ __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotArgs a) {
       a.counts[1] = (int32_t)min(pages, (int64_t)0x7fffffff);
       a.counts[2] = (int32_t)min(lost, (int64_t)0x7fffffff);
     }
+    return;
   }
-  const int64_t step = (int64_t)gridDim.x * kSlotThreads, at = (int64_t)blockIdx.x * kSlotThreads + tid;
+  const int64_t step = (int64_t)(gridDim.x - 1) * kSlotThreads, at = (int64_t)blockIdx.x * kSlotThreads + tid;
   for (int64_t j = at; j < pages; j += step) {
     const int b = last_at_most(page, B, j);
     const int64_t block = slot_request(a, b).held + j - page[b];
@@ -188,7 +211,8 @@ moe_status launch_kv_slots(const int32_t* cached, const int32_t* fresh, int B, c
   a.position_base = position_base;
   a.num_free = num_free;
   const int64_t blocks = (max_new + kSlotThreads - 1) / kSlotThreads;
-  const uint32_t grid = (uint32_t)(blocks < 1 ? 1 : (blocks > 512 ? 512 : blocks));
+  // two workgroups of 64 KB of LDS fit a CU: 512 run at once (one more: 7.8 -> 10.9 us)
+  const uint32_t grid = 1 + (uint32_t)(blocks < 1 ? 1 : (blocks > 511 ? 511 : blocks));
   hipLaunchKernelGGL(kv_slots_kernel, dim3(grid), dim3(kSlotThreads), 0, stream, a);
   return launch_status("moe_kv_slots");
 }

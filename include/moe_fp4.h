@@ -459,8 +459,8 @@ typedef struct {
  *                  + (cached_lens[b] + i) % page_size
  * position_base: the length of a prefix that lies before every request's own
  * tokens (moe_attn_decode).  A page that the free list no longer has is entered
- * as -1; tokens in it, and tokens past max_blocks pages, get slot -1 (and no
- * page).  Entries t >= cu_new[num_requests] of slots / positions are -1 / 0.
+ * as -1; tokens in it (also those of later calls), and tokens past max_blocks
+ * pages, get slot -1 (and no page).  Entries t >= cu_new[num_requests] of slots / positions are -1 / 0.
  *   cached_lens, new_lens int32 [num_requests]; free_pages int32 [num_free];
  *   block_table int32 [num_requests, max_blocks], rows table_stride apart;
  *   slots, positions int32 [max_new]; cu_new int32 [num_requests + 1];

@@ -948,3 +948,30 @@ def test_outputs_of_another_stream_outlive_their_readers(name):
     torch.cuda.synchronize()
     assert all(torch.equal(g, w) for g, w in zip(read, want))
     del junk
+
+
+# ----------------------------------------------- slots of requests that ran out of pages before
+@pytest.mark.parametrize("B,page,blocks", [(1, 16, 4), (70, 16, 8), (300, 4, 30), (1500, 32, 12), (4096, 8, 16)])
+def test_kv_slots_behind_a_short_free_list(B, page, blocks):
+    """Steps one after another where the free list ends inside the first: tokens that go into a page entered as -1 have
+    no slot, and are counted in every step."""
+    say(f"kv_slots after the pages ran out: B={B} page={page}")
+    rng = np.random.default_rng(B)
+    table = np.full((B, blocks), -1, np.int64)
+    dt = dev_i32(table)
+    cached, lost = np.zeros(B, np.int64), []
+    for step in range(4):
+        new = rng.integers(0, 2 * page if step == 0 else 3, B)
+        if B == 1:
+            new[:] = 10 if step == 0 else 1
+        free = rng.permutation(8 * B)[:(B // 2 if step == 0 else 3)] if B > 1 else np.zeros(0, np.int64)
+        most = int(new.sum()) + 1
+        want = oa.kv_slots(cached, new, free, table, page, most)
+        got = moe.kv_slots(dev_i32(cached), dev_i32(new), dev_i32(free), dt, page, most)
+        torch.cuda.synchronize()
+        for name, g, w in zip(("table", "slots", "positions", "cu_new", "counts"), (dt, *got), want):
+            assert np.array_equal(host(g), w), (step, name)
+        assert host(got[3])[2] == (host(got[0])[:new.sum()] < 0).sum()
+        table, cached = want[0], cached + new
+        lost.append(int(want[4][2]))
+    assert all(lost)
