@@ -24,7 +24,8 @@
 // of a key head share out evenly, whatever the lengths: each takes one run of the
 // list, across as many requests as it covers, without emptying its load pipeline
 // at more than the requests' ends.  All workgroups of a launch fit the chip at
-// once, so the wide ones' matrix work and the narrow ones' reads run side by side.
+// once, so the wide ones' matrix work and the narrow ones' reads run side by side
+// (decode_plan says when there are more).
 //
 // Measured: one request with 131072 own keys x 32/8 heads x 128: 83 us and 6 for the
 // join, 6.5 TB/s of the 6.9 that contiguous reads reach; 96 requests behind 32768
@@ -695,8 +696,17 @@ static DecodePlan decode_plan(int64_t B, int q_heads, int kv_heads, int64_t pref
   }
   p.chunk_p = tiles_p == 0 ? 0 : (int32_t)(up(tiles_p, parts) * 64);
   p.parts_p = tiles_p == 0 ? 0 : (int32_t)up(prefix_len, p.chunk_p);
-  // runs of the own keys: the rest of the chip, at least two narrow tiles in each
-  const int64_t left = (kDecSlots - p.parts_p * per_part) / per_run;
+  // Runs of the own keys, at least two narrow tiles in each: the rest of the chip.  Many
+  // rows on few prefix keys (one part) leave little of it or nothing, but end early: then
+  // as many runs as the whole chip holds, the last of which start when those are done,
+  // if that is sooner.  (512 requests x 64/8 x 128 behind 100 tokens, up to 2048 own keys:
+  // 576 -> 462 us; 1000 requests, whose prefix leaves room for one run: 33.6 -> 0.91 ms.)
+  int64_t places = kDecSlots - p.parts_p * per_part;
+  if (p.parts_p == 1 && max_len > 0) {
+    const int64_t prefix = up(per_part, kDecSlots) * (p.chunk_p / 64) * cost_p;
+    if (places < per_run || prefix + work_s / kDecSlots < work_s / places) places = kDecSlots;
+  }
+  const int64_t left = places / per_run;
   p.runs = max_len == 0 ? 0 : (int32_t)std::max<int64_t>(1, std::min(left, up(B * up(max_len, kNarrowKeys), 2)));
   return p;
 }

@@ -975,3 +975,15 @@ def test_kv_slots_behind_a_short_free_list(B, page, blocks):
         table, cached = want[0], cached + new
         lost.append(int(want[4][2]))
     assert all(lost)
+
+
+# ----------------------------------------------- more workgroups than the chip holds
+@pytest.mark.parametrize("B,Hq,Hkv,prefix,longest,D", [(520, 128, 16, 100, 700, 64), (300, 128, 8, 40, 900, 128)])
+def test_attn_decode_many_rows_behind_a_short_prefix(B, Hq, Hkv, prefix, longest, D):
+    """The prefix's row blocks take most of the chip or all of it; the own keys' workgroups come behind them."""
+    say(f"attn_decode {B} requests x {Hq}/{Hkv} x {D} behind {prefix}")
+    lens = [int(n) for n in np.random.default_rng(B).integers(0, 40, B)]
+    lens[3], lens[B - 2] = longest, 0
+    assert makes_parts(lens, prefix, Hq, Hkv, D, D)
+    _, _, case, *_ = run_decode(B, lens, prefix, 16, Hq, Hkv, D, D)
+    check_decode(*case, f"attn_decode {B} x {Hq}/{Hkv}")
