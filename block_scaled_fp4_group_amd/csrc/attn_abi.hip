@@ -108,7 +108,7 @@ moe_status moe_qk_norm_rope(const moe_heads* q, const moe_heads* k, const moe_he
   const char* fn = "moe_qk_norm_rope";
   set_error("");
   MOE_CHECK(p, "%s: params is NULL", fn);
-  MOE_CHECK(T >= 0 && p->q_heads >= 1 && p->kv_heads >= 1 && p->q_heads <= 65536 && p->kv_heads <= 65536,
+  MOE_CHECK(T >= 0 && T <= 0x7fffffff && p->q_heads >= 1 && p->kv_heads >= 1 && p->q_heads <= 65536 && p->kv_heads <= 65536,
             "%s: bad sizes", fn);
   MOE_CHECK(p->eps >= 0.0f && std::isfinite(p->eps), "%s: eps must be finite and not negative", fn);
   MOE_CHECK(p->rot_dim >= 0 && p->rot_dim <= p->head_dim && p->rot_dim % 16 == 0,
