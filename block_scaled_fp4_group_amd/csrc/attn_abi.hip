@@ -189,9 +189,16 @@ moe_status moe_attn_prompt(const moe_heads* q, const moe_heads* k, const moe_hea
                             *p, *out, lse, workspace, stream);
 }
 
+// sizes that a plan is made for: rows and keys in 31 bits
+static bool decode_sizes_fit(int32_t num_requests, int64_t prefix_len, int64_t max_len, const moe_attn_params& p) {
+  return max_len <= 0x7fffffff - 64 && prefix_len <= 0x7fffffff - 64 && num_requests * ((max_len + 31) / 32) < 0x7fffffff &&
+         (int64_t)num_requests * p.q_heads < ((int64_t)1 << 31);
+}
+
 size_t moe_attn_decode_workspace_bytes(int32_t num_requests, int64_t prefix_len, int64_t max_len,
                                        const moe_attn_params* p) {
-  if (!sizes_of_heads(p) || num_requests <= 0 || prefix_len < 0 || max_len < 0 || prefix_len > 0x7fffffff || max_len > 0x7fffffff)
+  if (!sizes_of_heads(p) || num_requests <= 0 || prefix_len < 0 || max_len < 0 ||
+      !decode_sizes_fit(num_requests, prefix_len, max_len, *p))
     return 0;
   return attn_decode_ws_bytes(num_requests, p->q_heads, p->kv_heads, p->k_dim, p->v_dim, prefix_len, max_len);
 }
@@ -218,11 +225,9 @@ moe_status moe_attn_decode(const moe_heads* q, const moe_kv_cache* cache, const 
   MOE_CHECK(prefix_len <= (int64_t)prefix_blocks * cache->page_size, "%s: prefix_len %lld needs more than %d pages", fn,
             (long long)prefix_len, prefix_blocks);
   MOE_CHECK(prefix_len == 0 || prefix_table, "%s: prefix_table is NULL", fn);
-  MOE_CHECK(max_len <= 0x7fffffff - 64 && prefix_len <= 0x7fffffff - 64 && num_requests * ((max_len + 31) / 32) < 0x7fffffff,
-            "%s: too many keys", fn);
+  MOE_CHECK(decode_sizes_fit(num_requests, prefix_len, max_len, *p), "%s: too many keys or rows", fn);
   MOE_CHECK(aligned4(lse), "%s: lse not 4-byte aligned", fn);
-  MOE_CHECK(attn_decode_grid(num_requests, p->q_heads, p->kv_heads, p->k_dim, p->v_dim, prefix_len, max_len) < ((int64_t)1 << 31) &&
-                (int64_t)num_requests * p->q_heads < ((int64_t)1 << 31),
+  MOE_CHECK(attn_decode_grid(num_requests, p->q_heads, p->kv_heads, p->k_dim, p->v_dim, prefix_len, max_len) < ((int64_t)1 << 31),
             "%s: too many rows", fn);
   const size_t need = attn_decode_ws_bytes(num_requests, p->q_heads, p->kv_heads, p->k_dim, p->v_dim, prefix_len, max_len);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))) {
