@@ -13,6 +13,7 @@ import dataclasses
 import functools
 import inspect
 import os
+import sysconfig
 from typing import Optional
 
 import torch  # loads the HIP runtime first, so the library binds to the same one
@@ -524,7 +525,8 @@ def attn_decode_workspace_bytes(num_requests: int, prefix_len: int, max_len: int
 
 
 def _setup_calls():
-    path = os.path.join(_PKG, "_calls.so")
+    # this Python's own: another one's has another tag (an extension without a tag would be taken by any)
+    path = os.path.join(_PKG, "_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
     if not os.path.exists(path):
         raise ImportError(f"{path} is not built; run `python block_scaled_fp4_group_amd/build.py`")
     from . import _calls

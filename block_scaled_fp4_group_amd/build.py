@@ -7,7 +7,7 @@
 Each HIP source compiles to its own object in parallel (the GEMM files hold
 many kernel instantiations), then one link step writes libmoefp4.so.  The
 Python side of the attention calls (csrc/calls.cpp, plain CPython) becomes
-_calls.so, linked to it.
+_calls.<this Python's tag>.so, linked to it.
 """
 from __future__ import annotations
 
@@ -21,7 +21,7 @@ import sysconfig
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libmoefp4.so")
-CALLS = os.path.join(PKG, "_calls.so")
+CALLS = os.path.join(PKG, "_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))   # this Python's own
 OBJ_DIR = os.path.join(PKG, "_build")
 ARCH = "gfx950"
 
@@ -96,6 +96,9 @@ def build(verbose: bool = True, jobs: int = 0) -> str:
         sys.stderr.write("\n".join(msgs) + "\n")
         raise RuntimeError(f"the compiler failed on calls.cpp with exit code {rc}")
     os.replace(tmp, CALLS)
+    untagged = os.path.join(PKG, "_calls.so")
+    if CALLS != untagged and os.path.exists(untagged):                # of before the tag: any Python would load it
+        os.remove(untagged)
     if verbose:
         print(f"built {LIB} from {len(srcs)} sources, {CALLS}", flush=True)
     return LIB
