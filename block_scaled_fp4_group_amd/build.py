@@ -49,10 +49,13 @@ def link_command(objs: list, out: str) -> list:
 
 
 def calls_command(out: str) -> list:
-    """Host code only: the system's compiler (the HIP header gives the stream's type)."""
+    """Host code only, by the compiler that builds the rest (the HIP header gives the stream's type)."""
+    python = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(python, "Python.h")):
+        raise RuntimeError(f"calls.cpp needs Python's headers, and {python}/Python.h is not there")
     rocm = os.path.dirname(os.path.dirname(hipcc())) if os.path.sep in hipcc() else "/opt/rocm"
-    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
-            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(rocm, "include"), "-I", os.path.join(ROOT, "include"),
+    return [hipcc(), "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+            "-I", python, "-I", os.path.join(rocm, "include"), "-I", os.path.join(ROOT, "include"),
             os.path.join(PKG, "csrc", "calls.cpp"), "-o", out, "-L", PKG, "-lmoefp4", "-Wl,-rpath,$ORIGIN"]
 
 
