@@ -45,6 +45,11 @@ class AttentionLayer:
         self.blocks = -(-max_context // page_size)
         dev, bf16, i32 = torch.device(device), torch.bfloat16, torch.int32
         H, n = weights.out.packed.shape[1], weights.qkv.packed.shape[1]
+        want = (1, (q_heads + kv_heads) * k_dim + kv_heads * v_dim, H // 2), (1, H, q_heads * v_dim // 2)
+        got = tuple(weights.qkv.packed.shape), tuple(weights.out.packed.shape)
+        if got != want:                       # the projections read rows of their weights' width
+            raise ValueError(f"packed weights of the projections are {got[0]} and {got[1]}, these heads need {want[0]} "
+                             f"and {want[1]}")
         self.k_cache = torch.zeros((num_pages, page_size, kv_heads, k_dim), dtype=bf16, device=dev)
         self.v_cache = torch.zeros((num_pages, page_size, kv_heads, v_dim), dtype=bf16, device=dev)
         # one row per request, the last for the prefix

@@ -7,6 +7,10 @@ moe = pytest.importorskip("block_scaled_fp4_group_amd")
 H, HQ, HKV, D = 512, 4, 2, 64
 
 
+def weights(n, k):
+    return moe.Weights(torch.zeros((1, n, k // 2), dtype=torch.uint8), torch.zeros((1, n, k // 32), dtype=torch.uint8))
+
+
 @pytest.fixture
 def layer(monkeypatch):
     """A layer in host memory; a launch would be an error."""
@@ -15,8 +19,6 @@ def layer(monkeypatch):
     for name in ("grouped_gemm", "kv_slots", "qk_norm_rope", "attn_prompt", "attn_decode", "combine"):
         monkeypatch.setattr(moe.attention, name, no_launch)
 
-    def weights(n, k):
-        return moe.Weights(torch.zeros((1, n, k // 2), dtype=torch.uint8), torch.zeros((1, n, k // 32), dtype=torch.uint8))
     w = moe.AttentionWeights(weights((HQ + 2 * HKV) * D, H), weights(H, HQ * D))
     return moe.AttentionLayer(w, HQ, HKV, D, D, torch.zeros((64, D)), 8, 16, 2, 32, 32, device="cpu")
 
@@ -53,3 +55,12 @@ def test_rows_off_a_16_byte_boundary_are_refused(layer, name):
 def test_rows_that_fit_reach_the_step(layer):
     with pytest.raises(AssertionError, match="launched"):
         layer.decode(rows(2), residual=rows(2), y=rows(2))
+
+
+@pytest.mark.parametrize("qkv,out", [((HQ * D, H), (H, HQ * D)), (((HQ + 2 * HKV) * D, 2 * H), (H, HQ * D)),
+                                     (((HQ + 2 * HKV) * D, H), (H, 2 * HQ * D)), (((HQ + 2 * HKV) * D, H), (2 * H, HQ * D))])
+def test_projections_that_do_not_fit_the_heads_are_refused(qkv, out):
+    """A projection reads rows as wide as its weights, from buffers made for the heads."""
+    with pytest.raises(ValueError, match="these heads need"):
+        moe.AttentionLayer(moe.AttentionWeights(weights(*qkv), weights(*out)), HQ, HKV, D, D, torch.zeros((64, D)), 8, 16, 2, 32,
+                           32, device="cpu")
