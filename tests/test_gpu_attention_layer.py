@@ -191,3 +191,30 @@ def test_results_go_to_y():
         want = step(a).clone()
         y = torch.full_like(want, float("nan"))
         assert step(b, y=y) is y and torch.equal(y, want)
+
+
+@pytest.mark.parametrize("D,Dv", [(64, 64), (128, 128), (192, 128)])
+def test_prompt_then_decode_agrees_with_prompt(D, Dv):
+    """Requests that are read as prompts and then answered: token t of each gives the output that it has in a whole
+    prompt, within the rounding of the attention's weights (as where a prefix and decode steps are compared)."""
+    say(f"attention layer: prompt, then decode {D}/{Dv}")
+    lens, cuts = [33, 18, 38], [30, 16, 37]                            # 16: the next token begins a page
+    first = np.concatenate([[0], np.cumsum(lens)])
+    x = dev_bf16(synth.random_bf16(11, (sum(lens), H)))
+    whole, (_, wo, *_) = make_layer(D, Dv)
+    y = whole.prompt(x, lens, residual=x).clone()
+    vmax = float(whole.v_cache.float().abs().max())
+    bound = 4 * R * vmax * np.abs(wo).sum(-1).max() + 2 * R * float(y.abs().max())   # (and the residual sum's own rounding)
+    layer, _ = make_layer(D, Dv)
+    xs = torch.cat([x[a:a + c] for a, c in zip(first, cuts)])
+    yp = layer.prompt(xs, cuts, residual=xs).clone()
+    at = 0
+    for a, c in zip(first, cuts):
+        assert torch.equal(yp[at:at + c], y[a:a + c])                  # rows do not depend on the rows after them
+        at += c
+    for i, n in enumerate((3, 2, 1)):                                  # all requests, then the first ones
+        rows = torch.tensor([f + c + i for f, c in zip(first, cuts[:n])], device="cuda")
+        xd = x[rows].contiguous()
+        yd = layer.decode(xd, residual=xd)
+        assert (yd.float() - y[rows].float()).abs().max() <= bound, i
+    assert layer.host_lens == lens + [0, 0]
