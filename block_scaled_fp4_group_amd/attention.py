@@ -12,6 +12,12 @@ that all requests share is kept once and lies before each request's own tokens
 (positions count from the prefix's start).  The host keeps the lengths that it
 hands out and so knows how many pages a step takes; tables, slots and positions
 are built on the GPU.
+
+One generation of requests: prompt() reads the first tokens of requests 0 .. n - 1
+together, decode() adds one token to each of requests 0 .. B - 1.  A request does not
+enter while others decode, gives no pages back, and takes no second prompt (attention
+of a prompt on keys in the cache is not built); behind a prefix its tokens come by
+decode() alone.
 """
 from __future__ import annotations
 

@@ -21,8 +21,8 @@
 // of the output itself).
 //
 // Rates: a wave's tile of 64 keys x 128 takes 32 MFMAs of 32 cycles (16 for the
-// scores, 16 for the values) and about 230 vector instructions; two waves per SIMD
-// overlap them.  The LDS reads have no bank conflicts in either product.
+// scores, 16 for the values) and about 230 vector instructions; the two to four
+// waves per SIMD (by head size) overlap them.  The LDS reads have no bank conflicts in either product.
 //
 // Layouts measured on the chip: 32x32x16 operands hold row l % 32, k = 8 (l / 32)
 // + j, j < 8; the accumulator holds column l % 32, row 8 (i / 4) + 4 (l / 32) +

@@ -650,9 +650,11 @@ __global__ __launch_bounds__(kSmallWaves * 64) void attn_decode_small_kernel(Dec
 // included, in as many rounds as the chip needs at a workgroup per CU; or the
 // reading of the own keys (half of the bound) at a little under the parts' rate.
 // Parts: 10000 for two launches, and the reading of all keys once.
-// Own keys up to 512, 32 requests of 8 key heads: 8 us for 16; 2000 behind a prefix
-// of 2000: 33 for 24.  Within 5% of the better one in 9 of 10 of 216 sizes tried, 1
-// to 96 requests with 16 to 2048 own keys.
+// 32/8 heads x 128: 32 requests with up to 700 own keys 13.7 us alone, 18.4 in parts; one
+// with 2048 behind a prefix of 2000 27.8 and 12.7.  Within 5% of the better one at 338 of 360 sizes tried,
+// 1 to 96 requests with up to 16 to 2048 own keys behind 0 to 2000, all head sizes
+// (of 64-wide ones' workgroups a CU holds two: 88 of 90).  The others are for the most
+// part batches of 33 to 64 rows behind 2000 keys, up to 1.5 times slower in parts.
 static bool small_is_sooner(int64_t B, int64_t G, int64_t kv_heads, int64_t prefix_len, int64_t max_len, int64_t dims) {
   if (G > 16) return false;
   const int64_t tiles_p = (prefix_len + 31) / 32, tiles_s = (max_len + 31) / 32, rounds = (B * kv_heads + 255) / 256;
@@ -679,7 +681,9 @@ static DecodePlan decode_plan(int64_t B, int q_heads, int kv_heads, int64_t pref
   // rows, 2.7 us of its share of the reads; 128-wide heads).  The own lengths are not
   // known here: one is counted at the bound, the others at half, and each request once
   // more for starting on it.  (One request with 7647 keys behind 12490, 32/8 heads: 31
-  // us with half of the bound and equal units for the narrow ones, 24 us so.)
+  // us with half of the bound and equal units for the narrow ones, 24 us so.  Over 80
+  // sizes own keys at 7 or 14 units take 3% longer on average, all own lengths at half 1%,
+  // equal units for the narrow ones 1%.)
   // (64 requests behind 8192 tokens: 79 us with shares by keys alone, of which the
   // prefix's workgroups worked 39.)
   const int64_t tiles_p = up(prefix_len, 64), tiles_s = max_len == 0 ? 0 : up((B + 1) * up(max_len, 64), 2) + B;

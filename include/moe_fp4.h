@@ -27,6 +27,8 @@
  *     The library allocates nothing and keeps no state between calls.
  *   - Every call is asynchronous on `stream`; results are deterministic
  *     (no floating-point atomics; integer atomics only where the sum is exact).
+ *     The launch goes to the current device, which has to be the stream's and
+ *     the data's.
  *   - Arguments are checked on the host before anything is launched; on an
  *     error nothing is written and the call returns a non-zero moe_status.
  *     moe_last_error() gives a message for the calling thread's last failure.
@@ -424,7 +426,10 @@ moe_status moe_quantize_nvfp4_planes(const void* x, int64_t rows, int32_t k, flo
  *
  * Heads: bf16 [tokens, heads, dim], strides in elements, dim contiguous; data
  * 16-byte aligned and strides multiples of 8.  Input rows may overlap or repeat
- * (stride 0); output rows may not.
+ * (stride 0); output rows may not, nor with an input's (moe_qk_norm_rope says
+ * where they may be the input's own).
+ * The attention calls' sums of values are float and divided at the end: values
+ * whose magnitude times 2^8 times their number passes 2^127 can overflow there.
  * Head sizes (k_dim, v_dim) of the attention calls: (64, 64), (128, 128) and
  * (192, 128), the asymmetric key / value heads of the "AxionML /
  * MiMo-V2.6-Flash-MOPD-NVFP4" deployment; others give MOE_ERR_UNSUPPORTED.
@@ -461,7 +466,8 @@ typedef struct {
  * tokens (moe_attn_decode).  A page that the free list no longer has is entered
  * as -1; tokens in it (also those of later calls), and tokens past max_blocks
  * pages, get slot -1 (and no page).  Entries t >= cu_new[num_requests] of slots / positions are -1 / 0.
- *   cached_lens, new_lens int32 [num_requests]; free_pages int32 [num_free];
+ *   cached_lens, new_lens int32 [num_requests]; free_pages int32 [num_free],
+ *   pages of the cache;
  *   block_table int32 [num_requests, max_blocks], rows table_stride apart;
  *   slots, positions int32 [max_new]; cu_new int32 [num_requests + 1];
  *   counts int32 [3]: free pages taken, pages needed, new tokens without a slot
