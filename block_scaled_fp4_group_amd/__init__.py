@@ -34,7 +34,9 @@ EXPORTS = ("moe_status_string", "moe_last_error", "moe_version", "moe_route", "m
            "moe_fp4_tile_weights", "moe_route_permute_noalloc", "moe_quantize_mxfp8", "moe_quantize_nvfp4_planes",
            "moe_route_gemv_workspace_bytes", "moe_route_gemv", "moe_reap_saliency_accumulate", "moe_fp4_compact_mx",
            "moe_kv_slots", "moe_qk_norm_rope", "moe_attn_prompt_workspace_bytes",
-           "moe_attn_prompt", "moe_attn_decode_workspace_bytes", "moe_attn_decode")
+           "moe_attn_prompt", "moe_attn_decode_workspace_bytes", "moe_attn_decode", "moe_qk_norm_rope_fp4",
+           "moe_attn_decode_fp4_workspace_bytes", "moe_attn_decode_fp4", "moe_kv_gather", "moe_kv_gather_fp4", "moe_kv_fork",
+           "moe_kv_free_pages", "moe_kv_compact_workspace_bytes", "moe_kv_compact", "moe_block_norm")
 
 
 class RouteParams(ctypes.Structure):
@@ -79,6 +81,20 @@ class RopeParams(ctypes.Structure):
 class AttnParams(ctypes.Structure):
     _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("k_dim", ctypes.c_int32),
                 ("v_dim", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class KvCacheFp4(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("k_global", ctypes.c_float),
+                ("v_global", ctypes.c_float)]
+
+
+class PageBuffers(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p * 8), ("page_bytes", ctypes.c_int64 * 8), ("count", ctypes.c_int32)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
 
 
 def _load() -> ctypes.CDLL:
@@ -139,6 +155,28 @@ def _load() -> ctypes.CDLL:
     lib.moe_attn_decode.restype = i32
     lib.moe_attn_decode.argtypes = [heads, cache, vp, i64, i32, vp, i32, i64, vp, i32, i64, ctypes.POINTER(AttnParams),
                                     heads, vp, vp, sz, vp]
+    cache4, buffers, rows = ctypes.POINTER(KvCacheFp4), ctypes.POINTER(PageBuffers), ctypes.POINTER(Rows)
+    lib.moe_qk_norm_rope_fp4.restype = i32
+    lib.moe_qk_norm_rope_fp4.argtypes = [heads, heads, heads, i64, ctypes.POINTER(RopeParams), vp, vp, vp, vp, heads, heads,
+                                         cache4, vp, vp]
+    lib.moe_attn_decode_fp4_workspace_bytes.restype = sz
+    lib.moe_attn_decode_fp4_workspace_bytes.argtypes = [i32, i64, i64, ctypes.POINTER(AttnParams)]
+    lib.moe_attn_decode_fp4.restype = i32
+    lib.moe_attn_decode_fp4.argtypes = [heads, cache4, vp, i64, i32, vp, i32, i64, vp, i32, i64, ctypes.POINTER(AttnParams),
+                                        heads, vp, vp, sz, vp]
+    for f, c in ((lib.moe_kv_gather, cache), (lib.moe_kv_gather_fp4, cache4)):
+        f.restype = i32
+        f.argtypes = [c, i32, i32, i32, vp, i64, i32, vp, i32, i64, vp, i32, i64, heads, heads, vp]
+    lib.moe_kv_fork.restype = i32
+    lib.moe_kv_fork.argtypes = [vp, i64, i32, i32, vp, vp, vp, i32, vp, i64, i32, buffers, i64, vp, vp]
+    lib.moe_kv_free_pages.restype = i32
+    lib.moe_kv_free_pages.argtypes = [vp, i64, i32, i32, vp, i32, i64, vp, vp, vp]
+    lib.moe_kv_compact_workspace_bytes.restype = sz
+    lib.moe_kv_compact_workspace_bytes.argtypes = [i64]
+    lib.moe_kv_compact.restype = i32
+    lib.moe_kv_compact.argtypes = [vp, i64, i32, i32, vp, i32, buffers, i64, vp, i64, vp, vp, sz, vp]
+    lib.moe_block_norm.restype = i32
+    lib.moe_block_norm.argtypes = [rows, i64, i32, rows, vp, rows, vp, f32, vp, f32, rows, rows, vp]
     lib.moe_fp4_tile_weights.restype = i32
     lib.moe_fp4_tile_weights.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp]
     return lib
@@ -501,7 +539,7 @@ def quantize_nvfp4_planes(x: torch.Tensor, input_scale: float = 1.0, planes=None
 
 
 # ----------------------------------------------------------------- attention
-# kv_slots, qk_norm_rope, attn_prompt and attn_decode are in _calls (csrc/calls.cpp):
+# These calls and those around their cache are in _calls (csrc/calls.cpp):
 # their kernels run in a few microseconds, and so do their checks there.
 def _bad(t, name: str, dtype, ndim: int, index: int):
     if not isinstance(t, torch.Tensor):
@@ -524,6 +562,41 @@ def attn_decode_workspace_bytes(num_requests: int, prefix_len: int, max_len: int
     return int(lib.moe_attn_decode_workspace_bytes(num_requests, prefix_len, max_len, p))
 
 
+def attn_decode_fp4_workspace_bytes(num_requests: int, prefix_len: int, max_len: int, q_heads: int, kv_heads: int, k_dim: int,
+                                    v_dim: int) -> int:
+    p = AttnParams(q_heads, kv_heads, k_dim, v_dim, 1.0)
+    return int(lib.moe_attn_decode_fp4_workspace_bytes(num_requests, prefix_len, max_len, p))
+
+
+def kv_compact_workspace_bytes(num_pages: int) -> int:
+    return int(lib.moe_kv_compact_workspace_bytes(num_pages))
+
+
+@dataclasses.dataclass
+class Fp4Cache:
+    """A paged cache held in NVFP4: value = E2M1 code x E4M3 scale (one for 16 values) x global scale (a power of two)."""
+    k: torch.Tensor                       # u8 [pages, heads, page_size, k_dim / 2]
+    k_scale: torch.Tensor                 # u8 [pages, heads, page_size, k_dim / 16]
+    v: torch.Tensor                       # u8 [pages, heads, page_size, v_dim / 2]
+    v_scale: torch.Tensor                 # u8 [pages, heads, v_dim / 16, page_size]
+    k_global: float = 1.0
+    v_global: float = 1.0
+
+    @classmethod
+    def zeros(cls, num_pages: int, page_size: int, kv_heads: int, k_dim: int, v_dim: int, k_global: float = 1.0,
+              v_global: float = 1.0, device="cuda") -> "Fp4Cache":
+        def u8(*shape):
+            return torch.zeros(shape, dtype=torch.uint8, device=device)
+        return cls(u8(num_pages, kv_heads, page_size, k_dim // 2), u8(num_pages, kv_heads, page_size, k_dim // 16),
+                   u8(num_pages, kv_heads, page_size, v_dim // 2), u8(num_pages, kv_heads, v_dim // 16, page_size), k_global,
+                   v_global)
+
+    @property
+    def buffers(self) -> tuple:
+        """The pool's tensors, for the page calls."""
+        return self.k, self.k_scale, self.v, self.v_scale
+
+
 def _setup_calls():
     # this Python's own: another one's has another tag (an extension without a tag would be taken by any)
     path = os.path.join(_PKG, "_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
@@ -541,6 +614,9 @@ def _setup_calls():
 _calls = _setup_calls()
 kv_slots, qk_norm_rope, attn_prompt, attn_decode = (
     _calls.kv_slots, _calls.qk_norm_rope, _calls.attn_prompt, _calls.attn_decode)
+qk_norm_rope_fp4, attn_decode_fp4, kv_gather, kv_gather_fp4, kv_fork, kv_free_pages, kv_compact, block_norm = (
+    _calls.qk_norm_rope_fp4, _calls.attn_decode_fp4, _calls.kv_gather, _calls.kv_gather_fp4, _calls.kv_fork,
+    _calls.kv_free_pages, _calls.kv_compact, _calls.block_norm)
 
 from .layer import MoELayer, LayerWeights  # noqa: E402  (composition of the calls above)
 from .attention import AttentionLayer, AttentionWeights  # noqa: E402

@@ -33,6 +33,8 @@
 #include "common.h"
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 namespace moe {
@@ -46,6 +48,61 @@ __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
 __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// The matrix cores' operand type.  bf16: keys, values and weights as they come.  f16
+// (caches held in 4 bits): a code times its block's scale is exact in it (6 significant
+// bits, 2^-10 to 2688), and a weight keeps 11 bits.  Its weights are lifted by 2^kLift, so
+// that those down to 2^-31 of a row's largest are not lost below its range (2^-24) while the
+// largest, 2^(kLift + kSlack) (see weights()) and twice that where m is rounded, stay under
+// 65504.
+struct AttnBf16 {
+  typedef bf16x8 v8;
+  static constexpr float kLift = 0.0f, kSlack = 8.0f;
+  static __device__ __forceinline__ f32x16 mfma(v8 a, v8 b, f32x16 c) { return mfma32(a, b, c); }
+  static __device__ __forceinline__ uint32_t pair(float a, float b) { return cvt_bf16x2(a, b); }
+};
+struct AttnF16 {
+  typedef f16x8 v8;
+  static constexpr float kLift = 7.0f, kSlack = 7.0f;
+  static __device__ __forceinline__ f32x16 mfma(v8 a, v8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pair(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
+  }
+};
+
+// a * b rounded, whatever comes after it
+__device__ __forceinline__ float mul_rounded(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
+}
+// Scores times c, less base, are formed in one rounding; base itself, the maximum's, was
+// rounded before.  Of scores over 2^20 (base 2) that difference would pass 2^-4 and lift
+// f16 weights out of their range: there s c is rounded like the maximum's.  The row's
+// own choice: (c, 1) or (1, c), to multiply the scores with before and in the exponent.
+__device__ __forceinline__ float2 split_scale(float base, float c) {
+  return fabsf(base) > 1048576.0f ? float2{c, 1.0f} : float2{1.0f, c};
+}
+
+// 8 query values as f16, times 2^-e.  e takes a row's largest magnitude to [2^14, 2^15): a
+// value of bf16's 8 bits is then exact down to 2^-28 of the largest and off by 2^-39 of it
+// below.  The row's scores are multiplied by 2^e (AttnWave and the like take that with
+// their scale).
+__device__ __forceinline__ f16x8 query_f16(u32x4 w, int e) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = AttnF16::pair(ldexpf(bf16_lo(w[i]), -e), ldexpf(bf16_hi(w[i]), -e));
+  return __builtin_bit_cast(f16x8, r);
+}
+__device__ __forceinline__ float query_most(u32x4 w, float most) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) most = fmaxf(most, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+  return most;
+}
+__device__ __forceinline__ int query_exponent(float most) {
+  return most == 0.0f ? 0 : (int)(__float_as_uint(most) >> 23) - 127 - 14;
 }
 
 // max / sum over the two lanes (l, l ^ 32) that share a query row
@@ -118,14 +175,15 @@ __device__ __forceinline__ void at_wait_barrier() {
 }
 
 // NB blocks of 32 keys per tile; DQ-wide keys, DV-wide values
-template <int DQ, int DV, int NB>
+template <int DQ, int DV, int NB, class T = AttnBf16>
 struct AttnWave {
+  typedef typename T::v8 v8;
   static constexpr int KQ = DQ / 16, OB = DV / 32;
   static constexpr int kKeyBytes = NB * 32 * DQ * 2, kValBytes = NB * 32 * DV * 2;
-  bf16x8 q[KQ];
+  v8 q[KQ];
   f32x16 o[OB];
   f32x16 s[NB];
-  bf16x8 p[2 * NB];
+  v8 p[2 * NB];
   float m, l;
   // This lane's byte offsets within a tile: of its first operand chunk of key row
   // l % 32, and of its 8 bytes of the transposing reads of value block 0, lower and
@@ -134,11 +192,24 @@ struct AttnWave {
   static constexpr int KA = DQ == 192 ? 4 : KQ;
   uint32_t k0, v0[2];
 
-  // q: this lane's query row (16-byte aligned)
-  __device__ __forceinline__ void init(const uint16_t* row, int lane) {
+  // q: this lane's query row (16-byte aligned).  f16: returns the exponent that its scores lack.
+  __device__ __forceinline__ int init(const uint16_t* row, int lane) {
     const int h = lane >> 5, r = lane & 31, g = lane >> 4, i16 = lane & 15;
+    int e = 0;
+    if constexpr (std::is_same<T, AttnBf16>::value) {
 #pragma unroll
-    for (int i = 0; i < KQ; ++i) q[i] = __builtin_bit_cast(bf16x8, *(const u32x4*)(row + 16 * i + 8 * h));
+      for (int i = 0; i < KQ; ++i) q[i] = __builtin_bit_cast(bf16x8, *(const u32x4*)(row + 16 * i + 8 * h));
+    } else {
+      u32x4 x[KQ];
+      float most = 0.0f;
+#pragma unroll
+      for (int i = 0; i < KQ; ++i) x[i] = *(const u32x4*)(row + 16 * i + 8 * h);
+#pragma unroll
+      for (int i = 0; i < KQ; ++i) most = query_most(x[i], most);
+      e = query_exponent(half_max(most));
+#pragma unroll
+      for (int i = 0; i < KQ; ++i) q[i] = query_f16(x[i], e);
+    }
     k0 = (uint32_t)(r * (DQ * 2) + (h ^ at_swz<DQ>(r)) * 16);
 #pragma unroll
     for (int jj = 0; jj < 2; ++jj) {
@@ -158,19 +229,20 @@ struct AttnWave {
     asm volatile("" : "+v"(k0), "+v"(v0[0]), "+v"(v0[1]));
 #pragma unroll
     for (int i = 0; i < KQ; ++i) asm volatile("" : "+v"(q[i]));
+    return e;
   }
 
   // operand of keys 32 b .. 32 b + 31, columns 16 k .. 16 k + 15
-  __device__ __forceinline__ bf16x8 read_k(const uint8_t* ks, int b, int k) const {
-    return *(const bf16x8*)(ks + (k0 ^ ((k % KA) * 32)) + (32 * b * (DQ * 2) + (k / KA) * (KA * 32)));
+  __device__ __forceinline__ v8 read_k(const uint8_t* ks, int b, int k) const {
+    return *(const v8*)(ks + (k0 ^ ((k % KA) * 32)) + (32 * b * (DQ * 2) + (k / KA) * (KA * 32)));
   }
   // operand of value columns 32 b .. 32 b + 31, keys 16 st .. 16 st + 15
-  __device__ __forceinline__ bf16x8 read_v(const uint8_t* vs, int st, int b) const {
+  __device__ __forceinline__ v8 read_v(const uint8_t* vs, int st, int b) const {
     s16x4 part[2];
 #pragma unroll
     for (int jj = 0; jj < 2; ++jj)
       part[jj] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at_lds_s16x4*)(vs + (v0[jj] ^ (b * 64)) + 16 * st * (DV * 2)));
-    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    return __builtin_bit_cast(v8, __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7));
   }
 
   // V's infinities and NaN as zeros
@@ -190,7 +262,7 @@ struct AttnWave {
   // reads one step ahead and waits for it in each.)
   static constexpr int kAhead = 2;                                  // 3, 4 and 6 measured the same
   static constexpr int kScoreOps = KQ * NB, kValueOps = 2 * NB * OB;
-  __device__ __forceinline__ bf16x8 operand(const uint8_t* ks, const uint8_t* vs, int i) const {
+  __device__ __forceinline__ v8 operand(const uint8_t* ks, const uint8_t* vs, int i) const {
     if (i < kScoreOps) return read_k(ks, i % NB, i / NB);
     i -= kScoreOps;
     return read_v(vs, i / OB, i % OB);
@@ -198,18 +270,18 @@ struct AttnWave {
   // operands FIRST .. LAST - 1: scores (s must be zero before the first), then values
   template <int FIRST, int LAST>
   __device__ __forceinline__ void products(const uint8_t* ks, const uint8_t* vs) {
-    bf16x8 f[kAhead];
+    v8 f[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) f[i] = operand(ks, vs, FIRST + i);
 #pragma unroll
     for (int i = FIRST; i < LAST; ++i) {
       __builtin_amdgcn_sched_barrier(0);
-      bf16x8& x = f[(i - FIRST) % kAhead];
+      v8& x = f[(i - FIRST) % kAhead];
       if (i < kScoreOps) {
-        s[i % NB] = mfma32(x, q[i / NB], s[i % NB]);
+        s[i % NB] = T::mfma(x, q[i / NB], s[i % NB]);
       } else {
         const int j = i - kScoreOps;
-        o[j % OB] = mfma32(x, p[j / OB], o[j % OB]);
+        o[j % OB] = T::mfma(x, p[j / OB], o[j % OB]);
       }
       if (i + kAhead < LAST) x = operand(ks, vs, i + kAhead);
     }
@@ -245,14 +317,14 @@ struct AttnWave {
   // precision), and a wave none of whose rows has grown so much skips the
   // multiplications.  The decision is the row's own, so its result does not
   // depend on the rows beside it.
-  static constexpr float kSlack = 8.0f;
+  static constexpr float kSlack = T::kSlack;
   __device__ __forceinline__ void weights(float c) {
     float mx = neg_inf();
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
-    mx = half_max(mx) * c;
+    mx = T::kLift == 0.0f ? half_max(mx) * c : mul_rounded(half_max(mx), c) - T::kLift;
     const bool grown = mx > m + kSlack;
     if (__any(grown)) {
       const float alpha = grown ? __builtin_amdgcn_exp2f(m - mx) : 1.0f;
@@ -266,6 +338,16 @@ struct AttnWave {
     // a row that has seen no key (or only scores of -inf) keeps m = -inf; its
     // weights are 2^-inf = 0
     const float base = m == neg_inf() ? 0.0f : m;
+    if constexpr (T::kLift != 0.0f) {
+      const float2 f = split_scale(base, c);
+      if (__any(f.y == 1.0f)) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[b][i] = mul_rounded(s[b][i], f.x);
+      }
+      c = f.y;
+    }
     float sum = 0.0f;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -278,7 +360,7 @@ struct AttnWave {
           sum += w[j];
         }
         p[2 * b + i / 8] = __builtin_bit_cast(
-            bf16x8, u32x4{cvt_bf16x2(w[0], w[1]), cvt_bf16x2(w[2], w[3]), cvt_bf16x2(w[4], w[5]), cvt_bf16x2(w[6], w[7])});
+            v8, u32x4{T::pair(w[0], w[1]), T::pair(w[2], w[3]), T::pair(w[4], w[5]), T::pair(w[6], w[7])});
       }
     l += half_sum(sum);
   }

@@ -34,6 +34,7 @@
 #include <algorithm>
 
 #include "attn_common.h"
+#include "attn_join.h"
 
 namespace moe {
 
@@ -424,103 +425,6 @@ __global__ __launch_bounds__(kDecThreads, 2) void attn_decode_kernel(DecodeArgs 
   decode_narrow<DQ, DV, NS, RB, false>(a, kvh, at, end - begin, row0, rows, entry0, mem);
 }
 
-// The parts of an output row joined: WPR waves per row take every WPR-th part.
-// Each wave first finds its parts' maximum (64 parts at a time, one per lane), so
-// the sums' loads follow without waiting for one another.
-template <int DV, int WPR>
-__global__ __launch_bounds__(WPR <= 4 ? 256 : WPR * 64) void attn_join_kernel(DecodeArgs a) {
-  constexpr int kWaves = WPR <= 4 ? 4 : WPR, kRows = kWaves / WPR;
-  __shared__ float2 red[kWaves][64];
-  __shared__ float2 ml[kWaves];
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = wv % WPR;
-  const int Hall = a.num_requests * a.q_heads;
-  const int at_row = blockIdx.x * kRows + wv / WPR;
-  const bool live = at_row < Hall;                                  // whole waves; a row's waves agree
-  const int b = min(at_row, Hall - 1) / a.q_heads, hq = min(at_row, Hall - 1) % a.q_heads;
-  constexpr int E = DV / 64;                                        // values per lane
-  float M = neg_inf(), L = 0.0f, o[2] = {0.0f, 0.0f};
-  if (live) {
-    const DecodePlan& p = a.plan;
-    // own parts: two for each run that the request's tiles lie in
-    const int np = p.parts_p * (p.wide ? 1 : 2);
-    int n = np, run0 = 0;
-    if (p.runs > 0) {
-      const int t0 = a.first[b], t1 = a.first[b + 1], each = (a.first[a.num_requests] + p.runs - 1) / p.runs;
-      if (t1 > t0) {
-        run0 = t0 / each;
-        n += 2 * ((t1 - 1) / each - run0 + 1);
-      }
-    }
-    const int G = a.q_heads / a.kv_heads, kvh = hq / G, g = hq % G, block = g / p.rows_s;
-    const int64_t own = a.own + ((int64_t)(kvh * p.blocks_s + block) * (p.runs + a.num_requests) + run0 + b) * 2 * p.rows_s +
-                        g - block * p.rows_s;
-    auto entry = [&](int x) { return x < np ? (int64_t)x * Hall + at_row : own + (int64_t)(x - np) * p.rows_s; };
-    const int mine = (n - sub + WPR - 1) / WPR;                     // parts sub, sub + WPR, ...
-    for (int base = 0; base < mine; base += 64) {
-      const int cnt = min(64, mine - base);
-      float2 x = float2{neg_inf(), 0.0f};
-      if (lane < cnt) x = a.part_ml[entry(sub + (base + lane) * WPR)];
-      float mx = x.x;
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
-      const float M1 = fmaxf(M, mx), ref = M1 == neg_inf() ? 0.0f : M1;
-      const float e = __builtin_amdgcn_exp2f(x.x - ref), e0 = __builtin_amdgcn_exp2f(M - ref);
-      float l = x.y * e;
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) l += __shfl_xor(l, d);
-      L = L * e0 + l;
-      M = M1;
-#pragma unroll
-      for (int j = 0; j < E; ++j) o[j] *= e0;
-      for (int q0 = 0; q0 < cnt; q0 += 8) {                         // 8 loads in flight
-        float y[8][2];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float* src = a.part_o + entry(sub + (base + min(q0 + u, cnt - 1)) * WPR) * DV + lane * E;
-          y[u][0] = src[0];
-          if (E == 2) y[u][1] = src[1];
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          if (q0 + u >= cnt) break;
-          const float ep = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e), q0 + u));
-          o[0] = fmaf(ep, y[u][0], o[0]);
-          if (E == 2) o[1] = fmaf(ep, y[u][1], o[1]);
-        }
-      }
-    }
-  }
-  if (WPR > 1) {
-    red[wv][lane] = float2{o[0], o[1]};
-    if (lane == 0) ml[wv] = float2{M, L};
-    __syncthreads();
-    if (sub != 0) return;
-    float M1 = M;
-#pragma unroll
-    for (int i = 1; i < WPR; ++i) M1 = fmaxf(M1, ml[wv + i].x);
-    const float ref = M1 == neg_inf() ? 0.0f : M1;
-    float e = __builtin_amdgcn_exp2f(M - ref);
-    L *= e;
-    o[0] *= e;
-    o[1] *= e;
-#pragma unroll
-    for (int i = 1; i < WPR; ++i) {
-      e = __builtin_amdgcn_exp2f(ml[wv + i].x - ref);
-      const float2 y = red[wv + i][lane];
-      L = fmaf(e, ml[wv + i].y, L);
-      o[0] = fmaf(e, y.x, o[0]);
-      o[1] = fmaf(e, y.y, o[1]);
-    }
-    M = M1;
-  }
-  if (!live) return;
-  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-  uint16_t* dst = a.out + b * a.o_ts + hq * a.o_hs + lane * E;
-  if (E == 2) *(uint32_t*)dst = cvt_bf16x2(o[0] * inv, o[1] * inv);
-  else *dst = (uint16_t)f32_to_bf16_bits(o[0] * inv);
-  if (a.lse && lane == 0) a.lse[at_row] = L == 0.0f ? neg_inf() : (M + __builtin_amdgcn_logf(L)) * kLn2;
-}
-
 // Few keys: a workgroup per request and key head answers alone, without parts and
 // a second launch.  Its eight waves take every eighth tile of 32 keys, prefix first,
 // each through registers into its own LDS, the next tile's loads under way while
@@ -754,13 +658,25 @@ static void launch_decode(const DecodeArgs& a, hipStream_t stream) {
     if (a.plan.rb == 1) hipLaunchKernelGGL((attn_decode_kernel<DQ, DV, 1>), dim3(grid), dim3(kDecThreads), 0, stream, a);
     else hipLaunchKernelGGL((attn_decode_kernel<DQ, DV, 2>), dim3(grid), dim3(kDecThreads), 0, stream, a);
   }
-  const uint32_t rows = (uint32_t)(a.num_requests * a.q_heads);
-  // waves per row: as many as leave each 8 parts or so, one round of loads (a
-  // request's own parts: two per run it lies in, on average runs / B of them)
-  const int parts = a.plan.parts_p * (a.plan.wide ? 1 : 2) + 2 * (1 + a.plan.runs / a.num_requests);
-  if (parts <= 16) hipLaunchKernelGGL((attn_join_kernel<DV, 1>), dim3((rows + 3) / 4), dim3(256), 0, stream, a);
-  else if (parts <= 48) hipLaunchKernelGGL((attn_join_kernel<DV, 4>), dim3(rows), dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((attn_join_kernel<DV, 16>), dim3(rows), dim3(1024), 0, stream, a);
+  JoinArgs j;
+  j.out = a.out;
+  j.o_ts = a.o_ts;
+  j.o_hs = a.o_hs;
+  j.lse = a.lse;
+  j.part_o = a.part_o;
+  j.part_ml = a.part_ml;
+  j.first = a.first;
+  j.own = a.own;
+  j.num_requests = a.num_requests;
+  j.q_heads = a.q_heads;
+  j.kv_heads = a.kv_heads;
+  j.prefix_parts = a.plan.parts_p * (a.plan.wide ? 1 : 2);
+  j.run_parts = 2;
+  j.runs = a.plan.runs;
+  j.blocks_s = a.plan.blocks_s;
+  j.rows_s = a.plan.rows_s;
+  j.v_scale = 1.0f;
+  launch_join<DV>(j, stream);
 }
 
 moe_status launch_attn_decode(const moe_heads& q, const moe_kv_cache& cache, const int32_t* table,

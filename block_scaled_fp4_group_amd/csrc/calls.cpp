@@ -1,4 +1,4 @@
-// Python's side of the attention calls: argument checks and marshalling for the C
+// Python's side of the attention calls and of those around their cache: argument checks and marshalling for the C
 // ABI, as a CPython extension (`_calls`).  Plain CPython: tensors are asked for
 // their shape, strides and address by their own Python methods, nothing of torch is
 // linked.  The kernels of a decode step take 4 to 10 us each, and the host's side of a
@@ -23,7 +23,7 @@ PyObject *g_bf16, *g_i32, *g_f32, *g_u8, *g_raw_stream, *g_check, *g_describe, *
 
 struct Names {
   PyObject *dtype, *shape, *stride, *data_ptr, *get_device, *is_contiguous, *new_empty, *record_stream, *cuda_stream,
-      *element_size, *numel, *split, *enter, *exit, *device_index;
+      *element_size, *numel, *split, *enter, *exit, *device_index, *k, *k_scale, *v, *v_scale, *k_global, *v_global, *dim;
 } n_;
 
 // An owned reference.
@@ -180,7 +180,7 @@ bool flat(PyObject* t, const char* name, PyObject* dtype, int ndim, int index, v
 bool table(PyObject* t, const char* name, int64_t rows, int index, void** p, int64_t* stride, int64_t* cols) {
   Shape s, st;
   if (!t || !is_tensor(t) || !has_dtype(t, g_i32) || device_of(t) != index || !shape_of(t, 2, &s) || !strides_of(t, 2, &st) ||
-      (s.d[1] > 1 && st.d[1] != 1)) {
+      (s.d[0] > 0 && s.d[1] > 1 && st.d[1] != 1)) {
     if (!PyErr_Occurred()) describe(t, name, g_i32, 2, index);
     return false;
   }
@@ -396,6 +396,144 @@ bool scale_of(PyObject* x, int64_t k_dim, float* scale) {
   if (given(x)) return as_float(x, scale);
   *scale = (float)(1.0 / std::sqrt((double)k_dim));
   return true;
+}
+
+// A cache held in 4 bits: an object with the tensors k, k_scale, v, v_scale (u8) and the
+// numbers k_global, v_global.
+bool cache_fp4(PyObject* x, int index, int64_t kv_heads, int64_t k_dim, moe_kv_cache_fp4* out, int64_t* heads_of, int64_t* k_of,
+               int64_t* v_dim) {
+  PyObject* const names[4] = {n_.k, n_.k_scale, n_.v, n_.v_scale};
+  static const char* const words[4] = {"cache.k", "cache.k_scale", "cache.v", "cache.v_scale"};
+  Shape s[4];
+  void* p[4];
+  for (int i = 0; i < 4; ++i) {
+    Ref t(PyObject_GetAttr(x, names[i]));
+    if (!t.p || !flat(t.p, words[i], g_u8, 4, index, &p[i], &s[i])) return false;
+  }
+  const int64_t P = s[0].d[0], H = s[0].d[1], page = s[0].d[2], D = 2 * s[0].d[3], Dv = 2 * s[2].d[3];
+  auto is = [](const Shape& a, int64_t w, int64_t x, int64_t y, int64_t z) {
+    return a.d[0] == w && a.d[1] == x && a.d[2] == y && a.d[3] == z;
+  };
+  if (D % 16 || Dv % 16 || !is(s[1], P, H, page, D / 16) || !is(s[2], P, H, page, Dv / 2) || !is(s[3], P, H, Dv / 16, page)) {
+    PyErr_SetString(PyExc_ValueError,
+                    "cache: k (pages, heads, page_size, k_dim / 2), k_scale (pages, heads, page_size, k_dim / 16), v (pages, "
+                    "heads, page_size, v_dim / 2) and v_scale (pages, heads, v_dim / 16, page_size) do not fit");
+    return false;
+  }
+  if ((kv_heads >= 0 && H != kv_heads) || (k_dim >= 0 && D != k_dim)) {
+    PyErr_Format(PyExc_ValueError, "cache of %lld heads x %lld does not fit (heads %lld, dim %lld; -1: any)", (long long)H,
+                 (long long)D, (long long)kv_heads, (long long)k_dim);
+    return false;
+  }
+  Ref kg(PyObject_GetAttr(x, n_.k_global)), vg(PyObject_GetAttr(x, n_.v_global));
+  if (!kg.p || !vg.p || !as_float(kg.p, &out->k_global) || !as_float(vg.p, &out->v_global) || !fits_i32(H, "heads") ||
+      !fits_i32(page, "page_size") || !fits_i32(Dv, "v_dim"))
+    return false;
+  out->k = p[0];
+  out->k_scale = p[1];
+  out->v = p[2];
+  out->v_scale = p[3];
+  out->num_pages = P;
+  out->page_size = (int32_t)page;
+  *heads_of = H;
+  *k_of = D;
+  *v_dim = Dv;
+  return true;
+}
+
+// bf16 [T, hidden], rows apart by any stride; want: the sizes that it must have, -1 for any.
+bool rows(PyObject* t, const char* name, int index, int64_t T, int64_t hidden, moe_rows* out, Shape* s) {
+  Shape st;
+  if (!t || !is_tensor(t) || !has_dtype(t, g_bf16) || device_of(t) != index || !shape_of(t, 2, s) || !strides_of(t, 2, &st) ||
+      (s->d[1] > 1 && st.d[1] != 1)) {
+    if (!PyErr_Occurred()) describe(t, name, g_bf16, 2, index);
+    return false;
+  }
+  if ((T >= 0 && s->d[0] != T) || (hidden >= 0 && s->d[1] != hidden)) {
+    PyErr_Format(PyExc_ValueError, "%s: shape (%lld, %lld) does not fit (%lld, %lld)", name, (long long)s->d[0],
+                 (long long)s->d[1], (long long)T, (long long)hidden);
+    return false;
+  }
+  out->stride = s->d[0] == 1 ? s->d[1] : st.d[0];
+  return address_of(t, &out->data);
+}
+
+// float32 [n], or None
+bool vector(PyObject* t, const char* name, int64_t n, int index, void** p) {
+  Shape s;
+  *p = nullptr;
+  if (!given(t)) return true;
+  if (!flat(t, name, g_f32, 1, index, p, &s)) return false;
+  if (s.d[0] == n) return true;
+  PyErr_Format(PyExc_ValueError, "%s needs %lld elements", name, (long long)n);
+  return false;
+}
+
+// int32 [n] that was given, or made; `at least` n elements.
+bool output_ints(PyObject* t, const char* name, PyObject* like, int index, int64_t n, Ref* made, PyObject** out, void** p) {
+  if (given(t)) {
+    Shape s;
+    if (!flat(t, name, g_i32, 1, index, p, &s)) return false;
+    if (s.d[0] < n) {
+      PyErr_Format(PyExc_ValueError, "%s needs %lld elements", name, (long long)n);
+      return false;
+    }
+    *out = t;
+    return true;
+  }
+  made->set(make(like, 1, &n, nullptr, p));
+  *out = made->p;
+  return made->p != nullptr;
+}
+
+// The tensors of a pool, pages first: a sequence of contiguous GPU tensors whose first
+// dimensions are equal.
+bool page_buffers(PyObject* x, int index, moe_page_buffers* out, int64_t* num_pages) {
+  Ref seq(PySequence_Fast(x, "buffers must be a sequence of tensors"));
+  if (!seq.p) return false;
+  const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq.p);
+  if (n < 1 || n > MOE_PAGE_BUFFERS) {
+    PyErr_Format(PyExc_ValueError, "buffers: 1 to %d tensors", MOE_PAGE_BUFFERS);
+    return false;
+  }
+  *out = moe_page_buffers{};
+  out->count = (int32_t)n;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    PyObject* t = PySequence_Fast_GET_ITEM(seq.p, i);
+    if (!is_tensor(t) || device_of(t) != index || !contiguous(t)) {
+      PyErr_Format(PyExc_ValueError, "buffers[%zd] must be a contiguous tensor on cuda:%d", i, index);
+      return false;
+    }
+    Ref shape(PyObject_GetAttr(t, n_.shape)), count(PyObject_CallMethodNoArgs(t, n_.numel)),
+        each(PyObject_CallMethodNoArgs(t, n_.element_size));
+    if (!shape.p || !count.p || !each.p || !PyTuple_Check(shape.p)) return false;
+    const int64_t pages = PyTuple_GET_SIZE(shape.p) > 0 ? PyLong_AsLongLong(PyTuple_GET_ITEM(shape.p, 0)) : 0;
+    if (i == 0) *num_pages = pages;
+    if (pages < 1 || pages != *num_pages) {
+      PyErr_Format(PyExc_ValueError, "buffers[%zd] has %lld pages, not %lld", i, (long long)pages, (long long)*num_pages);
+      return false;
+    }
+    out->page_bytes[i] = PyLong_AsLongLong(count.p) / pages * PyLong_AsLongLong(each.p);
+    if (PyErr_Occurred() || !address_of(t, &out->data[i])) return false;
+  }
+  return true;
+}
+
+// block_table and lens of the page calls.
+bool table_and_lens(PyObject* t, PyObject* l, int index, void** tab, int64_t* stride, int64_t* blocks, void** lens, Shape* ls) {
+  if (!flat(l, "lens", g_i32, 1, index, lens, ls) || !table(t, "block_table", ls->d[0], index, tab, stride, blocks)) return false;
+  return fits_i32(ls->d[0], "lens");
+}
+
+bool prefix_of(PyObject* t, PyObject* n, int index, void** tab, int64_t* blocks, int64_t* len) {
+  Shape s;
+  *tab = nullptr;
+  *blocks = *len = 0;
+  if (given(t)) {
+    if (!flat(t, "prefix_table", g_i32, 1, index, tab, &s) || !fits_i32(s.d[0], "prefix_table")) return false;
+    *blocks = s.d[0];
+  }
+  return !n || as_i64(n, len);
 }
 
 // -------------------------------------------------------------------- calls
@@ -633,6 +771,348 @@ PyObject* attn_decode(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObje
   return PyTuple_Pack(2, out, lse);
 }
 
+PyObject* qk_norm_rope_fp4(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+  NAMES("q", "k", "v", "positions", "cos_sin", "cache", "slots", "q_weight", "k_weight", "eps", "interleaved", "want_k", "q_out",
+        "k_out", "stream");
+  if (!parse("qk_norm_rope_fp4", args, nargs, kwnames, names, N, 7, a)) return nullptr;
+  int dev;
+  Placed placed;
+  moe_heads hq, hk, hv, ho, hko;
+  Shape qs, ks, s;
+  if (!gpu(a[0], "q", &dev) || !placed.enter(a[14], dev) || !heads(a[0], "q", dev, Shape{{-1, -1, -1, 0}}, &hq, &qs)) return nullptr;
+  const int64_t T = qs.d[0], D = qs.d[2];
+  if (!heads(a[1], "k", dev, Shape{{T, -1, D, 0}}, &hk, &ks)) return nullptr;
+  const int64_t Hkv = ks.d[1];
+  moe_rope_params prm = {(int32_t)qs.d[1], (int32_t)Hkv, (int32_t)D, 0, 0, 0, 0, 1e-6f};
+  void *pos = nullptr, *cs = nullptr, *w[2], *slots;
+  if (given(a[4])) {
+    Shape c;
+    if (!flat(a[4], "cos_sin", g_f32, 2, dev, &cs, &c) || !flat(a[3], "positions", g_i32, 1, dev, &pos, &s)) return nullptr;
+    if (s.d[0] < T) {
+      PyErr_SetString(PyExc_ValueError, "positions needs an entry for each token");
+      return nullptr;
+    }
+    if (!fits_i32(c.d[0], "cos_sin") || !fits_i32(c.d[1], "cos_sin")) return nullptr;
+    prm.max_position = (int32_t)c.d[0];
+    prm.rot_dim = (int32_t)c.d[1];
+  }
+  moe_kv_cache_fp4 c;
+  int64_t H, kd, v_dim;
+  if (!cache_fp4(a[5], dev, Hkv, D, &c, &H, &kd, &v_dim) || !heads(a[2], "v", dev, Shape{{T, Hkv, v_dim, 0}}, &hv, &s) ||
+      !flat(a[6], "slots", g_i32, 1, dev, &slots, &s))
+    return nullptr;
+  if (s.d[0] < T) {
+    PyErr_SetString(PyExc_ValueError, "slots needs an entry for each token");
+    return nullptr;
+  }
+  prm.v_dim = (int32_t)v_dim;
+  if (!vector(a[7], "q_weight", D, dev, &w[0]) || !vector(a[8], "k_weight", D, dev, &w[1]) || (a[9] && !as_float(a[9], &prm.eps)))
+    return nullptr;
+  if (a[10]) {
+    prm.interleaved = PyObject_IsTrue(a[10]);
+    if (prm.interleaved < 0) return nullptr;
+  }
+  const int keep = a[11] ? PyObject_IsTrue(a[11]) : 1;
+  if (keep < 0) return nullptr;
+  Ref mq, mk;
+  PyObject *q_out, *k_out = Py_None;
+  if (!output_heads(a[12], "q_out", a[0], dev, T, qs.d[1], D, &mq, &q_out, &ho)) return nullptr;
+  const bool write_k = given(a[13]) || keep;
+  if (write_k && !output_heads(a[13], "k_out", a[1], dev, T, Hkv, D, &mk, &k_out, &hko)) return nullptr;
+  PyObject* own[2] = {mq.p, mk.p};
+  hipStream_t stream;
+  if (!stream_of(a[14], dev, &stream) || !placed.known(own, 2)) return nullptr;
+  if (!check(moe_qk_norm_rope_fp4(&hq, &hk, &hv, T, &prm, (const int32_t*)pos, (const float*)cs, (const float*)w[0],
+                                  (const float*)w[1], &ho, write_k ? &hko : nullptr, &c, (const int32_t*)slots, stream),
+             "moe_qk_norm_rope_fp4"))
+    return nullptr;
+  return PyTuple_Pack(2, q_out, k_out);
+}
+
+PyObject* attn_decode_fp4(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+  NAMES("q", "cache", "block_table", "lens", "max_len", "prefix_table", "prefix_len", "scale", "workspace", "out", "lse",
+        "want_lse", "stream");
+  if (!parse("attn_decode_fp4", args, nargs, kwnames, names, N, 5, a)) return nullptr;
+  int dev;
+  Placed placed;
+  moe_heads hq, ho;
+  moe_kv_cache_fp4 c;
+  Shape qs, s;
+  void *tab, *lens, *prefix, *pl, *ws;
+  int64_t stride, blocks, most, prefix_blocks, prefix_len, v_dim, Hkv, kd;
+  if (!gpu(a[0], "q", &dev) || !placed.enter(a[12], dev) || !heads(a[0], "q", dev, Shape{{-1, -1, -1, 0}}, &hq, &qs))
+    return nullptr;
+  const int64_t B = qs.d[0], H = qs.d[1];
+  if (!cache_fp4(a[1], dev, -1, qs.d[2], &c, &Hkv, &kd, &v_dim) || !table(a[2], "block_table", B, dev, &tab, &stride, &blocks) ||
+      !flat(a[3], "lens", g_i32, 1, dev, &lens, &s))
+    return nullptr;
+  if (s.d[0] < B) {
+    PyErr_SetString(PyExc_ValueError, "lens needs an entry for each request");
+    return nullptr;
+  }
+  if (!prefix_of(a[5], a[6], dev, &prefix, &prefix_blocks, &prefix_len)) return nullptr;
+  moe_attn_params prm = {(int32_t)H, (int32_t)Hkv, (int32_t)qs.d[2], (int32_t)v_dim, 0.0f};
+  size_t bytes;
+  Ref mw, mo, ml;
+  PyObject *out, *lse;
+  if (!fits_i32(B, "q") || !as_i64(a[4], &most) || !scale_of(a[7], qs.d[2], &prm.scale) ||
+      !workspace(a[8], a[0], dev, moe_attn_decode_fp4_workspace_bytes((int32_t)B, prefix_len, most, &prm), &mw, &ws, &bytes) ||
+      !output_heads(a[9], "out", a[0], dev, B, H, v_dim, &mo, &out, &ho) ||
+      !output_lse(a[10], a[11], a[0], dev, B, H, &ml, &lse, &pl))
+    return nullptr;
+  PyObject* own[2] = {mo.p, ml.p};
+  hipStream_t stream;
+  if (!stream_of(a[12], dev, &stream) || !placed.known(own, 2)) return nullptr;
+  if (!check(moe_attn_decode_fp4(&hq, &c, (const int32_t*)tab, stride, (int32_t)blocks, (const int32_t*)lens, (int32_t)B, most,
+                                 (const int32_t*)prefix, (int32_t)prefix_blocks, prefix_len, &prm, &ho, (float*)pl, ws, bytes,
+                                 stream),
+             "moe_attn_decode_fp4"))
+    return nullptr;
+  return PyTuple_Pack(2, out, lse);
+}
+
+// The arguments behind the cache of both forms: block_table, cu_k, total, prefix_table,
+// prefix_len, k_out, v_out, stream.
+PyObject* gather(PyObject** a, int dev, Placed& placed, const moe_kv_cache* c, const moe_kv_cache_fp4* c4, PyObject* like,
+                 int64_t H, int64_t D, int64_t Dv) {
+  void *tab, *cu, *prefix;
+  int64_t stride, blocks, total, prefix_blocks, prefix_len;
+  Shape cs;
+  if (!flat(a[1], "cu_k", g_i32, 1, dev, &cu, &cs)) return nullptr;
+  if (cs.d[0] < 1) {
+    PyErr_SetString(PyExc_ValueError, "cu_k must have an entry for each sequence and the end");
+    return nullptr;
+  }
+  if (!fits_i32(cs.d[0], "cu_k") || !table(a[0], "block_table", cs.d[0] - 1, dev, &tab, &stride, &blocks) ||
+      !as_i64(a[2], &total) || !prefix_of(a[3], a[4], dev, &prefix, &prefix_blocks, &prefix_len))
+    return nullptr;
+  if (total < 0) {
+    PyErr_SetString(PyExc_ValueError, "total is negative");
+    return nullptr;
+  }
+  moe_heads hk, hv;
+  Ref mk, mv;
+  PyObject *k, *v;
+  // (bf16, whatever the cache is)
+  auto output = [&](PyObject* t, const char* name, int64_t dim, Ref* made, PyObject** out, moe_heads* h) {
+    if (given(t)) return output_heads(t, name, like, dev, total, H, dim, made, out, h);
+    const int64_t d[3] = {total, H, dim};
+    void* p;
+    made->set(make(like, 3, d, g_bf16, &p));
+    *out = made->p;
+    *h = moe_heads{p, H * dim, dim};
+    return made->p != nullptr;
+  };
+  if (!output(a[5], "k_out", D, &mk, &k, &hk) || !output(a[6], "v_out", Dv, &mv, &v, &hv)) return nullptr;
+  PyObject* own[2] = {mk.p, mv.p};
+  hipStream_t stream;
+  if (!stream_of(a[7], dev, &stream) || !placed.known(own, 2)) return nullptr;
+  const int32_t seqs = (int32_t)cs.d[0] - 1;
+  const moe_status st =
+      c ? moe_kv_gather(c, (int32_t)H, (int32_t)D, (int32_t)Dv, (const int32_t*)tab, stride, (int32_t)blocks,
+                        (const int32_t*)prefix, (int32_t)prefix_blocks, prefix_len, (const int32_t*)cu, seqs, total, &hk, &hv,
+                        stream)
+        : moe_kv_gather_fp4(c4, (int32_t)H, (int32_t)D, (int32_t)Dv, (const int32_t*)tab, stride, (int32_t)blocks,
+                            (const int32_t*)prefix, (int32_t)prefix_blocks, prefix_len, (const int32_t*)cu, seqs, total, &hk,
+                            &hv, stream);
+  if (!check(st, c ? "moe_kv_gather" : "moe_kv_gather_fp4")) return nullptr;
+  return PyTuple_Pack(2, k, v);
+}
+
+PyObject* kv_gather(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+  NAMES("k_cache", "v_cache", "block_table", "cu_k", "total", "prefix_table", "prefix_len", "k_out", "v_out", "stream");
+  if (!parse("kv_gather", args, nargs, kwnames, names, N, 5, a)) return nullptr;
+  int dev;
+  Placed placed;
+  moe_kv_cache c;
+  Shape ks;
+  int64_t v_dim;
+  if (!gpu(a[0], "k_cache", &dev) || !placed.enter(a[9], dev)) return nullptr;
+  if (!shape_of(a[0], 4, &ks)) {
+    if (!PyErr_Occurred()) describe(a[0], "k_cache", g_bf16, 4, dev);
+    return nullptr;
+  }
+  if (!cache(a[0], a[1], dev, -1, ks.d[3], &c, &v_dim) || !fits_i32(ks.d[3], "k_dim")) return nullptr;
+  return gather(a + 2, dev, placed, &c, nullptr, a[0], ks.d[2], ks.d[3], v_dim);
+}
+
+PyObject* kv_gather_fp4(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+  NAMES("cache", "block_table", "cu_k", "total", "prefix_table", "prefix_len", "k_out", "v_out", "stream");
+  if (!parse("kv_gather_fp4", args, nargs, kwnames, names, N, 4, a)) return nullptr;
+  int dev;
+  Placed placed;
+  moe_kv_cache_fp4 c;
+  int64_t H, D, Dv;
+  if (!gpu(a[2], "cu_k", &dev) || !placed.enter(a[8], dev) || !cache_fp4(a[0], dev, -1, -1, &c, &H, &D, &Dv) ||
+      !fits_i32(D, "k_dim"))
+    return nullptr;
+  return gather(a + 1, dev, placed, nullptr, &c, a[2], H, D, Dv);
+}
+
+PyObject* kv_fork(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+  NAMES("block_table", "lens", "parents", "children", "free_pages", "page_size", "buffers", "counts", "stream");
+  if (!parse("kv_fork", args, nargs, kwnames, names, N, 7, a)) return nullptr;
+  int dev;
+  Placed placed;
+  void *tab, *lens, *par, *chi, *pool, *cnt;
+  int64_t stride, blocks, pages;
+  Shape ls, ps, cs, fs;
+  int32_t page;
+  moe_page_buffers buf;
+  if (!gpu(a[1], "lens", &dev) || !placed.enter(a[8], dev) ||
+      !table_and_lens(a[0], a[1], dev, &tab, &stride, &blocks, &lens, &ls) || !flat(a[2], "parents", g_i32, 1, dev, &par, &ps) ||
+      !flat(a[3], "children", g_i32, 1, dev, &chi, &cs) || !flat(a[4], "free_pages", g_i32, 1, dev, &pool, &fs) ||
+      !as_i32(a[5], "page_size", &page) || !page_buffers(a[6], dev, &buf, &pages))
+    return nullptr;
+  if (ps.d[0] != cs.d[0]) {
+    PyErr_SetString(PyExc_ValueError, "parents and children must be of one length");
+    return nullptr;
+  }
+  Ref made;
+  PyObject* counts;
+  if (!fits_i32(ps.d[0], "parents") || !output_ints(a[7], "counts", a[1], dev, 2, &made, &counts, &cnt)) return nullptr;
+  hipStream_t stream;
+  if (!stream_of(a[8], dev, &stream) || !placed.known(&made.p, 1)) return nullptr;
+  if (!check(moe_kv_fork((int32_t*)tab, stride, (int32_t)ls.d[0], (int32_t)blocks, (int32_t*)lens, (const int32_t*)par,
+                         (const int32_t*)chi, (int32_t)ps.d[0], (const int32_t*)pool, fs.d[0], page, &buf, pages,
+                         (int32_t*)cnt, stream),
+             "moe_kv_fork"))
+    return nullptr;
+  Py_INCREF(counts);
+  return counts;
+}
+
+PyObject* kv_free_pages(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+  NAMES("block_table", "lens", "page_size", "num_pages", "free_pages", "counts", "stream");
+  if (!parse("kv_free_pages", args, nargs, kwnames, names, N, 4, a)) return nullptr;
+  int dev;
+  Placed placed;
+  void *tab, *lens, *p[2];
+  int64_t stride, blocks, pages;
+  Shape ls;
+  int32_t page;
+  if (!gpu(a[1], "lens", &dev) || !placed.enter(a[6], dev) ||
+      !table_and_lens(a[0], a[1], dev, &tab, &stride, &blocks, &lens, &ls) || !as_i32(a[2], "page_size", &page) ||
+      !as_i64(a[3], &pages))
+    return nullptr;
+  Ref made[2];
+  PyObject* out[2];
+  if (pages < 1) {
+    PyErr_SetString(PyExc_ValueError, "num_pages must be positive");
+    return nullptr;
+  }
+  if (!output_ints(a[4], "free_pages", a[1], dev, pages, &made[0], &out[0], &p[0]) ||
+      !output_ints(a[5], "counts", a[1], dev, 2, &made[1], &out[1], &p[1]))
+    return nullptr;
+  PyObject* own[2] = {made[0].p, made[1].p};
+  hipStream_t stream;
+  if (!stream_of(a[6], dev, &stream) || !placed.known(own, 2)) return nullptr;
+  if (!check(moe_kv_free_pages((const int32_t*)tab, stride, (int32_t)ls.d[0], (int32_t)blocks, (const int32_t*)lens, page, pages,
+                               (int32_t*)p[0], (int32_t*)p[1], stream),
+             "moe_kv_free_pages"))
+    return nullptr;
+  return PyTuple_Pack(2, out[0], out[1]);
+}
+
+PyObject* kv_compact(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+  NAMES("block_table", "lens", "page_size", "buffers", "out_table", "counts", "workspace", "stream");
+  if (!parse("kv_compact", args, nargs, kwnames, names, N, 4, a)) return nullptr;
+  int dev;
+  Placed placed;
+  void *tab, *lens, *cnt, *ws, *to;
+  int64_t stride, blocks, pages, out_stride, out_blocks;
+  Shape ls;
+  int32_t page;
+  moe_page_buffers buf;
+  if (!gpu(a[1], "lens", &dev) || !placed.enter(a[7], dev) ||
+      !table_and_lens(a[0], a[1], dev, &tab, &stride, &blocks, &lens, &ls) || !as_i32(a[2], "page_size", &page) ||
+      !page_buffers(a[3], dev, &buf, &pages))
+    return nullptr;
+  Ref mt, mc, mw;
+  PyObject *out, *counts;
+  size_t bytes;
+  if (given(a[4])) {
+    if (!table(a[4], "out_table", ls.d[0], dev, &to, &out_stride, &out_blocks)) return nullptr;
+    if (out_blocks < blocks) {
+      PyErr_Format(PyExc_ValueError, "out_table needs %lld columns", (long long)blocks);
+      return nullptr;
+    }
+    out = a[4];
+  } else {
+    const int64_t d[2] = {ls.d[0], blocks};
+    mt.set(make(a[0], 2, d, nullptr, &to));
+    if (!mt.p) return nullptr;
+    out = mt.p;
+    out_stride = blocks;
+  }
+  if (!output_ints(a[5], "counts", a[1], dev, 2, &mc, &counts, &cnt) ||
+      !workspace(a[6], a[1], dev, moe_kv_compact_workspace_bytes(pages), &mw, &ws, &bytes))
+    return nullptr;
+  PyObject* own[2] = {mt.p, mc.p};
+  hipStream_t stream;
+  if (!stream_of(a[7], dev, &stream) || !placed.known(own, 2)) return nullptr;
+  if (!check(moe_kv_compact((const int32_t*)tab, stride, (int32_t)ls.d[0], (int32_t)blocks, (const int32_t*)lens, page, &buf, pages,
+                            (int32_t*)to, out_stride, (int32_t*)cnt, ws, bytes, stream),
+             "moe_kv_compact"))
+    return nullptr;
+  return PyTuple_Pack(2, out, counts);
+}
+
+PyObject* block_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+  NAMES("x", "weight", "residual", "post_weight", "gate", "scale", "eps", "want_h", "h", "y", "stream");
+  if (!parse("block_norm", args, nargs, kwnames, names, N, 2, a)) return nullptr;
+  int dev;
+  Placed placed;
+  moe_rows x, r, g, h, y;
+  Shape xs, s;
+  void *w, *pw, *cg = nullptr;
+  if (!gpu(a[0], "x", &dev) || !placed.enter(a[10], dev) || !rows(a[0], "x", dev, -1, -1, &x, &xs)) return nullptr;
+  const int64_t T = xs.d[0], H = xs.d[1];
+  if (!fits_i32(H, "x") || !vector(a[1], "weight", H, dev, &w) || !vector(a[3], "post_weight", H, dev, &pw) ||
+      (given(a[2]) && !rows(a[2], "residual", dev, T, H, &r, &s)))
+    return nullptr;
+  bool per_value = false;
+  if (given(a[4])) {
+    // float32 [hidden]: of each channel; bf16 [T, hidden]: of each value
+    Ref d(is_tensor(a[4]) ? PyObject_CallMethodNoArgs(a[4], n_.dim) : nullptr);
+    const long dims = d.p ? PyLong_AsLong(d.p) : 1;
+    if (PyErr_Occurred()) return nullptr;
+    per_value = dims == 2;
+    if (per_value ? !rows(a[4], "gate", dev, T, H, &g, &s) : !vector(a[4], "gate", H, dev, &cg)) return nullptr;
+  }
+  float scale = 1.0f, eps = 1e-6f;
+  if ((a[5] && !as_float(a[5], &scale)) || (a[6] && !as_float(a[6], &eps))) return nullptr;
+  const int want = a[7] ? PyObject_IsTrue(a[7]) : 1;
+  if (want < 0) return nullptr;
+  const bool with_h = want || given(a[8]), with_y = given(a[1]);
+  Ref mh, my;
+  PyObject *oh = Py_None, *oy = Py_None;
+  auto output = [&](PyObject* t, const char* name, Ref* made, PyObject** out, moe_rows* to) {
+    if (given(t)) {
+      *out = t;
+      return rows(t, name, dev, T, H, to, &s);
+    }
+    const int64_t d[2] = {T, H};
+    made->set(make(a[0], 2, d, nullptr, &to->data));
+    to->stride = H;
+    *out = made->p;
+    return made->p != nullptr;
+  };
+  if (given(a[9]) && !with_y) {
+    PyErr_SetString(PyExc_ValueError, "y needs weight");
+    return nullptr;
+  }
+  if ((with_h && !output(a[8], "h", &mh, &oh, &h)) || (with_y && !output(a[9], "y", &my, &oy, &y))) return nullptr;
+  PyObject* own[2] = {mh.p, my.p};
+  hipStream_t stream;
+  if (!stream_of(a[10], dev, &stream) || !placed.known(own, 2)) return nullptr;
+  if (!check(moe_block_norm(&x, T, (int32_t)H, given(a[2]) ? &r : nullptr, (const float*)pw, per_value ? &g : nullptr,
+                            (const float*)cg, scale, (const float*)w, eps, with_h ? &h : nullptr, with_y ? &y : nullptr, stream),
+             "moe_block_norm"))
+    return nullptr;
+  return PyTuple_Pack(2, oh, oy);
+}
+
 PyObject* setup(PyObject*, PyObject* args) {
   PyObject *tensor, *bf16, *i32, *f32, *u8, *raw, *chk, *desc, *current, *under, *get, *device;
   if (!PyArg_ParseTuple(args, "OOOOOOOOOOOO", &tensor, &bf16, &i32, &f32, &u8, &raw, &chk, &desc, &current, &under, &get, &device))
@@ -689,6 +1169,46 @@ PyMethodDef methods[] = {
          "One query per request, q [B, Hq, D], over the paged cache: the shared prefix (``prefix_len`` keys in the pages\n"
          "``prefix_table``), then the request's own ``lens`` keys in its ``block_table`` pages (int32).  ``max_len``: a\n"
          "longest own length known on the host.  -> (out [B, Hq, Dv], lse float32 [B, Hq] or None).\n" STREAM_DOC),
+    CALL(qk_norm_rope_fp4,
+         "qk_norm_rope_fp4(q, k, v, positions, cos_sin, cache, slots, q_weight=None, k_weight=None, eps=1e-06, "
+         "interleaved=False, want_k=True, q_out=None, k_out=None, stream=None)\n--\n\n"
+         "qk_norm_rope() with a cache held in 4 bits (an Fp4Cache): the finished keys and v [T, Hkv, Dv] are quantised into\n"
+         "its rows ``slots``.  -> (q_out, k_out); k_out is None with ``want_k=False``.\n" STREAM_DOC),
+    CALL(attn_decode_fp4,
+         "attn_decode_fp4(q, cache, block_table, lens, max_len, prefix_table=None, prefix_len=0, scale=None, workspace=None, "
+         "out=None, lse=None, want_lse=False, stream=None)\n--\n\n"
+         "attn_decode() over a cache held in 4 bits (an Fp4Cache).  -> (out [B, Hq, Dv], lse float32 [B, Hq] or None).\n"
+         STREAM_DOC),
+    CALL(kv_gather,
+         "kv_gather(k_cache, v_cache, block_table, cu_k, total, prefix_table=None, prefix_len=0, k_out=None, v_out=None, "
+         "stream=None)\n--\n\n"
+         "Cached keys and values of packed sequences as contiguous rows, for attn_prompt(): rows cu_k[b] .. cu_k[b + 1] - 1\n"
+         "(of ``total``) are sequence b's first keys, those of the shared prefix before its own.  -> (k [total, H, D],\n"
+         "v [total, H, Dv]).\n" STREAM_DOC),
+    CALL(kv_gather_fp4,
+         "kv_gather_fp4(cache, block_table, cu_k, total, prefix_table=None, prefix_len=0, k_out=None, v_out=None, "
+         "stream=None)\n--\n\n"
+         "kv_gather() from a cache held in 4 bits (an Fp4Cache): the bf16 values that its codes stand for.\n" STREAM_DOC),
+    CALL(kv_fork,
+         "kv_fork(block_table, lens, parents, children, free_pages, page_size, buffers, counts=None, stream=None)\n--\n\n"
+         "Rows ``children`` of the table become copies of rows ``parents``: whole pages are shared, a last page that is not\n"
+         "full is copied to the next of ``free_pages``.  ``buffers``: the pool's tensors, pages first (k_cache and v_cache,\n"
+         "or an Fp4Cache's four).  block_table and lens are changed in place.  -> counts [2]: pages taken, pages needed.\n"
+         STREAM_DOC),
+    CALL(kv_free_pages,
+         "kv_free_pages(block_table, lens, page_size, num_pages, free_pages=None, counts=None, stream=None)\n--\n\n"
+         "The pages that no row of the table holds (a request is ended by setting its length to 0).  -> (free_pages\n"
+         "[num_pages]: ascending, then -1; counts [2]: free, held).\n" STREAM_DOC),
+    CALL(kv_compact,
+         "kv_compact(block_table, lens, page_size, buffers, out_table=None, counts=None, workspace=None, stream=None)\n--\n\n"
+         "Held pages moved to the front of the pool, in ``buffers`` (the pool's tensors, pages first).  -> (table with the new\n"
+         "pages, -1 elsewhere; counts [2]: held pages, moved pages).  ``out_table`` may be block_table.\n" STREAM_DOC),
+    CALL(block_norm,
+         "block_norm(x, weight, residual=None, post_weight=None, gate=None, scale=1.0, eps=1e-06, want_h=True, h=None, "
+         "y=None, stream=None)\n--\n\n"
+         "Between two blocks: b = x, or its RMS norm times ``post_weight``; h = residual + scale * gate * b; y = RMS norm of h\n"
+         "times ``weight``.  x, residual bf16 [T, H]; weights float32 [H]; gate float32 [H] or bf16 [T, H].  -> (h, y); h is\n"
+         "None with ``want_h=False``, y without ``weight``.  h and y may be x or residual.\n" STREAM_DOC),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "Argument checks and marshalling of the attention calls.", -1, methods,
@@ -702,7 +1222,9 @@ PyMODINIT_FUNC PyInit__calls(void) {
       !name(&n_.data_ptr, "data_ptr") || !name(&n_.get_device, "get_device") || !name(&n_.is_contiguous, "is_contiguous") ||
       !name(&n_.new_empty, "new_empty") || !name(&n_.record_stream, "record_stream") ||
       !name(&n_.cuda_stream, "cuda_stream") || !name(&n_.element_size, "element_size") || !name(&n_.numel, "numel") || !name(&n_.split, "unsafe_split_with_sizes") ||
-      !name(&n_.enter, "__enter__") || !name(&n_.exit, "__exit__") || !name(&n_.device_index, "device_index"))
+      !name(&n_.enter, "__enter__") || !name(&n_.exit, "__exit__") || !name(&n_.device_index, "device_index") ||
+      !name(&n_.k, "k") || !name(&n_.k_scale, "k_scale") || !name(&n_.v, "v") || !name(&n_.v_scale, "v_scale") ||
+      !name(&n_.k_global, "k_global") || !name(&n_.v_global, "v_global") || !name(&n_.dim, "dim"))
     return nullptr;
   return PyModule_Create(&module);
 }

@@ -562,6 +562,147 @@ moe_status moe_attn_decode(const moe_heads* q, const moe_kv_cache* cache, const 
                            const moe_attn_params* p, const moe_heads* out, float* lse, void* workspace,
                            size_t workspace_bytes, hipStream_t stream);
 
+/* ================================================ a cache held in 4 bits
+ * The same paged cache in NVFP4: E2M1 codes (two to a byte, the low nibble first), an
+ * E4M3 scale for every 16 values of a head's row, and one power-of-two scale each for
+ * all keys and all values: value = code x scale x global.  9/16 of a byte per value
+ * instead of 2.  A head's rows of a page lie together:
+ *   k        u8 [num_pages, kv_heads, page_size, k_dim / 2]
+ *   k_scale  u8 [num_pages, kv_heads, page_size, k_dim / 16]
+ *   v        u8 [num_pages, kv_heads, page_size, v_dim / 2]
+ *   v_scale  u8 [num_pages, kv_heads, v_dim / 16, page_size]
+ * contiguous, 16-byte aligned.  page_size: a power of two from 16 to 1024; num_pages *
+ * page_size < 2^31; k_global, v_global: powers of two from 2^-32 to 2^32 (blocks whose
+ * largest value passes 2688 of them saturate; best if most blocks' largest values are
+ * 0.1 to 1000 of them).  Slots are as in moe_kv_cache. */
+typedef struct {
+  void* k;
+  void* k_scale;
+  void* v;
+  void* v_scale;
+  int64_t num_pages;
+  int32_t page_size;
+  float k_global, v_global;
+} moe_kv_cache_fp4;
+
+/* moe_qk_norm_rope with such a cache: the finished key heads and the value heads of
+ * token t are quantised into row slots[t] by moe_quantize_nvfp4's rule (scale = E4M3 of
+ * the block's largest magnitude / (6 global), codes = E2M1 of value / (scale global), to
+ * the nearest, ties to even).  Keys are quantised as they come out of the rotation, not
+ * as k_out is rounded; norm and rotation of keys run in double.  rot_dim a multiple of 32
+ * (else MOE_ERR_UNSUPPORTED), v_dim of 16; k_out may be NULL.  Everything else as there. */
+moe_status moe_qk_norm_rope_fp4(const moe_heads* q, const moe_heads* k, const moe_heads* v, int64_t T,
+                                const moe_rope_params* p, const int32_t* positions, const float* cos_sin,
+                                const float* q_weight, const float* k_weight, const moe_heads* q_out,
+                                const moe_heads* k_out, const moe_kv_cache_fp4* cache, const int32_t* slots,
+                                hipStream_t stream);
+
+/* moe_attn_decode over such a cache: same arguments, same result as of the bf16 values
+ * that the codes stand for.  A query's values below 2^-28 of its largest count to 2^-39 of
+ * it, weights below 2^-31 of a row's largest may count as 0.  Rows of a page behind a
+ * request's end may hold anything. */
+size_t moe_attn_decode_fp4_workspace_bytes(int32_t num_requests, int64_t prefix_len, int64_t max_len,
+                                           const moe_attn_params* p);
+moe_status moe_attn_decode_fp4(const moe_heads* q, const moe_kv_cache_fp4* cache, const int32_t* block_table,
+                               int64_t table_stride, int32_t max_blocks, const int32_t* lens, int32_t num_requests,
+                               int64_t max_len, const int32_t* prefix_table, int32_t prefix_blocks, int64_t prefix_len,
+                               const moe_attn_params* p, const moe_heads* out, float* lse, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------- cached rows, contiguous again
+ * Keys and values of packed sequences as moe_attn_prompt takes them, so that a prompt
+ * can see what is in the cache: row cu_k[b] + i of k_out and v_out is key i of sequence
+ * b -- keys 0 .. prefix_len - 1 those of the shared prefix, the others the request's own.
+ * From a 4-bit cache the values that the codes stand for (exact in bf16).
+ *   cu_k int32 [num_seqs + 1], not descending, from 0 to total_k; rows outside the
+ *   ranges keep their values.  Rows whose page the table does not name (-1, or past
+ *   max_blocks) are zeros.  Head sizes: multiples of 16 up to 1024.
+ * num_seqs == 0 or total_k == 0 is a no-op.  One launch.
+ */
+moe_status moe_kv_gather(const moe_kv_cache* cache, int32_t kv_heads, int32_t k_dim, int32_t v_dim,
+                         const int32_t* block_table, int64_t table_stride, int32_t max_blocks, const int32_t* prefix_table,
+                         int32_t prefix_blocks, int64_t prefix_len, const int32_t* cu_k, int32_t num_seqs, int64_t total_k,
+                         const moe_heads* k_out, const moe_heads* v_out, hipStream_t stream);
+moe_status moe_kv_gather_fp4(const moe_kv_cache_fp4* cache, int32_t kv_heads, int32_t k_dim, int32_t v_dim,
+                             const int32_t* block_table, int64_t table_stride, int32_t max_blocks,
+                             const int32_t* prefix_table, int32_t prefix_blocks, int64_t prefix_len, const int32_t* cu_k,
+                             int32_t num_seqs, int64_t total_k, const moe_heads* k_out, const moe_heads* v_out,
+                             hipStream_t stream);
+
+/* =================================================================== pages
+ * Pages of a cache of any format.  A page is held while a row of the block table
+ * reaches it: row b its first ceil(lens[b] / page_size) entries (at most max_blocks;
+ * negative lengths count as 0, entries that are no page of the pool as none).  Rows may
+ * share pages; nothing is counted or kept between calls.  A shared prefix is a row of
+ * its own.  What a page holds is bytes to these calls: page p of buffer i is
+ * page_bytes[i] bytes (a multiple of 16) at data[i] + p * page_bytes[i]. */
+#define MOE_PAGE_BUFFERS 8
+typedef struct {
+  void* data[MOE_PAGE_BUFFERS];
+  int64_t page_bytes[MOE_PAGE_BUFFERS];
+  int32_t count;
+} moe_page_buffers;
+
+/* Requests that go on as several: row children[i] becomes a copy of row parents[i] --
+ * its length and its whole pages, which the two then share, and, if its last page is not
+ * full, a copy of that in the next page of free_pages (in the order of i), into which
+ * the child's next tokens go.  Without a page left the child gets the whole pages only.
+ * free_pages: pages of the pool that no row holds, each once.
+ *   parents, children int32 [num_forks], rows of the table; an i with a row outside it
+ *   or with children[i] == parents[i] does nothing.  No row may be a child twice, or
+ *   both child and parent (what its entries and length then are is unspecified).
+ *   counts int32 [2]: pages taken, pages needed.
+ * What a child held before is not given back by this call: nothing names it any more.
+ * num_forks <= 65536 (else MOE_ERR_UNSUPPORTED).  One launch. */
+moe_status moe_kv_fork(int32_t* block_table, int64_t table_stride, int32_t num_rows, int32_t max_blocks, int32_t* lens,
+                       const int32_t* parents, const int32_t* children, int32_t num_forks, const int32_t* free_pages,
+                       int64_t num_free, int32_t page_size, const moe_page_buffers* buffers, int64_t num_pages,
+                       int32_t* counts, hipStream_t stream);
+
+/* The pages that no row holds, ascending: a request is ended by setting its length to 0.
+ *   free_pages int32 [num_pages]: the free pages, then -1;
+ *   counts int32 [2]: free pages, held pages.
+ * num_pages <= 2^20 (else MOE_ERR_UNSUPPORTED).  One launch. */
+moe_status moe_kv_free_pages(const int32_t* block_table, int64_t table_stride, int32_t num_rows, int32_t max_blocks,
+                             const int32_t* lens, int32_t page_size, int64_t num_pages, int32_t* free_pages, int32_t* counts,
+                             hipStream_t stream);
+
+/* Held pages moved to the front of the pool: with n pages held, the i-th of them at or
+ * behind page n goes to the i-th page before it that no row holds; afterwards pages n ..
+ * num_pages - 1 are free.  Their old content stays where it was.
+ *   out_table int32 [num_rows, max_blocks], rows out_stride apart: the table with the
+ *   new pages, -1 where a row holds none; block_table itself, or apart from it;
+ *   counts int32 [2]: n, pages moved;
+ *   workspace: moe_kv_compact_workspace_bytes() bytes, 16-byte aligned; calls that share
+ *   one must not overlap.
+ * num_pages <= 2^20 (else MOE_ERR_UNSUPPORTED).  Two launches. */
+size_t moe_kv_compact_workspace_bytes(int64_t num_pages);
+moe_status moe_kv_compact(const int32_t* block_table, int64_t table_stride, int32_t num_rows, int32_t max_blocks,
+                          const int32_t* lens, int32_t page_size, const moe_page_buffers* buffers, int64_t num_pages,
+                          int32_t* out_table, int64_t out_stride, int32_t* counts, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream);
+
+/* ========================================== norms of the residual stream
+ * What lies between two blocks, in one pass over the rows:
+ *   b = x * rsqrt(mean(x^2) + eps) * post_weight    (post_weight NULL: b = x)
+ *   h = residual + scale * gate * b                 (NULL: without residual, without gate)
+ *   y = h * rsqrt(mean(h^2) + eps) * weight
+ * in float, h and y rounded once to bf16 (y comes from the unrounded h).
+ *   x, residual, h, y bf16 [T, hidden], rows `stride` elements apart; gate bf16 [T,
+ *   hidden] likewise, or channel_gate float [hidden]; weight, post_weight float [hidden].
+ *   h or y may be NULL, and may be x, residual or gate themselves (same rows).
+ *   Data 16-byte aligned, strides multiples of 8 (0: one row for all, of inputs).
+ * hidden: a multiple of 8, up to 32768 (else MOE_ERR_UNSUPPORTED).  T == 0 is a no-op.
+ */
+typedef struct {
+  void* data;
+  int64_t stride;
+} moe_rows;
+
+moe_status moe_block_norm(const moe_rows* x, int64_t T, int32_t hidden, const moe_rows* residual, const float* post_weight,
+                          const moe_rows* gate, const float* channel_gate, float scale, const float* weight, float eps,
+                          const moe_rows* h, const moe_rows* y, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
