@@ -71,6 +71,17 @@ __device__ __forceinline__ int f4_len_at(const Fp4Args& a, int b) {   // b unifo
 }
 __device__ __forceinline__ int f4_tiles(int keys) { return (keys + kF4Keys - 1) / kF4Keys; }
 
+// Inclusive sum over the wave's lanes: within rows of 16, then their last lanes on.
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);   // row_shr:1
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);   // row_bcast:15 into rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);   // row_bcast:31 into rows 2 and 3
+  return x;
+}
+
 __device__ __forceinline__ f16x2 f16_pair(uint32_t w) { return __builtin_bit_cast(f16x2, w); }
 
 // Two E4M3 bytes (word SEL of w) as f16: exact.
@@ -89,6 +100,11 @@ __device__ __forceinline__ f16x8 fp4x8_f16(uint32_t w, _Float16 s) {
   const f16x2 p = {s, s};
   return fp4x8_f16(w, p, p, p, p);
 }
+
+// Rows of one group of 16 keys: a buffer from their uniform address on, so that a load takes
+// the lane's 32-bit offset as it is.  (Of 64-bit addresses base and lane offset are added up
+// ahead of the loop, two registers for every load of a tile.)
+__device__ __forceinline__ rsrc_t group_rsrc(const uint8_t* p) { return make_rsrc(p, 0x7fffffffu); }
 
 typedef int f4_i32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) f4_i32x2 f4_lds_i32x2;
@@ -114,7 +130,7 @@ struct Fp4Wave {
   f16x8 p[RB][2];
   float m[RB], l[RB], c[RB];
   // a tile on its way
-  uint32_t kc[4][KS], kscale[4];
+  uint32_t kc[4][KS], kscale[4], kscale2[DQ == 192 ? 4 : 1];
   u32x4 vc[DV / 32];
   uint32_t vscale[DV / 64];
   uint32_t tr;                                                      // this lane's offset of the transposing reads
@@ -130,11 +146,15 @@ struct Fp4Wave {
     return s < 4 ? 32 * g + 8 * s : 128 + 16 * g + 8 * (s - 4);
   }
   // row: this lane's query row of block rb
-  __device__ __forceinline__ void init(int rb, const uint16_t* row, int lane, float scale) {
+  __device__ __forceinline__ void load_query(int rb, const uint16_t* row, int lane) {
+#pragma unroll
+    for (int k = 0; k < KS; ++k) q[rb][k] = __builtin_bit_cast(f16x8, *(const u32x4*)(row + column(lane >> 4, k)));
+  }
+  __device__ __forceinline__ void init(int rb, float scale) {
     u32x4 x[KS];
     float most = 0.0f;
 #pragma unroll
-    for (int k = 0; k < KS; ++k) x[k] = *(const u32x4*)(row + column(lane >> 4, k));
+    for (int k = 0; k < KS; ++k) x[k] = __builtin_bit_cast(u32x4, q[rb][k]);
 #pragma unroll
     for (int k = 0; k < KS; ++k) most = query_most(x[k], most);
     const int e = query_exponent(quarter_max(most));
@@ -146,53 +166,63 @@ struct Fp4Wave {
     m[rb] = neg_inf();
     l[rb] = 0.0f;
   }
-  // The tile's loads.  slot: lane's cache row (page << shift | row) of the tile's key
-  // kEntryKeys * (lane % (64 / kEntryKeys)), the last group of 16 keys for those behind it.
-  __device__ __forceinline__ void load(const Fp4Args& a, int kvh, int slot, int lane) {
+  // The tile's loads: keys of 16 at a time, and all values.  ONCE: nothing reads them again
+  // (non-temporal: 131072 own keys 33.2 -> 30.5 us).  slot: lane's cache row (page << shift |
+  // row) of the tile's key kEntryKeys * (lane % (64 / kEntryKeys)), the last group of 16 keys
+  // for those behind it.
+  // (rows of a head before a cache row: page * heads + head pages of them, and the row)
+  __device__ __forceinline__ static uint64_t rows_at(const Fp4Args& a, int kvh, uint32_t slot) {
+    return ((uint64_t)((int64_t)(slot >> a.page_shift) * a.kv_heads + kvh) << a.page_shift) + (slot & ((1u << a.page_shift) - 1u));
+  }
+  __device__ __forceinline__ static uint64_t group_at(const Fp4Args& a, int kvh, int slot, int t) {
+    return rows_at(a, kvh, (uint32_t)__builtin_amdgcn_readlane(slot, t * (16 / kEntryKeys)));
+  }
+  template <bool ONCE>
+  __device__ __forceinline__ void load_keys(const Fp4Args& a, int kvh, int slot, int lane, int t) {
     const int g = lane >> 4, r = lane & 15;
-    const int64_t heads = a.kv_heads;
-    const int mask = (1 << a.page_shift) - 1;
-    // rows of a head before a cache row: page * heads + head pages of them, and the row
-    auto rows_at = [&](uint32_t sl) {
-      return ((uint64_t)((int64_t)(sl >> a.page_shift) * heads + kvh) << a.page_shift) + (sl & mask);
-    };
+    const uint64_t at = group_at(a, kvh, slot, t);
+    const rsrc_t kp = group_rsrc(a.k + at * (DQ / 2)), sp = group_rsrc(a.ks + at * (DQ / 16));
+    if (DQ == 64) {
+      const u32x2 x = ONCE ? bload64_nt(kp, r * 32 + 8 * g, 0) : bload64(kp, r * 32 + 8 * g, 0);
+      kc[t][0] = x[0];
+      kc[t][1] = x[1];
+      kscale[t] = bload8(sp, r * 4 + g, 0);
+    } else {
+      const int at16 = r * (DQ / 2) + 16 * g;
+      const u32x4 x = ONCE ? bload128_nt(kp, at16, 0) : bload128(kp, at16, 0);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const uint64_t at = rows_at((uint32_t)__builtin_amdgcn_readlane(slot, t * (16 / kEntryKeys)));
-      const uint8_t* kp = a.k + at * (DQ / 2);
-      const uint8_t* sp = a.ks + at * (DQ / 16);
-      if (DQ == 64) {
-        const u32x2 x = *(const u32x2*)(kp + r * 32 + 8 * g);
-        kc[t][0] = x[0];
-        kc[t][1] = x[1];
-        kscale[t] = sp[r * 4 + g];
-      } else {
-        const u32x4 x = *(const u32x4*)(kp + r * (DQ / 2) + 16 * g);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) kc[t][k] = x[k];
-        kscale[t] = *(const uint16_t*)(sp + r * (DQ / 16) + 2 * g);
-        if (DQ == 192) {
-          const u32x2 y = *(const u32x2*)(kp + r * 96 + 64 + 8 * g);
-          kc[t][KS - 2] = y[0];
-          kc[t][KS - 1] = y[1];
-          kscale[t] |= (uint32_t)sp[r * 12 + 8 + g] << 16;
-        }
+      for (int k = 0; k < 4; ++k) kc[t][k] = x[k];
+      kscale[t] = bload16(sp, r * (DQ / 16) + 2 * g, 0);
+      if (DQ == 192) {
+        const int at8 = r * 96 + 64 + 8 * g;
+        const u32x2 y = ONCE ? bload64_nt(kp, at8, 0) : bload64(kp, at8, 0);
+        kc[t][KS - 2] = y[0];
+        kc[t][KS - 1] = y[1];
+        kscale2[t] = bload8(sp, r * 12 + 8 + g, 0);
       }
-      if (DV == 128) vc[t % (DV / 32)] = *(const u32x4*)(a.v + at * 64 + (lane >> 2) * 64 + ((lane & 3) ^ t) * 16);
     }
-    if (DV == 64) {
+  }
+  template <bool ONCE>
+  __device__ __forceinline__ void load_values(const Fp4Args& a, int kvh, int slot, int lane) {
+    if (DV == 128) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const rsrc_t vp = group_rsrc(a.v + group_at(a, kvh, slot, t) * 64);
+        const int at = (lane >> 2) * 64 + ((lane & 3) ^ t) * 16;
+        vc[t % (DV / 32)] = ONCE ? bload128_nt(vp, at, 0) : bload128(vp, at, 0);
+      }
+    } else {
       // two groups of 16 keys to a load: row 4 g' + i of group 2 h + t'
       const int p2 = lane >> 1, tt = (p2 >> 2) & 1, key = 4 * (p2 >> 3) + (p2 & 3);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane(slot, 2 * h * (16 / kEntryKeys));
-        const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane(slot, (2 * h + 1) * (16 / kEntryKeys));
-        vc[h] = *(const u32x4*)(a.v + (rows_at(tt ? hi : lo) + key) * 32 + ((lane & 1) ^ h) * 16);
+        const uint64_t lo = group_at(a, kvh, slot, 2 * h), hi = group_at(a, kvh, slot, 2 * h + 1);
+        vc[h] = *(const u32x4*)(a.v + ((tt ? hi : lo) + key) * 32 + ((lane & 1) ^ h) * 16);
       }
     }
     const int block = lane / (kF4Keys / kEntryKeys);
-    const uint64_t page = (uint64_t)((uint32_t)slot >> a.page_shift) * heads + kvh;
-    const uint8_t* vp = a.vs + ((page * OB + block) << a.page_shift) + (slot & mask);
+    const uint64_t page = (uint64_t)((uint32_t)slot >> a.page_shift) * a.kv_heads + kvh;
+    const uint8_t* vp = a.vs + ((page * OB + block) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
     if (DV == 128) {
       const u32x2 x = *(const u32x2*)vp;
       vscale[0] = x[0];
@@ -200,6 +230,12 @@ struct Fp4Wave {
     } else {
       vscale[0] = *(const uint32_t*)vp;
     }
+  }
+  template <bool ONCE>
+  __device__ __forceinline__ void load(const Fp4Args& a, int kvh, int slot, int lane) {
+    load_values<ONCE>(a, kvh, slot, lane);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) load_keys<ONCE>(a, kvh, slot, lane, t);
   }
   // Values' codes and scales of the tile that has come, into the wave's stage; those of keys
   // past `last` count as zero whatever lies there.
@@ -221,19 +257,28 @@ struct Fp4Wave {
       *(f16x4*)(mem + kCodes + block * (kF4Keys * 2) + g * 32 + t * 8) = f16x4{lo[0], lo[1], hi[0], hi[1]};
     }
   }
-  __device__ __forceinline__ void scores() {
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) s[rb][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // The tile's scores; MORE: the next tile's loads follow as soon as the registers they go to
+  // are free (values' codes are in LDS by now).
+  template <bool MORE, bool ONCE>
+  __device__ __forceinline__ void scores(const Fp4Args& a, int kvh, int slot, int lane) {
+    if (MORE) {
+      __builtin_amdgcn_sched_barrier(0);                            // (not earlier, into registers of their own)
+      load_values<ONCE>(a, kvh, slot, lane);
+    }
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const f16x2 s01 = scale_pair<false>(kscale[t]), s2 = scale_pair<true>(kscale[t]);
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) s[rb][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const f16x2 s01 = scale_pair<false>(kscale[t]), s2 = scale_pair<false>(kscale2[DQ == 192 ? t : 0]);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const f16x8 kf = fp4x8_f16(kc[t][k], k < 2 ? s01[0] : (k < 4 ? s01[1] : s2[0]));
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) s[rb][t] = mfma16_f16(kf, q[rb][k], s[rb][t]);
+      }
+      if (MORE) {
+        __builtin_amdgcn_sched_barrier(0);
+        load_keys<ONCE>(a, kvh, slot, lane, t);
       }
     }
   }
@@ -290,19 +335,30 @@ struct Fp4Wave {
       l[rb] += quarter_sum(sum);
     }
   }
+  // (LDS is read one block of columns ahead of the products; left to itself the compiler reads
+  // all of them at once, into registers that the loads under way need)
   __device__ __forceinline__ void values(const uint8_t* mem, int lane) {
     const uint8_t* sc = mem + kCodes + (lane >> 4) * 32;
+    f4_i32x2 w[2];
+    u32x4 sa[2], sb[2];
+    auto read = [&](int b) {
+      w[b & 1] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((f4_lds_i32x2*)(mem + (tr ^ ((b >> 1) * 16)) + (b & 1) * 8));
+      sa[b & 1] = *(const u32x4*)(sc + b * (kF4Keys * 2));
+      sb[b & 1] = *(const u32x4*)(sc + b * (kF4Keys * 2) + 16);
+    };
+    read(0);
 #pragma unroll
     for (int b = 0; b < OB; ++b) {
-      const f4_i32x2 w = __builtin_amdgcn_ds_read_tr4_b64_v2i32((f4_lds_i32x2*)(mem + (tr ^ ((b >> 1) * 16)) + (b & 1) * 8));
-      const u32x4 s0 = *(const u32x4*)(sc + b * (kF4Keys * 2)), s1 = *(const u32x4*)(sc + b * (kF4Keys * 2) + 16);
-      const f16x8 v0 = fp4x8_f16((uint32_t)w[0], f16_pair(s0[0]), f16_pair(s0[1]), f16_pair(s0[2]), f16_pair(s0[3]));
-      const f16x8 v1 = fp4x8_f16((uint32_t)w[1], f16_pair(s1[0]), f16_pair(s1[1]), f16_pair(s1[2]), f16_pair(s1[3]));
+      if (b + 1 < OB) read(b + 1);
+      const u32x4 s0 = sa[b & 1], s1 = sb[b & 1];
+      const f16x8 v0 = fp4x8_f16((uint32_t)w[b & 1][0], f16_pair(s0[0]), f16_pair(s0[1]), f16_pair(s0[2]), f16_pair(s0[3]));
+      const f16x8 v1 = fp4x8_f16((uint32_t)w[b & 1][1], f16_pair(s1[0]), f16_pair(s1[1]), f16_pair(s1[2]), f16_pair(s1[3]));
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
         o[rb][b] = mfma16_f16(v0, p[rb][0], o[rb][b]);
         o[rb][b] = mfma16_f16(v1, p[rb][1], o[rb][b]);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   // this wave's sums of block rb, maxima and weight sums into its region
@@ -339,14 +395,23 @@ __device__ __forceinline__ f32x4 join_waves(const uint8_t* mem, int row, int col
   return sum;
 }
 
-// Lane's cache row of the tile that begins at key `base` (of `len`): of key
-// KEYS * (lane % (64 / KEYS)), or in the last group of 16 where that is past the end.
+// Lane's part in finding a tile's rows: its key -- of the tile that begins at key `base` (of
+// `len`), key KEYS * (lane % (64 / KEYS)), or in the last group of 16 where that is past the
+// end -- and the table's entry for it.  The entry is loaded before the loads of the tile
+// before, so that it is there without a wait for those.
+struct Fp4Entry {
+  int at, page;
+  __device__ __forceinline__ int slot(const Fp4Args& a) const {
+    return (min(max(page, 0), a.num_pages - 1) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
+  }
+};
 template <int KEYS>
-__device__ __forceinline__ int f4_slot(const Fp4Args& a, const int32_t* table, int base, int len, int lane) {
+__device__ __forceinline__ Fp4Entry f4_entry(const Fp4Args& a, const int32_t* table, int base, int len, int lane) {
   const int key = base + KEYS * (lane % (kF4Keys / KEYS));
-  const int at = key < len ? key : ((len - 1) & ~15) + (key & 15);
-  const int e = table[at >> a.page_shift];
-  return (min(max(e, 0), a.num_pages - 1) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
+  Fp4Entry e;
+  e.at = key < len ? key : ((len - 1) & ~15) + (key & 15);
+  e.page = table[e.at >> a.page_shift];
+  return e;
 }
 
 // A wave's place in a list of tiles that its workgroup's waves share out in turn: tile
@@ -380,47 +445,62 @@ __device__ __forceinline__ void fp4_narrow(const Fp4Args& a, int kvh, Fp4Cursor<
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int G = a.q_heads / a.kv_heads;
   uint8_t* mine = mem + wv * W::kRegion;
-  auto slot_of = [&](const Fp4Cursor<PREFIX>& x) {
+  auto entry_of = [&](const Fp4Cursor<PREFIX>& x) {
     // (the prefix's part begins at a whole tile of the prefix)
-    return f4_slot<W::kEntryKeys>(a, x.table, x.key0 + x.tile * kF4Keys, x.key0 + x.len, lane);
+    return f4_entry<W::kEntryKeys>(a, x.table, x.key0 + x.tile * kF4Keys, x.key0 + x.len, lane);
   };
   W w;
   w.setup(lane);
-  Fp4Cursor<PREFIX> now = at, next;                                 // the tile that is computed on; the one after it
+  // The tile that is computed on, the one whose loads are under way by then, the one whose
+  // entries are (past the end: those of the one before once more).
+  Fp4Cursor<PREFIX> now = at;
   now.forward(a, wv);
-  int slot = 0;
-  if (now.left > 0) {
-    w.load(a, kvh, slot_of(now), lane);
-    next = now;
-    next.forward(a, kF4Waves);
-    if (next.left > 0) slot = slot_of(next);
-  }
-  // the requests of the list one after the other
-  for (int b = at.b, rest = at.left, tile = at.tile, tiles = at.tiles;;) {
+  Fp4Cursor<PREFIX> next = now;
+  next.forward(a, kF4Waves);
+  Fp4Cursor<PREFIX> far = next;
+  auto load_queries = [&](int b) {
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
       const int row = min(row0 + 16 * rb + (lane & 15), rows - 1);
       const int rq = PREFIX ? row / G : b, hq = kvh * G + (PREFIX ? row % G : row);
-      w.init(rb, a.q + rq * a.q_ts + hq * a.q_hs, lane, a.c);
+      w.load_query(rb, a.q + rq * a.q_ts + hq * a.q_hs, lane);
     }
-    while (now.left > 0 && now.b == b) {
-      const int last = now.len - 1 - now.tile * kF4Keys;
-      w.store(mine, lane, last);
-      w.scores();
-      const bool more = next.left > 0;
-      if (more) {
-        w.load(a, kvh, slot, lane);
-        now = next;
-        next.forward(a, kF4Waves);
-        if (next.left > 0) slot = slot_of(next);
-      }
-      if (last < kF4Keys - 1) w.mask(lane, last);
-      w.weights();
-      asm volatile("" ::: "memory");                                // (a wave's own LDS accesses stay in order)
-      w.values(mine, lane);
-      asm volatile("" ::: "memory");
-      if (!more) now.left = 0;
+  };
+  Fp4Entry entry = {0, 0};
+  load_queries(at.b);
+  if (now.left > 0) {
+    const int slot = entry_of(now).slot(a);
+    entry = entry_of(next);
+    w.template load<!PREFIX>(a, kvh, slot, lane);
+    far.forward(a, kF4Waves);
+  }
+  auto step = [&](auto more) {
+    const int last = now.len - 1 - now.tile * kF4Keys;
+    w.store(mine, lane, last);
+    if constexpr (decltype(more)::value) {
+      const int slot = entry.slot(a);
+      entry = entry_of(far);
+      w.template scores<true, !PREFIX>(a, kvh, slot, lane);
+    } else {
+      w.template scores<false, !PREFIX>(a, kvh, 0, lane);
     }
+    if (last < kF4Keys - 1) w.mask(lane, last);
+    w.weights();
+    asm volatile("" ::: "memory");                                  // (a wave's own LDS accesses stay in order)
+    w.values(mine, lane);
+    asm volatile("" ::: "memory");
+    now = next;
+    next = far;
+    far.forward(a, kF4Waves);
+  };
+  // the requests of the list one after the other
+  for (int b = at.b, rest = at.left, tile = at.tile, tiles = at.tiles;;) {
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) w.init(rb, a.c);
+    // (with and without a next tile apart: loads that may or may not have gone out would be
+    // waited for with the ones before them)
+    while (next.left > 0 && now.b == b) step(std::true_type());
+    if (now.left > 0 && now.b == b) step(std::false_type());
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
       w.leave(mine, rb, lane);
@@ -444,6 +524,7 @@ __device__ __forceinline__ void fp4_narrow(const Fp4Args& a, int kvh, Fp4Cursor<
     while (f4_len_at(a, b) == 0);
     tiles = f4_tiles(f4_len_at(a, b));
     tile = 0;
+    load_queries(b);
   }
 }
 
@@ -547,8 +628,11 @@ __device__ __forceinline__ void fp4_wide(const Fp4Args& a, int kvh, int part, in
   }
 }
 
+// Workgroups that a CU holds at once, by the registers of their waves.
+constexpr int fp4_per_cu(int k_dim, int rb, bool wide) { return rb == 1 && !wide ? (k_dim == 64 ? 4 : (k_dim == 128 ? 3 : 2)) : 2; }
+
 template <int DQ, int DV, int RB, bool WIDE>
-__global__ __launch_bounds__(kF4Waves * 64, 2) void attn_decode_fp4_kernel(Fp4Args a) {
+__global__ __launch_bounds__(kF4Waves * 64, fp4_per_cu(DQ, RB, WIDE)) void attn_decode_fp4_kernel(Fp4Args a) {
   constexpr int kNarrow = kF4Waves * Fp4Wave<DQ, DV, RB>::kRegion, kWide = WIDE ? 2 * kF4Keys * (DQ + DV) * 2 : 0;
   __shared__ __attribute__((aligned(16))) uint8_t mem[kNarrow > kWide ? kNarrow : kWide];
   const Fp4Plan& p = a.plan;
@@ -569,51 +653,45 @@ __global__ __launch_bounds__(kF4Waves * 64, 2) void attn_decode_fp4_kernel(Fp4Ar
   }
   item -= p.parts_p * p.blocks_p;
   const int run = item / p.blocks_s, block = item % p.blocks_s;
-  // tiles of all requests; the first workgroup writes down where each request's begin
+  // Tiles of all requests, 64 requests at a time; the first workgroup writes down where each
+  // request's begin.  Then the request that tile `begin` belongs to: the last whose tiles
+  // begin at or before it.
   const int B = a.num_requests;
-  const bool writes = blockIdx.x == (uint32_t)(p.parts_p * p.blocks_p * a.kv_heads);
-  int total = 0;
+  const bool writes = blockIdx.x == (uint32_t)(p.parts_p * p.blocks_p * a.kv_heads) && threadIdx.x < 64;
+  auto len_of = [&](int b0) { return b0 + lane < B ? f4_clamp_len(a, a.lens[b0 + lane]) : 0; };
+  int len = 0, n = 0, sum = 0, total = 0;
   for (int b0 = 0; b0 < B; b0 += 64) {
-    const int n = b0 + lane < B ? f4_tiles(f4_clamp_len(a, a.lens[b0 + lane])) : 0;
-    int sum = n;                                                    // inclusive over the lanes
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(sum, d);
-      if (lane >= d) sum += up;
-    }
-    if (writes && threadIdx.x < 64 && b0 + lane < B) a.first[b0 + lane] = total + sum - n;
+    len = len_of(b0);
+    n = f4_tiles(len);
+    sum = wave_scan(n);
+    if (writes && b0 + lane < B) a.first[b0 + lane] = total + sum - n;
     total += __builtin_amdgcn_readlane(sum, 63);
   }
-  if (writes && threadIdx.x == 0) a.first[B] = total;
+  if (writes && lane == 0) a.first[B] = total;
   const int each = (total + p.runs - 1) / p.runs, begin = run * each, end = min(begin + each, total);
   if (begin >= end) return;
-  // the request that tile `begin` belongs to: the last whose tiles begin at or before it
   Fp4Cursor<false> at;
-  int before = 0, b = 0;
+  at.b = at.tile = at.len = 0;
   for (int b0 = 0, sofar = 0; b0 < B; b0 += 64) {
-    const int n = b0 + lane < B ? f4_tiles(f4_clamp_len(a, a.lens[b0 + lane])) : 0;
-    int sum = n;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(sum, d);
-      if (lane >= d) sum += up;
+    if (B > 64) {                                                   // (else as above)
+      len = len_of(b0);
+      n = f4_tiles(len);
+      sum = wave_scan(n);
     }
     const uint64_t le = __ballot(sofar + sum - n <= begin && n > 0);
     if (le) {
       const int l = 63 - __builtin_clzll(le);
-      b = b0 + l;
-      before = sofar + __builtin_amdgcn_readlane(sum - n, l);
+      at.b = b0 + l;
+      at.tile = begin - sofar - __builtin_amdgcn_readlane(sum - n, l);
+      at.len = __builtin_amdgcn_readlane(len, l);
     }
     sofar += __builtin_amdgcn_readlane(sum, 63);
     if (sofar > begin) break;
   }
-  at.b = b;
-  at.tile = begin - before;
-  at.len = f4_len_at(a, b);
   at.tiles = f4_tiles(at.len);
   at.left = end - begin;
   at.key0 = 0;
-  at.table = a.table + b * a.table_stride;
+  at.table = a.table + at.b * a.table_stride;
   const int row0 = block * p.rows_s, rows = min(row0 + p.rows_s, a.q_heads / a.kv_heads);
   const int64_t entry0 = a.own + ((int64_t)(kvh * p.blocks_s + block) * (p.runs + B) + run) * p.rows_s;
   fp4_narrow<DQ, DV, RB, false>(a, kvh, at, row0, rows, entry0, mem);
@@ -632,32 +710,39 @@ __global__ __launch_bounds__(kF4Small * 64) void attn_decode_fp4_small_kernel(Fp
   const int tiles_p = f4_tiles(prefix), n_tiles = tiles_p + f4_tiles(len);
   const int32_t* own = a.table + b * a.table_stride;
   uint8_t* mine = mem + wv * W::kRegion;
-  auto slot_of = [&](int t) {
+  auto entry_of = [&](int t) {
     const bool front = t < tiles_p;
-    return f4_slot<W::kEntryKeys>(a, front ? a.prefix_table : own, (front ? t : t - tiles_p) * kF4Keys, front ? prefix : len, lane);
+    return f4_entry<W::kEntryKeys>(a, front ? a.prefix_table : own, (front ? t : t - tiles_p) * kF4Keys, front ? prefix : len, lane);
   };
-  int t = wv, slot = 0;
+  int t = wv;
   W w;
   w.setup(lane);
+  Fp4Entry entry = {0, 0};
+  w.load_query(0, a.q + b * a.q_ts + (int64_t)(kvh * G + min(lane & 15, G - 1)) * a.q_hs, lane);
   if (t < n_tiles) {
-    w.load(a, kvh, slot_of(t), lane);
-    if (t + kF4Small < n_tiles) slot = slot_of(t + kF4Small);
+    const int slot = entry_of(t).slot(a);
+    entry = entry_of(min(t + kF4Small, n_tiles - 1));
+    w.template load<false>(a, kvh, slot, lane);
   }
-  w.init(0, a.q + b * a.q_ts + (int64_t)(kvh * G + min(lane & 15, G - 1)) * a.q_hs, lane, a.c);
-  for (; t < n_tiles; t += kF4Small) {
+  w.init(0, a.c);
+  auto step = [&](auto more) {
     const int last = t < tiles_p ? prefix - 1 - t * kF4Keys : len - 1 - (t - tiles_p) * kF4Keys;
     w.store(mine, lane, last);
-    w.scores();
-    if (t + kF4Small < n_tiles) {
-      w.load(a, kvh, slot, lane);
-      if (t + 2 * kF4Small < n_tiles) slot = slot_of(t + 2 * kF4Small);
+    if constexpr (decltype(more)::value) {
+      const int slot = entry.slot(a);
+      entry = entry_of(min(t + 2 * kF4Small, n_tiles - 1));
+      w.template scores<true, false>(a, kvh, slot, lane);
+    } else {
+      w.template scores<false, false>(a, kvh, 0, lane);
     }
     if (last < kF4Keys - 1) w.mask(lane, last);
     w.weights();
     asm volatile("" ::: "memory");                                  // (a wave's own LDS accesses stay in order)
     w.values(mine, lane);
     asm volatile("" ::: "memory");
-  }
+  };
+  for (; t + kF4Small < n_tiles; t += kF4Small) step(std::true_type());
+  if (t < n_tiles) step(std::false_type());
   w.leave(mine, 0, lane);
   __syncthreads();
   const int row = threadIdx.x / (DV / 4), col = threadIdx.x % (DV / 4) * 4;
@@ -678,7 +763,8 @@ static bool fp4_small_is_sooner(int64_t B, int64_t G, int64_t kv_heads, int64_t 
   return 3500 + 250 * tiles * rounds * dims / 256 < 12000;
 }
 
-static Fp4Plan fp4_plan(int64_t B, int q_heads, int kv_heads, int64_t prefix_len, int64_t max_len, int dims) {
+static Fp4Plan fp4_plan(int64_t B, const moe_attn_params& a, int64_t prefix_len, int64_t max_len) {
+  const int q_heads = a.q_heads, kv_heads = a.kv_heads, dims = a.k_dim + a.v_dim;
   Fp4Plan p = {};
   const int64_t G = q_heads / kv_heads, rows = B * G;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
@@ -691,7 +777,7 @@ static Fp4Plan fp4_plan(int64_t B, int q_heads, int kv_heads, int64_t prefix_len
   p.rows_s = (int32_t)std::min<int64_t>(G, 16 * p.rb);
   // as the bf16 form's plan: units of work per 64 keys, the own lengths unknown (one at the
   // bound, the others at half)
-  const int64_t slots = 512;
+  const int64_t slots = 256 * fp4_per_cu(a.k_dim, p.rb, p.wide);
   const int64_t tiles_p = up(prefix_len, 64), tiles_s = max_len == 0 ? 0 : up((B + 1) * up(max_len, 64), 2) + B;
   const int64_t cost_p = p.wide ? 6 : 3, cost_s = 3;
   const int64_t per_part = kv_heads * p.blocks_p, per_run = kv_heads * p.blocks_s;
@@ -721,7 +807,7 @@ static int64_t fp4_entries(const Fp4Plan& p, int64_t B, int q_heads, int kv_head
 }
 
 size_t attn_decode_fp4_ws_bytes(int64_t B, const moe_attn_params& p, int64_t prefix_len, int64_t max_len) {
-  const Fp4Plan plan = fp4_plan(B, p.q_heads, p.kv_heads, prefix_len, max_len, p.k_dim + p.v_dim);
+  const Fp4Plan plan = fp4_plan(B, p, prefix_len, max_len);
   const int64_t entries = fp4_entries(plan, B, p.q_heads, p.kv_heads);
   return entries == 0 ? 0 : (size_t)entries * ((size_t)p.v_dim * 4 + 8) + ((size_t)B + 1) * 4;
 }
@@ -731,7 +817,7 @@ static int64_t fp4_grid(const Fp4Plan& p, int kv_heads) {
 }
 
 int64_t attn_decode_fp4_grid(int64_t B, const moe_attn_params& p, int64_t prefix_len, int64_t max_len) {
-  const Fp4Plan plan = fp4_plan(B, p.q_heads, p.kv_heads, prefix_len, max_len, p.k_dim + p.v_dim);
+  const Fp4Plan plan = fp4_plan(B, p, prefix_len, max_len);
   return plan.small ? B * p.kv_heads : fp4_grid(plan, p.kv_heads);
 }
 
@@ -800,7 +886,7 @@ moe_status launch_attn_decode_fp4(const moe_heads& q, const moe_kv_cache_fp4& ca
   a.page_shift = __builtin_ctz((unsigned)cache.page_size);
   a.c = p.scale * kLog2e * cache.k_global;
   a.v_scale = cache.v_global;
-  a.plan = fp4_plan(B, p.q_heads, p.kv_heads, prefix_len, max_len, p.k_dim + p.v_dim);
+  a.plan = fp4_plan(B, p, prefix_len, max_len);
   const int64_t entries = fp4_entries(a.plan, B, p.q_heads, p.kv_heads);
   a.part_o = (float*)ws;                            // (the sums first: they need 16-byte alignment)
   a.part_ml = (float2*)(a.part_o + entries * p.v_dim);
