@@ -36,7 +36,7 @@ EXPORTS = ("moe_status_string", "moe_last_error", "moe_version", "moe_route", "m
            "moe_kv_slots", "moe_qk_norm_rope", "moe_attn_prompt_workspace_bytes",
            "moe_attn_prompt", "moe_attn_decode_workspace_bytes", "moe_attn_decode", "moe_qk_norm_rope_fp4",
            "moe_attn_decode_fp4_workspace_bytes", "moe_attn_decode_fp4", "moe_kv_gather", "moe_kv_gather_fp4", "moe_kv_fork",
-           "moe_kv_free_pages", "moe_kv_compact_workspace_bytes", "moe_kv_compact", "moe_block_norm")
+           "moe_kv_free_pages_workspace_bytes", "moe_kv_free_pages", "moe_kv_compact_workspace_bytes", "moe_kv_compact", "moe_block_norm")
 
 
 class RouteParams(ctypes.Structure):
@@ -170,7 +170,9 @@ def _load() -> ctypes.CDLL:
     lib.moe_kv_fork.restype = i32
     lib.moe_kv_fork.argtypes = [vp, i64, i32, i32, vp, vp, vp, i32, vp, i64, i32, buffers, i64, vp, vp]
     lib.moe_kv_free_pages.restype = i32
-    lib.moe_kv_free_pages.argtypes = [vp, i64, i32, i32, vp, i32, i64, vp, vp, vp]
+    lib.moe_kv_free_pages.argtypes = [vp, i64, i32, i32, vp, i32, i64, vp, vp, vp, sz, vp]
+    lib.moe_kv_free_pages_workspace_bytes.restype = sz
+    lib.moe_kv_free_pages_workspace_bytes.argtypes = [i32, i32, i64]
     lib.moe_kv_compact_workspace_bytes.restype = sz
     lib.moe_kv_compact_workspace_bytes.argtypes = [i64]
     lib.moe_kv_compact.restype = i32
@@ -566,6 +568,10 @@ def attn_decode_fp4_workspace_bytes(num_requests: int, prefix_len: int, max_len:
                                     v_dim: int) -> int:
     p = AttnParams(q_heads, kv_heads, k_dim, v_dim, 1.0)
     return int(lib.moe_attn_decode_fp4_workspace_bytes(num_requests, prefix_len, max_len, p))
+
+
+def kv_free_pages_workspace_bytes(num_rows: int, max_blocks: int, num_pages: int) -> int:
+    return int(lib.moe_kv_free_pages_workspace_bytes(num_rows, max_blocks, num_pages))
 
 
 def kv_compact_workspace_bytes(num_pages: int) -> int:

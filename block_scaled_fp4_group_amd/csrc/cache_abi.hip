@@ -11,6 +11,7 @@ moe_status launch_kv_gather(const moe_kv_cache&, int, int, int, const int32_t*, 
                             const int32_t*, int, int64_t, const moe_heads&, const moe_heads&, hipStream_t);
 moe_status launch_kv_gather_fp4(const moe_kv_cache_fp4&, int, int, int, const int32_t*, int64_t, int, const int32_t*, int64_t,
                                 const int32_t*, int, int64_t, const moe_heads&, const moe_heads&, hipStream_t);
+int64_t kv_gather_grid(int64_t, int);
 size_t attn_decode_fp4_ws_bytes(int64_t, const moe_attn_params&, int64_t, int64_t);
 int64_t attn_decode_fp4_grid(int64_t, const moe_attn_params&, int64_t, int64_t);
 moe_status launch_attn_decode_fp4(const moe_heads&, const moe_kv_cache_fp4&, const int32_t*, int64_t, const int32_t*, int64_t,
@@ -20,7 +21,8 @@ int64_t kv_pages_most();
 size_t kv_compact_ws_bytes(int64_t);
 moe_status launch_kv_fork(int32_t*, int64_t, int, int, int32_t*, const int32_t*, const int32_t*, int, const int32_t*, int64_t,
                           int, const moe_page_buffers&, int64_t, int32_t*, hipStream_t);
-moe_status launch_kv_free_pages(const int32_t*, int64_t, int, int, const int32_t*, int, int64_t, int32_t*, int32_t*,
+size_t kv_free_ws_bytes(int64_t, int64_t, int64_t);
+moe_status launch_kv_free_pages(const int32_t*, int64_t, int, int, const int32_t*, int, int64_t, int32_t*, int32_t*, void*,
                                 hipStream_t);
 moe_status launch_kv_compact(const int32_t*, int64_t, int, int, const int32_t*, int, const moe_page_buffers&, int64_t, int32_t*,
                              int64_t, int32_t*, void*, hipStream_t);
@@ -60,6 +62,12 @@ static moe_status check_pool(const char* fn, int64_t num_pages) {
   return MOE_ERR_UNSUPPORTED;
 }
 
+static moe_status check_workspace(const char* fn, const void* workspace, size_t bytes, size_t need) {
+  if (need == 0 || (workspace != nullptr && bytes >= need && aligned16(workspace))) return MOE_OK;
+  set_error("%s: workspace %zu bytes < %zu (or NULL / unaligned)", fn, bytes, need);
+  return MOE_ERR_WORKSPACE;
+}
+
 static moe_status check_buffers(const char* fn, const moe_page_buffers* b) {
   MOE_CHECK(b && b->count >= 0 && b->count <= MOE_PAGE_BUFFERS, "%s: up to %d page buffers", fn, MOE_PAGE_BUFFERS);
   for (int i = 0; i < b->count; ++i)
@@ -87,6 +95,7 @@ static moe_status check_gather(const char* fn, int32_t kv_heads, int32_t k_dim, 
   MOE_CHECK(max_blocks >= 0 && prefix_blocks >= 0 && prefix_len >= 0, "%s: negative size", fn);
   MOE_CHECK(cu_k, "%s: cu_k is NULL", fn);
   MOE_CHECK(total_k <= 0x7fffffff, "%s: over 2^31 - 1 rows", fn);
+  MOE_CHECK(kv_gather_grid(total_k, kv_heads) < ((int64_t)1 << 31), "%s: too many rows", fn);
   MOE_CHECK(table_stride >= max_blocks && (max_blocks == 0 || block_table), "%s: block_table NULL or its stride too small", fn);
   MOE_CHECK(prefix_len <= (int64_t)prefix_blocks * page_size, "%s: prefix_len %lld needs more than %d pages", fn,
             (long long)prefix_len, prefix_blocks);
@@ -158,11 +167,7 @@ moe_status moe_attn_decode_fp4(const moe_heads* q, const moe_kv_cache_fp4* cache
   MOE_CHECK(decode_sizes_fit(num_requests, prefix_len, max_len, *p), "%s: too many keys or rows", fn);
   MOE_CHECK(aligned4(lse), "%s: lse not 4-byte aligned", fn);
   MOE_CHECK(attn_decode_fp4_grid(num_requests, *p, prefix_len, max_len) < ((int64_t)1 << 31), "%s: too many rows", fn);
-  const size_t need = attn_decode_fp4_ws_bytes(num_requests, *p, prefix_len, max_len);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))) {
-    set_error("%s: workspace %zu bytes < %zu (or NULL / unaligned)", fn, workspace_bytes, need);
-    return MOE_ERR_WORKSPACE;
-  }
+  MOE_PASS(check_workspace(fn, workspace, workspace_bytes, attn_decode_fp4_ws_bytes(num_requests, *p, prefix_len, max_len)));
   return launch_attn_decode_fp4(*q, *cache, block_table, table_stride, lens, num_requests, max_len, prefix_table, prefix_len,
                                 *p, *out, lse, workspace, stream);
 }
@@ -218,16 +223,22 @@ moe_status moe_kv_fork(int32_t* block_table, int64_t table_stride, int32_t num_r
                         __builtin_ctz((unsigned)page_size), *buffers, num_pages, counts, stream);
 }
 
+size_t moe_kv_free_pages_workspace_bytes(int32_t num_rows, int32_t max_blocks, int64_t num_pages) {
+  return num_rows < 0 || max_blocks < 0 || num_pages < 1 || num_pages > kv_pages_most() ? 0
+                                                                                       : kv_free_ws_bytes(num_rows, max_blocks, num_pages);
+}
+
 moe_status moe_kv_free_pages(const int32_t* block_table, int64_t table_stride, int32_t num_rows, int32_t max_blocks,
                              const int32_t* lens, int32_t page_size, int64_t num_pages, int32_t* free_pages, int32_t* counts,
-                             hipStream_t stream) {
+                             void* workspace, size_t workspace_bytes, hipStream_t stream) {
   const char* fn = "moe_kv_free_pages";
   set_error("");
   MOE_PASS(check_table(fn, block_table, table_stride, num_rows, max_blocks, lens, page_size, num_pages));
   MOE_PASS(check_pool(fn, num_pages));
   MOE_CHECK(free_pages && counts, "%s: free_pages or counts is NULL", fn);
+  MOE_PASS(check_workspace(fn, workspace, workspace_bytes, kv_free_ws_bytes(num_rows, max_blocks, num_pages)));
   return launch_kv_free_pages(block_table, table_stride, max_blocks == 0 ? 0 : num_rows, max_blocks, lens,
-                              __builtin_ctz((unsigned)page_size), num_pages, free_pages, counts, stream);
+                              __builtin_ctz((unsigned)page_size), num_pages, free_pages, counts, workspace, stream);
 }
 
 size_t moe_kv_compact_workspace_bytes(int64_t num_pages) {
@@ -252,11 +263,7 @@ moe_status moe_kv_compact(const int32_t* block_table, int64_t table_stride, int3
                   out_table + n * out_stride + max_blocks <= block_table || block_table + n * table_stride + max_blocks <= out_table,
               "%s: out_table overlaps block_table", fn);
   }
-  const size_t need = kv_compact_ws_bytes(num_pages);
-  if (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)) {
-    set_error("%s: workspace %zu bytes < %zu (or NULL / unaligned)", fn, workspace_bytes, need);
-    return MOE_ERR_WORKSPACE;
-  }
+  MOE_PASS(check_workspace(fn, workspace, workspace_bytes, kv_compact_ws_bytes(num_pages)));
   return launch_kv_compact(block_table, table_stride, max_blocks == 0 ? 0 : num_rows, max_blocks, lens,
                            __builtin_ctz((unsigned)page_size), *buffers, num_pages, out_table, out_stride, counts, workspace,
                            stream);

@@ -983,7 +983,7 @@ PyObject* kv_fork(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* 
 }
 
 PyObject* kv_free_pages(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
-  NAMES("block_table", "lens", "page_size", "num_pages", "free_pages", "counts", "stream");
+  NAMES("block_table", "lens", "page_size", "num_pages", "free_pages", "counts", "workspace", "stream");
   if (!parse("kv_free_pages", args, nargs, kwnames, names, N, 4, a)) return nullptr;
   int dev;
   Placed placed;
@@ -991,24 +991,27 @@ PyObject* kv_free_pages(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyOb
   int64_t stride, blocks, pages;
   Shape ls;
   int32_t page;
-  if (!gpu(a[1], "lens", &dev) || !placed.enter(a[6], dev) ||
+  if (!gpu(a[1], "lens", &dev) || !placed.enter(a[7], dev) ||
       !table_and_lens(a[0], a[1], dev, &tab, &stride, &blocks, &lens, &ls) || !as_i32(a[2], "page_size", &page) ||
       !as_i64(a[3], &pages))
     return nullptr;
-  Ref made[2];
+  Ref made[2], mw;
+  void* ws;
+  size_t bytes;
   PyObject* out[2];
   if (pages < 1) {
     PyErr_SetString(PyExc_ValueError, "num_pages must be positive");
     return nullptr;
   }
   if (!output_ints(a[4], "free_pages", a[1], dev, pages, &made[0], &out[0], &p[0]) ||
-      !output_ints(a[5], "counts", a[1], dev, 2, &made[1], &out[1], &p[1]))
+      !output_ints(a[5], "counts", a[1], dev, 2, &made[1], &out[1], &p[1]) ||
+      !workspace(a[6], a[1], dev, moe_kv_free_pages_workspace_bytes((int32_t)ls.d[0], (int32_t)blocks, pages), &mw, &ws, &bytes))
     return nullptr;
   PyObject* own[2] = {made[0].p, made[1].p};
   hipStream_t stream;
-  if (!stream_of(a[6], dev, &stream) || !placed.known(own, 2)) return nullptr;
+  if (!stream_of(a[7], dev, &stream) || !placed.known(own, 2)) return nullptr;
   if (!check(moe_kv_free_pages((const int32_t*)tab, stride, (int32_t)ls.d[0], (int32_t)blocks, (const int32_t*)lens, page, pages,
-                               (int32_t*)p[0], (int32_t*)p[1], stream),
+                               (int32_t*)p[0], (int32_t*)p[1], ws, bytes, stream),
              "moe_kv_free_pages"))
     return nullptr;
   return PyTuple_Pack(2, out[0], out[1]);
@@ -1196,7 +1199,8 @@ PyMethodDef methods[] = {
          "or an Fp4Cache's four).  block_table and lens are changed in place.  -> counts [2]: pages taken, pages needed.\n"
          STREAM_DOC),
     CALL(kv_free_pages,
-         "kv_free_pages(block_table, lens, page_size, num_pages, free_pages=None, counts=None, stream=None)\n--\n\n"
+         "kv_free_pages(block_table, lens, page_size, num_pages, free_pages=None, counts=None, workspace=None, "
+         "stream=None)\n--\n\n"
          "The pages that no row of the table holds (a request is ended by setting its length to 0).  -> (free_pages\n"
          "[num_pages]: ascending, then -1; counts [2]: free, held).\n" STREAM_DOC),
     CALL(kv_compact,

@@ -3,8 +3,9 @@
 // then the request's own.  From a bf16 cache a copy, from one held in 4 bits the values
 // that the codes stand for, code x scale x global, which bf16 holds exactly.
 //
-// Memory traffic is all there is.  A workgroup takes 32 rows: it finds their places
-// once, then its threads take 16 values each.
+// Memory traffic is all there is.  A workgroup takes 32 rows of one head's keys or values:
+// it finds their places, then its threads take 16 values each.  (With all heads of the rows
+// to a workgroup 364 rows x 8 x 128 took 13 us, 11 times one after the other.)
 #include "common.h"
 
 namespace moe {
@@ -40,7 +41,8 @@ template <bool FP4>
 __global__ __launch_bounds__(kGatherThreads) void kv_gather_kernel(GatherArgs a) {
   __shared__ int64_t slots[kGatherRows];                            // page << page_shift | row in it; or:
   constexpr int64_t kNoPage = -1, kNoSequence = -2;
-  const int64_t row0 = (int64_t)blockIdx.x * kGatherRows;
+  const int kind = blockIdx.x & 1, h = (int)((blockIdx.x >> 1) % (uint32_t)a.kv_heads);
+  const int64_t row0 = (int64_t)((blockIdx.x >> 1) / (uint32_t)a.kv_heads) * kGatherRows;
   const int64_t page_mask = ((int64_t)1 << a.page_shift) - 1;
   if (threadIdx.x < kGatherRows) {
     const int64_t row = row0 + threadIdx.x;
@@ -65,44 +67,34 @@ __global__ __launch_bounds__(kGatherThreads) void kv_gather_kernel(GatherArgs a)
   }
   __syncthreads();
   const int rows = (int)min((int64_t)kGatherRows, a.total - row0);
-  const int kb = a.k_dim / 16, vb = a.v_dim / 16;
-  for (int kind = 0; kind < 2; ++kind) {
-    const int blocks = kind == 0 ? kb : vb, dim = kind == 0 ? a.k_dim : a.v_dim, items = rows * a.kv_heads * blocks;
-    const uint8_t* from = kind == 0 ? a.k : a.v;
-    uint16_t* to = kind == 0 ? a.k_out : a.v_out;
-    const int64_t ts = kind == 0 ? a.ko_ts : a.vo_ts, hs = kind == 0 ? a.ko_hs : a.vo_hs;
-    for (int f = threadIdx.x; f < items; f += kGatherThreads) {
-      int r, h;
-      const int b = f % blocks;
-      if (FP4) {                                                    // a head's rows follow one another
-        r = f / blocks % rows;
-        h = f / blocks / rows;
-      } else {                                                      // a row's heads do
-        h = f / blocks % a.kv_heads;
-        r = f / blocks / a.kv_heads;
-      }
-      const int64_t slot = slots[r];
-      uint16_t* dst = to + (row0 + r) * ts + h * hs + 16 * b;
-      if (slot == kNoSequence) continue;                            // the row is left as it was
-      if (slot == kNoPage) {
-        *(u32x4*)dst = *(u32x4*)(dst + 8) = u32x4{0u, 0u, 0u, 0u};             // not one of the cache's pages
-        continue;
-      }
-      if (FP4) {
-        const int64_t page = slot >> a.page_shift, in = slot & page_mask, head = page * a.kv_heads + h;
-        const int64_t at = (head << a.page_shift) + in;
-        const u32x2 codes = *(const u32x2*)(from + at * (dim / 2) + 8 * b);
-        const uint8_t* s = kind == 0 ? a.k_scale + at * blocks + b : a.v_scale + ((head * blocks + b) << a.page_shift) + in;
-        store_fp4(dst, codes, e4m3_to_f32(*s) * (kind == 0 ? a.k_global : a.v_global));
-      } else {
-        const uint16_t* src = (const uint16_t*)from + (slot * a.kv_heads + h) * dim + 16 * b;
-        const u32x4 x = *(const u32x4*)src, y = *(const u32x4*)(src + 8);
-        *(u32x4*)dst = x;
-        *(u32x4*)(dst + 8) = y;
-      }
+  const int blocks = (kind == 0 ? a.k_dim : a.v_dim) / 16, dim = 16 * blocks;
+  const uint8_t* from = kind == 0 ? a.k : a.v;
+  uint16_t* to = kind == 0 ? a.k_out + row0 * a.ko_ts + h * a.ko_hs : a.v_out + row0 * a.vo_ts + h * a.vo_hs;
+  const int64_t ts = kind == 0 ? a.ko_ts : a.vo_ts;
+  for (int f = threadIdx.x; f < rows * blocks; f += kGatherThreads) {
+    const int b = f % blocks, r = f / blocks;
+    const int64_t slot = slots[r];
+    uint16_t* dst = to + r * ts + 16 * b;
+    if (slot == kNoSequence) continue;                              // the row is left as it was
+    if (slot == kNoPage) {
+      *(u32x4*)dst = *(u32x4*)(dst + 8) = u32x4{0u, 0u, 0u, 0u};   // not one of the cache's pages
+    } else if (FP4) {
+      const int64_t page = slot >> a.page_shift, in = slot & page_mask, head = page * a.kv_heads + h;
+      const int64_t at = (head << a.page_shift) + in;
+      const u32x2 codes = *(const u32x2*)(from + at * (dim / 2) + 8 * b);
+      const uint8_t* s = kind == 0 ? a.k_scale + at * blocks + b : a.v_scale + ((head * blocks + b) << a.page_shift) + in;
+      store_fp4(dst, codes, e4m3_to_f32(*s) * (kind == 0 ? a.k_global : a.v_global));
+    } else {
+      const uint16_t* src = (const uint16_t*)from + (slot * a.kv_heads + h) * dim + 16 * b;
+      const u32x4 x = *(const u32x4*)src, y = *(const u32x4*)(src + 8);
+      *(u32x4*)dst = x;
+      *(u32x4*)(dst + 8) = y;
     }
   }
 }
+
+// workgroups (host: in 31 bits)
+int64_t kv_gather_grid(int64_t total, int kv_heads) { return (total + kGatherRows - 1) / kGatherRows * kv_heads * 2; }
 
 static GatherArgs gather_args(int kv_heads, int k_dim, int v_dim, const int32_t* table, int64_t table_stride, int max_blocks,
                               const int32_t* prefix_table, int64_t prefix_len, const int32_t* cu, int num_seqs,
@@ -138,8 +130,7 @@ moe_status launch_kv_gather(const moe_kv_cache& c, int kv_heads, int k_dim, int 
   a.v = (const uint8_t*)c.v;
   a.num_pages = c.num_pages;
   a.page_shift = __builtin_ctz((unsigned)c.page_size);
-  hipLaunchKernelGGL(kv_gather_kernel<false>, dim3((uint32_t)((total + kGatherRows - 1) / kGatherRows)), dim3(kGatherThreads), 0,
-                     stream, a);
+  hipLaunchKernelGGL(kv_gather_kernel<false>, dim3((uint32_t)kv_gather_grid(total, kv_heads)), dim3(kGatherThreads), 0, stream, a);
   return launch_status("moe_kv_gather");
 }
 
@@ -157,8 +148,7 @@ moe_status launch_kv_gather_fp4(const moe_kv_cache_fp4& c, int kv_heads, int k_d
   a.page_shift = __builtin_ctz((unsigned)c.page_size);
   a.k_global = c.k_global;
   a.v_global = c.v_global;
-  hipLaunchKernelGGL(kv_gather_kernel<true>, dim3((uint32_t)((total + kGatherRows - 1) / kGatherRows)), dim3(kGatherThreads), 0,
-                     stream, a);
+  hipLaunchKernelGGL(kv_gather_kernel<true>, dim3((uint32_t)kv_gather_grid(total, kv_heads)), dim3(kGatherThreads), 0, stream, a);
   return launch_status("moe_kv_gather_fp4");
 }
 

@@ -134,20 +134,81 @@ __global__ __launch_bounds__(kForkThreads) void kv_fork_kernel(ForkArgs a) {
 }
 
 // ------------------------------------------------------------- live pages
-// The bitmap of live pages in LDS, by the whole workgroup; ends with a barrier.
-__device__ __forceinline__ void mark_pages(const TableArgs& t, uint32_t* bits, int words) {
-  for (int i = threadIdx.x; i < words; i += kMarkThreads) bits[i] = 0u;
-  __syncthreads();
-  // a wave per row, 64 entries at a time
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  for (int row = wv; row < t.rows; row += kMarkThreads / 64) {
-    const int n = held_pages(t, row);
-    const int32_t* e = t.table + row * t.stride;
-    for (int i = lane; i < n; i += 64) {
-      const int32_t p = e[i];
-      if (p >= 0 && p < t.num_pages) atomicOr(&bits[p >> 5], 1u << (p & 31));
+// Four rows' lengths, then 64 entries of each, under way at once: bits of the pages set by
+// `set`.  wave of `waves`.
+template <class Set>
+__device__ __forceinline__ void mark_rows(const TableArgs& t, int wave, int waves, Set set) {
+  const int lane = threadIdx.x & 63;
+  for (int row = 4 * wave; row < t.rows; row += 4 * waves) {
+    int n[4], most = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) n[u] = held_pages(t, min(row + u, t.rows - 1));
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      n[u] = row + u < t.rows ? n[u] : 0;
+      most = max(most, n[u]);
+    }
+    for (int i = lane; i < most; i += 64) {
+      int32_t p[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) p[u] = i < n[u] ? t.table[(row + u) * t.stride + i] : -1;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (p[u] >= 0 && p[u] < t.num_pages) set(p[u]);
     }
   }
+}
+
+// Of a large table or pool the marks are made in memory, a byte for each page, by all
+// workgroups (cleared by one launch, set by the next; plain stores of the same value need no
+// atomics), of a small one in LDS, a bit for each page, by the workgroup that uses them.
+// Entries 1500 x 256 of a pool of 190000 pages: 80 us by one workgroup, 12 us so (17 with a
+// bit for each page, set by atomics); 64 x 64 of 4000: 5 us by one.
+constexpr int64_t kMarkAlone = 16384;               // entries, and pages / 4
+static bool marks_alone(int64_t rows, int64_t max_blocks, int64_t num_pages) {
+  return rows * max_blocks <= kMarkAlone && num_pages <= 4 * kMarkAlone;
+}
+static int64_t mark_bytes(int64_t num_pages) { return (num_pages + 127) / 128 * 128; }
+// (list, if there is one: -1 everywhere, of which the sweep then overwrites the front)
+__global__ __launch_bounds__(256) void kv_clear_kernel(uint8_t* marks, int64_t bytes, int32_t* list, int pages) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 16;
+  if (i < bytes) *(u32x4*)(marks + i) = u32x4{0u, 0u, 0u, 0u};
+  if (!list) return;
+  const int base = blockIdx.x * 4096;
+  for (int j = base + threadIdx.x; j < min(base + 4096, pages); j += 256) list[j] = -1;
+}
+__global__ __launch_bounds__(256) void kv_mark_kernel(TableArgs t, uint8_t* marks) {
+  mark_rows(t, blockIdx.x * 4 + (threadIdx.x >> 6), gridDim.x * 4, [&](int p) { marks[p] = 1; });
+}
+// Marks of pages 32 w .. 32 w + 31 as bits: four bytes of 0 or 1 meet in a product's top
+// bits, each in one place.
+__device__ __forceinline__ uint32_t mark_word(const uint8_t* marks, int w) {
+  uint32_t bits = 0u;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const u32x4 x = *(const u32x4*)(marks + 32 * (int64_t)w + 16 * i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bits |= (x[j] * 0x10204080u) >> 28 << (16 * i + 4 * j);
+  }
+  return bits;
+}
+
+// Those of pages 32 w + 8 q .. 32 w + 8 q + 7.
+__device__ __forceinline__ uint32_t mark_byte(const uint8_t* marks, int w, int q) {
+  const u32x2 x = *(const u32x2*)(marks + 32 * (int64_t)w + 8 * q);
+  return (x[0] * 0x10204080u) >> 28 | (x[1] * 0x10204080u) >> 28 << 4;
+}
+
+// All marks as bits in LDS, by the whole workgroup: read, or made here.  Ends with a barrier.
+__device__ __forceinline__ void load_pages(const TableArgs& t, const uint8_t* marks, uint32_t* bits, int words) {
+  if (marks) {
+    for (int i = threadIdx.x; i < words; i += kMarkThreads) bits[i] = mark_word(marks, i);
+    __syncthreads();
+    return;
+  }
+  for (int i = threadIdx.x; i < words; i += kMarkThreads) bits[i] = 0u;
+  __syncthreads();
+  mark_rows(t, threadIdx.x >> 6, kMarkThreads / 64, [&](int p) { atomicOr(&bits[p >> 5], 1u << (p & 31)); });
   __syncthreads();
 }
 
@@ -175,30 +236,67 @@ __device__ __forceinline__ int scan_block(int x, int* all, int* part) {
 
 struct FreeArgs {
   TableArgs t;
+  const uint8_t* marks;                             // null: made by the one workgroup
   int32_t* free_pages;
   int32_t* counts;
 };
 
-// One workgroup marks and sweeps.
-__global__ __launch_bounds__(kMarkThreads) void kv_free_kernel(FreeArgs a) {
-  __shared__ uint32_t bits[kMarkPages / 32];
+// Workgroup i sweeps words kSweepWords i .. of the marks' bits (the only one: all); what it
+// finds free follows what there is before, which it counts itself.
+constexpr int kSweepWords = kMarkThreads / 4;       // 8 pages to a thread
+
+__global__ __launch_bounds__(kMarkThreads) void kv_sweep_kernel(FreeArgs a) {
+  __shared__ uint32_t bits[4 * kMarkAlone / 32];
+  __shared__ int32_t out[32 * kSweepWords];
   __shared__ int part[kMarkThreads / 64];
   const int P = (int)a.t.num_pages, words = (P + 31) / 32;
-  mark_pages(a.t, bits, words);
-  // each thread sweeps a run of words: what it finds free follows what those before it found
-  const int per = (words + kMarkThreads - 1) / kMarkThreads;
-  const int w0 = min((int)threadIdx.x * per, words), w1 = min(w0 + per, words);
-  auto free_of = [&](int w) { return ~bits[w] & (w == words - 1 && (P & 31) ? (1u << (P & 31)) - 1u : ~0u); };
-  int n = 0, all;
-  for (int w = w0; w < w1; ++w) n += __popc(free_of(w));
-  int at = scan_block(n, &all, part);
-  for (int w = w0; w < w1; ++w)
-    for (uint32_t f = free_of(w); f; f &= f - 1) a.free_pages[at++] = 32 * w + __builtin_ctz(f);
-  for (int i = all + threadIdx.x; i < P; i += kMarkThreads) a.free_pages[i] = -1;
-  if (threadIdx.x == 0) {
-    a.counts[0] = all;
-    a.counts[1] = P - all;
+  int w0 = 0, w1 = words, before = 0;                               // held pages before w0
+  if (a.marks) {
+    w0 = blockIdx.x * kSweepWords;
+    w1 = min(w0 + kSweepWords, words);
+    uint32_t x = 0u;                                                // (marks are 0 or 1)
+    for (int i = 16 * (int)threadIdx.x; i < 32 * w0; i += 8 * 16 * kMarkThreads) {
+      u32x4 v[8];                                                   // 16 pages each, 8 loads under way
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int at = i + u * 16 * kMarkThreads;
+        v[u] = at < 32 * w0 ? *(const u32x4*)(a.marks + at) : u32x4{0u, 0u, 0u, 0u};
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x = __builtin_amdgcn_sad_u8(v[u][j], 0u, x);
+    }
+    scan_block((int)x, &before, part);
+  } else {
+    load_pages(a.t, nullptr, bits, words);
   }
+  before = 32 * w0 - before;                                        // from here on: free ones
+  // the list of kSweepWords words at a time through LDS, so that it is stored in whole lines
+  for (int base = w0; base < w1; base += kSweepWords) {
+    const int w = base + (threadIdx.x >> 2), q = threadIdx.x & 3;
+    uint32_t f = 0u;                                                // 8 pages to a thread
+    if (w < w1) {
+      f = ~(a.marks ? mark_byte(a.marks, w, q) : bits[w] >> (8 * q)) & 255u;
+      const int pages = P - (32 * w + 8 * q);
+      if (pages < 8) f &= (1u << max(pages, 0)) - 1u;
+    }
+    int n;
+    int at = scan_block(__popc(f), &n, part);
+    for (; f; f &= f - 1) out[at++] = 32 * w + 8 * q + __builtin_ctz(f);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kMarkThreads) a.free_pages[before + i] = out[i];
+    before += n;
+    __syncthreads();
+  }
+  if (w1 < words) return;
+  // the last workgroup knows how many there are
+  if (threadIdx.x == 0) {
+    a.counts[0] = before;
+    a.counts[1] = P - before;
+  }
+  if (!a.marks)                                                     // (else done by the first launch)
+    for (int i = before + threadIdx.x; i < P; i += kMarkThreads) a.free_pages[i] = -1;
 }
 
 // ---------------------------------------------------------------- compact
@@ -206,6 +304,7 @@ __global__ __launch_bounds__(kMarkThreads) void kv_free_kernel(FreeArgs a) {
 // behind that number where it goes (-1: nowhere); then the moves' sources and targets.
 struct CompactArgs {
   TableArgs t;
+  const uint8_t* marks;                             // null: made by the planning workgroup
   int32_t* out;
   int64_t out_stride;
   int32_t* counts;
@@ -222,28 +321,28 @@ __global__ __launch_bounds__(kMarkThreads) void kv_compact_plan_kernel(CompactAr
   __shared__ uint32_t bits[kMarkPages / 32];
   __shared__ int part[kMarkThreads / 64];
   const int P = (int)a.t.num_pages, words = (P + 31) / 32;
-  mark_pages(a.t, bits, words);
-  const int per = (words + kMarkThreads - 1) / kMarkThreads;
-  const int w0 = min((int)threadIdx.x * per, words), w1 = min(w0 + per, words);
-  int x = 0, n, moves;
-  for (int w = w0; w < w1; ++w) x += __popc(bits[w]);
+  load_pages(a.t, a.marks, bits, words);
+  int x = 0, n, moves = 0;
+  for (int w = threadIdx.x; w < words; w += kMarkThreads) x += __popc(bits[w]);
   scan_block(x, &n, part);
-  auto below = [&](int w) { return w < n >> 5 ? ~0u : (w == n >> 5 ? (1u << (n & 31)) - 1u : 0u); };   // pages of word w before n
-  int holes = 0, far = 0;
-  for (int w = w0; w < w1; ++w) {
-    holes += __popc(~bits[w] & below(w));
-    far += __popc(bits[w] & ~below(w));
+  // 8 pages to a thread; holes before page n and held pages from it on counted in the halves
+  // of one number (at most 8192 in a step)
+  int holes = 0;
+  for (int base = 0; base < words; base += kMarkThreads / 4) {
+    const int w = base + (threadIdx.x >> 2), p = 32 * w + 8 * (int)(threadIdx.x & 3);
+    const uint32_t held = w < words ? bits[w] >> (8 * (threadIdx.x & 3)) & 255u : 0u;
+    const uint32_t front = p + 8 <= n ? 255u : (p >= n ? 0u : (1u << (n - p)) - 1u);   // pages before n
+    uint32_t f = ~held & front, g = held & ~front;
+    int all;
+    const int at = scan_block(__popc(f) | __popc(g) << 16, &all, part);
+    int at_hole = holes + (at & 0xffff), at_far = moves + (at >> 16);
+    for (; f; f &= f - 1) move_dst(a)[at_hole++] = p + __builtin_ctz(f);
+    for (; g; g &= g - 1) move_src(a)[at_far++] = p + __builtin_ctz(g);
+    holes += all & 0xffff;
+    moves += all >> 16;
   }
-  int at_hole = scan_block(holes, &moves, part), at_far = scan_block(far, &moves, part);
-  for (int w = w0; w < w1; ++w)
-    for (uint32_t f = ~bits[w] & below(w); f; f &= f - 1) move_dst(a)[at_hole++] = 32 * w + __builtin_ctz(f);
   __syncthreads();
-  for (int w = w0; w < w1; ++w)
-    for (uint32_t f = bits[w] & ~below(w); f; f &= f - 1) {
-      const int p = 32 * w + __builtin_ctz(f);
-      move_to(a)[p] = move_dst(a)[at_far];
-      move_src(a)[at_far++] = p;
-    }
+  for (int i = threadIdx.x; i < moves; i += kMarkThreads) move_to(a)[move_src(a)[i]] = move_dst(a)[i];
   if (threadIdx.x == 0) {
     a.ws[0] = n;
     a.ws[1] = moves;
@@ -299,7 +398,24 @@ static PageBuffers page_buffers(const moe_page_buffers& b, int64_t* all) {
 }
 
 int64_t kv_pages_most() { return kMarkPages; }
-size_t kv_compact_ws_bytes(int64_t num_pages) { return (size_t)(4 + num_pages + 2 * (num_pages / 2)) * 4; }
+size_t kv_free_ws_bytes(int64_t rows, int64_t max_blocks, int64_t num_pages) {
+  return marks_alone(rows, max_blocks, num_pages) ? 0 : (size_t)mark_bytes(num_pages);
+}
+// (the marks first: 16-byte aligned)
+size_t kv_compact_ws_bytes(int64_t num_pages) {
+  return (size_t)mark_bytes(num_pages) + (size_t)(4 + num_pages + 2 * (num_pages / 2)) * 4;
+}
+
+// The marks in memory, if they are made there.
+static uint8_t* launch_marks(const TableArgs& t, void* ws, int32_t* list, hipStream_t stream) {
+  if (marks_alone(t.rows, t.max_blocks, t.num_pages)) return nullptr;
+  uint8_t* marks = (uint8_t*)ws;
+  const int64_t bytes = mark_bytes(t.num_pages);
+  hipLaunchKernelGGL(kv_clear_kernel, dim3((uint32_t)((bytes + 4095) / 4096)), dim3(256), 0, stream, marks, bytes, list,
+                     (int)t.num_pages);
+  if (t.rows > 0) hipLaunchKernelGGL(kv_mark_kernel, dim3((uint32_t)((t.rows + 15) / 16)), dim3(256), 0, stream, t, marks);
+  return marks;
+}
 
 moe_status launch_kv_fork(int32_t* table, int64_t stride, int rows, int max_blocks, int32_t* lens, const int32_t* parents,
                           const int32_t* children, int num_forks, const int32_t* free_pages, int64_t num_free,
@@ -324,12 +440,16 @@ moe_status launch_kv_fork(int32_t* table, int64_t stride, int rows, int max_bloc
 }
 
 moe_status launch_kv_free_pages(const int32_t* table, int64_t stride, int rows, int max_blocks, const int32_t* lens,
-                                int page_shift, int64_t num_pages, int32_t* free_pages, int32_t* counts, hipStream_t stream) {
+                                int page_shift, int64_t num_pages, int32_t* free_pages, int32_t* counts, void* ws,
+                                hipStream_t stream) {
   FreeArgs a;
   a.t = table_args(table, stride, rows, max_blocks, lens, page_shift, num_pages);
   a.free_pages = free_pages;
   a.counts = counts;
-  hipLaunchKernelGGL(kv_free_kernel, dim3(1), dim3(kMarkThreads), 0, stream, a);
+  a.marks = launch_marks(a.t, ws, free_pages, stream);
+  const int64_t words = (num_pages + 31) / 32;
+  const uint32_t grid = a.marks ? (uint32_t)((words + kSweepWords - 1) / kSweepWords) : 1u;
+  hipLaunchKernelGGL(kv_sweep_kernel, dim3(grid), dim3(kMarkThreads), 0, stream, a);
   return launch_status("moe_kv_free_pages");
 }
 
@@ -341,8 +461,9 @@ moe_status launch_kv_compact(const int32_t* table, int64_t stride, int rows, int
   a.out = out;
   a.out_stride = out_stride;
   a.counts = counts;
-  a.ws = (int32_t*)ws;
+  a.ws = (int32_t*)((uint8_t*)ws + mark_bytes(num_pages));
   a.buffers = page_buffers(buffers, &a.page_bytes);
+  a.marks = launch_marks(a.t, ws, nullptr, stream);
   hipLaunchKernelGGL(kv_compact_plan_kernel, dim3(1), dim3(kMarkThreads), 0, stream, a);
   moe_status st = launch_status("moe_kv_compact");
   if (st != MOE_OK) return st;

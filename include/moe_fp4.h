@@ -661,11 +661,14 @@ moe_status moe_kv_fork(int32_t* block_table, int64_t table_stride, int32_t num_r
 
 /* The pages that no row holds, ascending: a request is ended by setting its length to 0.
  *   free_pages int32 [num_pages]: the free pages, then -1;
- *   counts int32 [2]: free pages, held pages.
- * num_pages <= 2^20 (else MOE_ERR_UNSUPPORTED).  One launch. */
+ *   counts int32 [2]: free pages, held pages;
+ *   workspace: moe_kv_free_pages_workspace_bytes() bytes, 16-byte aligned (may be NULL when
+ *   that is 0); calls that share one must not overlap.
+ * num_pages <= 2^20 (else MOE_ERR_UNSUPPORTED).  One launch; three with a workspace. */
+size_t moe_kv_free_pages_workspace_bytes(int32_t num_rows, int32_t max_blocks, int64_t num_pages);
 moe_status moe_kv_free_pages(const int32_t* block_table, int64_t table_stride, int32_t num_rows, int32_t max_blocks,
                              const int32_t* lens, int32_t page_size, int64_t num_pages, int32_t* free_pages, int32_t* counts,
-                             hipStream_t stream);
+                             void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Held pages moved to the front of the pool: with n pages held, the i-th of them at or
  * behind page n goes to the i-th page before it that no row holds; afterwards pages n ..
@@ -675,7 +678,7 @@ moe_status moe_kv_free_pages(const int32_t* block_table, int64_t table_stride, i
  *   counts int32 [2]: n, pages moved;
  *   workspace: moe_kv_compact_workspace_bytes() bytes, 16-byte aligned; calls that share
  *   one must not overlap.
- * num_pages <= 2^20 (else MOE_ERR_UNSUPPORTED).  Two launches. */
+ * num_pages <= 2^20 (else MOE_ERR_UNSUPPORTED).  Two launches; four for large tables. */
 size_t moe_kv_compact_workspace_bytes(int64_t num_pages);
 moe_status moe_kv_compact(const int32_t* block_table, int64_t table_stride, int32_t num_rows, int32_t max_blocks,
                           const int32_t* lens, int32_t page_size, const moe_page_buffers* buffers, int64_t num_pages,
