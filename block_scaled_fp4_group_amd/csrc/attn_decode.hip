@@ -39,22 +39,7 @@
 namespace moe {
 
 constexpr int kDecThreads = 256;
-constexpr int kDecSlots = 512;                      // two workgroups on each of 256 CUs
 constexpr int kWideKeys = 64, kNarrowKeys = 32;     // per tile
-
-// Where the waves of a CU's two workgroups could both go on, the older's would go
-// first and its workgroup end 20% before the other, which then runs alone.  So
-// they take turns by tiles, two to the younger's one (blocks are handed out in
-// order: the second half are the younger ones); and a narrow workgroup's few
-// instructions, which keep its reads going, come before a wide one's.  64 requests
-// behind 8192 tokens 78.5 -> 71.2 us (turns alone 75.0, the wide ones first 78.1),
-// 96 behind 32768 150 -> 145 us, one with 131072 tokens 98 -> 95 us.
-template <int LOW>
-__device__ __forceinline__ void take_turns(int t) {
-  const bool younger = blockIdx.x >= kDecSlots / 2;
-  if ((t % 3 != 0) == younger) __builtin_amdgcn_s_setprio(LOW + 1);
-  else __builtin_amdgcn_s_setprio(LOW);
-}
 
 struct DecodePlan {
   int32_t small;                                    // no parts, the rest is 0

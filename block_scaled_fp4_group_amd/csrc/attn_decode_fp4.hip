@@ -530,8 +530,10 @@ __device__ __forceinline__ void fp4_narrow(const Fp4Args& a, int kvh, Fp4Cursor<
 
 // Prefix part `part`, 128 rows from row0, 32 per wave; tiles of 64 keys in two stages.
 // A thread takes blocks of 16 values from memory to f16 rows in LDS, a tile ahead of the
-// products, their loads another tile ahead.
-template <int DQ, int DV>
+// products, their loads another tile ahead.  PAGED: pages hold 64 rows or more, so a tile's
+// blocks follow one another (rows past the end are the page's own, their values' scales
+// count as 0); otherwise each lane finds its rows (the last key's for those past the end).
+template <int DQ, int DV, bool PAGED>
 __device__ __forceinline__ void fp4_wide(const Fp4Args& a, int kvh, int part, int row0, uint8_t* mem) {
   using W = AttnWave<DQ, DV, kF4Keys / 32, AttnF16>;
   uint8_t* ks = mem;
@@ -546,14 +548,33 @@ __device__ __forceinline__ void fp4_wide(const Fp4Args& a, int kvh, int part, in
   const int mask = (1 << a.page_shift) - 1;
   // lane l looks up the cache row of key l of a tile (past the end: the last key)
   auto slot_of = [&](int t) {
-    const int key = key0 + min(t * kF4Keys + lane, n_keys - 1);
+    const int key = key0 + min(t * kF4Keys + (PAGED ? 0 : lane), n_keys - 1);
     const int e = a.prefix_table[key >> a.page_shift];
     return (min(max(e, 0), a.num_pages - 1) << a.page_shift) + (key & mask);
   };
   constexpr int KI = DQ / 64, VI = DV / 64, KB = DQ / 16, VB = DV / 16;   // blocks per thread; per row
   u32x2 kc[KI], vc[VI];
+  const uint32_t v_at = ((threadIdx.x % VB) << a.page_shift) + threadIdx.x / VB;   // this thread's first value scale
   uint32_t ksc[KI], vsc[VI];
   auto load = [&](int slot) {
+    if (PAGED) {
+      const uint32_t sl = (uint32_t)__builtin_amdgcn_readfirstlane(slot);
+      const uint64_t head = (uint64_t)(sl >> a.page_shift) * a.kv_heads + kvh, at = (head << a.page_shift) + (sl & mask);
+      const rsrc_t kr = make_rsrc(a.k + at * (DQ / 2), 0x7fffffffu), ksr = make_rsrc(a.ks + at * KB, 0x7fffffffu);
+      const rsrc_t vr = make_rsrc(a.v + at * (DV / 2), 0x7fffffffu);
+      const rsrc_t vsr = make_rsrc(a.vs + ((head * VB) << a.page_shift) + (sl & mask), 0x7fffffffu);
+#pragma unroll
+      for (int i = 0; i < KI; ++i) {
+        kc[i] = bload64(kr, threadIdx.x * 8, i * 2048);
+        ksc[i] = bload8(ksr, threadIdx.x, i * 256);
+      }
+#pragma unroll
+      for (int i = 0; i < VI; ++i) {
+        vc[i] = bload64(vr, threadIdx.x * 8, i * 2048);
+        vsc[i] = bload8(vsr, v_at, i * (256 / VB));
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < KI; ++i) {
       const int f = i * 256 + threadIdx.x, r = f / KB, blk = f % KB;
@@ -571,7 +592,7 @@ __device__ __forceinline__ void fp4_wide(const Fp4Args& a, int kvh, int part, in
       vsc[i] = a.vs[((head * VB + blk) << a.page_shift) + (sl & mask)];
     }
   };
-  auto put = [&](int st) {
+  auto put = [&](int st, int valid) {                               // valid: keys that are there
 #pragma unroll
     for (int i = 0; i < KI; ++i) {
       const int f = i * 256 + threadIdx.x, r = f / KB, blk = f % KB;
@@ -583,7 +604,7 @@ __device__ __forceinline__ void fp4_wide(const Fp4Args& a, int kvh, int part, in
 #pragma unroll
     for (int i = 0; i < VI; ++i) {
       const int f = i * 256 + threadIdx.x, r = f / VB, blk = f % VB;
-      const _Float16 s = scale_pair<false>(vsc[i])[0];
+      const _Float16 s = scale_pair<false>(PAGED && r >= valid ? 0u : vsc[i])[0];
       uint8_t* to = vs + st * W::kValBytes + r * (DV * 2);
 #pragma unroll
       for (int x = 0; x < 2; ++x) *(f16x8*)(to + ((2 * blk + x) ^ at_swz<DV>(r)) * 16) = fp4x8_f16(vc[i][x], s);
@@ -594,14 +615,15 @@ __device__ __forceinline__ void fp4_wide(const Fp4Args& a, int kvh, int part, in
   slot = slot_of(1);
   W w;
   const float c = ldexpf(a.c, w.init(a.q + b * a.q_ts + hq * a.q_hs, lane));
-  put(0);
+  put(0, n_keys);
   if (n_tiles > 1) load(slot);
   slot = slot_of(2);
   auto step = [&](auto stage, int t) {
     constexpr int st = decltype(stage)::value;
     // tile t is in its stage; everyone is done with tile t - 1, whose stage is refilled
     at_wait_barrier<63>();
-    if (t + 1 < n_tiles) put(st ^ 1);
+    take_turns<0>(t);
+    if (t + 1 < n_tiles) put(st ^ 1, n_keys - (t + 1) * kF4Keys);
     if (t + 2 < n_tiles) {
       load(slot);
       slot = slot_of(t + 3);
@@ -641,7 +663,8 @@ __global__ __launch_bounds__(kF4Waves * 64, fp4_per_cu(DQ, RB, WIDE)) void attn_
   if (item < p.parts_p * p.blocks_p) {
     // row blocks of one part side by side: they share the part's keys in L2
     const int part = item / p.blocks_p, block = item % p.blocks_p;
-    if (WIDE) return fp4_wide<DQ, DV>(a, kvh, part, block * 128, mem);
+    if (WIDE && a.page_shift >= 6) return fp4_wide<DQ, DV, true>(a, kvh, part, block * 128, mem);
+    if (WIDE) return fp4_wide<DQ, DV, false>(a, kvh, part, block * 128, mem);
     Fp4Cursor<true> at;
     at.b = at.tile = 0;
     at.key0 = part * p.chunk_p;
