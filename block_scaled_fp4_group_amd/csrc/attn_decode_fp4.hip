@@ -30,10 +30,9 @@ namespace moe {
 
 constexpr int kF4Keys = 64;                         // per tile
 constexpr int kF4Waves = 4;                         // of a workgroup that leaves parts
-constexpr int kF4Small = 8;                         // of one that answers alone
 
 struct Fp4Plan {
-  int32_t small;                                    // no parts, the rest is 0
+  int32_t small;                                    // waves of a workgroup that answers alone: no parts, the rest is 0
   int32_t wide;                                     // prefix workgroups are wide
   int32_t parts_p, chunk_p;                         // parts of the prefix, keys in each
   int32_t blocks_p;                                 // row blocks of B * G rows (wide 128, narrow 16 rb)
@@ -651,6 +650,7 @@ __device__ __forceinline__ void fp4_wide(const Fp4Args& a, int kvh, int part, in
 }
 
 // Workgroups that a CU holds at once, by the registers of their waves.
+constexpr int fp4_small_per_cu(int k_dim, int waves) { return (k_dim == 64 ? 16 : 12) / waves; }
 constexpr int fp4_per_cu(int k_dim, int rb, bool wide) { return rb == 1 && !wide ? (k_dim == 64 ? 4 : (k_dim == 128 ? 3 : 2)) : 2; }
 
 template <int DQ, int DV, int RB, bool WIDE>
@@ -723,10 +723,10 @@ __global__ __launch_bounds__(kF4Waves * 64, fp4_per_cu(DQ, RB, WIDE)) void attn_
 // Few keys: a workgroup per request and key head answers alone, without parts and a
 // second launch.  Its eight waves take every eighth tile, the prefix's first.  At most 16
 // heads of a key head.
-template <int DQ, int DV>
-__global__ __launch_bounds__(kF4Small * 64) void attn_decode_fp4_small_kernel(Fp4Args a) {
+template <int DQ, int DV, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, fp4_small_per_cu(DQ, WAVES)) void attn_decode_fp4_small_kernel(Fp4Args a) {
   using W = Fp4Wave<DQ, DV, 1>;
-  __shared__ __attribute__((aligned(16))) uint8_t mem[kF4Small * W::kRegion];
+  __shared__ __attribute__((aligned(16))) uint8_t mem[WAVES * W::kRegion];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kvh = blockIdx.x % (uint32_t)a.kv_heads, b = blockIdx.x / (uint32_t)a.kv_heads, G = a.q_heads / a.kv_heads;
   const int len = f4_len_at(a, b), prefix = (int)a.prefix_len;
@@ -744,7 +744,7 @@ __global__ __launch_bounds__(kF4Small * 64) void attn_decode_fp4_small_kernel(Fp
   w.load_query(0, a.q + b * a.q_ts + (int64_t)(kvh * G + min(lane & 15, G - 1)) * a.q_hs, lane);
   if (t < n_tiles) {
     const int slot = entry_of(t).slot(a);
-    entry = entry_of(min(t + kF4Small, n_tiles - 1));
+    entry = entry_of(min(t + WAVES, n_tiles - 1));
     w.template load<false>(a, kvh, slot, lane);
   }
   w.init(0, a.c);
@@ -753,7 +753,7 @@ __global__ __launch_bounds__(kF4Small * 64) void attn_decode_fp4_small_kernel(Fp
     w.store(mine, lane, last);
     if constexpr (decltype(more)::value) {
       const int slot = entry.slot(a);
-      entry = entry_of(min(t + 2 * kF4Small, n_tiles - 1));
+      entry = entry_of(min(t + 2 * WAVES, n_tiles - 1));
       w.template scores<true, false>(a, kvh, slot, lane);
     } else {
       w.template scores<false, false>(a, kvh, 0, lane);
@@ -764,36 +764,51 @@ __global__ __launch_bounds__(kF4Small * 64) void attn_decode_fp4_small_kernel(Fp
     w.values(mine, lane);
     asm volatile("" ::: "memory");
   };
-  for (; t + kF4Small < n_tiles; t += kF4Small) step(std::true_type());
+  for (; t + WAVES < n_tiles; t += WAVES) step(std::true_type());
   if (t < n_tiles) step(std::false_type());
   w.leave(mine, 0, lane);
   __syncthreads();
-  const int row = threadIdx.x / (DV / 4), col = threadIdx.x % (DV / 4) * 4;
-  if (row >= G) return;
-  float M, L;
-  const f32x4 sum = join_waves<DV, kF4Small, W::kRegion>(mem, row, col, &M, &L);
-  const float inv = L == 0.0f ? 0.0f : a.v_scale / L;
-  const int hq = kvh * G + row;
-  *(u32x2*)(a.out + b * a.o_ts + hq * a.o_hs + col) =
-      u32x2{cvt_bf16x2(sum[0] * inv, sum[1] * inv), cvt_bf16x2(sum[2] * inv, sum[3] * inv)};
-  if (a.lse && col == 0) a.lse[(int64_t)b * a.q_heads + hq] = L == 0.0f ? neg_inf() : (M + __builtin_amdgcn_logf(L)) * kLn2;
+  for (int f = threadIdx.x; f < G * (DV / 4); f += WAVES * 64) {
+    const int row = f / (DV / 4), col = f % (DV / 4) * 4;
+    float M, L;
+    const f32x4 sum = join_waves<DV, WAVES, W::kRegion>(mem, row, col, &M, &L);
+    const float inv = L == 0.0f ? 0.0f : a.v_scale / L;
+    const int hq = kvh * G + row;
+    *(u32x2*)(a.out + b * a.o_ts + hq * a.o_hs + col) =
+        u32x2{cvt_bf16x2(sum[0] * inv, sum[1] * inv), cvt_bf16x2(sum[2] * inv, sum[3] * inv)};
+    if (a.lse && col == 0) a.lse[(int64_t)b * a.q_heads + hq] = L == 0.0f ? neg_inf() : (M + __builtin_amdgcn_logf(L)) * kLn2;
+  }
 }
 
-static bool fp4_small_is_sooner(int64_t B, int64_t G, int64_t kv_heads, int64_t prefix_len, int64_t max_len, int64_t dims) {
-  if (G > 16) return false;
-  const int64_t tiles = (prefix_len + 63) / 64 + (max_len + 63) / 64, rounds = (B * kv_heads + 255) / 256;
-  if (tiles > 1024) return false;
-  return 3500 + 250 * tiles * rounds * dims / 256 < 12000;
+// Waves of a workgroup that answers a request's heads of one key head alone; 0: parts are
+// sooner.  Such a workgroup has no parts to write and no second launch, but its time grows
+// with its tiles, and it reads the prefix for its request only.  Measured, us, alone / in
+// parts (heads of 128 + 128, 8 key heads): 1 request of 1024 keys 8.5 / 9.0, of 2048 12.7 / 9.1;
+// 8 of 2048 13.0 / 13.3; 16 of 2048 13.5 / 16.0, of 4096 22.1 / 20.1; 32 of 4096 23.6 / 24.5;
+// 256 of 1024 40 / 55, of 4096 128 / 120.  256 requests behind 1024 + up to 1024 keys
+// 67 / 81, behind 2048 + 64 keys 74 / 54.  (192 + 128, 4 key heads: 64 of 4096 28 / 35,
+// 256 behind 2048 + 64 keys 51 / 64, behind 4096 91 / 78.)  Where they all run at once, 8
+// waves divide a request's tiles better (1 of 1024 8.5 us, 9.6 with 4); else three
+// workgroups of 4 on a CU leave less time idle than one of 8 (256 of 1024 40 us, 59 with 8).
+static int fp4_small_waves(int64_t B, int64_t G, int64_t kv_heads, int64_t prefix_len, int64_t max_len, int64_t k_dim) {
+  const int64_t tiles_p = (prefix_len + 63) / 64, tiles = tiles_p + (max_len + 63) / 64, items = B * kv_heads;
+  if (G > 16 || tiles > std::min<int64_t>(64, 16 + items / 4) || tiles_p * items > 32768) return 0;
+  return items <= 256 * fp4_small_per_cu(k_dim, 8) ? 8 : 4;
 }
 
 static Fp4Plan fp4_plan(int64_t B, const moe_attn_params& a, int64_t prefix_len, int64_t max_len) {
-  const int q_heads = a.q_heads, kv_heads = a.kv_heads, dims = a.k_dim + a.v_dim;
+  const int q_heads = a.q_heads, kv_heads = a.kv_heads;
   Fp4Plan p = {};
   const int64_t G = q_heads / kv_heads, rows = B * G;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  p.small = fp4_small_is_sooner(B, G, kv_heads, prefix_len, max_len, dims);
+  p.small = fp4_small_waves(B, G, kv_heads, prefix_len, max_len, a.k_dim);
   if (p.small) return p;
-  p.wide = prefix_len > 0 && rows > 32;
+  // Wide workgroups meet a tile with 128 rows and a quarter of the conversions, but each
+  // leaves parts for all its rows and needs several tiles to fill its stages.  Measured,
+  // us, wide / narrow: 128 rows of 8 key heads behind 8192 keys 30 / 26, behind 65536 69 / 70; of 4
+  // key heads with 192 + 128 behind 8192 28 / 23, behind 65536 46 / 49; 512 rows behind
+  // 8192 38 / 36.5, behind 65536 122 / 153; 16 rows of 8 key heads behind 65536 43 / 25.
+  p.wide = rows > 32 && rows * kv_heads * up(prefix_len, 64) >= 1 << 19;
   p.rb = G > 16 || (prefix_len > 0 && !p.wide && rows > 16) ? 2 : 1;
   p.blocks_p = (int32_t)up(rows, p.wide ? 128 : 16 * p.rb);
   p.blocks_s = (int32_t)up(G, 16 * p.rb);
@@ -820,7 +835,10 @@ static Fp4Plan fp4_plan(int64_t B, const moe_attn_params& a, int64_t prefix_len,
     if (places < per_run || prefix + work_s / slots < work_s / places) places = slots;
   }
   const int64_t left = places / per_run;
-  p.runs = max_len == 0 ? 0 : (int32_t)std::max<int64_t>(1, std::min(left, up(B * up(max_len, kF4Keys), kF4Waves)));
+  // (a run that holds several short requests takes them one after the other, so there are
+  // as many as keep each request's 4 tiles at a time apart: 32 requests of 64 keys 16.5 ->
+  // 9.2 us in parts, 8 behind 1024 + 16 20.5 -> 14.2)
+  p.runs = max_len == 0 ? 0 : (int32_t)std::max<int64_t>(1, std::min(left, B * up(max_len, kF4Keys * kF4Waves)));
   return p;
 }
 
@@ -847,8 +865,9 @@ int64_t attn_decode_fp4_grid(int64_t B, const moe_attn_params& p, int64_t prefix
 template <int DQ, int DV>
 static void launch_fp4(const Fp4Args& a, hipStream_t stream) {
   if (a.plan.small) {
-    hipLaunchKernelGGL((attn_decode_fp4_small_kernel<DQ, DV>), dim3((uint32_t)(a.num_requests * a.kv_heads)),
-                       dim3(kF4Small * 64), 0, stream, a);
+    const dim3 grid((uint32_t)(a.num_requests * a.kv_heads)), threads(a.plan.small * 64);
+    if (a.plan.small == 8) hipLaunchKernelGGL((attn_decode_fp4_small_kernel<DQ, DV, 8>), grid, threads, 0, stream, a);
+    else hipLaunchKernelGGL((attn_decode_fp4_small_kernel<DQ, DV, 4>), grid, threads, 0, stream, a);
     return;
   }
   const uint32_t grid = (uint32_t)fp4_grid(a.plan, a.kv_heads);

@@ -133,7 +133,7 @@ def check_run(run, what, **kw):
 @pytest.mark.parametrize("lens,prefix,page,Hq,Hkv", [
     ([1], 0, 16, 1, 1), ([0], 0, 16, 2, 1), ([5, 0, 33], 0, 16, 4, 2), ([0, 0], 7, 16, 8, 2), ([3, 64, 31, 32], 1, 16, 4, 1),
     ([130, 2, 0], 65, 64, 5, 1), ([300], 300, 32, 8, 8), ([17] * 9, 40, 16, 16, 2), ([63, 65, 15, 16], 0, 128, 16, 1),
-    ([2] * 40, 33, 1024, 2, 2)])
+    ([2] * 40, 33, 1024, 2, 2), ([3, 0, 70, 130, 1] * 26 + [64] * 3, 70, 16, 8, 4)])               # more workgroups than CUs
 def test_decode(D, Dv, lens, prefix, page, Hq, Hkv):
     what = f"attn_decode_fp4 {D}/{Dv} lens={lens[:4]} prefix={prefix} page={page} heads {Hq}/{Hkv}"
     say(what)
@@ -144,11 +144,45 @@ def test_decode(D, Dv, lens, prefix, page, Hq, Hkv):
 @pytest.mark.parametrize("lens,prefix,page,Hq,Hkv", [
     ([3000], 0, 16, 4, 1), ([3000, 0, 1, 65], 0, 64, 8, 2), ([70, 9, 2500], 130, 128, 40, 1),          # heads over 16
     ([700, 1, 5130], 260, 16, 2, 1), ([900, 30], 2600, 32, 8, 1),                                   # a narrow prefix
-    ([40, 0, 900] * 5, 2500, 32, 8, 2), ([5] * 70, 1100, 16, 2, 1), ([0] * 9, 3000, 64, 16, 1)])    # a wide one
+    ([40, 0, 900] * 5, 2500, 32, 8, 2), ([5] * 70, 1100, 16, 2, 1), ([0] * 9, 3000, 64, 16, 1)])    # many rows
 def test_decode_in_parts(D, Dv, lens, prefix, page, Hq, Hkv):
     what = f"attn_decode_fp4 {D}/{Dv} lens={lens[:4]} prefix={prefix} page={page} heads {Hq}/{Hkv}"
     say(what)
     check_run(run_decode(len(lens) * 17 + prefix + D, lens, prefix, page, Hq, Hkv, D, Dv), what)
+
+
+@pytest.mark.parametrize("D,Dv", HEADS)
+@pytest.mark.parametrize("lens,prefix,page,Hq,Hkv", [
+    ([70, 0, 1] * 5 + [64, 500], 30900, 64, 64, 4), ([9] * 20, 26300, 16, 64, 8), ([0] * 95 + [33], 22000, 1024, 16, 2)])
+def test_decode_behind_a_long_prefix(D, Dv, lens, prefix, page, Hq, Hkv):
+    """Workgroups of 128 rows (partial last blocks, pages inside a tile and over it); all requests in 64 bits on the device."""
+    what = f"attn_decode_fp4 {D}/{Dv} {len(lens)} requests prefix={prefix} page={page} heads {Hq}/{Hkv}"
+    say(what)
+    c, q, _, _, out, lse = run_decode(len(lens) + D, lens, prefix, page, Hq, Hkv, D, Dv)
+    k, v = (torch.from_numpy(x).cuda() for x in c.values())
+    qd, G, scale = torch.from_numpy(q).cuda(), Hq // Hkv, D ** -0.5
+    at = lambda pages, n: (torch.as_tensor(np.asarray(pages)[np.arange(n) // page], device="cuda"),
+                           torch.as_tensor(np.arange(n) % page, device="cuda"))
+    pk, pv = k[at(c.ptab, prefix)].transpose(0, 1), v[at(c.ptab, prefix)].transpose(0, 1)     # [Hkv, n, D]
+    worst = 0.0
+    for b, n in enumerate(lens):
+        kk = torch.cat((pk, k[at(c.table[b], n)].transpose(0, 1)), 1) if n else pk
+        vv = torch.cat((pv, v[at(c.table[b], n)].transpose(0, 1)), 1) if n else pv
+        N, qq = prefix + n, qd[b].view(Hkv, G, D)
+        s = qq @ kk.transpose(1, 2).contiguous() * scale
+        wl = s.logsumexp(-1, keepdim=True)
+        p = (s - wl).exp()
+        ref, mass = p @ vv, p @ vv.abs()
+        d = 2 * D * U * (qq.abs() @ kk.abs().transpose(1, 2).contiguous()).amax(-1, keepdim=True) * scale
+        d = d + 2.0 ** -39 * qq.abs().amax(-1, keepdim=True) * kk.abs().sum(-1).amax(-1)[:, None, None] * scale
+        t = 4 * U * (s.abs().amax(-1, keepdim=True) + 1) * 1.4427
+        bo = R * ref.abs() + (F + 2 * (d + t) + 2 * (8 + N) * U) * mass + N * 2.0 ** -32 * vv.abs().amax((1, 2))[:, None, None]
+        e = (out[b].double().view(Hkv, G, Dv) - ref).abs()
+        assert (e <= bo).all(), f"{what}: request {b}: {(e / bo).max()}"
+        el = (lse[b].double().view(Hkv, G, 1) - wl).abs()
+        assert (el <= d + t + (8 + N) * U + 2 * U * wl.abs()).all(), f"{what}: lse of request {b}"
+        worst = max(worst, float((e / bo).max()))
+    say(f"  {what}: worst error / bound {worst:.2f}")
 
 
 def test_decode_sharp_flat_and_scaled():
