@@ -101,13 +101,25 @@ __global__ __launch_bounds__(kForkThreads) void kv_fork_kernel(ForkArgs a) {
   if (lane == 0) part[wv] = before;
   __syncthreads();
   before = part[0] + part[1] + part[2] + part[3];
+  auto free_page = [&](int i) {                                     // -1: none left
+    const int64_t p = i < a.num_free ? a.free_pages[i] : -1;
+    return p < a.t.num_pages ? p : -1;
+  };
   if (last) {
-    __syncthreads();
-    if (lane == 0) part[wv] = all;
-    __syncthreads();
-    all = part[0] + part[1] + part[2] + part[3];
+    auto sum = [&](int x) {
+      __syncthreads();
+      if (lane == 0) part[wv] = x;
+      __syncthreads();
+      return part[0] + part[1] + part[2] + part[3];
+    };
+    all = sum(all);
+    int taken = 0;
+    for (int i = threadIdx.x; i < all; i += kForkThreads) taken += free_page(i) >= 0;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) taken += __shfl_xor(taken, d);
+    taken = sum(taken);
     if (threadIdx.x == 0) {
-      a.counts[0] = (int32_t)min((int64_t)all, a.num_free);
+      a.counts[0] = taken;
       a.counts[1] = all;
     }
   }
@@ -117,18 +129,18 @@ __global__ __launch_bounds__(kForkThreads) void kv_fork_kernel(ForkArgs a) {
   const int64_t len = length(p), whole = len >> a.t.page_shift;
   const bool cut = (len & mask) != 0;
   const int32_t* from = a.t.table + p * a.t.stride;
-  const int64_t fresh = cut && before < a.num_free ? a.free_pages[before] : -1;
+  const int64_t fresh = cut ? free_page(before) : -1;
   if (slice == 0) {
     int32_t* to = a.table + c * a.t.stride;
     for (int64_t i = threadIdx.x; i < whole; i += kForkThreads) to[i] = from[i];
     if (threadIdx.x == 0) {
-      if (cut) to[whole] = (int32_t)fresh;
+      if (cut) to[whole] = fresh < 0 ? -1 : (int32_t)fresh;
       a.lens[c] = (int32_t)(cut && fresh < 0 ? whole << a.t.page_shift : len);
     }
   }
   if (!cut) return;
   const int64_t old = from[whole];
-  if (fresh < 0 || fresh >= a.t.num_pages || old < 0 || old >= a.t.num_pages) return;
+  if (fresh < 0 || old < 0 || old >= a.t.num_pages) return;
   const int64_t each = ((a.page_bytes + a.slices - 1) / a.slices + 15) & ~(int64_t)15;
   copy_page(a.buffers, fresh, old, slice * each, min(a.page_bytes, (slice + 1) * each));
 }

@@ -647,7 +647,8 @@ typedef struct {
  * its length and its whole pages, which the two then share, and, if its last page is not
  * full, a copy of that in the next page of free_pages (in the order of i), into which
  * the child's next tokens go.  Without a page left the child gets the whole pages only.
- * free_pages: pages of the pool that no row holds, each once.
+ * free_pages: pages of the pool that no row holds, each once; entries that are no page
+ * of the pool (the -1 behind moe_kv_free_pages' list) are no page left.
  *   parents, children int32 [num_forks], rows of the table; an i with a row outside it
  *   or with children[i] == parents[i] does nothing.  No row may be a child twice, or
  *   both child and parent (what its entries and length then are is unspecified).

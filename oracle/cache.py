@@ -54,7 +54,7 @@ def fork(table, lens, parents, children, free_pages, page, buffers):
     table, lens, buffers = np.array(table), np.array(lens), [np.array(b) for b in buffers]
     n, blocks = table.shape
     pages = buffers[0].shape[0]
-    need = 0
+    need = taken = 0
     for p, c in zip(parents, children):
         if not (0 <= p < n and 0 <= c < n) or p == c:
             continue
@@ -63,15 +63,16 @@ def fork(table, lens, parents, children, free_pages, page, buffers):
         table[c, :whole] = table[p, :whole]
         lens[c] = length
         if length % page:
-            new = free_pages[need] if need < len(free_pages) else -1
+            new = free_pages[need] if need < len(free_pages) and 0 <= free_pages[need] < pages else -1
             need += 1
+            taken += new >= 0
             table[c, whole] = new
             if new < 0:
                 lens[c] = whole * page
-            elif new < pages and 0 <= table[p, whole] < pages:
+            elif 0 <= table[p, whole] < pages:
                 for b in buffers:
                     b[new] = b[table[p, whole]]
-    return table, lens, buffers, np.array([min(need, len(free_pages)), need])
+    return table, lens, buffers, np.array([taken, need])
 
 
 def live(table, lens, page, num_pages):

@@ -153,7 +153,8 @@ def test_decode_in_parts(D, Dv, lens, prefix, page, Hq, Hkv):
 
 @pytest.mark.parametrize("D,Dv", HEADS)
 @pytest.mark.parametrize("lens,prefix,page,Hq,Hkv", [
-    ([70, 0, 1] * 5 + [64, 500], 30900, 64, 64, 4), ([9] * 20, 26300, 16, 64, 8), ([0] * 95 + [33], 22000, 1024, 16, 2)])
+    ([70, 0, 1] * 5 + [64, 500], 30900, 64, 64, 4), ([9] * 20, 26300, 16, 64, 8), ([0] * 95 + [33], 22000, 1024, 16, 2),
+    ([33] * 30, 28000, 32, 40, 1)])                                                                   # heads over 16
 def test_decode_behind_a_long_prefix(D, Dv, lens, prefix, page, Hq, Hkv):
     """Workgroups of 128 rows (partial last blocks, pages inside a tile and over it); all requests in 64 bits on the device."""
     what = f"attn_decode_fp4 {D}/{Dv} {len(lens)} requests prefix={prefix} page={page} heads {Hq}/{Hkv}"
@@ -538,6 +539,23 @@ def test_fork(rows, blocks, page, forks, free, shapes):
     assert np.array_equal(host(dl), want[1]) and np.array_equal(host(counts), want[3])
     for g, w in zip(db, want[2]):
         assert np.array_equal(host(g), w)
+
+
+def test_fork_from_a_list_with_an_end():
+    """The whole list of kv_free_pages, -1 behind its pages, and an entry past the pool: no page left there."""
+    table, lens, bufs = pool(8, 12, 3, 16, 20, SHAPES, lens=[20, 33] + [0] * 10)
+    par, chi = np.array([0, 1, 0, 1, 0, 1]), np.arange(2, 8)
+    free, counts = moe.kv_free_pages(dev_i32(table)[:, :3], dev_i32(lens), 16, 20)
+    for fp in (host(free)[host(counts)[0] - 4:], np.concatenate([host(free)[:2], [20, 2 ** 31 - 1, -7], host(free)[2:]]), np.full(9, -1)):
+        say(f"kv_fork, free pages {fp.tolist()}")
+        want = oc.fork(table[:, :3], lens, par, chi, fp, 16, bufs)
+        dt, dl, db = dev_i32(table), dev_i32(lens), [dev_u8(b) for b in bufs]
+        got = moe.kv_fork(dt[:, :3], dl, dev_i32(par), dev_i32(chi), dev_i32(fp), 16, db)
+        torch.cuda.synchronize()
+        assert np.array_equal(host(dt)[:, :3], want[0]) and np.array_equal(host(dl), want[1])
+        assert np.array_equal(host(got), want[3])
+        for g, w in zip(db, want[2]):
+            assert np.array_equal(host(g), w)
 
 
 @pytest.mark.parametrize("rows,blocks,page,pages", [
