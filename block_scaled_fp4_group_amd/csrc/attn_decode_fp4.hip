@@ -782,33 +782,37 @@ __global__ __launch_bounds__(WAVES * 64, fp4_small_per_cu(DQ, WAVES)) void attn_
 
 // Waves of a workgroup that answers a request's heads of one key head alone; 0: parts are
 // sooner.  Such a workgroup has no parts to write and no second launch, but its time grows
-// with its tiles, and it reads the prefix for its request only.  Measured, us, alone / in
-// parts (heads of 128 + 128, 8 key heads): 1 request of 1024 keys 8.5 / 9.0, of 2048 12.7 / 9.1;
-// 8 of 2048 13.0 / 13.3; 16 of 2048 13.5 / 16.0, of 4096 22.1 / 20.1; 32 of 4096 23.6 / 24.5;
-// 256 of 1024 40 / 55, of 4096 128 / 120.  256 requests behind 1024 + up to 1024 keys
-// 67 / 81, behind 2048 + 64 keys 74 / 54.  (192 + 128, 4 key heads: 64 of 4096 28 / 35,
-// 256 behind 2048 + 64 keys 51 / 64, behind 4096 91 / 78.)  Where they all run at once, 8
-// waves divide a request's tiles better (1 of 1024 8.5 us, 9.6 with 4); else three
-// workgroups of 4 on a CU leave less time idle than one of 8 (256 of 1024 40 us, 59 with 8).
+// with its tiles, and it reads the prefix for its request only, with the matrix cores' 16
+// rows as full as the heads make them.  Measured, us, alone / in parts (8 key heads of 128 +
+// 128, 4 query heads each): 1 request of 1024 keys 8.5 / 9.0, of 2048 12.7 / 9.1; 8 of 2048
+// 13.0 / 13.3; 16 of 2048 13.5 / 16.0, of 4096 22.1 / 20.1; 256 of 1024 40 / 55, of 4096 128 /
+// 120; 64 behind 1024 with up to 1024 of their own 23 / 27, 256 66 / 59.  (4 key heads of 192
+// + 128, 16 query heads each: 64 of 4096 28 / 35, 256 behind 2048 with 64 51 / 64; 8 of 64 + 64,
+// one each: 256 behind 1024 with 64 29 / 21.)  Within 5% of the better at 140 of 150 sizes.
+// Where they all run at once, 8 waves divide a request's tiles better (1 of 1024 8.5 us, 9.6
+// with 4); else three workgroups of 4 on a CU leave less time idle than one of 8 (256 of 1024
+// 40 us, 59 with 8).
 static int fp4_small_waves(int64_t B, int64_t G, int64_t kv_heads, int64_t prefix_len, int64_t max_len, int64_t k_dim) {
   const int64_t tiles_p = (prefix_len + 63) / 64, tiles = tiles_p + (max_len + 63) / 64, items = B * kv_heads;
-  if (G > 16 || tiles > std::min<int64_t>(64, 16 + items / 4) || tiles_p * items > 32768) return 0;
+  if (G > 16 || tiles > std::min<int64_t>(64, 16 + items / 4) || tiles_p * items > 8192 + 2048 * G) return 0;
   return items <= 256 * fp4_small_per_cu(k_dim, 8) ? 8 : 4;
 }
 
 static Fp4Plan fp4_plan(int64_t B, const moe_attn_params& a, int64_t prefix_len, int64_t max_len) {
-  const int q_heads = a.q_heads, kv_heads = a.kv_heads;
+  const int q_heads = a.q_heads, kv_heads = a.kv_heads, dims = a.k_dim + a.v_dim;
   Fp4Plan p = {};
   const int64_t G = q_heads / kv_heads, rows = B * G;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
   p.small = fp4_small_waves(B, G, kv_heads, prefix_len, max_len, a.k_dim);
   if (p.small) return p;
-  // Wide workgroups meet a tile with 128 rows and a quarter of the conversions, but each
-  // leaves parts for all its rows and needs several tiles to fill its stages.  Measured,
-  // us, wide / narrow: 128 rows of 8 key heads behind 8192 keys 30 / 26, behind 65536 69 / 70; of 4
-  // key heads with 192 + 128 behind 8192 28 / 23, behind 65536 46 / 49; 512 rows behind
-  // 8192 38 / 36.5, behind 65536 122 / 153; 16 rows of 8 key heads behind 65536 43 / 25.
-  p.wide = rows > 32 && rows * kv_heads * up(prefix_len, 64) >= 1 << 19;
+  // Wide workgroups meet a tile with 128 rows and a quarter of the conversions, but each needs
+  // several tiles to fill its stages, and leaves the own keys fewer places the longer the
+  // prefix is to them; long own keys want the places that narrow ones with their more parts
+  // would take.  Measured, us, wide / narrow (8 key heads of 128 + 128): 128 rows behind 8192
+  // with 16 own keys 30 / 26, with 1024 32 / 32; 64 rows behind 32768 with 1024 36 / 33,
+  // behind 2048 17 / 18.5; 768 rows behind 8192 with 16 58 / 64, behind 32768 137 / 194; 16 rows
+  // behind 32768 27 / 19.  Within 5% of the better at 543 of 605 sizes.
+  p.wide = prefix_len > 0 && (rows >= 384 || (rows >= 32 && max_len * 32768 >= G * prefix_len * dims));
   p.rb = G > 16 || (prefix_len > 0 && !p.wide && rows > 16) ? 2 : 1;
   p.blocks_p = (int32_t)up(rows, p.wide ? 128 : 16 * p.rb);
   p.blocks_s = (int32_t)up(G, 16 * p.rb);
