@@ -52,9 +52,10 @@ class AttentionLayer:
                  cos_sin: torch.Tensor, num_pages: int, page_size: int, max_requests: int, max_context: int,
                  max_tokens: int, interleaved: bool = False, eps: float = 1e-6, device="cuda", cache: str = "bf16",
                  k_global: float = 1.0, v_global: float = 1.0):
-        """``cache``: "bf16" or "nvfp4" (k_global and v_global are then its global scales).  ``cos_sin``: float32 [positions, rotated dims] (cosines, then sines), a row for each position that a token
-        takes: the prefix's length and the longest request's own together.  ``max_context``: most tokens of a request,
-        the prefix not counted (and most of the prefix); ``max_tokens``: most tokens of one step."""
+        """``cache``: "bf16" or "nvfp4" (k_global and v_global are then its global scales).  ``cos_sin``: float32
+        [positions, rotated dims] (cosines, then sines), a row for each position that a token takes: the prefix's length
+        and the longest request's own together.  ``max_context``: most tokens of a request, the prefix not counted (and
+        most of the prefix); ``max_tokens``: most tokens of one step."""
         self.w, self.cos_sin, self.interleaved, self.eps = weights, cos_sin, interleaved, eps
         self.q_heads, self.kv_heads, self.k_dim, self.v_dim = q_heads, kv_heads, k_dim, v_dim
         self.page_size, self.max_requests, self.max_tokens = page_size, max_requests, max_tokens

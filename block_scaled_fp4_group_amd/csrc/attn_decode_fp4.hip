@@ -21,6 +21,19 @@
 //   the workgroup's waves join their sums in LDS.
 // wide (prefix, many rows): a workgroup's 128 rows meet 64 keys at a time, which its
 //   threads have turned into f16 rows in LDS; from there on it is the bf16 form's.
+// alone (few keys): a workgroup's waves share all tiles of a request and key head, join their
+//   sums in LDS and write the result: one launch.
+//
+// What bounds it.  Own keys: reads.  1 request of 131072 keys (32 / 8 heads of 128 + 128, 151 MB)
+// takes 30.8 us in the kernel and 5.4 in the join; each further key costs what 6.3 TB/s give
+// (contiguous reads reach 6.9), the rest are a few dependent trips at the start (lengths, table,
+// codes: 4 us), the waves' unequal ends and the join's launch.  48 requests of up to
+// 16384 keys (64 / 4 heads of 192 + 128, 268 MB): 54 + 5 us; their lists of unequal requests
+// end unevenly, a CU's older workgroups 10 us before its younger ones -- turns by wave
+// priority moved that by nothing.  Prefix: 96 requests behind 32768 keys 155 + 8 us, 0.83 PFLOP/s;
+// matrix cores 37% busy, vector work (conversions, exponentials) 45%, on two waves for each SIMD,
+// whose registers (213 to 241) leave no room for a third.  8 requests behind 777 keys, alone: 9.4 us,
+// five tiles one after the other.
 #include <algorithm>
 
 #include "attn_common.h"

@@ -5,6 +5,10 @@
 // the calls that need to know mark the pages that they reach in a bitmap, so a page
 // that several requests share counts once, and nothing has to be kept between calls.
 //
+// What bounds them: forks and moves copy pages (32 forks of 8 parents' last pages, 16.8 MB
+// read and written: 5.6 us; 538 moves of 72 KB, 79 MB: 16 us, 4.9 TB/s where a large copy reaches
+// 5.1, behind a plan of 5 us by one workgroup); the rest are launches that wait for each other.
+//
 // A page's content is bytes here: up to eight buffers (keys and values, bf16 or codes
 // and scales), page p of each at p * page_bytes.
 #include "common.h"
