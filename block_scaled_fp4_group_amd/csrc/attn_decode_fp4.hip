@@ -543,8 +543,9 @@ __device__ __forceinline__ void fp4_narrow(const Fp4Args& a, int kvh, Fp4Cursor<
 // Prefix part `part`, 128 rows from row0, 32 per wave; tiles of 64 keys in two stages.
 // A thread takes blocks of 16 values from memory to f16 rows in LDS, a tile ahead of the
 // products, their loads another tile ahead.  PAGED: pages hold 64 rows or more, so a tile's
-// blocks follow one another (rows past the end are the page's own, their values' scales
-// count as 0); otherwise each lane finds its rows (the last key's for those past the end).
+// blocks follow one another; otherwise those of 16 keys do (96 requests behind 32768 keys of 64
+// / 4 heads of 192 + 128: 158 us, 171 in pages of 16).  Rows past the end are the page's own,
+// or the last 16's; their values' scales count as 0.
 template <int DQ, int DV, bool PAGED>
 __device__ __forceinline__ void fp4_wide(const Fp4Args& a, int kvh, int part, int row0, uint8_t* mem) {
   using W = AttnWave<DQ, DV, kF4Keys / 32, AttnF16>;
@@ -558,50 +559,41 @@ __device__ __forceinline__ void fp4_wide(const Fp4Args& a, int kvh, int part, in
   const int key0 = part * a.plan.chunk_p, n_keys = (int)min((int64_t)a.plan.chunk_p, a.prefix_len - key0);
   const int n_tiles = f4_tiles(n_keys);
   const int mask = (1 << a.page_shift) - 1;
-  // lane l looks up the cache row of key l of a tile (past the end: the last key)
+  // cache row of a tile's first key, or lane by lane of the first key of its 16 (past the end:
+  // the last 16's)
   auto slot_of = [&](int t) {
-    const int key = key0 + min(t * kF4Keys + (PAGED ? 0 : lane), n_keys - 1);
+    const int key = key0 + (PAGED ? min(t * kF4Keys, n_keys - 1) : min(t * kF4Keys + (lane & ~15), (n_keys - 1) & ~15));
     const int e = a.prefix_table[key >> a.page_shift];
     return (min(max(e, 0), a.num_pages - 1) << a.page_shift) + (key & mask);
   };
   constexpr int KI = DQ / 64, VI = DV / 64, KB = DQ / 16, VB = DV / 16;   // blocks per thread; per row
   u32x2 kc[KI], vc[VI];
-  const uint32_t v_at = ((threadIdx.x % VB) << a.page_shift) + threadIdx.x / VB;   // this thread's first value scale
   uint32_t ksc[KI], vsc[VI];
+  // Buffers from a uniform cache row on (64-bit base, the lanes' 32-bit offsets): of the tile,
+  // or of the 16 keys that all lanes of a wave take blocks of (16 rows are 16, 8 or 12 x 16
+  // blocks: whole waves).
   auto load = [&](int slot) {
-    if (PAGED) {
-      const uint32_t sl = (uint32_t)__builtin_amdgcn_readfirstlane(slot);
-      const uint64_t head = (uint64_t)(sl >> a.page_shift) * a.kv_heads + kvh, at = (head << a.page_shift) + (sl & mask);
-      const rsrc_t kr = make_rsrc(a.k + at * (DQ / 2), 0x7fffffffu), ksr = make_rsrc(a.ks + at * KB, 0x7fffffffu);
-      const rsrc_t vr = make_rsrc(a.v + at * (DV / 2), 0x7fffffffu);
-      const rsrc_t vsr = make_rsrc(a.vs + ((head * VB) << a.page_shift) + (sl & mask), 0x7fffffffu);
-#pragma unroll
-      for (int i = 0; i < KI; ++i) {
-        kc[i] = bload64(kr, threadIdx.x * 8, i * 2048);
-        ksc[i] = bload8(ksr, threadIdx.x, i * 256);
-      }
-#pragma unroll
-      for (int i = 0; i < VI; ++i) {
-        vc[i] = bload64(vr, threadIdx.x * 8, i * 2048);
-        vsc[i] = bload8(vsr, v_at, i * (256 / VB));
-      }
-      return;
-    }
+    auto rows_at = [&](int i, int per_row, uint64_t* head) {        // (head: of the page's values' scales)
+      const uint32_t sl = (uint32_t)__builtin_amdgcn_readlane(slot, PAGED ? 0 : (i * 256 + 64 * wv) / (16 * per_row) * 16);
+      *head = (uint64_t)(sl >> a.page_shift) * a.kv_heads + kvh;
+      return (*head << a.page_shift) + (sl & mask);
+    };
+    auto first = [&](int i, int per_row) { return PAGED ? 0 : (i * 256 + 64 * wv) / (16 * per_row) * 16 * per_row; };
+    uint64_t head;
 #pragma unroll
     for (int i = 0; i < KI; ++i) {
-      const int f = i * 256 + threadIdx.x, r = f / KB, blk = f % KB;
-      const uint32_t sl = (uint32_t)__shfl(slot, r);
-      const uint64_t at = (((uint64_t)(sl >> a.page_shift) * a.kv_heads + kvh) << a.page_shift) + (sl & mask);
-      kc[i] = *(const u32x2*)(a.k + at * (DQ / 2) + blk * 8);
-      ksc[i] = a.ks[at * KB + blk];
+      const uint64_t at = rows_at(i, KB, &head);
+      const int f = i * 256 + threadIdx.x - first(i, KB);
+      kc[i] = bload64(make_rsrc(a.k + at * (DQ / 2), 0x7fffffffu), f * 8, 0);
+      ksc[i] = bload8(make_rsrc(a.ks + at * KB, 0x7fffffffu), f, 0);
     }
 #pragma unroll
     for (int i = 0; i < VI; ++i) {
-      const int f = i * 256 + threadIdx.x, r = f / VB, blk = f % VB;
-      const uint32_t sl = (uint32_t)__shfl(slot, r);
-      const uint64_t head = (uint64_t)(sl >> a.page_shift) * a.kv_heads + kvh;
-      vc[i] = *(const u32x2*)(a.v + ((head << a.page_shift) + (sl & mask)) * (DV / 2) + blk * 8);
-      vsc[i] = a.vs[((head * VB + blk) << a.page_shift) + (sl & mask)];
+      const uint64_t at = rows_at(i, VB, &head);
+      const int f = i * 256 + threadIdx.x - first(i, VB);
+      vc[i] = bload64(make_rsrc(a.v + at * (DV / 2), 0x7fffffffu), f * 8, 0);
+      vsc[i] = bload8(make_rsrc(a.vs + ((head * VB) << a.page_shift) + (at - (head << a.page_shift)), 0x7fffffffu),
+                      ((f % VB) << a.page_shift) + f / VB, 0);
     }
   };
   auto put = [&](int st, int valid) {                               // valid: keys that are there
@@ -616,7 +608,7 @@ __device__ __forceinline__ void fp4_wide(const Fp4Args& a, int kvh, int part, in
 #pragma unroll
     for (int i = 0; i < VI; ++i) {
       const int f = i * 256 + threadIdx.x, r = f / VB, blk = f % VB;
-      const _Float16 s = scale_pair<false>(PAGED && r >= valid ? 0u : vsc[i])[0];
+      const _Float16 s = scale_pair<false>(r >= valid ? 0u : vsc[i])[0];
       uint8_t* to = vs + st * W::kValBytes + r * (DV * 2);
 #pragma unroll
       for (int x = 0; x < 2; ++x) *(f16x8*)(to + ((2 * blk + x) ^ at_swz<DV>(r)) * 16) = fp4x8_f16(vc[i][x], s);
