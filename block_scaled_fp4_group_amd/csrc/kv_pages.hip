@@ -150,24 +150,26 @@ __global__ __launch_bounds__(kForkThreads) void kv_fork_kernel(ForkArgs a) {
 }
 
 // ------------------------------------------------------------- live pages
-// Four rows' lengths, then 64 entries of each, under way at once: bits of the pages set by
-// `set`.  wave of `waves`.
+// Four times 64 entries, lanes side by side on rows of fewer than 64 (so many lanes to a row as
+// the power of two that holds it), under way at once behind their rows' lengths: bits of the
+// pages set by `set`.  wave of `waves`.
 template <class Set>
 __device__ __forceinline__ void mark_rows(const TableArgs& t, int wave, int waves, Set set) {
-  const int lane = threadIdx.x & 63;
-  for (int row = 4 * wave; row < t.rows; row += 4 * waves) {
+  const int shift = t.max_blocks > 32 ? 6 : (t.max_blocks <= 1 ? 0 : 32 - __builtin_clz(t.max_blocks - 1));
+  const int lane = threadIdx.x & 63, sub = lane >> shift, per = 64 >> shift, step = 1 << shift;
+  for (int first = 4 * per * wave; first < t.rows; first += 4 * per * waves) {
     int n[4], most = 0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) n[u] = held_pages(t, min(row + u, t.rows - 1));
+    for (int u = 0; u < 4; ++u) n[u] = held_pages(t, min(first + u * per + sub, t.rows - 1));
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      n[u] = row + u < t.rows ? n[u] : 0;
+      n[u] = first + u * per + sub < t.rows ? n[u] : 0;
       most = max(most, n[u]);
     }
-    for (int i = lane; i < most; i += 64) {
+    for (int i = lane & (step - 1); i < most; i += step) {
       int32_t p[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) p[u] = i < n[u] ? t.table[(row + u) * t.stride + i] : -1;
+      for (int u = 0; u < 4; ++u) p[u] = i < n[u] ? t.table[(first + u * per + sub) * t.stride + i] : -1;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         if (p[u] >= 0 && p[u] < t.num_pages) set(p[u]);
@@ -179,10 +181,14 @@ __device__ __forceinline__ void mark_rows(const TableArgs& t, int wave, int wave
 // workgroups (cleared by one launch, set by the next; plain stores of the same value need no
 // atomics), of a small one in LDS, a bit for each page, by the workgroup that uses them.
 // Entries 1500 x 256 of a pool of 190000 pages: 80 us by one workgroup, 12 us so (17 with a
-// bit for each page, set by atomics); 64 x 64 of 4000: 5 us by one.
-constexpr int64_t kMarkAlone = 16384;               // entries, and pages / 4
-static bool marks_alone(int64_t rows, int64_t max_blocks, int64_t num_pages) {
-  return rows * max_blocks <= kMarkAlone && num_pages <= 4 * kMarkAlone;
+// bit for each page, set by atomics).  By one workgroup / by all, us: 64 x 64 of 4000 pages
+// freed 4.5 / 7.4, 256 x 64 of 16000 9.0 / 8.7, 100 x 160 of 60000 18 / 10 (its workgroup
+// sweeps all pages), 512 x 64 of 30000 15 / 9; 100 x 160 of 60000 compacted 22 / 24, 512 x 64 of 30000
+// 24 / 21.
+constexpr int64_t kMarkAlone = 16384;               // entries
+constexpr int64_t kSweepAlone = 16384, kPlanAlone = 65536;   // pages
+static bool marks_alone(int64_t rows, int64_t max_blocks, int64_t num_pages, int64_t pages) {
+  return rows * max_blocks <= kMarkAlone && num_pages <= pages;
 }
 static int64_t mark_bytes(int64_t num_pages) { return (num_pages + 127) / 128 * 128; }
 // (list, if there is one: -1 everywhere, of which the sweep then overwrites the front)
@@ -262,7 +268,7 @@ struct FreeArgs {
 constexpr int kSweepWords = kMarkThreads / 4;       // 8 pages to a thread
 
 __global__ __launch_bounds__(kMarkThreads) void kv_sweep_kernel(FreeArgs a) {
-  __shared__ uint32_t bits[4 * kMarkAlone / 32];
+  __shared__ uint32_t bits[kSweepAlone / 32];
   __shared__ int32_t out[32 * kSweepWords];
   __shared__ int part[kMarkThreads / 64];
   const int P = (int)a.t.num_pages, words = (P + 31) / 32;
@@ -415,7 +421,7 @@ static PageBuffers page_buffers(const moe_page_buffers& b, int64_t* all) {
 
 int64_t kv_pages_most() { return kMarkPages; }
 size_t kv_free_ws_bytes(int64_t rows, int64_t max_blocks, int64_t num_pages) {
-  return marks_alone(rows, max_blocks, num_pages) ? 0 : (size_t)mark_bytes(num_pages);
+  return marks_alone(rows, max_blocks, num_pages, kSweepAlone) ? 0 : (size_t)mark_bytes(num_pages);
 }
 // (the marks first: 16-byte aligned)
 size_t kv_compact_ws_bytes(int64_t num_pages) {
@@ -423,8 +429,8 @@ size_t kv_compact_ws_bytes(int64_t num_pages) {
 }
 
 // The marks in memory, if they are made there.
-static uint8_t* launch_marks(const TableArgs& t, void* ws, int32_t* list, hipStream_t stream) {
-  if (marks_alone(t.rows, t.max_blocks, t.num_pages)) return nullptr;
+static uint8_t* launch_marks(const TableArgs& t, int64_t alone, void* ws, int32_t* list, hipStream_t stream) {
+  if (marks_alone(t.rows, t.max_blocks, t.num_pages, alone)) return nullptr;
   uint8_t* marks = (uint8_t*)ws;
   const int64_t bytes = mark_bytes(t.num_pages);
   hipLaunchKernelGGL(kv_clear_kernel, dim3((uint32_t)((bytes + 4095) / 4096)), dim3(256), 0, stream, marks, bytes, list,
@@ -462,7 +468,7 @@ moe_status launch_kv_free_pages(const int32_t* table, int64_t stride, int rows, 
   a.t = table_args(table, stride, rows, max_blocks, lens, page_shift, num_pages);
   a.free_pages = free_pages;
   a.counts = counts;
-  a.marks = launch_marks(a.t, ws, free_pages, stream);
+  a.marks = launch_marks(a.t, kSweepAlone, ws, free_pages, stream);
   const int64_t words = (num_pages + 31) / 32;
   const uint32_t grid = a.marks ? (uint32_t)((words + kSweepWords - 1) / kSweepWords) : 1u;
   hipLaunchKernelGGL(kv_sweep_kernel, dim3(grid), dim3(kMarkThreads), 0, stream, a);
@@ -479,7 +485,7 @@ moe_status launch_kv_compact(const int32_t* table, int64_t stride, int rows, int
   a.counts = counts;
   a.ws = (int32_t*)((uint8_t*)ws + mark_bytes(num_pages));
   a.buffers = page_buffers(buffers, &a.page_bytes);
-  a.marks = launch_marks(a.t, ws, nullptr, stream);
+  a.marks = launch_marks(a.t, kPlanAlone, ws, nullptr, stream);
   hipLaunchKernelGGL(kv_compact_plan_kernel, dim3(1), dim3(kMarkThreads), 0, stream, a);
   moe_status st = launch_status("moe_kv_compact");
   if (st != MOE_OK) return st;

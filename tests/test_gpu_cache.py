@@ -560,7 +560,7 @@ def test_fork_from_a_list_with_an_end():
 
 @pytest.mark.parametrize("rows,blocks,page,pages", [
     (1, 1, 16, 1), (3, 4, 16, 31), (3, 4, 16, 32), (40, 9, 32, 33), (300, 20, 64, 5000), (20, 30, 1, 100000), (0, 3, 16, 70),
-    (64, 2000, 16, 1 << 20)])
+    (64, 2000, 16, 1 << 20), (900, 3, 16, 3000), (200, 33, 16, 9000), (90, 64, 16, 16385), (4000, 5, 16, 30000), (700, 1, 16, 500)])
 def test_free_pages(rows, blocks, page, pages):
     say(f"kv_free_pages {rows} rows of {blocks}, {pages} pages")
     table, lens, _ = pool(rows + pages, rows, blocks, page, pages, [])
@@ -575,7 +575,7 @@ def test_free_pages(rows, blocks, page, pages):
 
 
 @pytest.mark.parametrize("rows,blocks,page,pages", [(1, 1, 16, 1), (3, 4, 16, 31), (4, 9, 32, 40), (40, 20, 64, 2000), (0, 3, 16, 70),
-                                                    (30, 30, 1, 100000)])
+                                                    (30, 30, 1, 100000), (900, 3, 16, 3000), (500, 33, 16, 2000)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_compact(rows, blocks, page, pages, in_place):
     say(f"kv_compact {rows} rows of {blocks}, {pages} pages")
