@@ -218,3 +218,70 @@ def test_layer_refuses():
     with pytest.raises(ValueError, match="pages needed"):
         layer.extend(tokens(1, 20), [0], [20])
     assert layer.host_lens == [0, 30, 0]
+
+
+@pytest.mark.parametrize("cache", ["bf16", "nvfp4"])
+@pytest.mark.parametrize("seed,pages", [(1, 18), (2, 30)])
+def test_any_order_of_calls(cache, seed, pages):
+    """Requests that grow, are answered, fork, end and move in any order, in a pool that may be too small: a row once
+    written keeps its bits for every request that holds it, pages are shared only by forks, a refused call changes nothing."""
+    say(f"layer {cache}, calls in any order {seed}")
+    a, _ = make_layer(64, 64, requests=6, context=80, cache=cache, pages=pages)
+    a.prompt(tokens(9, 20), [20], prefix=True)
+    rng = np.random.default_rng(seed)
+    rows = [None] * 6                                                  # what each request's rows were when they were written
+
+    def read():
+        cu = np.concatenate([[0], np.cumsum(a.host_lens[:6])])
+        at = torch.tensor(cu, dtype=torch.int32).cuda()
+        k, v = (moe.kv_gather(a.k_cache, a.v_cache, a.table[:6], at, int(cu[-1])) if a.fp4 is None else
+                moe.kv_gather_fp4(a.fp4, a.table[:6], at, int(cu[-1])))
+        kv = np.concatenate([host_bf16_bits(k.flatten(1)), host_bf16_bits(v.flatten(1))], 1)
+        return [kv[cu[r]:cu[r + 1]] for r in range(6)]
+
+    done = dict.fromkeys(("extend", "decode", "fork", "release", "compact", "refused"), 0)
+    prefix = host(a.table)[-1, :2].tolist()
+    for i in range(60):
+        op = rng.choice(["extend", "extend", "decode", "decode", "fork", "release", "compact"])
+        some = sorted(rng.choice(6, int(rng.integers(1, 4)), replace=False).tolist())
+        before, lens = host(a.table).copy(), list(a.host_lens)
+        try:
+            if op == "extend":
+                new = rng.integers(1, 25, len(some)).tolist()
+                y = a.extend(tokens(100 + i, sum(new)), some, new)
+                assert torch.isfinite(y).all()
+            elif op == "decode":
+                y = a.decode(tokens(200 + i, some[-1] + 1))
+                assert torch.isfinite(y).all()
+            elif op == "fork":
+                free = [r for r in range(6) if not a.host_lens[r] and r != some[0]]
+                a.fork(some[0], free[:2])
+                for r in free[:2]:
+                    rows[r] = rows[some[0]]
+            elif op == "release":
+                a.release(some)
+                for r in some:
+                    rows[r] = None
+            else:
+                assert a.compact() == a._in_use()
+                prefix = host(a.table)[-1, :2].tolist()
+            done[op] += 1
+        except ValueError:
+            done["refused"] += 1
+            assert np.array_equal(host(a.table), before) and a.host_lens == lens, (i, op)
+        assert host(a.lens).tolist() == a.host_lens, (i, op)
+        for r, kv in enumerate(read()):
+            old = rows[r]
+            assert old is None or np.array_equal(kv[:len(old)], old), (i, op, r)
+            rows[r] = kv if len(kv) else None
+        table = host(a.table)
+        mine = [table[r, :-(-n // 16)].tolist() for r, n in enumerate(a.host_lens)]
+        assert mine[-1] == prefix and all(len(set(m)) == len(m) for m in mine)
+        used = set().union(*mine)
+        left = host(a.free)[a.taken:].tolist()
+        # (a request that a call replaced may have left pages that only release() or compact() finds)
+        assert not used & set(left) and len(used) == a._in_use() and len(set(left)) == len(left)
+        last = [m[-1] for r, m in enumerate(mine[:-1]) if a.host_lens[r] % 16]
+        assert len(set(last)) == len(last), "two requests write to one page"
+    say(f"  {done}")
+    assert all(n for what, n in done.items() if what != "refused" or pages < 30)      # (30 pages hold nearly all)
