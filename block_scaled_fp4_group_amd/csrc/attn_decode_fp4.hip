@@ -654,9 +654,13 @@ __device__ __forceinline__ void fp4_wide(const Fp4Args& a, int kvh, int part, in
   }
 }
 
-// Workgroups that a CU holds at once, by the registers of their waves.
+// Workgroups that a CU holds at once.  Two keep as many reads under way as memory takes, and
+// more lists of tiles begin and end more often; a third, for which 128-wide keys leave the
+// registers, took 36.0 us for 34.5 (1 request of 131072 keys), 21.7 for 19.1 (of 16 / 2 heads) and the same
+// for many requests.  64-wide keys need four to have as much under way (100 requests of up to 6000: two
+// 44.9 us, four 39.6).
 constexpr int fp4_small_per_cu(int k_dim, int waves) { return (k_dim == 64 ? 16 : 12) / waves; }
-constexpr int fp4_per_cu(int k_dim, int rb, bool wide) { return rb == 1 && !wide ? (k_dim == 64 ? 4 : (k_dim == 128 ? 3 : 2)) : 2; }
+constexpr int fp4_per_cu(int k_dim, int rb, bool wide) { return k_dim == 64 && rb == 1 && !wide ? 4 : 2; }
 
 template <int DQ, int DV, int RB, bool WIDE>
 __global__ __launch_bounds__(kF4Waves * 64, fp4_per_cu(DQ, RB, WIDE)) void attn_decode_fp4_kernel(Fp4Args a) {
