@@ -25,7 +25,7 @@
 //   sums in LDS and write the result: one launch.
 //
 // What bounds it.  Own keys: reads.  1 request of 131072 keys (32 / 8 heads of 128 + 128, 151 MB)
-// takes 30.8 us in the kernel and 5.4 in the join; each further key costs what 6.3 TB/s give
+// takes 29.5 us in the kernel and 5.5 in the join; each further key costs what 6.3 TB/s give
 // (contiguous reads reach 6.9), the rest are a few dependent trips at the start (lengths, table,
 // codes: 4 us), the waves' unequal ends and the join's launch.  48 requests of up to
 // 16384 keys (64 / 4 heads of 192 + 128, 268 MB): 54 + 5 us; their lists of unequal requests
