@@ -267,9 +267,10 @@ struct AttnWave {
     i -= kScoreOps;
     return read_v(vs, i / OB, i % OB);
   }
-  // operands FIRST .. LAST - 1: scores (s must be zero before the first), then values
-  template <int FIRST, int LAST>
-  __device__ __forceinline__ void products(const uint8_t* ks, const uint8_t* vs) {
+  // operands FIRST .. LAST - 1: scores (s must be zero before the first), then values.
+  // between(i): work of another kind that is to go out behind MFMA i.
+  template <int FIRST, int LAST, class Between>
+  __device__ __forceinline__ void products(const uint8_t* ks, const uint8_t* vs, Between between) {
     v8 f[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) f[i] = operand(ks, vs, FIRST + i);
@@ -284,9 +285,13 @@ struct AttnWave {
         o[j % OB] = T::mfma(x, p[j / OB], o[j % OB]);
       }
       if (i + kAhead < LAST) x = operand(ks, vs, i + kAhead);
+      between(i - FIRST);
     }
     __builtin_amdgcn_sched_barrier(0);
   }
+  struct Nothing {
+    __device__ __forceinline__ void operator()(int) const {}
+  };
   __device__ __forceinline__ void clear_scores() {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -294,13 +299,15 @@ struct AttnWave {
       for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
   }
   // s = the tile's raw scores
-  __device__ __forceinline__ void scores(const uint8_t* ks) {
+  template <class Between = Nothing>
+  __device__ __forceinline__ void scores(const uint8_t* ks, Between between = Between()) {
     clear_scores();
-    products<0, kScoreOps>(ks, nullptr);
+    products<0, kScoreOps>(ks, nullptr, between);
   }
   // o += the tile's values times their weights
-  __device__ __forceinline__ void values(const uint8_t* vs) {
-    products<kScoreOps, kScoreOps + kValueOps>(nullptr, vs);
+  template <class Between = Nothing>
+  __device__ __forceinline__ void values(const uint8_t* vs, Between between = Between()) {
+    products<kScoreOps, kScoreOps + kValueOps>(nullptr, vs, between);
   }
   // this lane's row sees keys 0 .. last of the tile (last may be negative or past the end)
   __device__ __forceinline__ void mask(int lane, int last) {

@@ -31,8 +31,8 @@
 // 16384 keys (64 / 4 heads of 192 + 128, 268 MB): 54 + 5 us; their lists of unequal requests
 // end unevenly, a CU's older workgroups 10 us before its younger ones -- turns by wave
 // priority moved that by nothing.  Prefix: 96 requests behind 32768 keys 155 + 8 us, 0.83 PFLOP/s;
-// matrix cores 37% busy, vector work (conversions, exponentials) 45%, on two waves for each SIMD,
-// whose registers (213 to 241) leave no room for a third.  8 requests behind 777 keys, alone: 9.4 us,
+// matrix cores 37% busy, vector work (conversions, exponentials) 45%, LDS 47%, on two waves for
+// each SIMD, whose registers (232 to 254) leave no room for a third.  8 requests behind 777 keys, alone: 9.4 us,
 // five tiles one after the other.
 #include <algorithm>
 
@@ -542,7 +542,11 @@ __device__ __forceinline__ void fp4_narrow(const Fp4Args& a, int kvh, Fp4Cursor<
 
 // Prefix part `part`, 128 rows from row0, 32 per wave; tiles of 64 keys in two stages.
 // A thread takes blocks of 16 values from memory to f16 rows in LDS, a tile ahead of the
-// products, their loads another tile ahead.  PAGED: pages hold 64 rows or more, so a tile's
+// products, their loads another tile ahead; half a block goes out behind every other product of
+// the scores, whose wave has no vector work of its own (96 requests behind 32768 keys of 192 + 128 165 ->
+// 157 us; behind the values' products 165, and a block's addresses must be one register and
+// constants, or registers spill).  All three of matrix cores, vector units and LDS reads (each
+// wave reads all of a tile for its 32 rows) are busy 40 to 50% of the time.  PAGED: pages hold 64 rows or more, so a tile's
 // blocks follow one another; otherwise those of 16 keys do (96 requests behind 32768 keys of 64
 // / 4 heads of 192 + 128: 158 us, 171 in pages of 16).  Rows past the end are the page's own,
 // or the last 16's; their values' scales count as 0.
@@ -562,7 +566,7 @@ __device__ __forceinline__ void fp4_wide(const Fp4Args& a, int kvh, int part, in
   // cache row of a tile's first key, or lane by lane of the first key of its 16 (past the end:
   // the last 16's)
   auto slot_of = [&](int t) {
-    const int key = key0 + (PAGED ? min(t * kF4Keys, n_keys - 1) : min(t * kF4Keys + (lane & ~15), (n_keys - 1) & ~15));
+    const int key = key0 + (PAGED ? min(t, n_tiles - 1) * kF4Keys : min(t * kF4Keys + (lane & ~15), (n_keys - 1) & ~15));
     const int e = a.prefix_table[key >> a.page_shift];
     return (min(max(e, 0), a.num_pages - 1) << a.page_shift) + (key & mask);
   };
@@ -572,68 +576,86 @@ __device__ __forceinline__ void fp4_wide(const Fp4Args& a, int kvh, int part, in
   // Buffers from a uniform cache row on (64-bit base, the lanes' 32-bit offsets): of the tile,
   // or of the 16 keys that all lanes of a wave take blocks of (16 rows are 16, 8 or 12 x 16
   // blocks: whole waves).
-  auto load = [&](int slot) {
-    auto rows_at = [&](int i, int per_row, uint64_t* head) {        // (head: of the page's values' scales)
-      const uint32_t sl = (uint32_t)__builtin_amdgcn_readlane(slot, PAGED ? 0 : (i * 256 + 64 * wv) / (16 * per_row) * 16);
-      *head = (uint64_t)(sl >> a.page_shift) * a.kv_heads + kvh;
-      return (*head << a.page_shift) + (sl & mask);
-    };
-    auto first = [&](int i, int per_row) { return PAGED ? 0 : (i * 256 + 64 * wv) / (16 * per_row) * 16 * per_row; };
+  // This thread's blocks: of keys of 4 or 8 blocks, block kblk of rows krow, krow + kRows, ...; of
+  // 12, blocks kblk, kblk + 4 and kblk + 8 of row krow; of values as of keys.  So their places
+  // differ by constants (the swizzle repeats every 16 rows, and keeps chunks of 8 together).
+  constexpr int kRows = KB == 12 ? 0 : 256 / KB, kBlocks = KB == 12 ? 4 : 0, vRows = 256 / VB;
+  const int krow = threadIdx.x / (KB == 12 ? 4 : KB), kblk = threadIdx.x % (KB == 12 ? 4 : KB);
+  const int vrow = threadIdx.x / VB, vblk = threadIdx.x % VB;
+  // the first block's 16 keys (one group for a wave's lanes), rows within them or the tile
+  const int kgroup = KB == 12 ? wv : 4 * wv / KB, vgroup = 4 * wv / VB;
+  const int kin = (PAGED ? krow : krow - 16 * kgroup) * KB + kblk, vin = PAGED ? vrow : vrow - 16 * vgroup;
+  const uint32_t kto = (uint32_t)(krow * (DQ * 2) + ((2 * kblk) ^ at_swz<DQ>(krow)) * 16);
+  const uint32_t vto = (uint32_t)(vrow * (DV * 2) + ((2 * vblk) ^ at_swz<DV>(vrow)) * 16);
+  const uint32_t vsin = ((uint32_t)vblk << a.page_shift) + vin;
+  auto rows_at = [&](int slot, int group, uint64_t* head) {          // (head: of the page's values' scales)
+    const uint32_t sl = (uint32_t)__builtin_amdgcn_readlane(slot, PAGED ? 0 : group * 16);
+    *head = (uint64_t)(sl >> a.page_shift) * a.kv_heads + kvh;
+    return (*head << a.page_shift) + (sl & mask);
+  };
+  auto load = [&](int slot, int i) {                                // block i of KI + VI
     uint64_t head;
-#pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      const uint64_t at = rows_at(i, KB, &head);
-      const int f = i * 256 + threadIdx.x - first(i, KB);
-      kc[i] = bload64(make_rsrc(a.k + at * (DQ / 2), 0x7fffffffu), f * 8, 0);
-      ksc[i] = bload8(make_rsrc(a.ks + at * KB, 0x7fffffffu), f, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < VI; ++i) {
-      const uint64_t at = rows_at(i, VB, &head);
-      const int f = i * 256 + threadIdx.x - first(i, VB);
-      vc[i] = bload64(make_rsrc(a.v + at * (DV / 2), 0x7fffffffu), f * 8, 0);
-      vsc[i] = bload8(make_rsrc(a.vs + ((head * VB) << a.page_shift) + (at - (head << a.page_shift)), 0x7fffffffu),
-                      ((f % VB) << a.page_shift) + f / VB, 0);
+    if (i < KI) {
+      const uint64_t at = rows_at(slot, kgroup + i * (kRows / 16), &head);
+      const int more = i * ((PAGED ? kRows * KB : 0) + kBlocks);
+      kc[i] = bload64(make_rsrc(a.k + at * (DQ / 2), 0x7fffffffu), kin * 8, more * 8);
+      ksc[i] = bload8(make_rsrc(a.ks + at * KB, 0x7fffffffu), kin, more);
+    } else {
+      i -= KI;
+      const uint64_t at = rows_at(slot, vgroup + i * (vRows / 16), &head);
+      const int more = PAGED ? i * vRows : 0;
+      vc[i] = bload64(make_rsrc(a.v + at * (DV / 2), 0x7fffffffu), (vin * VB + vblk) * 8, more * VB * 8);
+      vsc[i] = bload8(make_rsrc(a.vs + ((head * VB) << a.page_shift) + (at - (head << a.page_shift)), 0x7fffffffu), vsin, more);
     }
   };
-  auto put = [&](int st, int valid) {                               // valid: keys that are there
-#pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      const int f = i * 256 + threadIdx.x, r = f / KB, blk = f % KB;
+  auto put = [&](int st, int valid, int j) {                        // half j of 2 (KI + VI); valid: keys that are there
+    int i = j >> 1;
+    const uint32_t x = (j & 1) * 16;
+    if (i < KI) {
       const _Float16 s = scale_pair<false>(ksc[i])[0];
-      uint8_t* to = ks + st * W::kKeyBytes + r * (DQ * 2);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) *(f16x8*)(to + ((2 * blk + x) ^ at_swz<DQ>(r)) * 16) = fp4x8_f16(kc[i][x], s);
-    }
-#pragma unroll
-    for (int i = 0; i < VI; ++i) {
-      const int f = i * 256 + threadIdx.x, r = f / VB, blk = f % VB;
-      const _Float16 s = scale_pair<false>(r >= valid ? 0u : vsc[i])[0];
-      uint8_t* to = vs + st * W::kValBytes + r * (DV * 2);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) *(f16x8*)(to + ((2 * blk + x) ^ at_swz<DV>(r)) * 16) = fp4x8_f16(vc[i][x], s);
+      *(f16x8*)(ks + (kto ^ x) + st * W::kKeyBytes + i * (kRows * DQ * 2 + kBlocks * 32)) = fp4x8_f16(kc[i][j & 1], s);
+    } else {
+      i -= KI;
+      const _Float16 s = scale_pair<false>(vrow + i * vRows >= valid ? 0u : vsc[i])[0];
+      *(f16x8*)(vs + (vto ^ x) + st * W::kValBytes + i * (vRows * DV * 2)) = fp4x8_f16(vc[i][j & 1], s);
     }
   };
+  constexpr int kHalves = 2 * (KI + VI);
   int slot = slot_of(0);
-  load(slot);
+#pragma unroll
+  for (int i = 0; i < KI + VI; ++i) load(slot, i);
   slot = slot_of(1);
   W w;
   const float c = ldexpf(a.c, w.init(a.q + b * a.q_ts + hq * a.q_hs, lane));
-  put(0, n_keys);
-  if (n_tiles > 1) load(slot);
+#pragma unroll
+  for (int j = 0; j < kHalves; ++j) {
+    put(0, n_keys, j);
+    if (j & 1) load(slot, j >> 1);
+  }
   slot = slot_of(2);
   auto step = [&](auto stage, int t) {
     constexpr int st = decltype(stage)::value;
-    // tile t is in its stage; everyone is done with tile t - 1, whose stage is refilled
+    // tile t is in its stage; everyone is done with tile t - 1, whose stage is refilled (at the
+    // end with the last tile once more, which nothing reads)
     at_wait_barrier<63>();
     take_turns<0>(t);
-    if (t + 1 < n_tiles) put(st ^ 1, n_keys - (t + 1) * kF4Keys);
-    if (t + 2 < n_tiles) {
-      load(slot);
-      slot = slot_of(t + 3);
+    const int valid = n_keys - (t + 1) * kF4Keys, far = slot_of(t + 3);
+    auto refill = [&](int j) {
+      put(st ^ 1, valid, j);
+      if (j & 1) load(slot, j >> 1);
+    };
+    if (wrow >= rows) {
+#pragma unroll
+      for (int j = 0; j < kHalves; ++j) refill(j);
+      slot = far;
+      return;
     }
-    if (wrow >= rows) return;
-    w.scores(ks + st * W::kKeyBytes);
+    w.scores(ks + st * W::kKeyBytes, [&](int i) {
+#pragma unroll
+      for (int j = 0; j < kHalves; ++j)
+        if (i == j * W::kScoreOps / kHalves) refill(j);
+    });
+    slot = far;
     if (t == n_tiles - 1) w.mask(lane, n_keys - 1 - t * kF4Keys);
     w.weights(c);
     w.values(vs + st * W::kValBytes);
