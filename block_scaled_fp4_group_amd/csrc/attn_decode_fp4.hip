@@ -842,7 +842,7 @@ static Fp4Plan fp4_plan(int64_t B, const moe_attn_params& a, int64_t prefix_len,
   // would take.  Measured, us, wide / narrow (8 key heads of 128 + 128): 128 rows behind 8192
   // with 16 own keys 30 / 26, with 1024 32 / 32; 64 rows behind 32768 with 1024 36 / 33,
   // behind 2048 17 / 18.5; 768 rows behind 8192 with 16 58 / 64, behind 32768 137 / 194; 16 rows
-  // behind 32768 27 / 19.  Within 5% of the better at 540 of 605 sizes.
+  // behind 32768 27 / 19.  Within 5% of the better at 546 of 605 sizes.
   p.wide = prefix_len > 0 && (rows >= 384 || (rows >= 32 && max_len * 32768 >= G * prefix_len * dims));
   p.rb = G > 16 || (prefix_len > 0 && !p.wide && rows > 16) ? 2 : 1;
   p.blocks_p = (int32_t)up(rows, p.wide ? 128 : 16 * p.rb);
