@@ -6,9 +6,9 @@
 //
 // Memory traffic is all there is: a workgroup per row keeps the row in registers, so
 // x, residual and gate are read once and h and y written once.  8191 x 4096 with both norms and a
-// channel gate (268 MB): 55 us, 4.9 TB/s where a large copy reaches 5.1; non-temporal loads or
-// stores and 8 waves per row are within 5% of that.  64 x 4096: 3.2 us, a launch's latency.
-// Rows of up to 512 are one wave's (no barrier), of more than 8192 sixteen waves' (registers).
+// channel gate (268 MB): 54 us, 5.0 TB/s where a large copy reaches 5.1; non-temporal loads or
+// stores are within 5% of that, rows dealt to the XCDs in blocks 12% slower.  64 x 4096: 3.3 us, a
+// launch's latency.
 #include "common.h"
 
 namespace moe {
@@ -135,13 +135,9 @@ __global__ __launch_bounds__(WAVES * 64) void block_norm_kernel(BlockNormArgs a)
 
 int block_norm_max_hidden() { return 32768; }
 
-template <int WAVES>
+template <int WAVES, int N>
 static void launch_norm(const BlockNormArgs& a, int64_t T, hipStream_t stream) {
-  const int n = (a.hidden + WAVES * 512 - 1) / (WAVES * 512);
-  const dim3 grid((uint32_t)T), threads(WAVES * 64);
-  if (n <= 1) hipLaunchKernelGGL((block_norm_kernel<WAVES, 1>), grid, threads, 0, stream, a);
-  else if (n <= 2) hipLaunchKernelGGL((block_norm_kernel<WAVES, 2>), grid, threads, 0, stream, a);
-  else hipLaunchKernelGGL((block_norm_kernel<WAVES, 4>), grid, threads, 0, stream, a);
+  hipLaunchKernelGGL((block_norm_kernel<WAVES, N>), dim3((uint32_t)T), dim3(WAVES * 64), 0, stream, a);
 }
 
 moe_status launch_block_norm(const moe_rows& x, int64_t T, int hidden, const moe_rows* residual, const float* post_weight,
@@ -165,9 +161,16 @@ moe_status launch_block_norm(const moe_rows& x, int64_t T, int hidden, const moe
   a.scale = scale;
   a.eps = eps;
   a.inv = 1.0f / (float)hidden;
-  if (hidden <= 512) launch_norm<1>(a, T, stream);
-  else if (hidden <= 8192) launch_norm<4>(a, T, stream);
-  else launch_norm<16>(a, T, stream);
+  // as many waves as leave each thread one piece, if there are so many (8 for 4 with two pieces:
+  // 8191 x 4096 55.6 -> 53.8 us, 64 x 4096 4.3 -> 3.3; 16 for 4 with four: 4000 x 8192 59 -> 53; 2 for 4
+  // that are half empty: 20000 x 1024 42.6 -> 32.6)
+  if (hidden <= 512) launch_norm<1, 1>(a, T, stream);
+  else if (hidden <= 1024) launch_norm<2, 1>(a, T, stream);
+  else if (hidden <= 2048) launch_norm<4, 1>(a, T, stream);
+  else if (hidden <= 4096) launch_norm<8, 1>(a, T, stream);
+  else if (hidden <= 8192) launch_norm<16, 1>(a, T, stream);
+  else if (hidden <= 16384) launch_norm<16, 2>(a, T, stream);
+  else launch_norm<16, 4>(a, T, stream);
   return launch_status("moe_block_norm");
 }
 
