@@ -714,3 +714,33 @@ def test_block_norm_other_stream_and_graph():
         want = moe.block_norm(x, w, residual=r, post_weight=w)
         torch.cuda.synchronize()
         assert torch.equal(h, want[0]) and torch.equal(y, want[1]), i
+
+
+def test_two_calls_at_once():
+    """Two streams at the same time, each call with its own workspace and outputs, give the bits of one after the other."""
+    say("attn_decode_fp4, kv_free_pages, kv_compact, block_norm: two at once")
+    runs = [run_decode(15 + i, lens, prefix, 16, 8, 2, 128, 128) for i, (lens, prefix) in
+            enumerate((([6000, 3], 40), ([100, 900] * 20, 900)))]
+    tables = [pool(31 + i, 2000, 9, 16, 17000, SHAPES[:1]) for i in range(2)]
+    x = [bf16(40 + i, (300, 4096))[0] for i in range(2)]
+    w = dev_f32(np.linspace(0.5, 1.5, 4096).astype(np.float32))
+    inputs = [(r[2], r[3], dev_i32(t[0])[:, :9], dev_i32(t[1]), dev_u8(t[2][0]), dev_bf16(b)) for r, t, b in zip(runs, tables, x)]
+
+    def calls(at, **kw):
+        args, pre, table, lens, buf, rows = at
+        moved = buf.clone()
+        return [*moe.attn_decode_fp4(*args, **pre, want_lse=True, **kw), *moe.kv_free_pages(table, lens, 16, 17000, **kw),
+                *moe.kv_compact(table, lens, 16, [moved], **kw), moved, *moe.block_norm(rows, w, residual=rows, **kw)]
+
+    want = [calls(at) for at in inputs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for at, s in zip(inputs, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append(calls(at, stream=s))
+        torch.cuda.synchronize()
+        for g, h in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, h))
