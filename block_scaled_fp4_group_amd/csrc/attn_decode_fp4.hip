@@ -35,6 +35,7 @@
 // each SIMD, whose registers (232 to 254) leave no room for a third.  8 requests behind 777 keys, alone: 9.4 us,
 // five tiles one after the other.
 #include <algorithm>
+#include <cmath>
 
 #include "attn_common.h"
 #include "attn_join.h"
@@ -74,8 +75,17 @@ struct Fp4Args {
   int64_t own;
   int32_t num_requests, q_heads, kv_heads, num_pages, page_shift;
   float c, v_scale;
+  int32_t c_exp;                                    // scale times log2(e) times the keys' global is c 2^c_exp
   Fp4Plan plan;
 };
+
+// What a row's scores are multiplied by, its queries being f16 times 2^-e.  Multiplied by zero
+// or infinity a score of -inf (a key that is not there) or 0 would be NaN.  Scores are below
+// 2^34, so with the smallest normal number they are all next to zero, as with any below it; where
+// the factor passes 2^127, those whose row's largest query value counts pass float's range.
+__device__ __forceinline__ float score_factor(const Fp4Args& a, int e) {
+  return fminf(fmaxf(ldexpf(a.c, a.c_exp + e), 0x1p-126f), 0x1p127f);
+}
 
 __device__ __forceinline__ int f4_clamp_len(const Fp4Args& a, int len) { return (int)min((int64_t)max(len, 0), a.max_len); }
 __device__ __forceinline__ int f4_len_at(const Fp4Args& a, int b) {   // b uniform: a scalar load
@@ -162,7 +172,7 @@ struct Fp4Wave {
 #pragma unroll
     for (int k = 0; k < KS; ++k) q[rb][k] = __builtin_bit_cast(f16x8, *(const u32x4*)(row + column(lane >> 4, k)));
   }
-  __device__ __forceinline__ void init(int rb, float scale) {
+  __device__ __forceinline__ void init(int rb, const Fp4Args& a) {
     u32x4 x[KS];
     float most = 0.0f;
 #pragma unroll
@@ -172,7 +182,7 @@ struct Fp4Wave {
     const int e = query_exponent(quarter_max(most));
 #pragma unroll
     for (int k = 0; k < KS; ++k) q[rb][k] = query_f16(x[k], e);
-    c[rb] = ldexpf(scale, e);
+    c[rb] = score_factor(a, e);
 #pragma unroll
     for (int b = 0; b < OB; ++b) o[rb][b] = f32x4{0.f, 0.f, 0.f, 0.f};
     m[rb] = neg_inf();
@@ -508,7 +518,7 @@ __device__ __forceinline__ void fp4_narrow(const Fp4Args& a, int kvh, Fp4Cursor<
   // the requests of the list one after the other
   for (int b = at.b, rest = at.left, tile = at.tile, tiles = at.tiles;;) {
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) w.init(rb, a.c);
+    for (int rb = 0; rb < RB; ++rb) w.init(rb, a);
     // (with and without a next tile apart: loads that may or may not have gone out would be
     // waited for with the ones before them)
     while (next.left > 0 && now.b == b) step(std::true_type());
@@ -626,7 +636,7 @@ __device__ __forceinline__ void fp4_wide(const Fp4Args& a, int kvh, int part, in
   for (int i = 0; i < KI + VI; ++i) load(slot, i);
   slot = slot_of(1);
   W w;
-  const float c = ldexpf(a.c, w.init(a.q + b * a.q_ts + hq * a.q_hs, lane));
+  const float c = score_factor(a, w.init(a.q + b * a.q_ts + hq * a.q_hs, lane));
 #pragma unroll
   for (int j = 0; j < kHalves; ++j) {
     put(0, n_keys, j);
@@ -778,7 +788,7 @@ __global__ __launch_bounds__(WAVES * 64, fp4_small_per_cu(DQ, WAVES)) void attn_
     entry = entry_of(min(t + WAVES, n_tiles - 1));
     w.template load<false>(a, kvh, slot, lane);
   }
-  w.init(0, a.c);
+  w.init(0, a);
   auto step = [&](auto more) {
     const int last = t < tiles_p ? prefix - 1 - t * kF4Keys : len - 1 - (t - tiles_p) * kF4Keys;
     w.store(mine, lane, last);
@@ -962,7 +972,8 @@ moe_status launch_attn_decode_fp4(const moe_heads& q, const moe_kv_cache_fp4& ca
   a.kv_heads = p.kv_heads;
   a.num_pages = (int32_t)cache.num_pages;
   a.page_shift = __builtin_ctz((unsigned)cache.page_size);
-  a.c = p.scale * kLog2e * cache.k_global;
+  a.c = std::frexp(p.scale, &a.c_exp) * kLog2e;
+  a.c_exp += std::ilogb(cache.k_global);
   a.v_scale = cache.v_global;
   a.plan = fp4_plan(B, p, prefix_len, max_len);
   const int64_t entries = fp4_entries(a.plan, B, p.q_heads, p.kv_heads);

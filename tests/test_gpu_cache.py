@@ -278,6 +278,52 @@ def test_decode_queries_of_any_size():
     assert np.array_equal(bf16_to_f64(host_bf16_bits(got))[0, 2], v[pg[best], off[best], 0])
 
 
+FORMS = [([90, 0, 31], 40, 4, 1), ([5000, 3, 70], 0, 8, 2), ([90, 30], 2600, 8, 1), ([40, 0, 90] * 5, 2500, 8, 2)]   # alone, own keys in parts, prefix in parts, of 128 rows
+
+
+@pytest.mark.parametrize("D,Dv", HEADS)
+@pytest.mark.parametrize("lens,prefix,Hq,Hkv", FORMS)
+@pytest.mark.parametrize("kg", [1.0, 2.0 ** -20, 2.0 ** -32])
+def test_decode_tiny_queries_and_globals(D, Dv, lens, prefix, Hq, Hkv, kg):
+    """Scores next to zero weigh all keys alike, and keys that are not there count as none, however small the queries (the
+    smallest numbers of bf16 among them) and the keys' global scale are."""
+    say(f"attn_decode_fp4 {D}/{Dv} lens={lens[:3]} prefix={prefix}: tiny queries, keys of 2^{int(np.log2(kg))}")
+    c, q, args, pre, _, _ = run_decode(21, lens, prefix, 16, Hq, Hkv, D, Dv, kg=kg)
+    x = torch.from_numpy(q).float()
+    for h, e in enumerate((-101, -119, -126, -132)):
+        x[:, h::4] *= 2.0 ** e
+    x = x.to(torch.bfloat16)
+    out, lse = moe.attn_decode_fp4(x.cuda(), *args[1:], **pre, want_lse=True)
+    torch.cuda.synchronize()
+    check_decode(c, x.double().numpy(), D ** -0.5, bf16_to_f64(host_bf16_bits(out)), host(lse).astype(np.float64), "tiny queries")
+
+
+def test_decode_keys_of_zeros_and_huge_queries():
+    """Scores that are zero stay zero where the factor they are multiplied by is past float's range."""
+    say("attn_decode_fp4: keys of zeros, queries of 2^120, scales at both ends of float's range")
+    for lens, prefix, Hq, Hkv in FORMS:
+        c, q, args, pre, _, _ = run_decode(22, lens, prefix, 16, Hq, Hkv, 128, 128, kg=2.0 ** 32)
+        for t in (c.k, c.ks):
+            t[:] = 0
+        x = args[0] * 2.0 ** 120
+        assert torch.isfinite(x.float()).all()
+        out, lse = moe.attn_decode_fp4(x, c.cache(), *args[2:], **pre, want_lse=True)
+        torch.cuda.synchronize()
+        check_decode(c, bf16_to_f64(host_bf16_bits(x)), 128 ** -0.5, bf16_to_f64(host_bf16_bits(out)),
+                     host(lse).astype(np.float64), "keys of zeros")
+        # scale and global past float's range, the queries' size in it again: the bits of the same product at size one
+        c, q, args, pre, _, _ = run_decode(23, lens, prefix, 16, Hq, Hkv, 128, 128)
+        run = lambda q, cache, scale: moe.attn_decode_fp4(q, cache, *args[2:], **pre, scale=scale, want_lse=True)  # noqa: E731
+        want = run(args[0], args[1], 2.0 ** 29), run(args[0] * 0, args[1], 1.0)
+        c.kg = 2.0 ** 32
+        got = [run(args[0] * 2.0 ** -100, c.cache(), 2.0 ** 97)]
+        c.kg = 2.0 ** -32
+        got.append(run(args[0] * 2.0 ** 100, c.cache(), 2.0 ** -130))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
 def test_decode_other_stream_graph_and_workspace():
     say("attn_decode_fp4: repeated, on another stream, in graphs that share a workspace")
     for lens, prefix in (([100, 3], 40), ([5000, 3], 0), ([100, 3] * 20, 900)):
