@@ -54,8 +54,8 @@ __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
 // (caches held in 4 bits): a code times its block's scale is exact in it (6 significant
 // bits, 2^-10 to 2688), and a weight keeps 11 bits.  Its weights are lifted by 2^kLift, so
 // that those down to 2^-31 of a row's largest are not lost below its range (2^-24) while the
-// largest, 2^(kLift + kSlack) (see weights()) and twice that where m is rounded, stay under
-// 65504.
+// largest, 2^(kLift + kSlack) (see weights()) and twice that where a maximum less kLift is
+// rounded, by 1 at most, stay under 65504.
 struct AttnBf16 {
   typedef bf16x8 v8;
   static constexpr float kLift = 0.0f, kSlack = 8.0f;
@@ -72,6 +72,14 @@ struct AttnF16 {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
   }
 };
+
+// Whether a tile's maximum leaves a row's kept one behind.  Their difference, not the sum m +
+// kSlack: of scores past 2^24 that is rounded too, up to where a weight is 2^16, which f16 does
+// not hold.  (bf16 holds any weight.)
+template <class T>
+__device__ __forceinline__ bool has_grown(float mx, float m) {
+  return T::kLift == 0.0f ? mx > m + T::kSlack : mx - m > T::kSlack;
+}
 
 // a * b rounded, whatever comes after it
 __device__ __forceinline__ float mul_rounded(float a, float b) {
@@ -324,7 +332,6 @@ struct AttnWave {
   // precision), and a wave none of whose rows has grown so much skips the
   // multiplications.  The decision is the row's own, so its result does not
   // depend on the rows beside it.
-  static constexpr float kSlack = T::kSlack;
   __device__ __forceinline__ void weights(float c) {
     float mx = neg_inf();
 #pragma unroll
@@ -332,7 +339,7 @@ struct AttnWave {
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
     mx = T::kLift == 0.0f ? half_max(mx) * c : mul_rounded(half_max(mx), c) - T::kLift;
-    const bool grown = mx > m + kSlack;
+    const bool grown = has_grown<T>(mx, m);
     if (__any(grown)) {
       const float alpha = grown ? __builtin_amdgcn_exp2f(m - mx) : 1.0f;
       m = grown ? mx : m;

@@ -324,7 +324,7 @@ struct Fp4Wave {
 #pragma unroll
         for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[rb][t][i]);
       mx = mul_rounded(quarter_max(mx), c[rb]) - AttnF16::kLift;
-      const bool grown = mx > m[rb] + AttnF16::kSlack;
+      const bool grown = has_grown<AttnF16>(mx, m[rb]);
       if (__any(grown)) {
         const float alpha = grown ? __builtin_amdgcn_exp2f(m[rb] - mx) : 1.0f;
         m[rb] = grown ? mx : m[rb];

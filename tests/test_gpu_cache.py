@@ -324,6 +324,70 @@ def test_decode_keys_of_zeros_and_huge_queries():
             assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
 
 
+@pytest.mark.parametrize("lens,prefix,Hq,Hkv,every", [
+    ([1000], 0, 2, 1, 8), ([300] * 260, 0, 1, 1, 4),                                                  # alone: 8 and 4 waves
+    ([32798], 0, 8, 8, 4), ([9, 0, 70], 32790, 64, 8, 4), ([40, 0, 90] * 5, 2500, 8, 2, 1)])          # parts: own keys, prefix, 128 rows
+@pytest.mark.parametrize("bits", [24, 25, 26])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_decode_maxima_that_rise_by_8_far_from_zero(lens, prefix, Hq, Hkv, every, bits, sign):
+    """Scores of +-1.25 x 2^24 .. 2^26 (base 2), where maxima are rounded to multiples of 2 to 8, the largest in some tiles 8
+    over those in others: of a wave's successive tiles the second's has weights 2^8 the first's.
+
+    Scores are integers that float holds and the scale times log2(e) is 1 in float, so the weights are powers of two, exactly:
+    what is left is the result's rounding and that of the sums.  lse: the scale, ln 2, and the maximum with the weights' sum
+    are each rounded once, and the scale is 2^-24 off ln 2: 6 U of it."""
+    say(f"attn_decode_fp4 lens={lens[:2]} prefix={prefix}: maxima of {sign} x 1.25 x 2^{bits} that rise by 8")
+    c = Paged(24, lens, prefix, 16, Hkv, 128, 128)
+    c.k[:], c.ks[:] = 0, 0
+
+    def key(pages, n):
+        low = high = 0
+        for t in range(-(-n // 64)):
+            rows = [(pages[j // 16], j % 16) for j in range(64 * t, min(64 * t + 64, n))]
+            if sign < 0:                                              # the others far below
+                for p, r in rows:
+                    c.k[p, :, r, 0], c.ks[p, :, r, 0] = 7, 0x78       # 6 x 256
+            p, r = rows[0]
+            c.k[p, :, r, 0], c.ks[p, :, r, 0] = 6, 0x78               # 4 x 256
+            if t // every % 2:
+                c.k[p, :, r, 8], c.ks[p, :, r, 1] = 2, 0x38           # 1
+                high += 1
+            else:
+                low += 1
+        return low, high
+
+    counts = [key(c.ptab, prefix)] + [key(c.table[b], n) for b, n in enumerate(lens)]
+    q = np.zeros((len(lens), Hq, 128))
+    q[:, :, 0], q[:, :, 16] = sign * 1.25 * 2.0 ** (bits - 10), 8.0
+    out, lse = moe.attn_decode_fp4(torch.from_numpy(q).to(torch.bfloat16).cuda(), c.cache(), dev_i32(c.table)[:, :c.blocks],
+                                   dev_i32(np.array(lens)), max(lens), prefix_table=dev_i32(c.ptab), prefix_len=prefix,
+                                   scale=float(np.float32(np.log(2.0))), want_lse=True)
+    torch.cuda.synchronize()
+    out, lse = bf16_to_f64(host_bf16_bits(out)), host(lse).astype(np.float64)
+    values = c.values()[1]
+
+    def sums(pages, n):
+        s = np.zeros((2, Hkv, 128))
+        for t in range(-(-n // 64)):
+            s[t // every % 2] += values[pages[64 * t // 16], 0]       # a tile's first key is a page's first row
+        return s
+
+    front, G = sums(c.ptab, prefix), Hq // Hkv
+    for b, n in enumerate(lens):
+        s = front + sums(c.table[b], n)
+        low, high = counts[0][0] + counts[b + 1][0], counts[0][1] + counts[b + 1][1]
+        if low + high == 0:
+            assert np.all(out[b] == 0) and np.all(lse[b] == -np.inf)
+            continue
+        w = 2.0 ** -8 if high else 1.0
+        top, mass = sign * 1.25 * 2.0 ** bits + (8 if high else 0), w * low + high
+        want = ((w * s[0] + s[1]) / mass).repeat(G, 0)
+        # sums of low + high weights and products, the division
+        assert np.all(np.abs(out[b] - want) <= R * np.abs(want) + 2 * (low + high + 8) * U * np.abs(values[np.isfinite(values)]).max()), b
+        wl = top * np.log(2.0) + np.log(mass)
+        assert np.all(np.abs(lse[b] - wl) <= 6 * U * abs(wl) + (low + high + 8) * U), (b, lse[b], wl)
+
+
 def test_decode_other_stream_graph_and_workspace():
     say("attn_decode_fp4: repeated, on another stream, in graphs that share a workspace")
     for lens, prefix in (([100, 3], 40), ([5000, 3], 0), ([100, 3] * 20, 900)):
