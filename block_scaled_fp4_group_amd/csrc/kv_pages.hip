@@ -153,15 +153,16 @@ __global__ __launch_bounds__(kForkThreads) void kv_fork_kernel(ForkArgs a) {
 // ------------------------------------------------------------- live pages
 // Four times 64 entries, lanes side by side on rows of fewer than 64 (so many lanes to a row as
 // the power of two that holds it), under way at once behind their rows' lengths: bits of the
-// pages set by `set`.  wave of `waves`.
+// pages set by `set`.  wave of `waves`.  (Rows in 64 bits: all waves' together may be 16 times as
+// many as the table has.)
 template <class Set>
 __device__ __forceinline__ void mark_rows(const TableArgs& t, int wave, int waves, Set set) {
   const int shift = t.max_blocks > 32 ? 6 : (t.max_blocks <= 1 ? 0 : 32 - __builtin_clz(t.max_blocks - 1));
   const int lane = threadIdx.x & 63, sub = lane >> shift, per = 64 >> shift, step = 1 << shift;
-  for (int first = 4 * per * wave; first < t.rows; first += 4 * per * waves) {
+  for (int64_t first = (int64_t)(4 * per) * wave; first < t.rows; first += (int64_t)(4 * per) * waves) {
     int n[4], most = 0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) n[u] = held_pages(t, min(first + u * per + sub, t.rows - 1));
+    for (int u = 0; u < 4; ++u) n[u] = held_pages(t, (int)min(first + u * per + sub, (int64_t)t.rows - 1));
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       n[u] = first + u * per + sub < t.rows ? n[u] : 0;
@@ -377,8 +378,8 @@ __global__ __launch_bounds__(kMarkThreads) void kv_compact_plan_kernel(CompactAr
 // Rows of the table, and pages in chunks, by all workgroups.
 __global__ __launch_bounds__(256) void kv_compact_move_kernel(CompactArgs a) {
   const int n = a.ws[0], moves = a.ws[1];
-  for (int row = blockIdx.x; row < a.t.rows; row += gridDim.x) {
-    const int held = held_pages(a.t, row);
+  for (int64_t row = blockIdx.x; row < a.t.rows; row += gridDim.x) {
+    const int held = held_pages(a.t, (int)row);
     const int32_t* e = a.t.table + row * a.t.stride;
     int32_t* o = a.out + row * a.out_stride;
     for (int i = threadIdx.x; i < a.t.max_blocks; i += 256) {
@@ -436,7 +437,8 @@ static uint8_t* launch_marks(const TableArgs& t, int64_t alone, void* ws, int32_
   const int64_t bytes = mark_bytes(t.num_pages);
   hipLaunchKernelGGL(kv_clear_kernel, dim3((uint32_t)((bytes + 4095) / 4096)), dim3(256), 0, stream, marks, bytes, list,
                      (int)t.num_pages);
-  if (t.rows > 0) hipLaunchKernelGGL(kv_mark_kernel, dim3((uint32_t)((t.rows + 15) / 16)), dim3(256), 0, stream, t, marks);
+  const int64_t wgs = ((int64_t)t.rows + 15) / 16;                   // (they go on where there are more rows)
+  if (t.rows > 0) hipLaunchKernelGGL(kv_mark_kernel, dim3((uint32_t)(wgs < 65536 ? wgs : 65536)), dim3(256), 0, stream, t, marks);
   return marks;
 }
 

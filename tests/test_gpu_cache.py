@@ -700,6 +700,28 @@ def test_compact(rows, blocks, page, pages, in_place):
     assert np.array_equal(host(dt)[:, blocks:], table[:, blocks:]) and (in_place or np.array_equal(host(dt), table))
 
 
+@pytest.mark.parametrize("rows,blocks", [((1 << 25) + 70, 1), ((1 << 26) + 70, 2), ((1 << 20) + 300, 40)])
+def test_pages_of_tables_of_many_rows(rows, blocks):
+    """Row numbers that, taken 256 at a time by every wave, pass 2^31; more rows than one turn of all workgroups."""
+    say(f"kv_free_pages, kv_compact: {rows} rows of {blocks}")
+    page, pages = 16, 3000
+    rng = np.random.default_rng(blocks)
+    at = np.unique(np.concatenate([rng.integers(0, rows, 800), [0, 255, rows // 2, rows - 71, rows - 70, rows - 1]]))
+    lens, table = torch.zeros(rows, dtype=torch.int32, device="cuda"), torch.full((rows, blocks), -1, dtype=torch.int32, device="cuda")
+    n, entries = rng.integers(1, page * blocks + 1, len(at)), rng.integers(0, pages, (len(at), blocks))
+    lens[torch.from_numpy(at).cuda()], table[torch.from_numpy(at).cuda()] = dev_i32(n), dev_i32(entries)
+    want, counts = oc.free_pages(entries, n, page, pages)
+    f, c = moe.kv_free_pages(table, lens, page, pages)
+    buf = np.arange(pages * 16).astype(np.uint8).reshape(pages, 16) ^ rng.integers(0, 256, (pages, 1)).astype(np.uint8)
+    wt, (wb,), wc = oc.compact(entries, n, page, [buf])
+    db = dev_u8(buf)
+    out, cc = moe.kv_compact(table, lens, page, [db])
+    torch.cuda.synchronize()
+    assert np.array_equal(host(f), want) and np.array_equal(host(c), counts)
+    assert np.array_equal(host(out[torch.from_numpy(at).cuda()]), wt) and int((out >= 0).sum()) == int((wt >= 0).sum())
+    assert np.array_equal(host(db), wb) and np.array_equal(host(cc), wc)
+
+
 def test_pages_other_stream_and_graph():
     say("kv_fork, kv_free_pages, kv_compact: on another stream, in a graph")
     table, lens, bufs = pool(5, 30, 6, 16, 200, SHAPES, lens=[50] * 20 + [0] * 10)
