@@ -287,17 +287,19 @@ class AttentionLayer:
             self.held[c] = self.held[parent][:n // page] + (self._new_pages(1) if need else [])
 
     def release(self, requests: Sequence[int]):
-        """Requests end: what only they hold is free again."""
+        """Requests end: what only they hold is free again.  (Pools of up to 2^20 pages, as for compact().)"""
         requests = list(requests)
         if any(not 0 <= r < self.max_requests for r in requests):
             raise ValueError(f"requests are 0 .. {self.max_requests - 1}")
         if not requests:
             return
-        self.lens[torch.tensor(requests).to(self.lens.device)] = 0
+        lens, pages = self.lens.clone(), self.pool.numel()
+        lens[torch.tensor(requests).to(lens.device)] = 0
+        # (refused, for one of pools past its 2^20 pages, it leaves the layer as it was)
+        kv_free_pages(self.table, lens, self.page_size, pages, free_pages=self.pool, counts=self.counts[:2])
+        self.lens.copy_(lens)
         for r in requests:
             self.host_lens[r], self.held[r] = 0, []
-        pages = self.pool.numel()
-        kv_free_pages(self.table, self.lens, self.page_size, pages, free_pages=self.pool, counts=self.counts[:2])
         self.taken, self.free = 0, self.pool[:pages - self._in_use()]
 
     def compact(self) -> int:

@@ -147,3 +147,22 @@ def test_fork_without_a_page_left_is_refused(counting):
     with pytest.raises(ValueError, match="1 pages needed, 0 free"):
         layer.fork(0, [1])
     assert layer.host_lens == [20, 0, 0] and layer.calls[-1] != "kv_fork"
+
+
+def test_a_refused_page_call_leaves_the_layer_as_it_was(counting, monkeypatch):
+    """release() and compact() of pools that the page calls do not take: requests keep their tokens and pages."""
+    layer = counting
+
+    def refuse(*a, **kw):
+        raise RuntimeError("pages, at most")
+    layer.extend(rows(20), [0], [20])
+    layer.fork(0, [1])
+    layer.lens[:2] = 20
+    for name in ("kv_free_pages", "kv_compact"):
+        monkeypatch.setattr(moe.attention, name, refuse)
+    for call in (lambda: layer.release([0]), lambda: layer.release([0, 1]), layer.compact):
+        free, held = layer.free, [list(h) for h in layer.held]
+        with pytest.raises(RuntimeError, match="at most"):
+            call()
+        assert layer.lens.tolist() == [20, 20, 0] and layer.host_lens == [20, 20, 0]
+        assert layer.held == held and layer.free is free and layer.taken == 3
