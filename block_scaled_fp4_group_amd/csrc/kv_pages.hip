@@ -11,6 +11,8 @@
 //
 // A page's content is bytes here: up to eight buffers (keys and values, bf16 or codes
 // and scales), page p of each at p * page_bytes.
+#include <algorithm>
+
 #include "common.h"
 
 namespace moe {
@@ -77,8 +79,11 @@ struct ForkArgs {
 };
 
 // Workgroup (fork, slice): whether fork i needs a page, and how many before it do, is
-// counted by every workgroup itself (512 forks 7 us, 4096 20; 65536 1.9 ms).  Slice 0 writes the
-// child's row.
+// counted by every workgroup itself (of a last page that is whole only by slice 0), which writes
+// the child's row as slice 0 and copies its slice of the last page.  Pages of 16 KB, one slice: 512
+// forks 7 us, 4096 20, 16384 0.32 ms, 65536 7.8 ms.  Pages of 1 MB: 32 forks in 64 slices 10 us,
+// 512 in 8 98 us (1 GB), 4096 in one, 512 of them with a page left, 0.19 ms; in 64 slices, which all
+// count, 0.85 ms, and 16384 20 ms for 0.48.
 __global__ __launch_bounds__(kForkThreads) void kv_fork_kernel(ForkArgs a) {
   __shared__ int part[kForkThreads / 64];
   const int fork = blockIdx.x / (uint32_t)a.slices, slice = blockIdx.x % (uint32_t)a.slices;
@@ -90,6 +95,10 @@ __global__ __launch_bounds__(kForkThreads) void kv_fork_kernel(ForkArgs a) {
   };
   const int64_t mask = ((int64_t)1 << a.t.page_shift) - 1, cap = (int64_t)a.t.max_blocks << a.t.page_shift;
   auto length = [&](int row) { return min((int64_t)max(a.t.lens[row], 0), cap); };
+  if (slice > 0) {                                                  // only the page's copy: is there one?
+    int p, c;
+    if (!valid(fork, p, c) || (length(p) & mask) == 0) return;
+  }
   const bool last = fork == max(a.num_forks, 1) - 1 && slice == 0;
   int before = 0, all = 0;
   for (int i = threadIdx.x; i < (last ? a.num_forks : fork); i += kForkThreads) {
@@ -458,7 +467,10 @@ moe_status launch_kv_fork(int32_t* table, int64_t stride, int rows, int max_bloc
   a.num_forks = num_forks;
   a.buffers = page_buffers(buffers, &a.page_bytes);
   const int64_t slices = (a.page_bytes + kCopyChunk - 1) / kCopyChunk;
-  a.slices = (int)(slices < 1 ? 1 : (slices > 64 ? 64 : slices));
+  // (a page's copy by so many workgroups, as long as all forks' are not more than the chip holds
+  // twice over: each of them counts)
+  const int64_t most = std::min<int64_t>(64, std::max<int64_t>(1, 4096 / std::max(num_forks, 1)));
+  a.slices = (int)std::max<int64_t>(1, std::min(slices, most));
   const uint32_t grid = num_forks == 0 ? 1u : (uint32_t)num_forks * (uint32_t)a.slices;
   hipLaunchKernelGGL(kv_fork_kernel, dim3(grid), dim3(kForkThreads), 0, stream, a);
   return launch_status("moe_kv_fork");

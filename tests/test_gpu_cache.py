@@ -651,6 +651,25 @@ def test_fork(rows, blocks, page, forks, free, shapes):
         assert np.array_equal(host(g), w)
 
 
+@pytest.mark.parametrize("forks,free", [(1, 1), (6, 6), (700, 690), (5000, 60)])
+def test_fork_of_large_pages(forks, free):
+    """Pages that several workgroups copy, in the last part not a whole step; by fewer each for many forks, by one for 5000."""
+    say(f"kv_fork {forks} of large pages, {free} free")
+    rng = np.random.default_rng(forks)
+    shape = (1 << 20) + (1 << 14) + 48 if forks <= 6 else 100016 if forks < 1000 else 40000
+    rows, used = 2 * forks, 12
+    table, lens, (buf,) = pool(forks, rows, 3, 16, used, [(shape,)], beyond=free)
+    buf = np.concatenate([buf, np.zeros((free, shape), np.uint8)])
+    parents, children = rng.integers(0, forks, forks), forks + rng.permutation(forks)
+    fp = used + rng.permutation(free)
+    want = oc.fork(table[:, :3], lens, parents, children, fp, 16, [buf])
+    dt, dl, db = dev_i32(table), dev_i32(lens), dev_u8(buf)
+    counts = moe.kv_fork(dt[:, :3], dl, dev_i32(parents), dev_i32(children), dev_i32(fp), 16, [db])
+    torch.cuda.synchronize()
+    assert np.array_equal(host(dt)[:, :3], want[0]) and np.array_equal(host(dl), want[1]) and np.array_equal(host(counts), want[3])
+    assert np.array_equal(host(db), want[2][0])
+
+
 def test_fork_from_a_list_with_an_end():
     """The whole list of kv_free_pages, -1 behind its pages, and an entry past the pool: no page left there."""
     table, lens, bufs = pool(8, 12, 3, 16, 20, SHAPES, lens=[20, 33] + [0] * 10)
