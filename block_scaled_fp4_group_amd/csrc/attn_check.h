@@ -97,6 +97,9 @@ inline bool sizes_of_heads(const moe_attn_params* p) {
          p->k_dim >= 1 && p->k_dim <= 1024 && p->v_dim >= 1 && p->v_dim <= 1024;
 }
 
+// a launch's threads are counted in 32 bits
+inline bool launch_fits(int64_t workgroups, int64_t threads) { return workgroups * threads < ((int64_t)1 << 32); }
+
 // sizes that a plan is made for: rows and keys in 31 bits
 inline bool decode_sizes_fit(int32_t num_requests, int64_t prefix_len, int64_t max_len, const moe_attn_params& p) {
   return max_len <= 0x7fffffff - 64 && prefix_len <= 0x7fffffff - 64 && num_requests * ((max_len + 31) / 32) < 0x7fffffff &&

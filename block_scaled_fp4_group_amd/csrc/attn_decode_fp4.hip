@@ -903,9 +903,12 @@ static int64_t fp4_grid(const Fp4Plan& p, int kv_heads) {
   return ((int64_t)p.parts_p * p.blocks_p + (int64_t)p.runs * p.blocks_s) * kv_heads;
 }
 
-int64_t attn_decode_fp4_grid(int64_t B, const moe_attn_params& p, int64_t prefix_len, int64_t max_len) {
+// Threads of the larger of both launches.
+int64_t attn_decode_fp4_threads(int64_t B, const moe_attn_params& p, int64_t prefix_len, int64_t max_len) {
   const Fp4Plan plan = fp4_plan(B, p, prefix_len, max_len);
-  return plan.small ? B * p.kv_heads : fp4_grid(plan, p.kv_heads);
+  if (plan.small) return B * p.kv_heads * plan.small * 64;
+  return std::max(fp4_grid(plan, p.kv_heads) * kF4Waves * 64,
+                  (B * p.q_heads + 3) * 64 * join_waves(plan.parts_p, 1, plan.runs, (int)B));
 }
 
 template <int DQ, int DV>

@@ -139,14 +139,19 @@ __global__ __launch_bounds__(WPR <= 4 ? 256 : WPR * 64) void attn_join_kernel(Jo
   if (a.lse && lane == 0) a.lse[at_row] = L == 0.0f ? neg_inf() : (M + __builtin_amdgcn_logf(L)) * kLn2;
 }
 
+// Waves per row: as many as leave each 8 parts or so, one round of loads (a request's own
+// parts: run_parts per run it lies in, on average runs / requests of them).
+inline int join_waves(int prefix_parts, int run_parts, int runs, int num_requests) {
+  const int parts = prefix_parts + run_parts * (1 + runs / num_requests);
+  return parts <= 16 ? 1 : (parts <= 48 ? 4 : 16);
+}
+
 template <int DV>
 static void launch_join(const JoinArgs& a, hipStream_t stream) {
   const uint32_t rows = (uint32_t)(a.num_requests * a.q_heads);
-  // waves per row: as many as leave each 8 parts or so, one round of loads (a
-  // request's own parts: run_parts per run it lies in, on average runs / requests of them)
-  const int parts = a.prefix_parts + a.run_parts * (1 + a.runs / a.num_requests);
-  if (parts <= 16) hipLaunchKernelGGL((attn_join_kernel<DV, 1>), dim3((rows + 3) / 4), dim3(256), 0, stream, a);
-  else if (parts <= 48) hipLaunchKernelGGL((attn_join_kernel<DV, 4>), dim3(rows), dim3(256), 0, stream, a);
+  const int waves = join_waves(a.prefix_parts, a.run_parts, a.runs, a.num_requests);
+  if (waves == 1) hipLaunchKernelGGL((attn_join_kernel<DV, 1>), dim3((rows + 3) / 4), dim3(256), 0, stream, a);
+  else if (waves == 4) hipLaunchKernelGGL((attn_join_kernel<DV, 4>), dim3(rows), dim3(256), 0, stream, a);
   else hipLaunchKernelGGL((attn_join_kernel<DV, 16>), dim3(rows), dim3(1024), 0, stream, a);
 }
 

@@ -9,6 +9,8 @@
 // channel gate (268 MB): 54 us, 5.0 TB/s where a large copy reaches 5.1; non-temporal loads or
 // stores are within 5% of that, rows dealt to the XCDs in blocks 12% slower.  64 x 4096: 3.3 us, a
 // launch's latency.
+#include <algorithm>
+
 #include "common.h"
 
 namespace moe {
@@ -135,9 +137,18 @@ __global__ __launch_bounds__(WAVES * 64) void block_norm_kernel(BlockNormArgs a)
 
 int block_norm_max_hidden() { return 32768; }
 
+// (2^21 rows at a time: a launch's threads are counted in 32 bits)
 template <int WAVES, int N>
-static void launch_norm(const BlockNormArgs& a, int64_t T, hipStream_t stream) {
-  hipLaunchKernelGGL((block_norm_kernel<WAVES, N>), dim3((uint32_t)T), dim3(WAVES * 64), 0, stream, a);
+static void launch_norm(BlockNormArgs a, int64_t T, hipStream_t stream) {
+  const int64_t most = (int64_t)1 << 21;
+  for (; T > 0; T -= most) {
+    hipLaunchKernelGGL((block_norm_kernel<WAVES, N>), dim3((uint32_t)std::min(T, most)), dim3(WAVES * 64), 0, stream, a);
+    a.x += most * a.x_ts;
+    a.residual += a.residual ? most * a.r_ts : 0;
+    a.gate += a.gate ? most * a.g_ts : 0;
+    a.h += a.h ? most * a.h_ts : 0;
+    a.y += a.y ? most * a.y_ts : 0;
+  }
 }
 
 moe_status launch_block_norm(const moe_rows& x, int64_t T, int hidden, const moe_rows* residual, const float* post_weight,

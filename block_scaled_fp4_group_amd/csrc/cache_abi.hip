@@ -12,8 +12,9 @@ moe_status launch_kv_gather(const moe_kv_cache&, int, int, int, const int32_t*, 
 moe_status launch_kv_gather_fp4(const moe_kv_cache_fp4&, int, int, int, const int32_t*, int64_t, int, const int32_t*, int64_t,
                                 const int32_t*, int, int64_t, const moe_heads&, const moe_heads&, hipStream_t);
 int64_t kv_gather_grid(int64_t, int);
+int64_t qk_norm_rope_fp4_threads(int64_t, const moe_rope_params&);
 size_t attn_decode_fp4_ws_bytes(int64_t, const moe_attn_params&, int64_t, int64_t);
-int64_t attn_decode_fp4_grid(int64_t, const moe_attn_params&, int64_t, int64_t);
+int64_t attn_decode_fp4_threads(int64_t, const moe_attn_params&, int64_t, int64_t);
 moe_status launch_attn_decode_fp4(const moe_heads&, const moe_kv_cache_fp4&, const int32_t*, int64_t, const int32_t*, int64_t,
                                   int64_t, const int32_t*, int64_t, const moe_attn_params&, const moe_heads&, float*, void*,
                                   hipStream_t);
@@ -95,7 +96,7 @@ static moe_status check_gather(const char* fn, int32_t kv_heads, int32_t k_dim, 
   MOE_CHECK(max_blocks >= 0 && prefix_blocks >= 0 && prefix_len >= 0, "%s: negative size", fn);
   MOE_CHECK(cu_k, "%s: cu_k is NULL", fn);
   MOE_CHECK(total_k <= 0x7fffffff, "%s: over 2^31 - 1 rows", fn);
-  MOE_CHECK(kv_gather_grid(total_k, kv_heads) < ((int64_t)1 << 31), "%s: too many rows", fn);
+  MOE_CHECK(launch_fits(kv_gather_grid(total_k, kv_heads), 256), "%s: too many rows", fn);
   MOE_CHECK(table_stride >= max_blocks && (max_blocks == 0 || block_table), "%s: block_table NULL or its stride too small", fn);
   MOE_CHECK(prefix_len <= (int64_t)prefix_blocks * page_size, "%s: prefix_len %lld needs more than %d pages", fn,
             (long long)prefix_len, prefix_blocks);
@@ -129,7 +130,7 @@ moe_status moe_qk_norm_rope_fp4(const moe_heads* q, const moe_heads* k, const mo
   MOE_PASS(check_cache_fp4(fn, cache));
   MOE_CHECK(slots, "%s: slots is NULL", fn);
   MOE_PASS(check_heads(fn, "v", v, p->kv_heads, p->v_dim, 0));
-  MOE_CHECK(T * (p->q_heads + 2 * (int64_t)p->kv_heads) < ((int64_t)1 << 31), "%s: too many heads", fn);
+  MOE_CHECK(launch_fits(qk_norm_rope_fp4_threads(T, *p), 1), "%s: too many heads", fn);
   return launch_qk_norm_rope_fp4(*q, *k, *v, T, *p, positions, cos_sin, q_weight, k_weight, *q_out, k_out, *cache, slots,
                                  stream);
 }
@@ -166,7 +167,7 @@ moe_status moe_attn_decode_fp4(const moe_heads* q, const moe_kv_cache_fp4* cache
   MOE_CHECK(prefix_len == 0 || prefix_table, "%s: prefix_table is NULL", fn);
   MOE_CHECK(decode_sizes_fit(num_requests, prefix_len, max_len, *p), "%s: too many keys or rows", fn);
   MOE_CHECK(aligned4(lse), "%s: lse not 4-byte aligned", fn);
-  MOE_CHECK(attn_decode_fp4_grid(num_requests, *p, prefix_len, max_len) < ((int64_t)1 << 31), "%s: too many rows", fn);
+  MOE_CHECK(launch_fits(attn_decode_fp4_threads(num_requests, *p, prefix_len, max_len), 1), "%s: too many rows", fn);
   MOE_PASS(check_workspace(fn, workspace, workspace_bytes, attn_decode_fp4_ws_bytes(num_requests, *p, prefix_len, max_len)));
   return launch_attn_decode_fp4(*q, *cache, block_table, table_stride, lens, num_requests, max_len, prefix_table, prefix_len,
                                 *p, *out, lse, workspace, stream);

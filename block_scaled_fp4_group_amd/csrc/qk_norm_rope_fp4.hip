@@ -281,24 +281,31 @@ __global__ __launch_bounds__(kRopeThreads) void qk_norm_rope_fp4_kernel(RopeFp4A
 // all three takes their times one after the other (64 tokens x 16/2 x 64: 9 us a token at a
 // time, 4 us eight).  No more than that: the rows of a token lie together (8191 x 64/4 x 192:
 // 92 us one at a time, 99 us four or sixteen).
+static int lanes_per_item(int head_dim) { return head_dim == 64 ? 4 : (head_dim == 128 ? 8 : 16); }
+static int64_t rope_fp4_tokens(int64_t groups, int64_t heads, int lanes) {
+  int64_t n = 1;
+  while (n * groups * lanes % 64 != 0 || n * heads * lanes % 64 != 0) n *= 2;   // (up to 64 / lanes)
+  return n;
+}
+static int64_t rope_fp4_items(int64_t T, const moe_rope_params& p) {
+  const int64_t groups = (p.q_heads + QH - 1) / QH, heads = p.kv_heads, n = rope_fp4_tokens(groups, heads, lanes_per_item(p.head_dim));
+  return (T + n - 1) / n * n * (groups + 2 * heads);
+}
+int64_t qk_norm_rope_fp4_threads(int64_t T, const moe_rope_params& p) { return rope_fp4_items(T, p) * lanes_per_item(p.head_dim) + kRopeThreads; }
+
 template <int D, bool INTERLEAVED, bool FAR>
-static void launch_items(RopeFp4Args p, hipStream_t stream) {
-  constexpr int kLanes = D / 16;
-  constexpr int LPH = kLanes <= 4 ? 4 : (kLanes <= 8 ? 8 : 16);
-  const int64_t groups = (p.r.q_heads + QH - 1) / QH, heads = p.r.kv_heads, per = kRopeThreads / LPH;
-  p.tokens = 1;
-  while (p.tokens * groups * LPH % 64 != 0 || p.tokens * heads * LPH % 64 != 0) p.tokens *= 2;   // (up to 64 / LPH)
-  const int64_t items = (p.r.T + p.tokens - 1) / p.tokens * p.tokens * (groups + 2 * heads);
+static void launch_items(const RopeFp4Args& p, int64_t items, hipStream_t stream) {
+  const int64_t per = kRopeThreads / lanes_per_item(D);
   hipLaunchKernelGGL((qk_norm_rope_fp4_kernel<D, INTERLEAVED, FAR>), dim3((uint32_t)((items + per - 1) / per)),
                      dim3(kRopeThreads), 0, stream, p);
 }
 
 template <int D>
-static void launch_rope_fp4(const RopeFp4Args& p, bool interleaved, hipStream_t stream) {
+static void launch_rope_fp4(const RopeFp4Args& p, int64_t items, bool interleaved, hipStream_t stream) {
   // (outputs larger than half of the 256 MB cache before HBM: see qk_norm_rope.hip)
   const bool far = p.r.T * p.r.q_heads * D * 2 > ((int64_t)128 << 20);
-  if (interleaved) far ? launch_items<D, true, true>(p, stream) : launch_items<D, true, false>(p, stream);
-  else far ? launch_items<D, false, true>(p, stream) : launch_items<D, false, false>(p, stream);
+  if (interleaved) far ? launch_items<D, true, true>(p, items, stream) : launch_items<D, true, false>(p, items, stream);
+  else far ? launch_items<D, false, true>(p, items, stream) : launch_items<D, false, false>(p, items, stream);
 }
 
 moe_status launch_qk_norm_rope_fp4(const moe_heads& q, const moe_heads& k, const moe_heads& v, int64_t T,
@@ -314,11 +321,13 @@ moe_status launch_qk_norm_rope_fp4(const moe_heads& q, const moe_heads& k, const
   a.v_codes = (uint8_t*)cache.v;
   a.v_scales = (uint8_t*)cache.v_scale;
   a.page_shift = __builtin_ctz((unsigned)cache.page_size);
+  a.tokens = (uint32_t)rope_fp4_tokens((p.q_heads + QH - 1) / QH, p.kv_heads, lanes_per_item(p.head_dim));
+  const int64_t items = rope_fp4_items(T, p);
   a.k_inv = 1.0f / cache.k_global;
   a.v_inv = 1.0f / cache.v_global;
-  if (p.head_dim == 64) launch_rope_fp4<64>(a, p.interleaved, stream);
-  else if (p.head_dim == 128) launch_rope_fp4<128>(a, p.interleaved, stream);
-  else launch_rope_fp4<192>(a, p.interleaved, stream);
+  if (p.head_dim == 64) launch_rope_fp4<64>(a, items, p.interleaved, stream);
+  else if (p.head_dim == 128) launch_rope_fp4<128>(a, items, p.interleaved, stream);
+  else launch_rope_fp4<192>(a, items, p.interleaved, stream);
   return launch_status("moe_qk_norm_rope_fp4");
 }
 

@@ -175,6 +175,20 @@ def test_block_norm_refuses():
     refuses(norm(T=0), OK)
 
 
+def test_sizes_past_a_launch_are_refused():
+    """A launch's threads are counted in 32 bits: by name, not by the launch."""
+    for kw in (dict(q_heads=64, kv_heads=8, head_dim=192, T=1 << 23), dict(q_heads=4, kv_heads=2, head_dim=64, T=1 << 28)):
+        D, hq, hkv = kw["head_dim"], kw["q_heads"], kw["kv_heads"]
+        refuses(rope(q=heads(hq, D), k=heads(hkv, D), v=heads(hkv, 128), qo=heads(hq, D), **kw), INVALID)
+        assert b"too many heads" in moe.lib.moe_last_error()
+    for kw in (dict(B=1 << 20, hq=64, hkv=64, most=100), dict(B=1 << 20, hq=64, hkv=1, most=1 << 13, blocks=512, stride=512)):
+        refuses(decode(**{**dict(prefix=0), **kw}), INVALID)
+        assert b"too many rows" in moe.lib.moe_last_error()
+    for fp4 in (True, False):
+        refuses(gather(fp4, total=1 << 25, H=16, ko=heads(16, 64), vo=heads(16, 64)), INVALID)
+        assert b"too many rows" in moe.lib.moe_last_error()
+
+
 # --------------------------------------------------------------- Python's side
 def test_wrappers_refuse_before_the_library():
     x, i = torch.zeros((2, 2, 128), dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)

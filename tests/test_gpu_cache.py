@@ -844,6 +844,18 @@ def test_block_norm_one_row_for_all_zeros_and_infinities():
     assert h.shape == (0, 64) and y.shape == (0, 64)
 
 
+def test_block_norm_more_rows_than_a_launch_takes():
+    say("block_norm: 2^26 rows and some")
+    T, hidden = (1 << 26) + 5, 8
+    x = torch.empty((T, hidden), dtype=torch.bfloat16, device="cuda").normal_()
+    r, g = x[:1].expand(T, hidden), x.flip(1)
+    w = dev_f32(np.linspace(0.5, 1.5, hidden).astype(np.float32))
+    h, y = moe.block_norm(x, w, residual=r, gate=g)
+    for a, b in ((0, 300), ((1 << 21) - 150, (1 << 21) + 150), (33 * (1 << 20), 33 * (1 << 20) + 300), (T - 300, T)):
+        hs, ys = moe.block_norm(x[a:b], w, residual=r[a:b], gate=g[a:b])
+        assert torch.equal(h[a:b], hs) and torch.equal(y[a:b], ys), a
+
+
 def test_block_norm_other_stream_and_graph():
     say("block_norm: on another stream, in a graph")
     x, r = (dev_bf16(synth.random_bf16(i, (100, 1024))) for i in (1, 2))
