@@ -221,6 +221,22 @@ def test_decode_agrees_with_the_gathered_cache(D, Dv, lens, prefix):
     assert (out.float() - ref.float()).abs().max() <= 4 * R * vmax
 
 
+@pytest.mark.parametrize("D,Dv", HEADS)
+@pytest.mark.parametrize("lens,prefix", [([33, 200, 0], 50), ([33, 6000, 0], 0), ([33, 0, 200] * 6, 1500)])
+def test_decode_lse_agrees_with_the_gathered_cache(D, Dv, lens, prefix):
+    """-inf for the same rows, a number for every other, as near as test_decode_agrees_with_the_gathered_cache asks."""
+    say(f"attn_decode_fp4 against attn_decode {D}/{Dv} {lens[:3]}: lse")
+    c, q, args, pre, out, lse = run_decode(6, lens, prefix, 16, 8, 2, D, Dv)
+    k, v = c.values()
+    to = lambda a: dev_f32(np.nan_to_num(a, nan=0.0).astype(np.float32)).to(torch.bfloat16)  # noqa: E731
+    ref, rl = moe.attn_decode(args[0], to(k), to(v), *args[2:], **pre, want_lse=True)
+    torch.cuda.synchronize()
+    none = torch.tensor([n + prefix == 0 for n in lens], device="cuda")[:, None].expand(lse.shape)
+    assert torch.equal(lse == -np.inf, none) and torch.equal(rl == -np.inf, none)
+    assert torch.isfinite(lse[~none]).all() and torch.isfinite(rl[~none]).all() and torch.isfinite(out.float()).all()
+    assert (lse[~none] - rl[~none]).abs().max() < 1e-4
+
+
 def test_decode_bad_entries_stay_inside():
     """Table entries that are no page never address memory outside the cache (results of those requests: unspecified)."""
     say("attn_decode_fp4: bad table entries")
@@ -907,3 +923,46 @@ def test_two_calls_at_once():
         torch.cuda.synchronize()
         for g, h in zip(got, want):
             assert all(torch.equal(a, b) for a, b in zip(g, h))
+
+
+def test_two_writes_forks_and_read_backs_at_once():
+    """Two streams at the same time, each with a cache and a table of its own."""
+    say("qk_norm_rope_fp4, kv_fork, kv_gather_fp4, kv_gather: two at once")
+    T, H, D, page, rows = 700, 4, 128, 16, 40
+    cs = dev_f32(synth.random_bf16(3, (T, 64)).astype(np.float32) / 65536)
+    at = []
+    for i in range(2):
+        x = dev_bf16(bf16(50 + i, (T, 3 * H, D))[0])
+        table, lens, _ = pool(60 + i, rows, 4, page, 100, [], lens=[37, 20] * (rows // 2))
+        order = np.random.default_rng(i).permutation(rows)
+        par, chi = dev_i32(np.repeat(order[:8], 2)), dev_i32(order[8:24])
+        cache = moe.Fp4Cache.zeros(130, page, H, D, D)
+        wide = dev_bf16(bf16(70 + i, (130, page, H, D))[0])
+        slots = dev_i32(np.random.default_rng(9 + i).permutation(130 * page)[:T])
+        at.append((x, dev_i32(table)[:, :4], dev_i32(lens), par, chi, cache, wide, slots))
+    positions, free = dev_i32(np.arange(T)), dev_i32(100 + np.arange(30))
+    cu = dev_i32(np.arange(rows + 1) * 20)
+
+    def calls(a, **kw):
+        x, table, lens, par, chi, cache, wide, slots = a
+        for t in cache.buffers:
+            t.zero_()
+        table, lens, wide = table.clone(), lens.clone(), wide.clone()
+        q, k = moe.qk_norm_rope_fp4(x[:, :H], x[:, H:2 * H], x[:, 2 * H:], positions, cs, cache, slots, **kw)
+        counts = moe.kv_fork(table, lens, par, chi, free, page, [*cache.buffers, wide], **kw)
+        return [q, k, counts, table, lens, *moe.kv_gather_fp4(cache, table, cu, 20 * rows, **kw),
+                *moe.kv_gather(wide, wide, table, cu, 20 * rows, **kw), *(t.clone() for t in cache.buffers)]
+
+    want = [calls(a) for a in at]
+    torch.cuda.synchronize()
+    assert all((w[0] != 0).any() and (w[5] != 0).any() and (w[7] != 0).any() and host(w[2]).tolist() == [16, 16] for w in want)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for a, s in zip(at, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append(calls(a, stream=s))
+        torch.cuda.synchronize()
+        for g, h in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(g, h))
