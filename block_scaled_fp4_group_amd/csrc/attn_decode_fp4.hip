@@ -30,10 +30,13 @@
 // codes: 4 us), the waves' unequal ends and the join's launch.  48 requests of up to
 // 16384 keys (64 / 4 heads of 192 + 128, 268 MB): 54 + 5 us; their lists of unequal requests
 // end unevenly, a CU's older workgroups 10 us before its younger ones -- turns by wave
-// priority moved that by nothing.  Prefix: 96 requests behind 32768 keys 155 + 8 us, 0.83 PFLOP/s;
-// matrix cores 37% busy, vector work (conversions, exponentials) 45%, LDS 47%, on two waves for
-// each SIMD, whose registers (232 to 254) leave no room for a third.  8 requests behind 777 keys, alone: 9.4 us,
-// five tiles one after the other.
+// priority moved that by nothing.  Prefix: 96 requests behind 32768 keys (64 / 4 heads of 192 +
+// 128) 155 + 8 us, 0.83 PFLOP/s; matrix cores 39% busy, vector work (conversions, exponentials)
+// 45%, LDS 40%, on two waves for each SIMD, whose registers (232 to 255) leave no room for a
+// third.  64 behind 8192 (64 / 8 of 128 + 128) 38 + 7 us, 0.45 PFLOP/s, 17%, 27%, 18%: a workgroup
+// has few tiles to its fill, its parts (29 MB in all) and the join.  8 requests behind 777 keys,
+// alone: 9.3 us, 64 workgroups on 256 CUs, whose waves take up to three tiles one after the other
+// (of one tile 6.4 us, of two 8.6, of four 12.8, of eight 21.4: 2.1 each).
 #include <algorithm>
 #include <cmath>
 
@@ -762,7 +765,7 @@ __global__ __launch_bounds__(kF4Waves * 64, fp4_per_cu(DQ, RB, WIDE)) void attn_
 }
 
 // Few keys: a workgroup per request and key head answers alone, without parts and a
-// second launch.  Its eight waves take every eighth tile, the prefix's first.  At most 16
+// second launch.  Its WAVES waves take every WAVES-th tile, the prefix's first.  At most 16
 // heads of a key head.
 template <int DQ, int DV, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, fp4_small_per_cu(DQ, WAVES)) void attn_decode_fp4_small_kernel(Fp4Args a) {
@@ -852,7 +855,10 @@ static Fp4Plan fp4_plan(int64_t B, const moe_attn_params& a, int64_t prefix_len,
   // would take.  Measured, us, wide / narrow (8 key heads of 128 + 128): 128 rows behind 8192
   // with 16 own keys 30 / 26, with 1024 32 / 32; 64 rows behind 32768 with 1024 36 / 33,
   // behind 2048 17 / 18.5; 768 rows behind 8192 with 16 58 / 64, behind 32768 137 / 194; 16 rows
-  // behind 32768 27 / 19.  Within 5% of the better at 546 of 605 sizes.
+  // behind 32768 27 / 19.  Within 5% of the better at 546 of 605 sizes, 25% or more behind it at
+  // 15, with few own keys: 192 rows behind 32768 with 300 55 / 79 (narrow taken), 256 of one query
+  // head behind 8192 with 16 38 / 58 (narrow), 768 of 4 key heads of 192 + 128 behind 32768 with 16
+  // 129 / 100 (wide).
   p.wide = prefix_len > 0 && (rows >= 384 || (rows >= 32 && max_len * 32768 >= G * prefix_len * dims));
   p.rb = G > 16 || (prefix_len > 0 && !p.wide && rows > 16) ? 2 : 1;
   p.blocks_p = (int32_t)up(rows, p.wide ? 128 : 16 * p.rb);
