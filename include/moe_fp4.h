@@ -617,7 +617,7 @@ moe_status moe_attn_decode_fp4(const moe_heads* q, const moe_kv_cache_fp4* cache
  *   cu_k int32 [num_seqs + 1], not descending, from 0 to total_k; rows outside the
  *   ranges keep their values.  Rows whose page the table does not name (-1, or past
  *   max_blocks) are zeros.  Head sizes: multiples of 16 up to 1024.
- * num_seqs == 0 or total_k == 0 is a no-op.  One launch; total_k * kv_heads up to 2^28 - 2^20.
+ * num_seqs == 0 or total_k == 0 is a no-op.  One launch; (total_k + 31) * kv_heads < 2^28.
  */
 moe_status moe_kv_gather(const moe_kv_cache* cache, int32_t kv_heads, int32_t k_dim, int32_t v_dim,
                          const int32_t* block_table, int64_t table_stride, int32_t max_blocks, const int32_t* prefix_table,
