@@ -277,11 +277,11 @@ __global__ __launch_bounds__(kRopeThreads) void qk_norm_rope_fp4_kernel(RopeFp4A
   }
 }
 
+static int lanes_per_item(int head_dim) { return head_dim == 64 ? 4 : (head_dim == 128 ? 8 : 16); }
 // As few tokens together as make whole waves of items of one kind: a wave whose lanes are of
 // all three takes their times one after the other (64 tokens x 16/2 x 64: 9 us a token at a
 // time, 4 us eight).  No more than that: the rows of a token lie together (8191 x 64/4 x 192:
 // 92 us one at a time, 99 us four or sixteen).
-static int lanes_per_item(int head_dim) { return head_dim == 64 ? 4 : (head_dim == 128 ? 8 : 16); }
 static int64_t rope_fp4_tokens(int64_t groups, int64_t heads, int lanes) {
   int64_t n = 1;
   while (n * groups * lanes % 64 != 0 || n * heads * lanes % 64 != 0) n *= 2;   // (up to 64 / lanes)
@@ -291,7 +291,10 @@ static int64_t rope_fp4_items(int64_t T, const moe_rope_params& p) {
   const int64_t groups = (p.q_heads + QH - 1) / QH, heads = p.kv_heads, n = rope_fp4_tokens(groups, heads, lanes_per_item(p.head_dim));
   return (T + n - 1) / n * n * (groups + 2 * heads);
 }
-int64_t qk_norm_rope_fp4_threads(int64_t T, const moe_rope_params& p) { return rope_fp4_items(T, p) * lanes_per_item(p.head_dim) + kRopeThreads; }
+// (a last workgroup's idle threads among them)
+int64_t qk_norm_rope_fp4_threads(int64_t T, const moe_rope_params& p) {
+  return rope_fp4_items(T, p) * lanes_per_item(p.head_dim) + kRopeThreads;
+}
 
 template <int D, bool INTERLEAVED, bool FAR>
 static void launch_items(const RopeFp4Args& p, int64_t items, hipStream_t stream) {
