@@ -529,6 +529,33 @@ def test_write(T, Hq, Hkv, D, Dv, rot, inter, norm, page, keep):
         assert np.array_equal(host(g), w), name
 
 
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,inter", [(33, 5, 5, 192, 64, True), (70, 16, 4, 64, 32, False), (129, 6, 2, 128, 128, False),
+                                                  (6000, 64, 4, 192, 64, True), (6000, 64, 4, 192, 96, False)])   # the last two past 128 MB
+def test_write_in_place(T, Hq, Hkv, D, rot, inter):
+    """q_out and k_out the rows of the projection that q and k come from: the same bits, v and the columns beside them kept."""
+    say(f"qk_norm_rope_fp4 in place, T={T} heads {Hq}/{Hkv} x {D}")
+    torch.manual_seed(T + D)
+    rows = torch.randn((T, (Hq + 2 * Hkv) * D + 8), device="cuda").to(torch.bfloat16)
+    w = torch.rand((2, D), device="cuda") + 0.5
+    cs = torch.rand((T, rot), device="cuda") * 2 - 1
+    pages = -(-T // 16)
+    slots = torch.randperm(pages * 16, device="cuda")[:T].int()
+
+    def call(rows, **kw):
+        q, k, v = (rows[:, i * D:(i + h) * D].unflatten(1, (h, D)) for i, h in ((0, Hq), (Hq, Hkv), (Hq + Hkv, Hkv)))
+        cache = moe.Fp4Cache.zeros(pages, 16, Hkv, D, D)
+        kw = dict(q_out=q, k_out=k) if kw else {}
+        return [*moe.qk_norm_rope_fp4(q, k, v, torch.arange(T, device="cuda").int(), cs, cache, slots, w[0], w[1], 1e-6, inter, **kw),
+                *cache.buffers]
+
+    want = call(rows)
+    own = rows.clone()
+    got = call(own, in_place=True)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(own[:, (Hq + Hkv) * D:], rows[:, (Hq + Hkv) * D:])
+    assert not torch.equal(own[:, :D], rows[:, :D])
+
+
 def test_write_special_values():
     """Without norm and rotation the rows are quantize_nvfp4's, byte for byte, infinities, NaN and ties among them."""
     say("qk_norm_rope_fp4: any bf16 values, against quantize_nvfp4")
